@@ -69,8 +69,8 @@ VARIANT_NAMES = {
 
 LIB_PATH = _build.LIB_PATH
 
-# The exported symbols, as declared in include/retro_out_prod.h and
-# include/retro_probe.h.
+# The exported symbols, as declared in include/retro_out_prod.h,
+# include/retro_mx.h and include/retro_probe.h.
 EXPORTS = ("retro_out_prod", "retro_out_prod_variant", "retro_out_prod_strided", "retro_out_prod_strided_variant",
            "retro_dequantize", "retro_out_prod_supported", "retro_out_prod_choice", "retro_out_prod_variant_applies",
            "retro_out_prod_strided_variant_applies", "retro_out_prod_batched", "retro_out_prod_batched_variant",
@@ -81,6 +81,9 @@ EXPORTS = ("retro_out_prod", "retro_out_prod_variant", "retro_out_prod_strided",
            "retro_mul_mat", "retro_mul_mat_variant", "retro_mul_mat_choice", "retro_mul_mat_variant_applies",
            "retro_mul_mat_plan", "retro_mul_mat_row_split",
            "retro_row_bytes", "retro_strerror",
+           "retro_quantize", "retro_mx_code_bytes", "retro_mx_scale_bytes", "retro_mx_quantize",
+           "retro_mx_dequantize", "retro_mx_from_blocks", "retro_mx_mul_mat", "retro_mx_linear",
+           "retro_mx_linear_workspace_size", "retro_moe", "retro_moe_workspace_size",
            "retro_probe_sink_floats", "retro_probe_mfma", "retro_probe_mfma_valu", "retro_probe_copy")
 
 PROBE_MFMA_F32 = 0
@@ -158,6 +161,28 @@ def _load() -> ctypes.CDLL:
     lib.retro_out_prod_variant_applies.argtypes = [i32, i32, i64, i64, i64]
     lib.retro_row_bytes.restype = i64
     lib.retro_row_bytes.argtypes = [i32, i64]
+    lib.retro_quantize.restype = i32
+    lib.retro_quantize.argtypes = [i32, i32, vp, i64, vp, i64, i64, vp]
+    for name in ("retro_mx_code_bytes", "retro_mx_scale_bytes"):
+        getattr(lib, name).restype = i64
+        getattr(lib, name).argtypes = [i64, i64]
+    lib.retro_mx_quantize.restype = i32
+    lib.retro_mx_quantize.argtypes = [i32, vp, i64, i64, i64, vp, vp, vp, vp, vp]
+    lib.retro_mx_dequantize.restype = i32
+    lib.retro_mx_dequantize.argtypes = [i32, vp, vp, vp, i64, i64, i64, vp]
+    lib.retro_mx_from_blocks.restype = i32
+    lib.retro_mx_from_blocks.argtypes = [vp, vp, vp, i64, i64, vp]
+    lib.retro_mx_mul_mat.restype = i32
+    lib.retro_mx_mul_mat.argtypes = [i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp]
+    lib.retro_mx_linear.restype = i32
+    lib.retro_mx_linear.argtypes = [i32, vp, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp]
+    lib.retro_mx_linear_workspace_size.restype = i64
+    lib.retro_mx_linear_workspace_size.argtypes = [i32, i64, i64, i64]
+    lib.retro_moe.restype = i32
+    lib.retro_moe.argtypes = [i32, vp, i64, i32, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32, vp,
+                              i64, vp]
+    lib.retro_moe_workspace_size.restype = i64
+    lib.retro_moe_workspace_size.argtypes = [i32, i64, i64, i64, i64, i64]
     lib.retro_probe_sink_floats.restype = i64
     lib.retro_probe_sink_floats.argtypes = []
     lib.retro_probe_mfma.restype = i32
@@ -635,3 +660,7 @@ def dequantize(wtype: int, W, K: int, N: int, out=None, stream=None):
             raise ValueError("out must be float32 N x K")
     _check(lib.retro_dequantize(int(wtype), _ptr(W), _ptr(out), int(K), int(N), _stream_handle(stream)))
     return out
+
+
+from .mx import (MXMatrix, mx_dequantize, mx_from_blocks, mx_linear, mx_linear_backward, mx_moe,  # noqa: E402
+                 mx_mul_mat, mx_quantize, mx_quantize_both, quantize)

@@ -1,0 +1,57 @@
+// retro_mx_device.h - device pieces shared by the microscaled 4-bit kernels
+// and the expert layer: float loads and stores, the block scale, and the
+// addresses of a microscaled matrix (layout: retro_mx.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace retro {
+namespace mx {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kStep = 256;       // elements of a codes/scales step along K
+constexpr int kStepBytes = 128;  // its code bytes in a row
+constexpr int kStepScales = 8;   // its scale bytes in a row
+
+// 256-element steps of a row
+__host__ __device__ inline int64_t steps_of(int64_t K) { return (K + kStep - 1) / kStep; }
+
+// 2^(e - 127) for a scale byte e below 255 (2^-127 is subnormal).
+__device__ __forceinline__ float scale_value(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
+
+// The scale byte of a block from the largest magnitude's bits: the exponent
+// field of amax less 2 (a subnormal amax, field 0, gives 0, as does amax = 0);
+// an infinity or NaN, whose bits are the largest of all, gives 255.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+    const uint32_t field = amax_bits >> 23;
+    return field == 255u ? 255u : field > 2u ? field - 2u : 0u;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(_Float16 v) { return float(v); }
+__device__ __forceinline__ float to_f32(__bf16 v) { return float(v); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float v) { return T(v); }
+
+// Two values to a byte of E2M1 codes, a in the low nibble: v / scale rounded to
+// nearest even, saturated to 6. The conversion takes only the scale's exponent.
+template <int BYTE>
+__device__ __forceinline__ uint32_t to_fp4(uint32_t old, float a, float b, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, BYTE);
+}
+
+}  // namespace mx
+}  // namespace retro

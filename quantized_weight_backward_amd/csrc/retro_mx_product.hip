@@ -1,0 +1,157 @@
+// retro_mx_product.hip - Y = A B^T of two microscaled matrices on the scaled
+// matrix cores, and the product with A quantised in the call (retro_mx.h).
+#include "retro_mx_device.h"
+#include "retro_mx_host.h"
+
+namespace retro {
+namespace mx {
+namespace {
+
+// Y[t][n] = sum over blocks b of 2^(ea + eb - 254) * (sum of 32 E2M1 products).
+// v_mfma_scale_f32_32x32x64_f8f6f4 takes, per lane, a row's block of 32 codes
+// (16 bytes: lane % 32 the row, lane / 32 one of two blocks) and that block's
+// scale byte, and adds both blocks' scaled sums. Which of a row's blocks meet in
+// one instruction is free as long as A and B agree: in a step of 256 elements
+// lane half h takes blocks 4h .. 4h + 3 in turn, so one 32-bit word holds its
+// four scale bytes.
+
+// Simple form: a wave a 32 x 32 tile of Y, operands straight from memory.
+template <typename TY>
+__global__ __launch_bounds__(64) void product_simple_kernel(const uint8_t* __restrict__ ac,
+                                                            const uint8_t* __restrict__ as,
+                                                            const uint8_t* __restrict__ bc,
+                                                            const uint8_t* __restrict__ bs, TY* __restrict__ Y,
+                                                            int64_t ldy, int64_t steps, int64_t N, int64_t T,
+                                                            uint32_t tiles_n) {
+    const int lane = threadIdx.x, r = lane & 31, h = lane >> 5;
+    const int64_t t0 = int64_t(blockIdx.x / tiles_n) * 32, n0 = int64_t(blockIdx.x % tiles_n) * 32;
+    const int64_t ra = min(t0 + r, T - 1), rb = min(n0 + r, N - 1);
+    const uint8_t* pa = ac + ra * steps * kStepBytes + h * 64;
+    const uint8_t* pb = bc + rb * steps * kStepBytes + h * 64;
+    const uint8_t* sa = as + ra * kStepScales + h * 4;
+    const uint8_t* sb = bs + rb * kStepScales + h * 4;
+    f32x16 acc = {};
+    for (int64_t c = 0; c < steps; ++c) {
+        const int ea = *reinterpret_cast<const int*>(sa + c * T * kStepScales);
+        const int eb = *reinterpret_cast<const int*>(sb + c * N * kStepScales);
+        i32x8 a[4] = {}, b[4] = {};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const i32x4 va = *reinterpret_cast<const i32x4*>(pa + c * kStepBytes + s * 16);
+            const i32x4 vb = *reinterpret_cast<const i32x4*>(pb + c * kStepBytes + s * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[s][i] = va[i];
+                b[s][i] = vb[i];
+            }
+        }
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[0], b[0], acc, 4, 4, 0, ea, 0, eb);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[1], b[1], acc, 4, 4, 1, ea, 1, eb);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[2], b[2], acc, 4, 4, 2, ea, 2, eb);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[3], b[3], acc, 4, 4, 3, ea, 3, eb);
+    }
+    if (n0 + r >= N) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t t = t0 + (i / 4) * 8 + h * 4 + i % 4;
+        if (t < T) Y[t * ldy + n0 + r] = from_f32<TY>(acc[i]);
+    }
+}
+
+}  // namespace
+
+int launch_product(int ytype, const void* ac, const void* as, const void* bc, const void* bs, void* Y, int64_t ldy,
+                   int64_t K, int64_t N, int64_t T, hipStream_t st) {
+    return with_float(ytype, [&](auto* tag) {
+        using TY = std::remove_pointer_t<decltype(tag)>;
+        const int64_t tiles_n = host::cdiv(N, 32), tiles_t = host::cdiv(T, 32);
+        host::clear_last_error();
+        product_simple_kernel<TY><<<dim3(uint32_t(tiles_n * tiles_t)), dim3(64), 0, st>>>(
+            static_cast<const uint8_t*>(ac), static_cast<const uint8_t*>(as), static_cast<const uint8_t*>(bc),
+            static_cast<const uint8_t*>(bs), static_cast<TY*>(Y), ldy, steps_of(K), N, T, uint32_t(tiles_n));
+        return host::launch_status();
+    });
+}
+
+}  // namespace mx
+}  // namespace retro
+
+using namespace retro;
+using namespace retro::mx;
+
+namespace {
+
+// The shape and operand checks of both products. The grid of 32 x 32 tiles
+// bounds T * N.
+int check_product(int ytype, const void* bc, const void* bs, const void* Y, int64_t ldy, int64_t K, int64_t N,
+                  int64_t T, int64_t& y_bytes) {
+    const int size = float_bytes(ytype);
+    if (!size) return RETRO_E_TYPE;
+    if (!dim_ok(K) || !dim_ok(N) || !dim_ok(T)) return RETRO_E_SHAPE;
+    y_bytes = span_bytes(T, N, ldy, size);
+    if (y_bytes < 0 || host::cdiv(N, 32) * host::cdiv(T, 32) >= host::kGridLimit) return RETRO_E_SHAPE;
+    if (N == 0 || T == 0) return RETRO_OK;
+    if (!Y || (K && (!bc || !bs))) return RETRO_E_NULL;
+    if (!aligned(bc, 16) || !aligned(bs, 16) || !aligned(Y, size)) return RETRO_E_ALIGN;
+    if (overlap({Y, y_bytes}, {bc, code_bytes(N, K)}) || overlap({Y, y_bytes}, {bs, scale_bytes(N, K)}))
+        return RETRO_E_ALIAS;
+    return RETRO_OK;
+}
+
+int64_t linear_workspace(int64_t K, int64_t T) {
+    // codes, then scales on a 16-byte boundary (code rows are multiples of 128)
+    return code_bytes(T, K) + scale_bytes(T, K);
+}
+
+}  // namespace
+
+extern "C" {
+
+int retro_mx_mul_mat(int ytype, const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,
+                     void* Y, int64_t ldy, int64_t K, int64_t N, int64_t T, void* stream) {
+    int64_t yb = 0;
+    const int rc = check_product(ytype, b_codes, b_scales, Y, ldy, K, N, T, yb);
+    if (rc != RETRO_OK || N == 0 || T == 0) return rc;
+    if (K && (!a_codes || !a_scales)) return RETRO_E_NULL;
+    if (!aligned(a_codes, 16) || !aligned(a_scales, 16)) return RETRO_E_ALIGN;
+    if (overlap({Y, yb}, {a_codes, code_bytes(T, K)}) || overlap({Y, yb}, {a_scales, scale_bytes(T, K)}))
+        return RETRO_E_ALIAS;
+    return launch_product(ytype, a_codes, a_scales, b_codes, b_scales, Y, ldy, K, N, T,
+                          static_cast<hipStream_t>(stream));
+}
+
+int64_t retro_mx_linear_workspace_size(int xtype, int64_t K, int64_t N, int64_t T) {
+    if (!float_bytes(xtype)) return RETRO_E_TYPE;
+    if (!dim_ok(K) || !dim_ok(N) || !dim_ok(T)) return RETRO_E_SHAPE;
+    return N == 0 ? 0 : linear_workspace(K, T);
+}
+
+int retro_mx_linear(int xtype, const void* X, int64_t ldx, const void* b_codes, const void* b_scales, void* Y,
+                    int64_t ldy, int64_t K, int64_t N, int64_t T, void* workspace, int64_t workspace_bytes,
+                    void* stream) {
+    int64_t yb = 0;
+    int rc = check_product(xtype, b_codes, b_scales, Y, ldy, K, N, T, yb);
+    if (rc != RETRO_OK) return rc;
+    const int64_t xb = span_bytes(T, K, ldx, float_bytes(xtype));
+    if (xb < 0) return RETRO_E_SHAPE;
+    if (N == 0 || T == 0) return RETRO_OK;
+    if (K && !X) return RETRO_E_NULL;
+    if (!aligned(X, float_bytes(xtype))) return RETRO_E_ALIGN;
+    if (overlap({Y, yb}, {X, xb})) return RETRO_E_ALIAS;
+    const int64_t need = retro_mx_linear_workspace_size(xtype, K, N, T);
+    const Span w{workspace, need};
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16) || overlap(w, {X, xb}) ||
+                 overlap(w, {Y, yb}) || overlap(w, {b_codes, code_bytes(N, K)}) ||
+                 overlap(w, {b_scales, scale_bytes(N, K)})))
+        return RETRO_E_WORKSPACE;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    uint8_t* codes = static_cast<uint8_t*>(workspace);
+    uint8_t* scales = codes + code_bytes(T, K);
+    if (K) {
+        rc = launch_quantize_rows(xtype, X, ldx, T, K, codes, scales, st);
+        if (rc != RETRO_OK) return rc;
+    }
+    return launch_product(xtype, codes, scales, b_codes, b_scales, Y, ldy, K, N, T, st);
+}
+
+}  // extern "C"
