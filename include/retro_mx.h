@@ -89,6 +89,33 @@ int retro_mx_mul_mat(int ytype, const void *a_codes, const void *a_scales, const
                      void *Y, int64_t ldy, int64_t K, int64_t N, int64_t T, void *stream);
 
 /*
+ * Kernels of the product, for tests and benchmarks (retro_mx_mul_mat chooses
+ * one by shape):
+ *   RETRO_MX_VARIANT_SIMPLE   a wave a 32 x 32 tile, operands from memory; any
+ *                             shape, and the only one for sizes whose offsets
+ *                             pass 32 bits within a tile
+ *   RETRO_MX_VARIANT_TILE_*   rows of A x rows of B a workgroup, staged in LDS
+ */
+enum {
+    RETRO_MX_VARIANT_AUTO = 0,
+    RETRO_MX_VARIANT_SIMPLE = 1,
+    RETRO_MX_VARIANT_TILE_256x256 = 2,
+    RETRO_MX_VARIANT_TILE_256x128 = 3,
+    RETRO_MX_VARIANT_TILE_128x128 = 4,
+    RETRO_MX_VARIANT_TILE_64x64 = 5
+};
+
+/* retro_mx_mul_mat with a forced kernel; RETRO_E_VARIANT when it does not take
+ * the shape. */
+int retro_mx_mul_mat_variant(int variant, int ytype, const void *a_codes, const void *a_scales, const void *b_codes,
+                             const void *b_scales, void *Y, int64_t ldy, int64_t K, int64_t N, int64_t T,
+                             void *stream);
+
+/* The kernel retro_mx_mul_mat runs for a shape, or a negative error code.
+ * Touches no device. */
+int retro_mx_mul_mat_choice(int ytype, int64_t ldy, int64_t K, int64_t N, int64_t T);
+
+/*
  * retro_mx_mul_mat with A quantised from X (T x K floats of xtype) in the call,
  * Y of X's type. workspace holds the quantised X where the kernel chosen for
  * the shape needs it: retro_mx_linear_workspace_size bytes (0 when it needs

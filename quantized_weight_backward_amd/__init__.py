@@ -82,7 +82,8 @@ EXPORTS = ("retro_out_prod", "retro_out_prod_variant", "retro_out_prod_strided",
            "retro_mul_mat_plan", "retro_mul_mat_row_split",
            "retro_row_bytes", "retro_strerror",
            "retro_quantize", "retro_mx_code_bytes", "retro_mx_scale_bytes", "retro_mx_quantize",
-           "retro_mx_dequantize", "retro_mx_from_blocks", "retro_mx_mul_mat", "retro_mx_linear",
+           "retro_mx_dequantize", "retro_mx_from_blocks", "retro_mx_mul_mat", "retro_mx_mul_mat_variant",
+           "retro_mx_mul_mat_choice", "retro_mx_linear",
            "retro_mx_linear_workspace_size", "retro_moe", "retro_moe_workspace_size",
            "retro_probe_sink_floats", "retro_probe_mfma", "retro_probe_mfma_valu", "retro_probe_copy")
 
@@ -174,6 +175,10 @@ def _load() -> ctypes.CDLL:
     lib.retro_mx_from_blocks.argtypes = [vp, vp, vp, i64, i64, vp]
     lib.retro_mx_mul_mat.restype = i32
     lib.retro_mx_mul_mat.argtypes = [i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp]
+    lib.retro_mx_mul_mat_variant.restype = i32
+    lib.retro_mx_mul_mat_variant.argtypes = [i32, i32, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp]
+    lib.retro_mx_mul_mat_choice.restype = i32
+    lib.retro_mx_mul_mat_choice.argtypes = [i32, i64, i64, i64, i64]
     lib.retro_mx_linear.restype = i32
     lib.retro_mx_linear.argtypes = [i32, vp, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp]
     lib.retro_mx_linear_workspace_size.restype = i64
@@ -662,5 +667,5 @@ def dequantize(wtype: int, W, K: int, N: int, out=None, stream=None):
     return out
 
 
-from .mx import (MXMatrix, mx_dequantize, mx_from_blocks, mx_linear, mx_linear_backward, mx_moe,  # noqa: E402
-                 mx_mul_mat, mx_quantize, mx_quantize_both, quantize)
+from .mx import (MX_VARIANT_NAMES, MXMatrix, mx_dequantize, mx_from_blocks, mx_linear, mx_linear_backward, mx_moe,  # noqa: E402
+                 mx_mul_mat, mx_mul_mat_choice, mx_quantize, mx_quantize_both, quantize)

@@ -56,8 +56,10 @@ int with_float(int type, F&& f) {
 // Launches shared between files (arguments checked by the caller).
 int launch_quantize_rows(int xtype, const void* X, int64_t ldx, int64_t rows, int64_t K, void* codes, void* scales,
                          hipStream_t st);
-int launch_product(int ytype, const void* ac, const void* as, const void* bc, const void* bs, void* Y, int64_t ldy,
-                   int64_t K, int64_t N, int64_t T, hipStream_t st);
+int launch_product(int variant, int ytype, const void* ac, const void* as, const void* bc, const void* bs, void* Y,
+                   int64_t ldy, int64_t K, int64_t N, int64_t T, hipStream_t st);
+// Whether a variant takes a shape and row stride of Y (of elements of `size` bytes).
+bool product_applies(int variant, int size, int64_t ldy, int64_t K, int64_t N, int64_t T);
 
 }  // namespace mx
 }  // namespace retro

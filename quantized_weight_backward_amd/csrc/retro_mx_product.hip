@@ -2,6 +2,7 @@
 // matrix cores, and the product with A quantised in the call (retro_mx.h).
 #include "retro_mx_device.h"
 #include "retro_mx_host.h"
+#include "retro_mx_tile.h"
 
 namespace retro {
 namespace mx {
@@ -58,18 +59,83 @@ __global__ __launch_bounds__(64) void product_simple_kernel(const uint8_t* __res
     }
 }
 
+using Tile256x256 = Tile<2, 2, 4, 4>;
+using Tile256x128 = Tile<2, 2, 4, 2>;
+using Tile128x128 = Tile<2, 2, 2, 2>;
+using Tile64x64 = Tile<2, 2, 1, 1>;
+
+struct Args {
+    const uint8_t *ac, *as, *bc, *bs;
+    int64_t ldy, K, N, T;
+    hipStream_t st;
+};
+
+template <typename TY>
+int launch_simple(const Args& p, TY* Y) {
+    const int64_t tiles_n = host::cdiv(p.N, 32), tiles_t = host::cdiv(p.T, 32);
+    host::clear_last_error();
+    product_simple_kernel<TY><<<dim3(uint32_t(tiles_n * tiles_t)), dim3(64), 0, p.st>>>(
+        p.ac, p.as, p.bc, p.bs, Y, p.ldy, steps_of(p.K), p.N, p.T, uint32_t(tiles_n));
+    return host::launch_status();
+}
+
+template <class Z, typename TY>
+int launch_tile(const Args& p, TY* Y) {
+    const int64_t tiles_n = host::cdiv(p.N, Z::kRowsN), tiles_t = host::cdiv(p.T, Z::kRowsT);
+    const double row = double(steps_of(p.K)) * (kStepBytes + kStepScales);
+    const int group = host::group_height(tiles_t, tiles_n, Z::kPerCU, double(p.T) * row, double(p.N) * row);
+    host::clear_last_error();
+    product_tile_kernel<TY, Z><<<dim3(uint32_t(tiles_n * tiles_t)), dim3(Z::kWaves * 64), 0, p.st>>>(
+        p.ac, p.as, p.bc, p.bs, Y, p.ldy, uint32_t(steps_of(p.K)), p.N, p.T, uint32_t(tiles_n), uint32_t(tiles_t),
+        uint32_t(group));
+    return host::launch_status();
+}
+
+// The tiles address 256 rows of codes, all rows' scales of a step and five rows
+// of Y with 32-bit offsets.
+bool tiles_apply(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
+    return K > 0 && steps_of(K) * kStepBytes * 256 < (int64_t(1) << 32) && std::max(N, T) < (int64_t(1) << 28) &&
+           (ldy * 5 + 32) * size < (int64_t(1) << 32);
+}
+
+int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
+    if (!tiles_apply(size, ldy, K, N, T)) return RETRO_MX_VARIANT_SIMPLE;
+    auto tiles = [&](int64_t t, int64_t n) { return host::cdiv(T, t) * host::cdiv(N, n); };
+    if (tiles(256, 256) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_256x256;
+    if (tiles(256, 128) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_256x128;
+    if (tiles(128, 128) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_128x128;
+    return RETRO_MX_VARIANT_TILE_64x64;
+}
+
 }  // namespace
 
-int launch_product(int ytype, const void* ac, const void* as, const void* bc, const void* bs, void* Y, int64_t ldy,
-                   int64_t K, int64_t N, int64_t T, hipStream_t st) {
+bool product_applies(int variant, int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
+    switch (variant) {
+        case RETRO_MX_VARIANT_AUTO:
+        case RETRO_MX_VARIANT_SIMPLE: return true;
+        case RETRO_MX_VARIANT_TILE_256x256:
+        case RETRO_MX_VARIANT_TILE_256x128:
+        case RETRO_MX_VARIANT_TILE_128x128:
+        case RETRO_MX_VARIANT_TILE_64x64: return tiles_apply(size, ldy, K, N, T);
+        default: return false;
+    }
+}
+
+int launch_product(int variant, int ytype, const void* ac, const void* as, const void* bc, const void* bs, void* Y,
+                   int64_t ldy, int64_t K, int64_t N, int64_t T, hipStream_t st) {
+    const Args p{static_cast<const uint8_t*>(ac), static_cast<const uint8_t*>(as), static_cast<const uint8_t*>(bc),
+                 static_cast<const uint8_t*>(bs), ldy, K, N, T, st};
+    if (variant == RETRO_MX_VARIANT_AUTO) variant = choose(float_bytes(ytype), ldy, K, N, T);
     return with_float(ytype, [&](auto* tag) {
         using TY = std::remove_pointer_t<decltype(tag)>;
-        const int64_t tiles_n = host::cdiv(N, 32), tiles_t = host::cdiv(T, 32);
-        host::clear_last_error();
-        product_simple_kernel<TY><<<dim3(uint32_t(tiles_n * tiles_t)), dim3(64), 0, st>>>(
-            static_cast<const uint8_t*>(ac), static_cast<const uint8_t*>(as), static_cast<const uint8_t*>(bc),
-            static_cast<const uint8_t*>(bs), static_cast<TY*>(Y), ldy, steps_of(K), N, T, uint32_t(tiles_n));
-        return host::launch_status();
+        TY* y = static_cast<TY*>(Y);
+        switch (variant) {
+            case RETRO_MX_VARIANT_TILE_256x256: return launch_tile<Tile256x256>(p, y);
+            case RETRO_MX_VARIANT_TILE_256x128: return launch_tile<Tile256x128>(p, y);
+            case RETRO_MX_VARIANT_TILE_128x128: return launch_tile<Tile128x128>(p, y);
+            case RETRO_MX_VARIANT_TILE_64x64: return launch_tile<Tile64x64>(p, y);
+            default: return launch_simple(p, y);
+        }
     });
 }
 
@@ -109,6 +175,19 @@ extern "C" {
 
 int retro_mx_mul_mat(int ytype, const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,
                      void* Y, int64_t ldy, int64_t K, int64_t N, int64_t T, void* stream) {
+    return retro_mx_mul_mat_variant(RETRO_MX_VARIANT_AUTO, ytype, a_codes, a_scales, b_codes, b_scales, Y, ldy, K, N,
+                                    T, stream);
+}
+
+int retro_mx_mul_mat_choice(int ytype, int64_t ldy, int64_t K, int64_t N, int64_t T) {
+    const int size = float_bytes(ytype);
+    if (!size) return RETRO_E_TYPE;
+    if (!dim_ok(K) || !dim_ok(N) || !dim_ok(T) || span_bytes(T, N, ldy, size) < 0) return RETRO_E_SHAPE;
+    return choose(size, ldy, K, N, T);
+}
+
+int retro_mx_mul_mat_variant(int variant, int ytype, const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,
+                             void* Y, int64_t ldy, int64_t K, int64_t N, int64_t T, void* stream) {
     int64_t yb = 0;
     const int rc = check_product(ytype, b_codes, b_scales, Y, ldy, K, N, T, yb);
     if (rc != RETRO_OK || N == 0 || T == 0) return rc;
@@ -116,7 +195,8 @@ int retro_mx_mul_mat(int ytype, const void* a_codes, const void* a_scales, const
     if (!aligned(a_codes, 16) || !aligned(a_scales, 16)) return RETRO_E_ALIGN;
     if (overlap({Y, yb}, {a_codes, code_bytes(T, K)}) || overlap({Y, yb}, {a_scales, scale_bytes(T, K)}))
         return RETRO_E_ALIAS;
-    return launch_product(ytype, a_codes, a_scales, b_codes, b_scales, Y, ldy, K, N, T,
+    if (!product_applies(variant, float_bytes(ytype), ldy, K, N, T)) return RETRO_E_VARIANT;
+    return launch_product(variant, ytype, a_codes, a_scales, b_codes, b_scales, Y, ldy, K, N, T,
                           static_cast<hipStream_t>(stream));
 }
 
@@ -151,7 +231,7 @@ int retro_mx_linear(int xtype, const void* X, int64_t ldx, const void* b_codes, 
         rc = launch_quantize_rows(xtype, X, ldx, T, K, codes, scales, st);
         if (rc != RETRO_OK) return rc;
     }
-    return launch_product(xtype, codes, scales, b_codes, b_scales, Y, ldy, K, N, T, st);
+    return launch_product(RETRO_MX_VARIANT_AUTO, xtype, codes, scales, b_codes, b_scales, Y, ldy, K, N, T, st);
 }
 
 }  // extern "C"

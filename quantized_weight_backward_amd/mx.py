@@ -23,6 +23,11 @@ from . import (BF16, E_SHAPE, E_TYPE, F16, F32, MXFP4, TYPES, _check, _device_te
                row_bytes)
 
 _FLOAT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+MX_VARIANT_AUTO, MX_VARIANT_SIMPLE, MX_VARIANT_TILE_256x256, MX_VARIANT_TILE_256x128, MX_VARIANT_TILE_128x128, \
+    MX_VARIANT_TILE_64x64 = range(6)
+MX_VARIANT_NAMES = {MX_VARIANT_SIMPLE: "simple", MX_VARIANT_TILE_256x256: "tile_256x256",
+                    MX_VARIANT_TILE_256x128: "tile_256x128", MX_VARIANT_TILE_128x128: "tile_128x128",
+                    MX_VARIANT_TILE_64x64: "tile_64x64"}
 _QUIET = contextlib.nullcontext()
 
 
@@ -189,7 +194,12 @@ def mx_from_blocks(W, K: int, N: int, stream=None) -> MXMatrix:
     return m
 
 
-def mx_mul_mat(a: MXMatrix, b: MXMatrix, dtype=torch.float32, out=None, stream=None):
+def mx_mul_mat_choice(K: int, N: int, T: int, dtype=torch.float32) -> int:
+    """The kernel mx_mul_mat runs for a contiguous T x N result (a key of MX_VARIANT_NAMES)."""
+    return int(lib.retro_mx_mul_mat_choice(_FLOAT[dtype], int(N), int(K), int(N), int(T)))
+
+
+def mx_mul_mat(a: MXMatrix, b: MXMatrix, dtype=torch.float32, out=None, variant: int = MX_VARIANT_AUTO, stream=None):
     """Y[t][n] = sum_k a[t][k] b[n][k] (T x N of dtype)."""
     _matrix(a, "a")
     _matrix(b, "b")
@@ -200,8 +210,9 @@ def mx_mul_mat(a: MXMatrix, b: MXMatrix, dtype=torch.float32, out=None, stream=N
     _same_device(a.codes, b.codes)
     with _on(a, stream):
         out, ld = _out(out, (a.rows, b.rows), dtype, a.codes)
-        _check(lib.retro_mx_mul_mat(_FLOAT[dtype], _ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales),
-                                    _ptr(out), ld, a.K, b.rows, a.rows, _stream_handle(stream)))
+        _check(lib.retro_mx_mul_mat_variant(int(variant), _FLOAT[dtype], _ptr(a.codes), _ptr(a.scales),
+                                            _ptr(b.codes), _ptr(b.scales), _ptr(out), ld, a.K, b.rows, a.rows,
+                                            _stream_handle(stream)))
     return out
 
 

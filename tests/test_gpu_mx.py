@@ -180,6 +180,24 @@ def test_product(q, dtype, TNK):
 
 
 @pytest.mark.parametrize("TNK", PRODUCTS, ids=str)
+def test_every_kernel_of_the_product(q, TNK):
+    T, N, K = TNK
+    a, b = ref.random_planes(gen(T), T, K), ref.random_planes(gen(N + 1), N, K)
+    A, B = q.MXMatrix(a[0].cuda(), a[1].cuda(), K), q.MXMatrix(b[0].cuda(), b[1].cuda(), K)
+    want = a[2] @ b[2].T
+    for dtype in (torch.float32, torch.bfloat16):
+        bound = ref.product_bound(a[2], b[2], K, ref.OUT_ULP[dtype])
+        for variant, name in q.MX_VARIANT_NAMES.items():
+            print(name, dtype, flush=True)
+            try:
+                y = q.mx_mul_mat(A, B, dtype, variant=variant)
+            except q.RetroError as e:
+                assert e.code == q.E_VARIANT and variant != q.mx_mul_mat_choice(K, N, T, dtype)
+                continue
+            assert ((y.cpu().double() - want).abs() <= bound).all(), name
+
+
+@pytest.mark.parametrize("TNK", PRODUCTS, ids=str)
 def test_linear_is_the_product_of_the_quantized_rows(q, TNK):
     T, N, K = TNK
     for dtype in FLOATS:

@@ -84,6 +84,20 @@ def test_mx_mul_mat(change, code):
     assert product(**change) == code
 
 
+def test_mx_variants():
+    args = (q.F32, addr(1), addr(2), addr(3), addr(4), addr(5), 50, 300, 50, 20, None)
+    assert q.lib.retro_mx_mul_mat_variant(99, *args) == q.E_VARIANT
+    assert q.lib.retro_mx_mul_mat_variant(-1, *args) == q.E_VARIANT
+    K = 1 << 30  # 256 rows of codes pass 32 bits: the simple kernel alone
+    assert q.MX_VARIANT_NAMES[q.mx_mul_mat_choice(K, 100, 300)] == "simple"
+    big = (q.F32, addr(1), addr(2), addr(3), addr(4), addr(5), 50, K, 50, 20, None)
+    for variant, name in q.MX_VARIANT_NAMES.items():
+        if name.startswith("tile"):
+            assert q.lib.retro_mx_mul_mat_variant(variant, *big) == q.E_VARIANT
+    assert q.lib.retro_mx_mul_mat_choice(q.Q4_0, 50, 300, 50, 20) == q.E_TYPE
+    assert q.lib.retro_mx_mul_mat_choice(q.F32, 49, 300, 50, 20) == q.E_SHAPE
+
+
 def linear(**k):
     a = dict(xtype=q.BF16, X=addr(1), ldx=3000, bc=addr(3), bs=addr(4), Y=addr(5), ldy=500, K=3000, N=500, T=200,
              ws=addr(6), n=1 << 30) | k
