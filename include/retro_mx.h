@@ -95,14 +95,17 @@ int retro_mx_mul_mat(int ytype, const void *a_codes, const void *a_scales, const
  *                             shape, and the only one for sizes whose offsets
  *                             pass 32 bits within a tile
  *   RETRO_MX_VARIANT_TILE_*   rows of A x rows of B a workgroup, staged in LDS
+ *   RETRO_MX_VARIANT_SKINNY   T <= 64: 16 rows of B a workgroup, K dealt to its
+ *                             waves, B read once from memory
  */
 enum {
     RETRO_MX_VARIANT_AUTO = 0,
     RETRO_MX_VARIANT_SIMPLE = 1,
     RETRO_MX_VARIANT_TILE_256x256 = 2,
-    RETRO_MX_VARIANT_TILE_256x128 = 3,
-    RETRO_MX_VARIANT_TILE_128x128 = 4,
-    RETRO_MX_VARIANT_TILE_64x64 = 5
+    RETRO_MX_VARIANT_TILE_128x128 = 3,
+    RETRO_MX_VARIANT_TILE_64x128 = 4,
+    RETRO_MX_VARIANT_TILE_64x64 = 5,
+    RETRO_MX_VARIANT_SKINNY = 6
 };
 
 /* retro_mx_mul_mat with a forced kernel; RETRO_E_VARIANT when it does not take

@@ -53,5 +53,40 @@ __device__ __forceinline__ uint32_t to_fp4(uint32_t old, float a, float b, float
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, BYTE);
 }
 
+// 8 elements of a row, the first `left` of them (zeros past them): one 16-byte
+// load, or two, where the row allows it.
+template <typename TX>
+__device__ __forceinline__ void load8(const TX* x, int64_t left, float v[8]) {
+    typedef TX vec __attribute__((ext_vector_type(16 / sizeof(TX))));
+    constexpr int kPer = 16 / sizeof(TX);
+    if (left >= 8 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0) {
+#pragma unroll
+        for (int j = 0; j < 8 / kPer; ++j) {
+            const vec w = reinterpret_cast<const vec*>(x)[j];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) v[j * kPer + i] = to_f32(w[i]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(x[i]) : 0.f;
+}
+
+// A quarter of a block of 32: four neighbouring lanes, each with its 8 elements,
+// agree on the scale byte `e`; returns the lane's 8 codes.
+__device__ __forceinline__ uint32_t quantize8(const float v[8], uint32_t& e) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    m = max(m, uint32_t(__shfl_xor(int(m), 1)));
+    m = max(m, uint32_t(__shfl_xor(int(m), 2)));
+    e = scale_byte(m);
+    const float s = scale_value(e);
+    uint32_t q = to_fp4<0>(0, v[0], v[1], s);
+    q = to_fp4<1>(q, v[2], v[3], s);
+    q = to_fp4<2>(q, v[4], v[5], s);
+    return to_fp4<3>(q, v[6], v[7], s);
+}
+
 }  // namespace mx
 }  // namespace retro

@@ -2,6 +2,7 @@
 // matrix cores, and the product with A quantised in the call (retro_mx.h).
 #include "retro_mx_device.h"
 #include "retro_mx_host.h"
+#include "retro_mx_skinny.h"
 #include "retro_mx_tile.h"
 
 namespace retro {
@@ -59,9 +60,9 @@ __global__ __launch_bounds__(64) void product_simple_kernel(const uint8_t* __res
     }
 }
 
-using Tile256x256 = Tile<2, 2, 4, 4>;
-using Tile256x128 = Tile<2, 2, 4, 2>;
+using Tile256x256 = Tile<2, 4, 4, 2>;
 using Tile128x128 = Tile<2, 2, 2, 2>;
+using Tile64x128 = Tile<2, 2, 1, 2>;
 using Tile64x64 = Tile<2, 2, 1, 1>;
 
 struct Args {
@@ -94,15 +95,57 @@ int launch_tile(const Args& p, TY* Y) {
 // The tiles address 256 rows of codes, all rows' scales of a step and five rows
 // of Y with 32-bit offsets.
 bool tiles_apply(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
-    return K > 0 && steps_of(K) * kStepBytes * 256 < (int64_t(1) << 32) && std::max(N, T) < (int64_t(1) << 28) &&
+    return K > 0 && steps_of(K) * kStepBytes * 256 < (int64_t(1) << 32) &&
+           steps_of(K) * std::max(N, T) * kStepScales < (int64_t(1) << 32) &&
            (ldy * 5 + 32) * size < (int64_t(1) << 32);
 }
 
+// The skinny kernel holds up to 64 rows of A; its step counts are 32-bit.
+constexpr int64_t kSkinnyMaxT = 64;
+bool skinny_applies(int64_t K, int64_t T) { return K > 0 && T <= kSkinnyMaxT; }
+
+template <int TB, int U, typename TY>
+int launch_skinny_blocks(const Args& p, TY* Y) {
+    host::clear_last_error();
+    product_skinny_kernel<TY, TB, U>
+        <<<dim3(uint32_t(host::cdiv(p.N, kSkinnyRows))), dim3(kSkinnyWaves * 64), 0, p.st>>>(
+            p.ac, p.as, p.bc, p.bs, Y, p.ldy, int(steps_of(p.K)), p.N, int(p.T));
+    return host::launch_status();
+}
+
+template <typename TY>
+int launch_skinny(const Args& p, TY* Y) {
+    switch (host::cdiv(p.T, 16)) {
+        case 1: return launch_skinny_blocks<1, 4>(p, Y);
+        case 2: return launch_skinny_blocks<2, 2>(p, Y);
+        case 3: return launch_skinny_blocks<3, 2>(p, Y);
+        default: return launch_skinny_blocks<4, 2>(p, Y);
+    }
+}
+
+// A linear layer quantises x in the product's own kernel where that is few
+// elements a workgroup: 8 a thread at the limit.
+constexpr int64_t kFusedElements = 32768;
+bool fuse_linear(int64_t K, int64_t T) {
+    return T <= 16 && T * steps_of(K) * kStep <= kFusedElements;
+}
+
+template <typename TX>
+int launch_linear_skinny(const Args& p, const TX* X, int64_t ldx, TX* Y) {
+    host::clear_last_error();
+    const int64_t steps = steps_of(p.K);
+    linear_skinny_kernel<TX, 4>
+        <<<dim3(uint32_t(host::cdiv(p.N, kSkinnyRows))), dim3(kSkinnyWaves * 64),
+           size_t(p.T * steps * (kStepBytes + kStepScales)), p.st>>>(X, ldx, p.bc, p.bs, Y, p.ldy, int(p.K),
+                                                                     int(steps), p.N, int(p.T));
+    return host::launch_status();
+}
+
 int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
+    if (skinny_applies(K, T)) return RETRO_MX_VARIANT_SKINNY;
     if (!tiles_apply(size, ldy, K, N, T)) return RETRO_MX_VARIANT_SIMPLE;
     auto tiles = [&](int64_t t, int64_t n) { return host::cdiv(T, t) * host::cdiv(N, n); };
     if (tiles(256, 256) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_256x256;
-    if (tiles(256, 128) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_256x128;
     if (tiles(128, 128) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_128x128;
     return RETRO_MX_VARIANT_TILE_64x64;
 }
@@ -114,9 +157,10 @@ bool product_applies(int variant, int size, int64_t ldy, int64_t K, int64_t N, i
         case RETRO_MX_VARIANT_AUTO:
         case RETRO_MX_VARIANT_SIMPLE: return true;
         case RETRO_MX_VARIANT_TILE_256x256:
-        case RETRO_MX_VARIANT_TILE_256x128:
+        case RETRO_MX_VARIANT_TILE_64x128:
         case RETRO_MX_VARIANT_TILE_128x128:
         case RETRO_MX_VARIANT_TILE_64x64: return tiles_apply(size, ldy, K, N, T);
+        case RETRO_MX_VARIANT_SKINNY: return skinny_applies(K, T);
         default: return false;
     }
 }
@@ -131,9 +175,10 @@ int launch_product(int variant, int ytype, const void* ac, const void* as, const
         TY* y = static_cast<TY*>(Y);
         switch (variant) {
             case RETRO_MX_VARIANT_TILE_256x256: return launch_tile<Tile256x256>(p, y);
-            case RETRO_MX_VARIANT_TILE_256x128: return launch_tile<Tile256x128>(p, y);
+            case RETRO_MX_VARIANT_TILE_64x128: return launch_tile<Tile64x128>(p, y);
             case RETRO_MX_VARIANT_TILE_128x128: return launch_tile<Tile128x128>(p, y);
             case RETRO_MX_VARIANT_TILE_64x64: return launch_tile<Tile64x64>(p, y);
+            case RETRO_MX_VARIANT_SKINNY: return launch_skinny(p, y);
             default: return launch_simple(p, y);
         }
     });
@@ -203,7 +248,7 @@ int retro_mx_mul_mat_variant(int variant, int ytype, const void* a_codes, const 
 int64_t retro_mx_linear_workspace_size(int xtype, int64_t K, int64_t N, int64_t T) {
     if (!float_bytes(xtype)) return RETRO_E_TYPE;
     if (!dim_ok(K) || !dim_ok(N) || !dim_ok(T)) return RETRO_E_SHAPE;
-    return N == 0 ? 0 : linear_workspace(K, T);
+    return N == 0 || fuse_linear(K, T) ? 0 : linear_workspace(K, T);
 }
 
 int retro_mx_linear(int xtype, const void* X, int64_t ldx, const void* b_codes, const void* b_scales, void* Y,
@@ -225,6 +270,13 @@ int retro_mx_linear(int xtype, const void* X, int64_t ldx, const void* b_codes, 
                  overlap(w, {b_scales, scale_bytes(N, K)})))
         return RETRO_E_WORKSPACE;
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (K && fuse_linear(K, T))
+        return with_float(xtype, [&](auto* tag) {
+            using TX = std::remove_pointer_t<decltype(tag)>;
+            const Args p{nullptr, nullptr, static_cast<const uint8_t*>(b_codes),
+                         static_cast<const uint8_t*>(b_scales), ldy, K, N, T, st};
+            return launch_linear_skinny(p, static_cast<const TX*>(X), ldx, static_cast<TX*>(Y));
+        });
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* scales = codes + code_bytes(T, K);
     if (K) {

@@ -19,21 +19,10 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const TX* __res
     const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
     const uint32_t row = u / units, k = (u - row * units) * 8;
     if (row >= rows) return;  // whole blocks: units is a multiple of 32
-    const TX* x = X + int64_t(row) * ldx + k;
     float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? to_f32(x[i]) : 0.f;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-    m = max(m, uint32_t(__shfl_xor(int(m), 1)));
-    m = max(m, uint32_t(__shfl_xor(int(m), 2)));
-    const uint32_t e = scale_byte(m);
-    const float s = scale_value(e);
-    uint32_t q = to_fp4<0>(0, v[0], v[1], s);
-    q = to_fp4<1>(q, v[2], v[3], s);
-    q = to_fp4<2>(q, v[4], v[5], s);
-    q = to_fp4<3>(q, v[6], v[7], s);
+    load8(X + int64_t(row) * ldx + k, int64_t(K) - k, v);
+    uint32_t e;
+    const uint32_t q = quantize8(v, e);
     *reinterpret_cast<uint32_t*>(codes + int64_t(row) * units * 4 + k / 2) = q;
     if ((k & 31) == 0)
         scales[(int64_t(k / kStep) * all_rows + row) * kStepScales + (k % kStep) / 32] = uint8_t(e);

@@ -52,11 +52,13 @@ __device__ __forceinline__ void copy_step(__amdgpu_buffer_rsrc_t a, __amdgpu_buf
     }
 }
 
-// Every wave's copies into LDS have landed, and every wave is here. A wave's
-// memory counter covers its own copies only, so the wait comes first.
+// Every wave's copies into LDS have landed, its reads are done, and every wave is
+// here. A wave's counters cover its own work only, so the wait comes before the
+// barrier.
 __device__ __forceinline__ void copies_done_for_all() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 template <typename TY, class Z>
