@@ -94,8 +94,10 @@ int retro_mx_mul_mat(int ytype, const void *a_codes, const void *a_scales, const
  *   RETRO_MX_VARIANT_SIMPLE   a wave a 32 x 32 tile, operands from memory; any
  *                             shape, and the only one for sizes whose offsets
  *                             pass 32 bits within a tile
- *   RETRO_MX_VARIANT_TILE_*   rows of A x rows of B a workgroup, staged in LDS
- *   RETRO_MX_VARIANT_SKINNY   T <= 64: 16 rows of B a workgroup, K dealt to its
+ *   RETRO_MX_VARIANT_TILE_*   rows of A x rows of B a workgroup, staged in LDS;
+ *                             _K4: four groups of waves take K's steps in turn
+ *                             and add their sums
+ *   RETRO_MX_VARIANT_SKINNY   T <= 32: 16 rows of B a workgroup, K dealt to its
  *                             waves, B read once from memory
  */
 enum {
@@ -105,7 +107,9 @@ enum {
     RETRO_MX_VARIANT_TILE_128x128 = 3,
     RETRO_MX_VARIANT_TILE_64x128 = 4,
     RETRO_MX_VARIANT_TILE_64x64 = 5,
-    RETRO_MX_VARIANT_SKINNY = 6
+    RETRO_MX_VARIANT_SKINNY = 6,
+    RETRO_MX_VARIANT_TILE_64x64_K4 = 7,
+    RETRO_MX_VARIANT_TILE_32x64_K4 = 8
 };
 
 /* retro_mx_mul_mat with a forced kernel; RETRO_E_VARIANT when it does not take

@@ -64,6 +64,8 @@ using Tile256x256 = Tile<2, 4, 4, 2>;
 using Tile128x128 = Tile<2, 2, 2, 2>;
 using Tile64x128 = Tile<2, 2, 1, 2>;
 using Tile64x64 = Tile<2, 2, 1, 1>;
+using Tile64x64K4 = Tile<2, 2, 1, 1, 4>;
+using Tile32x64K4 = Tile<1, 2, 1, 1, 4>;
 
 struct Args {
     const uint8_t *ac, *as, *bc, *bs;
@@ -86,7 +88,7 @@ int launch_tile(const Args& p, TY* Y) {
     const double row = double(steps_of(p.K)) * (kStepBytes + kStepScales);
     const int group = host::group_height(tiles_t, tiles_n, Z::kPerCU, double(p.T) * row, double(p.N) * row);
     host::clear_last_error();
-    product_tile_kernel<TY, Z><<<dim3(uint32_t(tiles_n * tiles_t)), dim3(Z::kWaves * 64), 0, p.st>>>(
+    product_tile_kernel<TY, Z><<<dim3(uint32_t(tiles_n * tiles_t)), dim3(Z::kThreads), 0, p.st>>>(
         p.ac, p.as, p.bc, p.bs, Y, p.ldy, uint32_t(steps_of(p.K)), p.N, p.T, uint32_t(tiles_n), uint32_t(tiles_t),
         uint32_t(group));
     return host::launch_status();
@@ -100,8 +102,8 @@ bool tiles_apply(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
            (ldy * 5 + 32) * size < (int64_t(1) << 32);
 }
 
-// The skinny kernel holds up to 64 rows of A; its step counts are 32-bit.
-constexpr int64_t kSkinnyMaxT = 64;
+// Rows of A the skinny kernel takes.
+constexpr int64_t kSkinnyMaxT = 32;
 bool skinny_applies(int64_t K, int64_t T) { return K > 0 && T <= kSkinnyMaxT; }
 
 template <int TB, int U, typename TY>
@@ -115,12 +117,7 @@ int launch_skinny_blocks(const Args& p, TY* Y) {
 
 template <typename TY>
 int launch_skinny(const Args& p, TY* Y) {
-    switch (host::cdiv(p.T, 16)) {
-        case 1: return launch_skinny_blocks<1, 4>(p, Y);
-        case 2: return launch_skinny_blocks<2, 2>(p, Y);
-        case 3: return launch_skinny_blocks<3, 2>(p, Y);
-        default: return launch_skinny_blocks<4, 2>(p, Y);
-    }
+    return p.T <= 16 ? launch_skinny_blocks<1, 4>(p, Y) : launch_skinny_blocks<2, 2>(p, Y);
 }
 
 // A linear layer quantises x in the product's own kernel where that is few
@@ -142,12 +139,42 @@ int launch_linear_skinny(const Args& p, const TX* X, int64_t ldx, TX* Y) {
 }
 
 int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
-    if (skinny_applies(K, T)) return RETRO_MX_VARIANT_SKINNY;
-    if (!tiles_apply(size, ldy, K, N, T)) return RETRO_MX_VARIANT_SIMPLE;
     auto tiles = [&](int64_t t, int64_t n) { return host::cdiv(T, t) * host::cdiv(N, n); };
-    if (tiles(256, 256) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_256x256;
-    if (tiles(128, 128) >= host::kNumCUs) return RETRO_MX_VARIANT_TILE_128x128;
-    return RETRO_MX_VARIANT_TILE_64x64;
+    // Few rows of A and of B: 16 rows of B a workgroup put more CUs to work than
+    // tiles do. T = 16, N = 4096, K = 14336: 10.0 us against 14.7 for 32 x 64
+    // tiles; N = 14336, K = 4096: 10.8 against 9.2. T = 32: 13.8 against 15.6 and
+    // 14.6 against 9.7.
+    if (skinny_applies(K, T) && tiles(32, 64) < 128) return RETRO_MX_VARIANT_SKINNY;
+    if (!tiles_apply(size, ldy, K, N, T)) return skinny_applies(K, T) ? RETRO_MX_VARIANT_SKINNY : RETRO_MX_VARIANT_SIMPLE;
+    // Time of a round of workgroups over the CUs at K = 4096, in us, with one and
+    // with as many a CU as fit, measured at T x N = 4096 x 14336 and 128 .. 1024 x
+    // 4096; it grows with K alike for all. The last round has as many a CU as it
+    // needs.
+    struct Cost {
+        int variant, rows_t, rows_n, per_cu;
+        double one, full;
+    };
+    constexpr Cost costs[] = {
+        {RETRO_MX_VARIANT_TILE_256x256, 256, 256, Tile256x256::kPerCU, 34, 34},
+        {RETRO_MX_VARIANT_TILE_128x128, 128, 128, Tile128x128::kPerCU, 15, 22.5},
+        {RETRO_MX_VARIANT_TILE_64x128, 64, 128, Tile64x128::kPerCU, 12, 19},
+        {RETRO_MX_VARIANT_TILE_64x64, 64, 64, Tile64x64::kPerCU, 9.5, 15.5},
+        {RETRO_MX_VARIANT_TILE_64x64_K4, 64, 64, Tile64x64K4::kPerCU, 6.2, 6.2},
+        {RETRO_MX_VARIANT_TILE_32x64_K4, 32, 64, Tile32x64K4::kPerCU, 4.8, 4.8},
+    };
+    int best = 0;
+    double least = 0;
+    for (const Cost& c : costs) {
+        const int64_t n = tiles(c.rows_t, c.rows_n), round = int64_t(host::kNumCUs) * c.per_cu;
+        const int64_t rest = host::cdiv(n % round, host::kNumCUs);
+        double cost = double(n / round) * c.full;
+        if (rest) cost += c.one + (c.per_cu > 1 ? (c.full - c.one) * double(rest - 1) / (c.per_cu - 1) : 0);
+        if (!best || cost < least) {
+            best = c.variant;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -159,7 +186,9 @@ bool product_applies(int variant, int size, int64_t ldy, int64_t K, int64_t N, i
         case RETRO_MX_VARIANT_TILE_256x256:
         case RETRO_MX_VARIANT_TILE_64x128:
         case RETRO_MX_VARIANT_TILE_128x128:
-        case RETRO_MX_VARIANT_TILE_64x64: return tiles_apply(size, ldy, K, N, T);
+        case RETRO_MX_VARIANT_TILE_64x64:
+        case RETRO_MX_VARIANT_TILE_64x64_K4:
+        case RETRO_MX_VARIANT_TILE_32x64_K4: return tiles_apply(size, ldy, K, N, T);
         case RETRO_MX_VARIANT_SKINNY: return skinny_applies(K, T);
         default: return false;
     }
@@ -179,6 +208,8 @@ int launch_product(int variant, int ytype, const void* ac, const void* as, const
             case RETRO_MX_VARIANT_TILE_128x128: return launch_tile<Tile128x128>(p, y);
             case RETRO_MX_VARIANT_TILE_64x64: return launch_tile<Tile64x64>(p, y);
             case RETRO_MX_VARIANT_SKINNY: return launch_skinny(p, y);
+            case RETRO_MX_VARIANT_TILE_64x64_K4: return launch_tile<Tile64x64K4>(p, y);
+            case RETRO_MX_VARIANT_TILE_32x64_K4: return launch_tile<Tile32x64K4>(p, y);
             default: return launch_simple(p, y);
         }
     });

@@ -28,59 +28,166 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const TX* __res
         scales[(int64_t(k / kStep) * all_rows + row) * kStepScales + (k % kStep) / 32] = uint8_t(e);
 }
 
-// Columns: a thread takes the block of 32 rows of one column.
-template <typename TX>
-__global__ __launch_bounds__(kThreads) void quantize_cols_kernel(const TX* __restrict__ X, int64_t ldx, int64_t rows,
-                                                                 uint32_t cols, uint32_t col_groups, uint32_t steps,
-                                                                 int64_t block0, uint8_t* __restrict__ codes,
-                                                                 uint8_t* __restrict__ scales) {
-    const int64_t tb = block0 + blockIdx.x / col_groups;  // block of 32 rows
-    const uint32_t c = (blockIdx.x % col_groups) * kThreads + threadIdx.x;
-    if (c >= cols) return;
-    const TX* x = X + tb * 32 * ldx + c;
-    const int n = int(min(int64_t(32), rows - tb * 32));  // may be negative: a padded block
-    float v[32];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        v[i] = i < n ? to_f32(x[int64_t(i) * ldx]) : 0.f;
-        m = max(m, abs_bits(v[i]));
-    }
-    const uint32_t e = scale_byte(m);
-    const float s = scale_value(e);
-    u32x4 q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t w = to_fp4<0>(0, v[8 * i], v[8 * i + 1], s);
-        w = to_fp4<1>(w, v[8 * i + 2], v[8 * i + 3], s);
-        w = to_fp4<2>(w, v[8 * i + 4], v[8 * i + 5], s);
-        q[i] = to_fp4<3>(w, v[8 * i + 6], v[8 * i + 7], s);
-    }
-    *reinterpret_cast<u32x4*>(codes + int64_t(c) * steps * kStepBytes + tb * 16) = q;
-    scales[(tb / 8 * cols + c) * kStepScales + tb % 8] = uint8_t(e);
+// The largest of 16 neighbouring lanes' values, in all of them: exchanges in
+// pairs, in fours, and of the halves' mirror images.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xf, 0xf, true)));   // lanes 1 0 3 2
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xf, 0xf, true)));   // lanes 2 3 0 1
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xf, 0xf, true)));  // half rows mirrored
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xf, 0xf, true)));  // rows mirrored
+    return v;
 }
 
-// Packed MXFP4 blocks: a thread a block.
+constexpr int kTileRows = 256, kTileCols = 128;  // a workgroup's part of X
+constexpr int kTileWaves = 8;                    // each 32 rows
+constexpr int kColPitch = kStepBytes + 16, kRowPitch = kTileCols / 2 + 16;
+
+// Columns, or columns and rows from one reading of X. A wave takes 32 rows, a
+// lane two neighbouring columns of them: a column's block lies in one lane, a
+// row's in 16 lanes. 256 rows make whole 128-byte steps of the columns' codes,
+// which are gathered in LDS and written as such (and 64-byte pieces of the
+// rows').
+template <typename TX, bool ROWS>
+__global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
+    const TX* __restrict__ X, int64_t ldx, int64_t rows, uint32_t cols, uint32_t groups, int64_t tile0,
+    uint32_t row_steps, uint32_t col_steps, uint8_t* __restrict__ row_codes, uint8_t* __restrict__ row_scales,
+    uint8_t* __restrict__ col_codes, uint8_t* __restrict__ col_scales) {
+    __shared__ __align__(16) uint8_t by_col[kTileCols * kColPitch];
+    __shared__ __align__(16) uint8_t col_e[kTileCols * kStepScales];
+    __shared__ __align__(16) uint8_t by_row[ROWS ? kTileRows * kRowPitch : 16];
+    __shared__ __align__(16) uint8_t row_e[ROWS ? kTileRows * 4 : 16];
+    const int64_t tile = tile0 + blockIdx.x / groups;  // of 256 rows
+    const uint32_t c0 = (blockIdx.x % groups) * kTileCols;
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int64_t r0 = tile * kTileRows + wave * 32;
+    const uint32_t c = c0 + 2 * lane;
+    const int n = int(min(max(rows - r0, int64_t(0)), int64_t(32)));
+    float v[2][32];
+    const TX* x = X + r0 * ldx + c;
+    if (c + 1 < cols) {
+        // one load for both columns, at whatever alignment the row has
+        struct __attribute__((packed, aligned(sizeof(TX)))) Pair {
+            TX a, b;
+        };
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[0][i] = v[1][i] = 0.f;
+            if (i < n) {
+                const Pair p = *reinterpret_cast<const Pair*>(x + i * ldx);
+                v[0][i] = to_f32(p.a);
+                v[1][i] = to_f32(p.b);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[0][i] = i < n && c < cols ? to_f32(x[i * ldx]) : 0.f;
+            v[1][i] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = max(m, abs_bits(v[j][i]));
+        const uint32_t e = scale_byte(m);
+        const float s = scale_value(e);
+        u32x4 q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w = to_fp4<0>(0, v[j][8 * i], v[j][8 * i + 1], s);
+            w = to_fp4<1>(w, v[j][8 * i + 2], v[j][8 * i + 3], s);
+            w = to_fp4<2>(w, v[j][8 * i + 4], v[j][8 * i + 5], s);
+            q[i] = to_fp4<3>(w, v[j][8 * i + 6], v[j][8 * i + 7], s);
+        }
+        *reinterpret_cast<u32x4*>(by_col + (2 * lane + j) * kColPitch + wave * 16) = q;
+        col_e[(2 * lane + j) * kStepScales + wave] = uint8_t(e);
+    }
+    if constexpr (ROWS) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t e = scale_byte(max16(max(abs_bits(v[0][i]), abs_bits(v[1][i]))));
+            by_row[(wave * 32 + i) * kRowPitch + lane] = uint8_t(to_fp4<0>(0, v[0][i], v[1][i], scale_value(e)));
+            if ((lane & 15) == 0) row_e[(wave * 32 + i) * 4 + lane / 16] = uint8_t(e);
+        }
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < kTileCols * 8; o += kTileWaves * 64) {
+        const uint32_t cc = o / 8, part = o % 8;
+        if (c0 + cc < cols)
+            *reinterpret_cast<u32x4*>(col_codes + (int64_t(c0 + cc) * col_steps + tile) * kStepBytes + part * 16) =
+                *reinterpret_cast<const u32x4*>(by_col + cc * kColPitch + part * 16);
+    }
+    if (threadIdx.x < kTileCols && c0 + threadIdx.x < cols)
+        *reinterpret_cast<u32x2*>(col_scales + (tile * cols + c0 + threadIdx.x) * kStepScales) =
+            *reinterpret_cast<const u32x2*>(col_e + threadIdx.x * kStepScales);
+    if constexpr (ROWS) {
+        const int64_t t0 = tile * kTileRows;
+        for (int o = threadIdx.x; o < kTileRows * 4; o += kTileWaves * 64) {
+            const int r = o / 4, part = o % 4;
+            if (t0 + r < rows)
+                *reinterpret_cast<u32x4*>(row_codes + (t0 + r) * row_steps * kStepBytes + c0 / 2 + part * 16) =
+                    *reinterpret_cast<const u32x4*>(by_row + r * kRowPitch + part * 16);
+        }
+        if (threadIdx.x < kTileRows && t0 + threadIdx.x < rows)
+            *reinterpret_cast<uint32_t*>(row_scales + (int64_t(c0 / kStep) * rows + t0 + threadIdx.x) * kStepScales +
+                                         (c0 % kStep) / 32) =
+                *reinterpret_cast<const uint32_t*>(row_e + threadIdx.x * 4);
+    }
+}
+
+// PER neighbouring elements of a row, a 16-byte load where the row allows it.
+template <typename TX, int PER>
+__device__ __forceinline__ void load_few(const TX* x, float v[PER]) {
+    typedef TX vec __attribute__((ext_vector_type(PER)));
+    if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0) {
+        const vec w = *reinterpret_cast<const vec*>(x);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[i] = to_f32(w[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = to_f32(x[i]);
+}
+
+// Words at any byte address.
+struct __attribute__((packed)) AnyWord {
+    uint32_t w;
+};
+
+// Packed MXFP4 blocks: a lane takes 16 bytes of X, 8 (F32) or 4 lanes a block.
+// A lane of the first half of a block has the low nibbles of its bytes, the lane
+// half a block on their high ones.
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void quantize_mxfp4_kernel(const TX* __restrict__ X, int64_t ldx, uint32_t rows,
-                                                                  uint32_t blocks, uint8_t* __restrict__ W) {
+                                                                  uint32_t units, uint8_t* __restrict__ W) {
+    constexpr int PER = 16 / sizeof(TX), kLanes = 32 / PER;
     const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
-    const uint32_t row = u / blocks, b = u - row * blocks;
-    if (row >= rows) return;
-    const TX* x = X + int64_t(row) * ldx + int64_t(b) * 32;
-    float v[32];
+    const uint32_t row = u / units, at = u - row * units;
+    if (row >= rows) return;  // whole blocks: units is a multiple of kLanes
+    float v[PER];
+    load_few<TX, PER>(X + int64_t(row) * ldx + int64_t(at) * PER, v);
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        v[i] = to_f32(x[i]);
-        m = max(m, abs_bits(v[i]));
-    }
-    const uint32_t e = scale_byte(m);
-    const float s = scale_value(e);
-    uint8_t* w = W + (int64_t(row) * blocks + b) * 17;
-    w[0] = uint8_t(e);
+    for (int i = 0; i < PER; ++i) m = max(m, abs_bits(v[i]));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[1 + i] = uint8_t(to_fp4<0>(0, v[i], v[16 + i], s));
+    for (int d = 1; d < kLanes; d *= 2) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    const uint32_t e = scale_byte(m), lane = at % kLanes;
+    const float s = scale_value(e);
+    uint8_t* w = W + (int64_t(row) * (units / kLanes) + at / kLanes) * 17;
+    if (lane == 0) w[0] = uint8_t(e);
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+        // one code a byte, with the other half's in the nibble above
+        uint32_t mine = 0;
+        mine = to_fp4<0>(mine, v[i], 0.f, s);
+        mine = to_fp4<1>(mine, v[i + 1], 0.f, s);
+        mine = to_fp4<2>(mine, v[i + 2], 0.f, s);
+        mine = to_fp4<3>(mine, v[i + 3], 0.f, s);
+        const uint32_t other = uint32_t(__shfl_xor(int(mine), kLanes / 2));
+        if (lane < kLanes / 2)
+            reinterpret_cast<AnyWord*>(w + 1 + lane * PER + i)->w = mine | other << 4;
+    }
 }
 
 // The E4M3 scale of a sub-block nearest to amax / 6. The quotient in F32 is
@@ -95,45 +202,47 @@ __device__ __forceinline__ uint32_t e4m3_scale(uint32_t amax_bits) {
 
 // |v| / S to the nearest E2M1 code: |v| against S times the middles of the
 // grid, products of at most 7 bits and therefore exact, where the quotient
-// would round. A middle itself goes to the even code.
+// would round; a middle itself goes to the even code. Three comparisons find the
+// code's bits from the top.
 __device__ __forceinline__ uint32_t nvfp4_code(float v, float S) {
     const float a = fabsf(v);
-    uint32_t c = uint32_t(a > 0.25f * S) + uint32_t(a >= 0.75f * S) + uint32_t(a > 1.25f * S) +
-                 uint32_t(a >= 1.75f * S) + uint32_t(a > 2.5f * S) + uint32_t(a >= 3.5f * S) +
-                 uint32_t(a > 5.0f * S);
-    c = S > 0.f ? c : 0u;
+    const bool b2 = a >= 1.75f * S;
+    const bool b1 = a >= (b2 ? 3.5f : 0.75f) * S;
+    const float last = b2 ? (b1 ? 5.0f : 2.5f) : (b1 ? 1.25f : 0.25f);
+    const bool b0 = a > last * S;
+    const uint32_t c = S > 0.f ? uint32_t(b2) * 4 + uint32_t(b1) * 2 + uint32_t(b0) : 0u;
     return c | (__float_as_uint(v) >> 31 << 3);
 }
 
-// Packed NVFP4 blocks: a thread a sub-block of 16.
+// Packed NVFP4 blocks: a lane takes 16 bytes of X, 4 (F32) or 2 lanes a
+// sub-block of 16, nibbles as above.
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void quantize_nvfp4_kernel(const TX* __restrict__ X, int64_t ldx, uint32_t rows,
-                                                                  uint32_t subs, uint8_t* __restrict__ W) {
+                                                                  uint32_t units, uint8_t* __restrict__ W) {
+    constexpr int PER = 16 / sizeof(TX), kLanes = 16 / PER;
     const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
-    const uint32_t row = u / subs, b = u - row * subs;
+    const uint32_t row = u / units, at = u - row * units;
     if (row >= rows) return;
-    const TX* x = X + int64_t(row) * ldx + int64_t(b) * 16;
-    float v[16];
+    float v[PER];
+    load_few<TX, PER>(X + int64_t(row) * ldx + int64_t(at) * PER, v);
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[i] = to_f32(x[i]);
-        m = max(m, abs_bits(v[i]));
-    }
-    const uint32_t e = e4m3_scale(m);
-    const float S = __builtin_amdgcn_cvt_f32_fp8(int(e), 0);
-    uint8_t* w = W + (int64_t(row) * subs + (b & ~3u)) / 4 * 36;
-    w[b & 3] = uint8_t(e);
-    uint32_t lo = 0, hi = 0;
+    for (int i = 0; i < PER; ++i) m = max(m, abs_bits(v[i]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo |= (nvfp4_code(v[i], S) | nvfp4_code(v[8 + i], S) << 4) << (8 * i);
-        hi |= (nvfp4_code(v[4 + i], S) | nvfp4_code(v[12 + i], S) << 4) << (8 * i);
-    }
+    for (int d = 1; d < kLanes; d *= 2) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    const uint32_t e = e4m3_scale(m), lane = at % kLanes, sub = at / kLanes;
+    const float S = __builtin_amdgcn_cvt_f32_fp8(int(e), 0);
+    uint8_t* w = W + (int64_t(row) * (units / (4 * kLanes)) + sub / 4) * 36;
+    if (lane == 0) w[sub & 3] = uint8_t(e);
     // rows of 36-byte blocks are 4-byte aligned
-    uint32_t* d = reinterpret_cast<uint32_t*>(w + 4 + 8 * (b & 3));
-    d[0] = lo;
-    d[1] = hi;
+    uint32_t* d = reinterpret_cast<uint32_t*>(w + 4 + 8 * (sub & 3) + lane * PER);
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+        const uint32_t mine = nvfp4_code(v[i], S) | nvfp4_code(v[i + 1], S) << 8 | nvfp4_code(v[i + 2], S) << 16 |
+                              nvfp4_code(v[i + 3], S) << 24;
+        const uint32_t other = uint32_t(__shfl_xor(int(mine), kLanes / 2));
+        if (lane < kLanes / 2) d[i / 4] = mine | other << 4;
+    }
 }
 
 // Values of a microscaled matrix: a thread 8 elements of a row.
@@ -155,6 +264,18 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
     v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
     v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
     TY* y = Y + int64_t(row) * ldy + k;
+    constexpr int kPer = 16 / sizeof(TY);
+    typedef TY vec __attribute__((ext_vector_type(kPer)));
+    if (k + 8 <= K && (reinterpret_cast<uintptr_t>(y) & 15u) == 0) {
+#pragma unroll
+        for (int j = 0; j < 8 / kPer; ++j) {
+            vec o;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) o[i] = from_f32<TY>(v[(j * kPer + i) / 2][i % 2] * s);
+            reinterpret_cast<vec*>(y)[j] = o;
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (k + i < K) y[i] = from_f32<TY>(v[i / 2][i % 2] * s);
@@ -199,16 +320,18 @@ int in_row_ranges(int64_t rows, int64_t units, F&& f) {
     return RETRO_OK;
 }
 
-template <typename TX>
-int launch_cols(const TX* X, int64_t ldx, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
-                hipStream_t st) {
-    const int64_t steps = steps_of(rows), groups = host::cdiv(cols, kThreads);
+template <bool ROWS, typename TX>
+int launch_tiles(const TX* X, int64_t ldx, int64_t rows, int64_t cols, uint8_t* row_codes, uint8_t* row_scales,
+                 uint8_t* col_codes, uint8_t* col_scales, hipStream_t st) {
+    // with rows wanted the columns' padding is written too
+    const int64_t tiles = steps_of(rows), groups = ROWS ? steps_of(cols) * 2 : host::cdiv(cols, kTileCols);
     const int64_t most = std::max<int64_t>(1, kMaxBlocks / groups);
-    for (int64_t b = 0; b < steps * 8; b += most) {
-        const int64_t n = std::min(most, steps * 8 - b);
+    for (int64_t b = 0; b < tiles; b += most) {
+        const int64_t n = std::min(most, tiles - b);
         host::clear_last_error();
-        quantize_cols_kernel<TX><<<dim3(uint32_t(n * groups)), dim3(kThreads), 0, st>>>(
-            X, ldx, rows, uint32_t(cols), uint32_t(groups), uint32_t(steps), b, codes, scales);
+        quantize_tile_kernel<TX, ROWS><<<dim3(uint32_t(n * groups)), dim3(kTileWaves * 64), 0, st>>>(
+            X, ldx, rows, uint32_t(cols), uint32_t(groups), b, uint32_t(steps_of(cols)), uint32_t(tiles), row_codes,
+            row_scales, col_codes, col_scales);
         const int rc = host::launch_status();
         if (rc != RETRO_OK) return rc;
     }
@@ -261,7 +384,7 @@ int retro_quantize(int type, int xtype, const void* X, int64_t ldx, void* W, int
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_float(xtype, [&](auto* tag) {
         using TX = std::remove_pointer_t<decltype(tag)>;
-        const int64_t units = type == RETRO_MXFP4 ? K / 32 : K / 16, rb = host::row_bytes_of(type, K);
+        const int64_t units = K / (16 / int64_t(sizeof(TX))), rb = host::row_bytes_of(type, K);
         return in_row_ranges(N, units, [&](int64_t r, uint32_t n, uint32_t blocks) {
             const TX* x = static_cast<const TX*>(X) + r * ldx;
             uint8_t* w = static_cast<uint8_t*>(W) + r * rb;
@@ -295,15 +418,14 @@ int retro_mx_quantize(int xtype, const void* X, int64_t ldx, int64_t rows, int64
         for (int j = 0; j < i; ++j)
             if (overlap(spans[i], spans[j])) return RETRO_E_ALIAS;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (row_codes) {
-        const int rc = launch_quantize_rows(xtype, X, ldx, rows, cols, row_codes, row_scales, st);
-        if (rc != RETRO_OK) return rc;
-    }
-    if (!col_codes) return RETRO_OK;
+    if (!col_codes) return launch_quantize_rows(xtype, X, ldx, rows, cols, row_codes, row_scales, st);
     return with_float(xtype, [&](auto* tag) {
         using TX = std::remove_pointer_t<decltype(tag)>;
-        return launch_cols(static_cast<const TX*>(X), ldx, rows, cols, static_cast<uint8_t*>(col_codes),
-                           static_cast<uint8_t*>(col_scales), st);
+        const TX* x = static_cast<const TX*>(X);
+        uint8_t *rc = static_cast<uint8_t*>(row_codes), *rs = static_cast<uint8_t*>(row_scales),
+                *cc = static_cast<uint8_t*>(col_codes), *cs = static_cast<uint8_t*>(col_scales);
+        return row_codes ? launch_tiles<true>(x, ldx, rows, cols, rc, rs, cc, cs, st)
+                         : launch_tiles<false>(x, ldx, rows, cols, rc, rs, cc, cs, st);
     });
 }
 

@@ -18,15 +18,19 @@ __device__ __forceinline__ f32x16 mfma32(const i32x4& a, const i32x4& b, const f
 
 // Workgroup of WT x WN waves, each BT x BN blocks of 32 x 32 outputs, so a tile
 // of (32 WT BT) x (32 WN BN). A step is 256 elements of K: 128 code bytes a row.
-template <int WT_, int WN_, int BT_, int BN_>
+// KG such groups of waves take the steps of K in turn and add their sums at the
+// end: for few tiles, where a CU would wait on one step's copies after another.
+template <int WT_, int WN_, int BT_, int BN_, int KG_ = 1>
 struct Tile {
-    static constexpr int WT = WT_, WN = WN_, BT = BT_, BN = BN_;
-    static constexpr int kWaves = WT * WN;
+    static constexpr int WT = WT_, WN = WN_, BT = BT_, BN = BN_, KG = KG_;
+    static constexpr int kWaves = WT * WN;  // of a group
     static constexpr int kRowsT = 32 * WT * BT, kRowsN = 32 * WN * BN;
     static constexpr int kBytes = (kRowsT + kRowsN) * kStepBytes;  // LDS of one step
     static constexpr int kCopies = kBytes / (1024 * kWaves);       // 1 KB copies a wave and step
     // workgroups a CU, by their two steps of LDS
-    static constexpr int kPerCU = 160 * 1024 / (2 * kBytes) < 4 ? 160 * 1024 / (2 * kBytes) : 4;
+    static constexpr int kFit = 160 * 1024 / (2 * kBytes * KG), kPerCU = kFit < 4 ? kFit : 4;
+    static constexpr int kThreads = kWaves * KG * 64;
+    static constexpr int kPerSimd = kWaves * KG * kPerCU / 4 < 8 ? (kWaves * KG * kPerCU + 3) / 4 : 8;
     static_assert(kRowsT * kStepBytes % (1024 * kWaves) == 0 && kRowsN * kStepBytes % (1024 * kWaves) == 0,
                   "a copy lies in one operand");
 };
@@ -62,14 +66,16 @@ __device__ __forceinline__ void copies_done_for_all() {
 }
 
 template <typename TY, class Z>
-__global__ __launch_bounds__(Z::kWaves * 64, Z::kWaves / 4 * Z::kPerCU) void product_tile_kernel(
+__global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_tile_kernel(
     const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as, const uint8_t* __restrict__ bc,
     const uint8_t* __restrict__ bs, TY* __restrict__ Y, int64_t ldy, uint32_t steps, int64_t N, int64_t T,
     uint32_t tiles_n, uint32_t tiles_t, uint32_t group) {
     constexpr int WN = Z::WN, BT = Z::BT, BN = Z::BN;
-    __shared__ __align__(1024) uint8_t lds0[Z::kBytes];
-    __shared__ __align__(1024) uint8_t lds1[Z::kBytes];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    __shared__ __align__(1024) uint8_t all0[Z::KG * Z::kBytes];
+    __shared__ __align__(1024) uint8_t all1[Z::KG * Z::kBytes];
+    const int wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int wave = wave_of_all % Z::kWaves, kg = wave_of_all / Z::kWaves;
+    uint8_t *lds0 = all0 + kg * Z::kBytes, *lds1 = all1 + kg * Z::kBytes;
     const int r = lane & 31, h = lane >> 5, wt = wave / WN, wn = wave % WN;
 
     // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous range of
@@ -121,18 +127,20 @@ __global__ __launch_bounds__(Z::kWaves * 64, Z::kWaves / 4 * Z::kPerCU) void pro
     // block s + 1 are issued ahead of block s's products; before the last
     // block's, everyone has read all of cur and the next step's copies are in
     // `nxt`, so cur is refilled with the step after that. Past the last step the
-    // last one is copied again, so that the loop has no branches.
+    // last one is copied again, so that the loop has no branches. `live` is false
+    // where the last round has no step left for this group.
     int ea[2][BT], eb[2][BN];
-    auto run = [&](uint8_t* cur, const uint8_t* nxt, uint32_t step, int (&ca)[BT], int (&cb)[BN]) {
+    auto run = [&](uint8_t* cur, const uint8_t* nxt, uint32_t round, int (&ca)[BT], int (&cb)[BN], bool live) {
         auto block = [&](auto which) {
-            constexpr int S = decltype(which)::value;
+            constexpr int B = decltype(which)::value;
+            if (!live) return;
 #pragma unroll
             for (int i = 0; i < BT; ++i)
 #pragma unroll
                 for (int j = 0; j < BN; ++j)
-                    acc[i][j] = mfma32<S>(fa[S % 2][i], fb[S % 2][j], acc[i][j], ca[i], cb[j]);
+                    acc[i][j] = mfma32<B>(fa[B % 2][i], fb[B % 2][j], acc[i][j], ca[i], cb[j]);
         };
-        const uint32_t after = min(step + 2, steps - 1);
+        const uint32_t after = min((round + 2) * Z::KG + kg, steps - 1);
         read(cur, 1, fa[1], fb[1]);
         __builtin_amdgcn_sched_barrier(0);
         block(std::integral_constant<int, 0>{});
@@ -150,20 +158,50 @@ __global__ __launch_bounds__(Z::kWaves * 64, Z::kWaves / 4 * Z::kPerCU) void pro
         load_scales(ca, cb, after);
     };
 
-    if (steps > 0) {
-        copy_step<Z>(ra, rb, lds0, pitch, 0, wave, lane);
-        load_scales(ea[0], eb[0], 0);
-        copies_done_for_all();
-        copy_step<Z>(ra, rb, lds1, pitch, min(1u, steps - 1), wave, lane);
-        load_scales(ea[1], eb[1], min(1u, steps - 1));
-        read(lds0, 0, fa[0], fb[0]);
-        uint32_t step = 0;
-        for (; step + 1 < steps; step += 2) {
-            run(lds0, lds1, step, ea[0], eb[0]);
-            run(lds1, lds0, step + 1, ea[1], eb[1]);
-        }
-        if (step < steps) run(lds0, lds1, step, ea[0], eb[0]);
-        copies_done_for_all();  // the copies past the end are done before LDS is given up
+    const uint32_t first = min(uint32_t(kg), steps - 1), second = min(uint32_t(Z::KG + kg), steps - 1);
+    copy_step<Z>(ra, rb, lds0, pitch, first, wave, lane);
+    load_scales(ea[0], eb[0], first);
+    copies_done_for_all();
+    copy_step<Z>(ra, rb, lds1, pitch, second, wave, lane);
+    load_scales(ea[1], eb[1], second);
+    read(lds0, 0, fa[0], fb[0]);
+    const uint32_t whole_rounds = steps / Z::KG;
+    uint32_t round = 0;
+    for (; round + 2 <= whole_rounds; round += 2) {
+        run(lds0, lds1, round, ea[0], eb[0], true);
+        run(lds1, lds0, round + 1, ea[1], eb[1], true);
+    }
+    if (Z::KG == 1) {
+        if (round < whole_rounds) run(lds0, lds1, round, ea[0], eb[0], true);
+    } else {
+        if (round * Z::KG < steps) run(lds0, lds1, round, ea[0], eb[0], round * Z::KG + kg < steps);
+        if ((round + 1) * Z::KG < steps) run(lds1, lds0, round + 1, ea[1], eb[1], (round + 1) * Z::KG + kg < steps);
+    }
+    copies_done_for_all();  // the copies past the end are done before LDS is given up or used again
+
+    if constexpr (Z::KG > 1) {
+        // the groups' sums, added in the order of the groups by the first
+        static_assert((Z::KG - 1) * Z::kRowsT * Z::kRowsN * 4 <= Z::KG * Z::kBytes, "the sums fit");
+        float* sums = reinterpret_cast<float*>(all0) + (kg - 1) * Z::kRowsT * Z::kRowsN;
+        const int mine = wave * BT * BN * 16 * 64 + lane;
+        if (kg > 0)
+#pragma unroll
+            for (int i = 0; i < BT; ++i)
+#pragma unroll
+                for (int j = 0; j < BN; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) sums[mine + ((i * BN + j) * 16 + v) * 64] = acc[i][j][v];
+        __syncthreads();
+        if (kg > 0) return;
+        for (int k = 0; k < Z::KG - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < BT; ++i)
+#pragma unroll
+                for (int j = 0; j < BN; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        acc[i][j][v] += reinterpret_cast<const float*>(
+                            all0)[k * Z::kRowsT * Z::kRowsN + mine + ((i * BN + j) * 16 + v) * 64];
     }
 
     // A register holds one row for 32 lanes: 32 neighbouring outputs a store.
