@@ -15,11 +15,9 @@ the operands' device); outputs and scratch it allocates belong to that stream.
 
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
-from . import (BF16, E_SHAPE, E_TYPE, F16, F32, MXFP4, TYPES, _check, _device_tensor, _ptr, _stream_handle, lib,
+from . import (BF16, E_SHAPE, E_TYPE, F16, F32, MXFP4, TYPES, _check, _current_device, _device_tensor, _raw_stream, lib,
                row_bytes)
 
 _FLOAT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -29,52 +27,62 @@ MX_VARIANT_NAMES = {MX_VARIANT_SIMPLE: "simple", MX_VARIANT_TILE_256x256: "tile_
                     MX_VARIANT_TILE_128x128: "tile_128x128", MX_VARIANT_TILE_64x128: "tile_64x128",
                     MX_VARIANT_TILE_64x64: "tile_64x64", MX_VARIANT_SKINNY: "skinny",
                     MX_VARIANT_TILE_64x64_K4: "tile_64x64_k4", MX_VARIANT_TILE_32x64_K4: "tile_32x64_k4"}
-_QUIET = contextlib.nullcontext()
+
+
+def _elsewhere(t, stream) -> bool:
+    """Whether a call on t has to be made under another current stream or device."""
+    return stream is not None or t.get_device() != _device()
 
 
 def _on(t, stream):
-    """The context of a call on t's device and `stream`: what is allocated in
-    it belongs to that stream."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return _QUIET
+    """t's device, and `stream` or its current stream, as torch's current ones:
+    what a call allocates belongs to the stream that it runs on."""
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(t.device)
 
 
-def _float_type(t, name) -> int:
-    code = _FLOAT.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16")
-    return code
+# the current device, and its current stream's handle
+if _raw_stream is not None and _current_device is not None:
+    _device = _current_device
+
+    def _handle():
+        return _raw_stream(_device())
+else:
+    _device = torch.cuda.current_device
+
+    def _handle():
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _floats(t, name):
     """(type, row stride) of a 2-D float view with contiguous rows."""
-    _device_tensor(t, name, contiguous=False)
-    code = _float_type(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    code = _FLOAT.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    along_rows, along_cols = t.stride()
+    if cols > 1 and along_cols != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return code, (t.stride(0) if rows > 1 else cols)
+    return code, (along_rows if rows > 1 else cols)
 
 
-def _same_device(*tensors):
-    if any(t.device != tensors[0].device for t in tensors[1:]):
-        raise ValueError("all operands must be on one device")
+def _one_device(a, *others):
+    at = a.get_device()
+    for t in others:
+        if t.get_device() != at:
+            raise ValueError("all operands must be on one device")
 
 
-def _out(out, shape, dtype, like, name="out"):
-    """The output and its row stride."""
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device), shape[1]
-    _device_tensor(out, name, contiguous=False)
-    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    _same_device(out, like)
-    return out, _floats(out, name)[1]
+def _given(out, rows, cols, dtype, like):
+    """The row stride of a caller's output."""
+    ld = _floats(out, "out")[1]
+    if out.dtype != dtype or out.shape[0] != rows or out.shape[1] != cols:
+        raise ValueError(f"out must be {dtype} of shape {(rows, cols)}")
+    _one_device(like, out)
+    return ld
 
 
 class MXMatrix:
@@ -87,18 +95,48 @@ class MXMatrix:
     in the layout of include/retro_mx.h (codes past K are zero).
     """
 
-    __slots__ = ("codes", "scales", "K", "rows")
+    __slots__ = ("_codes", "_scales", "_both", "K", "rows", "_code_ptr", "_scale_ptr")
 
     def __init__(self, codes, scales, K: int):
         _device_tensor(codes, "codes")
         _device_tensor(scales, "scales")
-        steps = -(-int(K) // 256)
-        if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[1] != steps * 128:
+        steps = -(-K // 256)
+        shape = codes.shape
+        if codes.dtype is not torch.uint8 or len(shape) != 2 or shape[1] != steps * 128:
             raise ValueError(f"codes must be uint8 [rows, {steps * 128}] for K = {K}")
-        if scales.dtype != torch.uint8 or tuple(scales.shape) != (steps, codes.shape[0], 8):
-            raise ValueError(f"scales must be uint8 [{steps}, {codes.shape[0]}, 8]")
-        _same_device(codes, scales)
-        self.codes, self.scales, self.K, self.rows = codes, scales, int(K), int(codes.shape[0])
+        if scales.dtype is not torch.uint8 or scales.shape != (steps, shape[0], 8):
+            raise ValueError(f"scales must be uint8 [{steps}, {shape[0]}, 8]")
+        _one_device(codes, scales)
+        self._codes, self._scales, self._both, self.K, self.rows = codes, scales, None, K, shape[0]
+        self._code_ptr, self._scale_ptr = codes.data_ptr(), scales.data_ptr()
+
+    @classmethod
+    def _new(cls, rows: int, K: int, like):
+        """Both arrays in one allocation on like's device and the current stream."""
+        m = cls.__new__(cls)
+        steps = -(-K // 256)
+        m._codes = m._scales = None
+        m._both = torch.empty(rows * steps * 136, dtype=torch.uint8, device=like.device)
+        m.K, m.rows = K, rows
+        m._code_ptr = m._both.data_ptr()
+        m._scale_ptr = m._code_ptr + rows * steps * 128
+        return m
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._both[:self.rows * self._steps * 128].view(self.rows, self._steps * 128)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._both[self.rows * self._steps * 128:].view(self._steps, self.rows, 8)
+        return self._scales
+
+    @property
+    def _steps(self):
+        return -(-self.K // 256)
 
     @property
     def shape(self):
@@ -106,51 +144,37 @@ class MXMatrix:
 
     @property
     def device(self):
-        return self.codes.device
+        return (self._codes if self._both is None else self._both).device
 
-    @staticmethod
-    def empty(rows: int, K: int, device):
-        steps = -(-K // 256)
-        return MXMatrix(torch.empty((rows, steps * 128), dtype=torch.uint8, device=device),
-                        torch.empty((steps, rows, 8), dtype=torch.uint8, device=device), K)
+    def get_device(self) -> int:
+        return (self._codes if self._both is None else self._both).get_device()
 
 
 def _matrix(m, name):
     if not isinstance(m, MXMatrix):
         raise ValueError(f"{name} must be an MXMatrix")
-    return m
 
 
 def quantize(wtype: int, x, out=None, stream=None):
     """Packed blocks (uint8 [N, row_bytes(wtype, K)]) of an N x K float tensor
     with contiguous rows, wtype MXFP4 or NVFP4."""
     xtype, ldx = _floats(x, "x")
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return quantize(wtype, x, out)
     N, K = x.shape
     rb = row_bytes(wtype, K)
     if rb < 0:
         _check(E_SHAPE if wtype in TYPES.values() else E_TYPE)
-    with _on(x, stream):
-        if out is None:
-            out = torch.empty((N, rb), dtype=torch.uint8, device=x.device)
-        else:
-            _device_tensor(out, "out")
-            if out.dtype != torch.uint8 or out.numel() != N * rb:
-                raise ValueError(f"out must hold {N * rb} bytes")
-            _same_device(out, x)
-        _check(lib.retro_quantize(int(wtype), xtype, _ptr(x), ldx, _ptr(out), K, N, _stream_handle(stream)))
+    if out is None:
+        out = torch.empty((N, rb), dtype=torch.uint8, device=x.device)
+    else:
+        _device_tensor(out, "out")
+        if out.dtype != torch.uint8 or out.numel() != N * rb:
+            raise ValueError(f"out must hold {N * rb} bytes")
+        _one_device(x, out)
+    _check(lib.retro_quantize(wtype, xtype, x.data_ptr(), ldx, out.data_ptr(), K, N, _handle()))
     return out
-
-
-def _quantize(x, rows: bool, cols: bool, stream):
-    xtype, ldx = _floats(x, "x")
-    T, K = x.shape
-    with _on(x, stream):
-        r = MXMatrix.empty(T, K, x.device) if rows else None
-        c = MXMatrix.empty(K, T, x.device) if cols else None
-        _check(lib.retro_mx_quantize(xtype, _ptr(x), ldx, T, K, _ptr(r.codes) if rows else None,
-                                     _ptr(r.scales) if rows else None, _ptr(c.codes) if cols else None,
-                                     _ptr(c.scales) if cols else None, _stream_handle(stream)))
-    return r, c
 
 
 def mx_quantize(x, axis: int = 1, stream=None) -> MXMatrix:
@@ -159,24 +183,48 @@ def mx_quantize(x, axis: int = 1, stream=None) -> MXMatrix:
     columns."""
     if axis not in (0, 1, -1):
         raise ValueError("axis must be 0, 1 or -1")
-    r, c = _quantize(x, axis != 0, axis == 0, stream)
-    return c if axis == 0 else r
+    xtype, ldx = _floats(x, "x")
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return mx_quantize(x, axis)
+    T, K = x.shape
+    if axis == 0:
+        m = MXMatrix._new(K, T, x)
+        _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, None, None, m._code_ptr, m._scale_ptr, _handle()))
+    else:
+        m = MXMatrix._new(T, K, x)
+        _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, m._code_ptr, m._scale_ptr, None, None, _handle()))
+    return m
 
 
 def mx_quantize_both(x, stream=None) -> tuple[MXMatrix, MXMatrix]:
     """mx_quantize along axis 1 and axis 0 from one reading of x."""
-    return _quantize(x, True, True, stream)
+    xtype, ldx = _floats(x, "x")
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return mx_quantize_both(x)
+    T, K = x.shape
+    r, c = MXMatrix._new(T, K, x), MXMatrix._new(K, T, x)
+    _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, r._code_ptr, r._scale_ptr, c._code_ptr, c._scale_ptr,
+                                 _handle()))
+    return r, c
 
 
 def mx_dequantize(m: MXMatrix, dtype=torch.float32, out=None, stream=None):
     """The values of a microscaled matrix, rows x K of dtype."""
     _matrix(m, "m")
-    if dtype not in _FLOAT:
+    ytype = _FLOAT.get(dtype)
+    if ytype is None:
         raise ValueError("dtype must be float32, float16 or bfloat16")
-    with _on(m, stream):
-        out, ld = _out(out, m.shape, dtype, m.codes)
-        _check(lib.retro_mx_dequantize(_FLOAT[dtype], _ptr(m.codes), _ptr(m.scales), _ptr(out), ld, m.K, m.rows,
-                                       _stream_handle(stream)))
+    if _elsewhere(m, stream):
+        with _on(m, stream):
+            return mx_dequantize(m, dtype, out)
+    rows, ld = m.rows, m.K
+    if out is None:
+        out = torch.empty((rows, ld), dtype=dtype, device=m.device)
+    else:
+        ld = _given(out, rows, ld, dtype, m)
+    _check(lib.retro_mx_dequantize(ytype, m._code_ptr, m._scale_ptr, out.data_ptr(), ld, m.K, rows, _handle()))
     return out
 
 
@@ -188,10 +236,11 @@ def mx_from_blocks(W, K: int, N: int, stream=None) -> MXMatrix:
         _check(E_SHAPE)
     if W.numel() * W.element_size() != N * rb:
         raise ValueError(f"W holds {W.numel() * W.element_size()} bytes, expected N*row_bytes = {N * rb}")
-    with _on(W, stream):
-        m = MXMatrix.empty(N, K, W.device)
-        _check(lib.retro_mx_from_blocks(_ptr(W), _ptr(m.codes), _ptr(m.scales), int(K), int(N),
-                                        _stream_handle(stream)))
+    if _elsewhere(W, stream):
+        with _on(W, stream):
+            return mx_from_blocks(W, K, N)
+    m = MXMatrix._new(N, K, W)
+    _check(lib.retro_mx_from_blocks(W.data_ptr(), m._code_ptr, m._scale_ptr, K, N, _handle()))
     return m
 
 
@@ -206,14 +255,20 @@ def mx_mul_mat(a: MXMatrix, b: MXMatrix, dtype=torch.float32, out=None, variant:
     _matrix(b, "b")
     if a.K != b.K:
         raise ValueError(f"a has K = {a.K}, b has K = {b.K}")
-    if dtype not in _FLOAT:
+    ytype = _FLOAT.get(dtype)
+    if ytype is None:
         raise ValueError("dtype must be float32, float16 or bfloat16")
-    _same_device(a.codes, b.codes)
-    with _on(a, stream):
-        out, ld = _out(out, (a.rows, b.rows), dtype, a.codes)
-        _check(lib.retro_mx_mul_mat_variant(int(variant), _FLOAT[dtype], _ptr(a.codes), _ptr(a.scales),
-                                            _ptr(b.codes), _ptr(b.scales), _ptr(out), ld, a.K, b.rows, a.rows,
-                                            _stream_handle(stream)))
+    _one_device(a, b)
+    if _elsewhere(a, stream):
+        with _on(a, stream):
+            return mx_mul_mat(a, b, dtype, out, variant)
+    T, N = a.rows, b.rows
+    if out is None:
+        out, ld = torch.empty((T, N), dtype=dtype, device=a.device), N
+    else:
+        ld = _given(out, T, N, dtype, a)
+    _check(lib.retro_mx_mul_mat_variant(variant, ytype, a._code_ptr, a._scale_ptr, b._code_ptr, b._scale_ptr,
+                                        out.data_ptr(), ld, a.K, N, T, _handle()))
     return out
 
 
@@ -223,15 +278,21 @@ def mx_linear(x, w: MXMatrix, out=None, stream=None):
     xtype, ldx = _floats(x, "x")
     _matrix(w, "w")
     T, K = x.shape
+    N = w.rows
     if K != w.K:
         raise ValueError(f"x has K = {K}, w has K = {w.K}")
-    _same_device(x, w.codes)
-    with _on(x, stream):
-        out, ld = _out(out, (T, w.rows), x.dtype, x)
-        need = lib.retro_mx_linear_workspace_size(xtype, K, w.rows, T)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
-        _check(lib.retro_mx_linear(xtype, _ptr(x), ldx, _ptr(w.codes), _ptr(w.scales), _ptr(out), ld, K, w.rows, T,
-                                   _ptr(ws), max(need, 0), _stream_handle(stream)))
+    _one_device(x, w)
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return mx_linear(x, w, out)
+    if out is None:
+        out, ld = torch.empty((T, N), dtype=x.dtype, device=x.device), N
+    else:
+        ld = _given(out, T, N, x.dtype, x)
+    need = lib.retro_mx_linear_workspace_size(xtype, K, N, T)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
+    _check(lib.retro_mx_linear(xtype, x.data_ptr(), ldx, w._code_ptr, w._scale_ptr, out.data_ptr(), ld, K, N, T,
+                               None if ws is None else ws.data_ptr(), need, _handle()))
     return out
 
 
@@ -250,12 +311,13 @@ def mx_linear_backward(dy, x, wt: MXMatrix, stream=None):
     T, N = dy.shape
     if x.shape[0] != T or wt.shape != (x.shape[1], N):
         raise ValueError("dy must be T x N, x T x K and wt K x N")
-    _same_device(dy, x, wt.codes)
-    with _on(dy, stream):
-        dy_rows, dy_cols = mx_quantize_both(dy, stream=stream)
-        dx = mx_mul_mat(dy_rows, wt, dy.dtype, stream=stream)
-        dw = mx_mul_mat(dy_cols, mx_quantize(x, axis=0, stream=stream), torch.float32, stream=stream)
-    return dx, dw
+    _one_device(dy, x, wt)
+    if _elsewhere(dy, stream):
+        with _on(dy, stream):
+            return mx_linear_backward(dy, x, wt)
+    dy_rows, dy_cols = mx_quantize_both(dy)
+    dx = mx_mul_mat(dy_rows, wt, dy.dtype)
+    return dx, mx_mul_mat(dy_cols, mx_quantize(x, axis=0), torch.float32)
 
 
 def mx_moe(x, router, gate_up: MXMatrix, down: MXMatrix, top_k: int, renormalize: bool = True, out=None, stream=None):
@@ -271,16 +333,21 @@ def mx_moe(x, router, gate_up: MXMatrix, down: MXMatrix, top_k: int, renormalize
     _matrix(down, "down")
     T, D = x.shape
     E, F = router.shape[0], down.K
-    if router.shape[1] != D or gate_up.shape != (E * 2 * F, D) or down.rows != E * D:
+    if router.shape[1] != D or gate_up.rows != E * 2 * F or gate_up.K != D or down.rows != E * D:
         raise ValueError("router must be E x D, gate_up E * 2F x D and down E * D x F")
-    _same_device(x, router, gate_up.codes, down.codes)
-    with _on(x, stream):
-        out, ld = _out(out, (T, D), x.dtype, x)
-        need = lib.retro_moe_workspace_size(xtype, T, D, F, E, int(top_k))
-        if need < 0:
-            _check(need)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        _check(lib.retro_moe(xtype, _ptr(x), ldx, rtype, _ptr(router), ldr, _ptr(gate_up.codes), _ptr(gate_up.scales),
-                             _ptr(down.codes), _ptr(down.scales), _ptr(out), ld, T, D, F, E, int(top_k),
-                             int(bool(renormalize)), _ptr(ws), need, _stream_handle(stream)))
+    _one_device(x, router, gate_up, down)
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return mx_moe(x, router, gate_up, down, top_k, renormalize, out)
+    if out is None:
+        out, ld = torch.empty((T, D), dtype=x.dtype, device=x.device), D
+    else:
+        ld = _given(out, T, D, x.dtype, x)
+    need = lib.retro_moe_workspace_size(xtype, T, D, F, E, top_k)
+    if need < 0:
+        _check(need)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _check(lib.retro_moe(xtype, x.data_ptr(), ldx, rtype, router.data_ptr(), ldr, gate_up._code_ptr,
+                         gate_up._scale_ptr, down._code_ptr, down._scale_ptr, out.data_ptr(), ld, T, D, F, E, top_k,
+                         int(bool(renormalize)), None if ws is None else ws.data_ptr(), need, _handle()))
     return out
