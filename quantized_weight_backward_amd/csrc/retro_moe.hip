@@ -5,9 +5,10 @@
 // so their bytes bound it; T <= 64 tokens leave at most 64 columns an expert.
 // Launches:
 //   router   logits, and x in bf16 parts with zeros up to whole 256-element steps
-//   choose   top-k of each token
+//   choose   top-k of each token, the list of chosen experts and their pairs
 //   gate_up  a workgroup: 16 features of one chosen expert, all its tokens
-//   down     a workgroup: 16 outputs, all chosen experts, all tokens
+//   down     a workgroup: some outputs of all tokens, over all chosen experts or
+//            a part of them; the parts are added by a last launch (combine)
 // Weights are decoded exactly to bf16 (E2M1 times a power of two) and meet x
 // and h on v_mfma_f32_16x16x32_bf16 with F32 sums. x and h are cut into bf16
 // parts that add up to them: one for a BF16 x, two for F16 (11 bits), three for
@@ -20,16 +21,20 @@ namespace retro {
 namespace mx {
 namespace {
 
+// A pair is a token's j-th choice, number t * k + j.
 struct Layer {
     int T, E, k;
     int64_t D, F;
-    int64_t steps_d, steps_f;    // 256-element steps
+    int64_t steps_d, steps_f;  // 256-element steps
     const uint8_t *guc, *gus, *dc, *ds;
-    float* logits;               // T x E
-    int* ids;                    // T x k, expert of each pair
-    float* share;                // T x k
-    __bf16* xp;                  // parts x T x Dp
-    __bf16* hp;                  // parts x (T * k) x Fp
+    float* logits;   // T x E
+    float* share;    // T x k
+    int* lists;      // number of chosen experts, then for each in order of index: expert, first place, pairs
+    int16_t* order;  // the pairs, by expert
+    int8_t* choice;  // chosen expert x T: which of the token's choices it is, or -1
+    __bf16* xp;      // parts x T x Dp
+    __bf16* hp;      // parts x (T * k) x Fp: share times h
+    float* sums;     // splits x T x D
 };
 
 // v as bf16 parts that add up to it (up to the last part's rounding). What does
@@ -45,32 +50,59 @@ __device__ __forceinline__ void cut(float v, __bf16 part[P]) {
 }
 
 constexpr int kRouterWaves = 4;
+constexpr int kRouterTokens = 4;  // a wave
 
-// logits: a wave one expert and one token. Workgroups past the experts cut x.
+// logits: a wave one expert and a few tokens, 8 elements a lane at a time.
+// Workgroups past the experts cut x.
 template <typename TX, typename TR, int PX>
 __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, const TX* __restrict__ X, int64_t ldx,
                                                                        const TR* __restrict__ R, int64_t ldr,
                                                                        int expert_groups) {
-    const int t = blockIdx.y;
-    const TX* x = X + int64_t(t) * ldx;
+    const int lane = threadIdx.x % 64, t0 = blockIdx.y * kRouterTokens, n = min(kRouterTokens, L.T - t0);
     if (int(blockIdx.x) < expert_groups) {
-        const int e = blockIdx.x * kRouterWaves + threadIdx.x / 64, lane = threadIdx.x % 64;
+        const int e = blockIdx.x * kRouterWaves + threadIdx.x / 64;
         if (e >= L.E) return;
         const TR* r = R + int64_t(e) * ldr;
-        float s = 0.f;
-        for (int64_t d = lane; d < L.D; d += 64) s = fmaf(to_f32(x[d]), to_f32(r[d]), s);
+        float s[kRouterTokens] = {};
+#pragma unroll 4
+        for (int64_t d = lane * 8; d < L.D; d += 512) {
+            float a[8];
+            load8(r + d, L.D - d, a);
 #pragma unroll
-        for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
-        if (lane == 0) L.logits[t * L.E + e] = s;
+            for (int t = 0; t < kRouterTokens; ++t) {
+                if (t >= n) continue;
+                float x[8];
+                load8(X + int64_t(t0 + t) * ldx + d, L.D - d, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[t] = fmaf(x[i], a[i], s[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kRouterTokens; ++t) {
+#pragma unroll
+            for (int m = 32; m; m >>= 1) s[t] += __shfl_xor(s[t], m);
+            if (lane == 0 && t < n) L.logits[(t0 + t) * L.E + e] = s[t];
+        }
         return;
     }
     const int64_t Dp = L.steps_d * kStep;
-    const int64_t d = int64_t(blockIdx.x - expert_groups) * (kRouterWaves * 64) + threadIdx.x;
+    const int64_t d = (int64_t(blockIdx.x - expert_groups) * (kRouterWaves * 64) + threadIdx.x) * 8;
     if (d >= Dp) return;
-    __bf16 part[PX];
-    cut<PX>(d < L.D ? to_f32(x[d]) : 0.f, part);
+    for (int t = t0; t < t0 + n; ++t) {
+        float x[8];
+        load8(X + int64_t(t) * ldx + d, L.D - d, x);
+        bf16x8 out[PX];
 #pragma unroll
-    for (int i = 0; i < PX; ++i) L.xp[(int64_t(i) * L.T + t) * Dp + d] = part[i];
+        for (int j = 0; j < 8; ++j) {
+            __bf16 part[PX];
+            cut<PX>(x[j], part);
+#pragma unroll
+            for (int i = 0; i < PX; ++i) out[i][j] = part[i];
+        }
+#pragma unroll
+        for (int i = 0; i < PX; ++i)
+            *reinterpret_cast<bf16x8*>(L.xp + (int64_t(i) * L.T + t) * Dp + d) = out[i];
+    }
 }
 
 // Larger logits first, equal ones by index, NaN last: a 64-bit key.
@@ -80,95 +112,114 @@ __device__ __forceinline__ uint64_t key_of(float v, int e) {
     return uint64_t(b) << 32 | uint32_t(~e);
 }
 
-// A wave a token; lane l holds experts l, 64 + l, 128 + l, 192 + l.
-__global__ __launch_bounds__(64) void moe_choose_kernel(Layer L, int renormalize) {
-    const int t = blockIdx.x, lane = threadIdx.x;
-    uint64_t key[4];
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = 64 * i + lane;
-        v[i] = e < L.E ? L.logits[t * L.E + e] : -__builtin_inff();
-        key[i] = e < L.E ? key_of(v[i], e) : 0;
-    }
-    float top = 0.f, chosen_sum = 0.f, mine = 0.f;
-    for (int j = 0; j < L.k; ++j) {
-        uint64_t best = key[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i) best = key[i] > best ? key[i] : best;
-#pragma unroll
-        for (int m = 32; m; m >>= 1) {
-            const uint64_t o = __shfl_xor((unsigned long long)best, m);
-            best = o > best ? o : best;
-        }
-        const int e = int(~uint32_t(best));
-        float l = 0.f;
+constexpr int kChooseWaves = 16;
+
+// One workgroup. A wave a token at a time, lane l holding experts l, 64 + l,
+// 128 + l, 192 + l; then the lists by expert. Where a pair stands in its
+// expert's list changes no result, so places are taken by atomics in LDS.
+__global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(Layer L, int renormalize) {
+    __shared__ int16_t ids[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];
+    __shared__ int count[RETRO_MOE_MAX_E], rank[RETRO_MOE_MAX_E], place[RETRO_MOE_MAX_E];
+    __shared__ int wave_chosen[4], wave_pairs[4], n_chosen;
+    __shared__ int8_t choice[RETRO_MOE_MAX_E * RETRO_MOE_MAX_T];
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    if (threadIdx.x < RETRO_MOE_MAX_E) count[threadIdx.x] = 0;
+    for (int t = wave; t < L.T; t += kChooseWaves) {
+        uint64_t key[4];
+        float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float got = __shfl(v[i], e & 63);
-            if (e >> 6 == i) l = got;
-            if (key[i] == best) key[i] = 0;
+            const int e = 64 * i + lane;
+            v[i] = e < L.E ? L.logits[t * L.E + e] : -__builtin_inff();
+            key[i] = e < L.E ? key_of(v[i], e) : 0;
         }
-        if (j == 0) top = l;
-        const float p = expf(l - top);
-        chosen_sum += p;
-        if (lane == j) {
-            mine = p;
-            L.ids[t * L.k + j] = e;
-        }
-    }
-    float sum = chosen_sum;
-    if (!renormalize) {
-        sum = 0.f;
+        float top = 0.f, chosen_sum = 0.f, mine = 0.f;
+        for (int j = 0; j < L.k; ++j) {
+            uint64_t best = key[0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (64 * i + lane < L.E) sum += expf(v[i] - top);
+            for (int i = 1; i < 4; ++i) best = key[i] > best ? key[i] : best;
 #pragma unroll
-        for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
-    }
-    if (lane < L.k) L.share[t * L.k + lane] = mine / sum;
-}
-
-// The chosen experts in order of index, as a bit set in LDS.
-__device__ __forceinline__ void chosen_set(const Layer& L, uint64_t set[4]) {
-    if (threadIdx.x < 4) set[threadIdx.x] = 0;
-    __syncthreads();
-    for (int p = threadIdx.x; p < L.T * L.k; p += blockDim.x) {
-        const int e = L.ids[p];
-        atomicOr(reinterpret_cast<unsigned long long*>(&set[e >> 6]), 1ull << (e & 63));
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ int count_set(const uint64_t set[4]) {
-    return __popcll(set[0]) + __popcll(set[1]) + __popcll(set[2]) + __popcll(set[3]);
-}
-
-// The expert of rank n among the chosen ones (n below their number).
-__device__ __forceinline__ int expert_of_rank(const uint64_t set[4], int n) {
-    for (int w = 0; w < 4; ++w) {
-        uint64_t b = set[w];
-        const int c = __popcll(b);
-        if (n < c) {
-            for (; n > 0; --n) b &= b - 1;
-            return 64 * w + __ffsll((unsigned long long)b) - 1;
+            for (int m = 32; m; m >>= 1) {
+                const uint64_t o = __shfl_xor((unsigned long long)best, m);
+                best = o > best ? o : best;
+            }
+            const int e = int(~uint32_t(best));
+            float l = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float got = __shfl(v[i], e & 63);
+                if (e >> 6 == i) l = got;
+                if (key[i] == best) key[i] = 0;
+            }
+            if (j == 0) top = l;
+            const float p = expf(l - top);
+            chosen_sum += p;
+            if (lane == j) {
+                mine = p;
+                ids[t * L.k + j] = int16_t(e);
+            }
         }
-        n -= c;
+        float sum = chosen_sum;
+        if (!renormalize) {
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (64 * i + lane < L.E) sum += expf(v[i] - top);
+#pragma unroll
+            for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+        }
+        if (lane < L.k) L.share[t * L.k + lane] = mine / sum;
     }
-    return 0;
-}
-
-// The pairs of one expert, in order, by one wave; returns their number.
-__device__ __forceinline__ int pairs_of(const Layer& L, int e, int16_t* list) {
-    const int lane = threadIdx.x & 63;
-    int n = 0;
-    for (int p0 = 0; p0 < L.T * L.k; p0 += 64) {
-        const bool hit = p0 + lane < L.T * L.k && L.ids[p0 + lane] == e;
-        const uint64_t m = __ballot(hit);
-        if (hit) list[n + __popcll(m & ((1ull << lane) - 1))] = int16_t(p0 + lane);
-        n += __popcll(m);
+    __syncthreads();
+    const int pairs = L.T * L.k, p = threadIdx.x;  // at most a pair a thread
+    if (p < pairs) atomicAdd(&count[ids[p]], 1);
+    __syncthreads();
+    // ranks of the chosen experts, and where their pairs begin
+    int n = 0, before_pairs = 0, before = 0;
+    if (threadIdx.x < RETRO_MOE_MAX_E) {
+        n = count[threadIdx.x];
+        const uint64_t m = __ballot(n > 0);
+        before = __popcll(m & ((1ull << lane) - 1));
+        int run = n;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(run, d);
+            if (lane >= d) run += o;
+        }
+        before_pairs = run - n;
+        if (lane == 63) {
+            wave_chosen[wave] = __popcll(m);
+            wave_pairs[wave] = run;
+        }
     }
-    return n;
+    __syncthreads();
+    if (threadIdx.x < RETRO_MOE_MAX_E) {
+        for (int w = 0; w < wave; ++w) {
+            before += wave_chosen[w];
+            before_pairs += wave_pairs[w];
+        }
+        rank[threadIdx.x] = before;
+        place[threadIdx.x] = before_pairs;
+        if (n > 0) {
+            L.lists[1 + before * 3] = threadIdx.x;
+            L.lists[2 + before * 3] = before_pairs;
+            L.lists[3 + before * 3] = n;
+        }
+        if (threadIdx.x == RETRO_MOE_MAX_E - 1) {
+            n_chosen = before + (n > 0);
+            L.lists[0] = n_chosen;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_chosen * L.T; i += kChooseWaves * 64) choice[i] = -1;
+    __syncthreads();
+    if (p < pairs) {
+        const int e = ids[p];
+        L.order[atomicAdd(&place[e], 1)] = int16_t(p);
+        choice[rank[e] * L.T + p / L.k] = int8_t(p % L.k);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_chosen * L.T; i += kChooseWaves * 64) L.choice[i] = choice[i];
 }
 
 // 32 codes of a row's block (16 bytes) times their scale, as bf16: four
@@ -185,52 +236,70 @@ __device__ __forceinline__ void decode_block(const u32x4& q, uint32_t e, bf16x8 
     }
 }
 
+// Address of block b (32 codes) of a row, and of its scale byte, in a matrix of
+// `rows` rows of `steps` steps.
+__device__ __forceinline__ u32x4 block_codes(const uint8_t* codes, int64_t row, int64_t steps, int64_t b) {
+    return *reinterpret_cast<const u32x4*>(codes + row * steps * kStepBytes + b * 16);
+}
+__device__ __forceinline__ uint32_t block_scale(const uint8_t* scales, int64_t rows, int64_t row, int64_t b) {
+    return scales[(b / 8 * rows + row) * kStepScales + b % 8];
+}
+
 constexpr int kGateWaves = 8;
 
 // 16 features of one chosen expert: rows f0 .. f0 + 15 of gate and up times x of
 // the expert's tokens, 16 tokens at a time. The waves share the 128-element
-// pieces of D; their sums are added in LDS in the order of the waves.
-template <int PX, int PH>
-__global__ __launch_bounds__(kGateWaves * 64) void moe_gate_up_kernel(Layer L) {
-    __shared__ uint64_t set[4];
-    __shared__ int16_t list[RETRO_MOE_MAX_T];
-    __shared__ int n_pairs;
+// pieces of D, U at a time so that their loads are in flight together; the
+// waves' sums are added in LDS in their order.
+template <int PX, int PH, int U>
+__global__ __launch_bounds__(kGateWaves * 64, 4) void moe_gate_up_kernel(Layer L) {
     __shared__ float part[kGateWaves][2][16][17];
-    chosen_set(L, set);
-    if (int(blockIdx.y) >= count_set(set)) return;
-    const int e = expert_of_rank(set, blockIdx.y);
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, r = lane & 15, g = lane >> 4;
-    if (wave == 0) {
-        const int n = pairs_of(L, e, list);
-        if (lane == 0) n_pairs = n;
-    }
-    __syncthreads();
+    if (int(blockIdx.y) >= L.lists[0]) return;
+    const int e = L.lists[1 + blockIdx.y * 3], first = L.lists[2 + blockIdx.y * 3], n = L.lists[3 + blockIdx.y * 3];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int r = lane & 15, g = lane >> 4;
     const int64_t rows = int64_t(L.E) * 2 * L.F, Dp = L.steps_d * kStep, Fp = L.steps_f * kStep;
     const int64_t f0 = int64_t(blockIdx.x) * 16, f = min(f0 + r, L.F - 1);
     const int64_t row[2] = {int64_t(e) * 2 * L.F + f, int64_t(e) * 2 * L.F + L.F + f};
-    for (int p0 = 0; p0 < n_pairs; p0 += 16) {
-        const int pair = list[min(p0 + r, n_pairs - 1)];
+    const int pieces = f0 < L.F ? int(L.steps_d) * 2 : 0;  // past F only the zeros that pad h are written
+    for (int p0 = 0; p0 < n; p0 += 16) {
+        const bool used = p0 + r < n;  // columns past the pairs are computed from what is there and dropped
+        const int pair = L.order[first + (used ? p0 + r : p0)];
         const __bf16* x = L.xp + int64_t(pair / L.k) * Dp;
         f32x4 acc[2] = {};
-        // past F only the zeros that pad h are left to write
-        for (int64_t b = f0 < L.F ? int64_t(wave) * 4 + g : L.steps_d * 8; b < L.steps_d * 8; b += kGateWaves * 4) {
-            bf16x8 v[PX][4];
+        for (int c0 = wave; c0 < pieces; c0 += kGateWaves * U) {
+            u32x4 q[U][2];
+            uint32_t s[U][2];
+            bf16x8 v[U][PX][4];
 #pragma unroll
-            for (int p = 0; p < PX; ++p)
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * kGateWaves;
+                if (c >= pieces) continue;
+                const int64_t b = c * 4 + g;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[p][i] = *reinterpret_cast<const bf16x8*>(x + int64_t(p) * L.T * Dp + b * 32 + i * 8);
+                for (int m = 0; m < 2; ++m) {
+                    q[u][m] = block_codes(L.guc, row[m], L.steps_d, b);
+                    s[u][m] = block_scale(L.gus, rows, row[m], b);
+                }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const u32x4 q = *reinterpret_cast<const u32x4*>(L.guc + row[m] * L.steps_d * kStepBytes + b * 16);
-                const uint32_t s = L.gus[(b / 8 * rows + row[m]) * kStepScales + b % 8];
-                bf16x8 w[4];
-                decode_block(q, s, w);
-#pragma unroll
-                for (int p = PX - 1; p >= 0; --p)
+                for (int p = 0; p < PX; ++p)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], v[p][i], acc[m], 0, 0, 0);
+                        v[u][p][i] = *reinterpret_cast<const bf16x8*>(x + int64_t(p) * L.T * Dp + b * 32 + i * 8);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * kGateWaves >= pieces) continue;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    bf16x8 w[4];
+                    decode_block(q[u][m], s[u][m], w);
+#pragma unroll
+                    for (int p = PX - 1; p >= 0; --p)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], v[u][p][i], acc[m], 0, 0, 0);
+                }
             }
         }
         __syncthreads();  // the last round's sums are read
@@ -240,82 +309,137 @@ __global__ __launch_bounds__(kGateWaves * 64) void moe_gate_up_kernel(Layer L) {
             for (int i = 0; i < 4; ++i) part[wave][m][4 * g + i][r] = acc[m][i];
         __syncthreads();
         const int ff = threadIdx.x & 15, c = threadIdx.x >> 4;
-        if (c < 16 && p0 + c < n_pairs) {
+        if (c < 16 && p0 + c < n) {
             float gate = 0.f, up = 0.f;
 #pragma unroll
             for (int w = 0; w < kGateWaves; ++w) {
                 gate += part[w][0][ff][c];
                 up += part[w][1][ff][c];
             }
-            const float h = f0 + ff < L.F ? gate / (1.f + expf(-gate)) * up : 0.f;
+            const int pr = L.order[first + p0 + c];
+            const float h = f0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * L.share[pr] : 0.f;
             __bf16 cutp[PH];
             cut<PH>(h, cutp);
 #pragma unroll
-            for (int p = 0; p < PH; ++p)
-                L.hp[(int64_t(p) * L.T * L.k + list[p0 + c]) * Fp + f0 + ff] = cutp[p];
+            for (int p = 0; p < PH; ++p) L.hp[(int64_t(p) * L.T * L.k + pr) * Fp + f0 + ff] = cutp[p];
         }
     }
 }
 
-constexpr int kDownWaves = 16;
-constexpr int kDownRows = 16;
-
-// 16 outputs d: rows of every chosen expert's down matrix times h of its
-// tokens. A wave takes (expert, part of F) items in turn and leaves each pair's
-// 16 sums in LDS; then one thread adds up a token's pairs in order.
-template <typename TY, int PH>
-__global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(Layer L, TY* __restrict__ Y, int64_t ldy,
-                                                                   int max_parts) {
-    __shared__ uint64_t set[4];
-    __shared__ int16_t lists[kDownWaves][RETRO_MOE_MAX_T];
-    extern __shared__ float sums[];  // parts x pairs x 16
-    chosen_set(L, set);
-    const int n_chosen = count_set(set), pairs = L.T * L.k;
-    const int parts = max(1, min(max_parts, (3 * kDownWaves + n_chosen - 1) / n_chosen));
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, r = lane & 15, g = lane >> 4;
-    const int64_t rows = int64_t(L.E) * L.D, Fp = L.steps_f * kStep;
-    const int64_t d0 = int64_t(blockIdx.x) * kDownRows, d = min(d0 + r, L.D - 1);
-    const int64_t chunks = L.steps_f * 2;  // 128-element pieces of F
-    for (int item = wave; item < n_chosen * parts; item += kDownWaves) {
-        const int e = expert_of_rank(set, item / parts), part = item % parts;
-        const int n = pairs_of(L, e, lists[wave]);
-        const int64_t c0 = chunks * part / parts, c1 = chunks * (part + 1) / parts;
-        const int64_t row = int64_t(e) * L.D + d;
-        for (int p0 = 0; p0 < n; p0 += 16) {
-            const int pair = lists[wave][min(p0 + r, n - 1)];
-            const __bf16* h = L.hp + int64_t(pair) * Fp;
-            f32x4 acc = {};
-            for (int64_t c = c0; c < c1; ++c) {
-                const int64_t b = c * 4 + g;
-                const u32x4 q = *reinterpret_cast<const u32x4*>(L.dc + row * L.steps_f * kStepBytes + b * 16);
-                const uint32_t s = L.ds[(b / 8 * rows + row) * kStepScales + b % 8];
-                bf16x8 w[4];
-                decode_block(q, s, w);
-#pragma unroll
-                for (int p = PH - 1; p >= 0; --p)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bf16x8 v = *reinterpret_cast<const bf16x8*>(h + int64_t(p) * pairs * Fp + b * 32 + i * 8);
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], v, acc, 0, 0, 0);
-                    }
-            }
-            if (p0 + r < n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sums[(part * pairs + pair) * 16 + 4 * g + i] = acc[i];
-        }
-    }
+// 16 RF outputs of all tokens: y[t] is the sum over the chosen experts of down
+// times share times h of the token's pair with it, zero where it has none, so
+// the experts' rows are one long contraction with the tokens as columns. The
+// (expert, 128-element piece of F) items are cut into gridDim.y equal parts, a
+// part is dealt to the waves, U items at a time; their sums are added in LDS in
+// the order of the waves. One part writes Y, several write their sums.
+template <typename TY, int PH, int TB, int RF, int U, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, TB == 1 ? 4 : 2) void moe_down_kernel(Layer L, TY* __restrict__ Y,
+                                                                               int64_t ldy) {
+    __shared__ float part[WAVES][16 * TB][16 * RF + 1];
+    extern __shared__ int8_t choice[];  // chosen expert x T
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int r = lane & 15, g = lane >> 4, n_chosen = L.lists[0], pairs = L.T * L.k;
+    for (int i = threadIdx.x; i < n_chosen * L.T; i += WAVES * 64) choice[i] = L.choice[i];
     __syncthreads();
-    for (int o = threadIdx.x; o < L.T * 16; o += kDownWaves * 64) {
-        const int t = o / 16, dd = o % 16;
-        if (d0 + dd >= L.D) continue;
-        float y = 0.f;
-        for (int j = 0; j < L.k; ++j) {
-            float s = 0.f;
-            for (int p = 0; p < parts; ++p) s += sums[(p * pairs + t * L.k + j) * 16 + dd];
-            y = fmaf(L.share[t * L.k + j], s, y);
+    const int64_t rows = int64_t(L.E) * L.D, Fp = L.steps_f * kStep;
+    const int64_t d0 = int64_t(blockIdx.x) * (16 * RF);
+    int64_t d[RF];
+#pragma unroll
+    for (int m = 0; m < RF; ++m) d[m] = min(d0 + 16 * m + r, L.D - 1);
+    const int pieces = int(L.steps_f) * 2;
+    const int64_t items = int64_t(n_chosen) * pieces;
+    const int lo = int(items * blockIdx.y / gridDim.y), hi = int(items * (blockIdx.y + 1) / gridDim.y);
+    f32x4 acc[RF][TB] = {};
+    for (int i0 = lo + wave; i0 < hi; i0 += WAVES * U) {
+        u32x4 q[U][RF];
+        uint32_t s[U][RF];
+        int pair[U][TB];
+        int64_t b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int item = i0 + u * WAVES;
+            if (item >= hi) continue;
+            const int i = item / pieces, e = L.lists[1 + i * 3];
+            b[u] = (item - i * pieces) * 4 + g;
+#pragma unroll
+            for (int m = 0; m < RF; ++m) {
+                const int64_t row = int64_t(e) * L.D + d[m];
+                q[u][m] = block_codes(L.dc, row, L.steps_f, b[u]);
+                s[u][m] = block_scale(L.ds, rows, row, b[u]);
+            }
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const int token = 16 * t + r, j = token < L.T ? choice[i * L.T + token] : -1;
+                pair[u][t] = j < 0 ? -1 : token * L.k + j;
+            }
         }
-        Y[int64_t(t) * ldy + d0 + dd] = from_f32<TY>(y);
+        bf16x8 v[U][TB == 1 ? PH : 1][4];
+        auto load_h = [&](int u, int t, int p, bf16x8 (&to)[4]) {
+            const __bf16* h = L.hp + (int64_t(p) * pairs + max(pair[u][t], 0)) * Fp + b[u] * 32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                to[i] = bf16x8{};
+                if (pair[u][t] >= 0) to[i] = *reinterpret_cast<const bf16x8*>(h + i * 8);
+            }
+        };
+        if constexpr (TB == 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * WAVES < hi)
+#pragma unroll
+                    for (int p = 0; p < PH; ++p) load_h(u, 0, p, v[u][p]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * WAVES >= hi) continue;
+            bf16x8 w[RF][4];
+#pragma unroll
+            for (int m = 0; m < RF; ++m) decode_block(q[u][m], s[u][m], w[m]);
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                // a block of 16 tokens that none of this expert's are in
+                if (TB > 1 && !__any(pair[u][t] >= 0)) continue;
+#pragma unroll
+                for (int p = PH - 1; p >= 0; --p) {
+                    bf16x8(&h)[4] = v[u][TB == 1 ? p : 0];
+                    if (TB > 1) load_h(u, t, p, h);
+#pragma unroll
+                    for (int m = 0; m < RF; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[m][i], h[i], acc[m][t], 0, 0, 0);
+                }
+            }
+        }
     }
+#pragma unroll
+    for (int m = 0; m < RF; ++m)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[wave][16 * t + r][16 * m + 4 * g + i] = acc[m][t][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < L.T * 16 * RF; o += WAVES * 64) {
+        const int t = o / (16 * RF), c = o % (16 * RF);
+        if (d0 + c >= L.D) continue;
+        float y = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) y += part[w][t][c];
+        if (gridDim.y == 1)
+            Y[int64_t(t) * ldy + d0 + c] = from_f32<TY>(y);
+        else
+            L.sums[(int64_t(blockIdx.y) * L.T + t) * L.D + d0 + c] = y;
+    }
+}
+
+// The parts of the down product, added in their order.
+template <typename TY>
+__global__ __launch_bounds__(256) void moe_combine_kernel(Layer L, int splits, TY* __restrict__ Y, int64_t ldy) {
+    const int64_t d = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int t = blockIdx.y;
+    if (d >= L.D) return;
+    float y = 0.f;
+    for (int s = 0; s < splits; ++s) y += L.sums[(int64_t(s) * L.T + t) * L.D + d];
+    Y[int64_t(t) * ldy + d] = from_f32<TY>(y);
 }
 
 // bf16 parts of x and h for a type of x.
@@ -326,9 +450,17 @@ template <> constexpr int type_of<float>() { return RETRO_F32; }
 template <> constexpr int type_of<_Float16>() { return RETRO_F16; }
 template <> constexpr int type_of<__bf16>() { return RETRO_BF16; }
 
+// Workgroups along the experts of the down kernel: enough for two a CU.
+int down_splits(int64_t T, int64_t D, int64_t F, int64_t E, int64_t k, int rf) {
+    const int64_t slabs = host::cdiv(D, 16 * rf), items = std::min(E, T * k) * steps_of(F) * 2;
+    return int(std::max<int64_t>(1, std::min(host::cdiv(2 * host::kNumCUs, slabs), items / 16)));
+}
+// Outputs (in sixteens) of a workgroup of the down kernel.
+int down_rows(int64_t T) { return T <= 16 ? 2 : 4; }
+
 // The workspace's pieces, each on a 256-byte boundary.
 struct Pieces {
-    int64_t logits, ids, share, xp, hp, all;
+    int64_t logits, share, lists, order, choice, xp, hp, sums, all;
 };
 
 Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
@@ -338,36 +470,47 @@ Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) 
         where = at;
         at += host::cdiv(bytes, 256) * 256;
     };
+    const int64_t chosen = std::min(E, T * k);
     put(p.logits, T * E * 4);
-    put(p.ids, T * k * 4);
     put(p.share, T * k * 4);
+    put(p.lists, (1 + 3 * chosen) * 4);
+    put(p.order, T * k * 2);
+    put(p.choice, chosen * T);
     put(p.xp, x_parts(xtype) * T * steps_of(D) * kStep * 2);
     put(p.hp, h_parts(xtype) * T * k * steps_of(F) * kStep * 2);
+    const int splits = down_splits(T, D, F, E, k, down_rows(T));
+    put(p.sums, splits > 1 ? splits * T * D * 4 : 0);
     p.all = at;
     return p;
 }
 
-// LDS for the pairs' sums of the down kernel.
-constexpr int64_t kSumBytes = 128 * 1024;
-
 template <typename TX, typename TR>
-int launch_layer(Layer L, const TX* X, int64_t ldx, const TR* R, int64_t ldr, TX* Y, int64_t ldy, int renormalize,
-                 hipStream_t st) {
+int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t ldr, TX* Y, int64_t ldy,
+                 int renormalize, hipStream_t st) {
     constexpr int PX = x_parts(type_of<TX>()), PH = h_parts(type_of<TX>());
+    constexpr int UG = PX == 1 ? 2 : 1, UD = PH == 2 ? 2 : 1;
     const int groups = int(host::cdiv(L.E, kRouterWaves));
-    const int64_t cuts = host::cdiv(L.steps_d * kStep, kRouterWaves * 64);
+    const int64_t cuts = host::cdiv(L.steps_d * kStep, kRouterWaves * 64 * 8);
+    const int chosen = std::min(L.E, L.T * L.k);
     host::clear_last_error();
     moe_router_kernel<TX, TR, PX>
-        <<<dim3(uint32_t(groups + cuts), L.T), dim3(kRouterWaves * 64), 0, st>>>(L, X, ldx, R, ldr, groups);
-    moe_choose_kernel<<<dim3(L.T), dim3(64), 0, st>>>(L, renormalize);
-    const int most = std::min(L.E, L.T * L.k);
-    moe_gate_up_kernel<PX, PH>
-        <<<dim3(uint32_t(L.steps_f * (kStep / 16)), most), dim3(kGateWaves * 64), 0, st>>>(L);
-    const int64_t pair_bytes = int64_t(L.T) * L.k * 16 * 4;
-    const int parts = int(std::max<int64_t>(1, std::min<int64_t>(L.steps_f * 2, kSumBytes / pair_bytes)));
-    moe_down_kernel<TX, PH>
-        <<<dim3(uint32_t(host::cdiv(L.D, kDownRows))), dim3(kDownWaves * 64), size_t(parts * pair_bytes), st>>>(
-            L, Y, ldy, parts);
+        <<<dim3(uint32_t(groups + cuts), uint32_t(host::cdiv(L.T, kRouterTokens))), dim3(kRouterWaves * 64), 0, st>>>(
+            L, X, ldx, R, ldr, groups);
+    moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
+    moe_gate_up_kernel<PX, PH, UG>
+        <<<dim3(uint32_t(L.steps_f * (kStep / 16)), chosen), dim3(kGateWaves * 64), 0, st>>>(L);
+    const int rf = down_rows(L.T), splits = down_splits(L.T, L.D, L.F, L.E, L.k, rf);
+    const dim3 grid(uint32_t(host::cdiv(L.D, 16 * rf)), splits);
+    const size_t lds = size_t(chosen) * L.T;
+    if (L.T <= 16)
+        moe_down_kernel<TX, PH, 1, 2, UD, 8><<<grid, dim3(512), lds, st>>>(L, Y, ldy);
+    else if (L.T <= 32)
+        moe_down_kernel<TX, PH, 2, 4, 1, 8><<<grid, dim3(512), lds, st>>>(L, Y, ldy);
+    else
+        moe_down_kernel<TX, PH, 4, 4, 1, 8><<<grid, dim3(512), lds, st>>>(L, Y, ldy);
+    if (splits > 1)
+        moe_combine_kernel<TX>
+            <<<dim3(uint32_t(host::cdiv(L.D, 256)), L.T), dim3(256), 0, st>>>(L, splits, Y, ldy);
     return host::launch_status();
 }
 
@@ -441,10 +584,13 @@ int retro_moe(int xtype, const void* X, int64_t ldx, int rtype, const void* R, i
     L.dc = static_cast<const uint8_t*>(down_codes);
     L.ds = static_cast<const uint8_t*>(down_scales);
     L.logits = reinterpret_cast<float*>(base + p.logits);
-    L.ids = reinterpret_cast<int*>(base + p.ids);
     L.share = reinterpret_cast<float*>(base + p.share);
+    L.lists = reinterpret_cast<int*>(base + p.lists);
+    L.order = reinterpret_cast<int16_t*>(base + p.order);
+    L.choice = reinterpret_cast<int8_t*>(base + p.choice);
     L.xp = reinterpret_cast<__bf16*>(base + p.xp);
     L.hp = reinterpret_cast<__bf16*>(base + p.hp);
+    L.sums = reinterpret_cast<float*>(base + p.sums);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_float(xtype, [&](auto* tag) {
         using TX = std::remove_pointer_t<decltype(tag)>;
