@@ -52,29 +52,58 @@ __device__ __forceinline__ void cut(float v, __bf16 part[P]) {
 constexpr int kRouterWaves = 4;
 constexpr int kRouterTokens = 4;  // a wave
 
-// logits: a wave one expert and a few tokens, 8 elements a lane at a time.
-// Workgroups past the experts cut x.
+// 8 elements on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void load8_aligned(const T* x, float v[8]) {
+    typedef T vec __attribute__((ext_vector_type(16 / sizeof(T))));
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int j = 0; j < 8 / kPer; ++j) {
+        const vec w = reinterpret_cast<const vec*>(x)[j];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[j * kPer + i] = to_f32(w[i]);
+    }
+}
+
+// logits: a wave one expert and a few tokens, 8 elements a lane at a time; whole
+// steps of 512 elements without branches where all rows are `aligned` to 16
+// bytes. Workgroups past the experts cut x.
 template <typename TX, typename TR, int PX>
 __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, const TX* __restrict__ X, int64_t ldx,
                                                                        const TR* __restrict__ R, int64_t ldr,
-                                                                       int expert_groups) {
+                                                                       int expert_groups, bool aligned) {
     const int lane = threadIdx.x % 64, t0 = blockIdx.y * kRouterTokens, n = min(kRouterTokens, L.T - t0);
     if (int(blockIdx.x) < expert_groups) {
         const int e = blockIdx.x * kRouterWaves + threadIdx.x / 64;
         if (e >= L.E) return;
-        const TR* r = R + int64_t(e) * ldr;
+        const TR* r = R + int64_t(e) * ldr + lane * 8;
+        const TX* x[kRouterTokens];
+#pragma unroll
+        for (int t = 0; t < kRouterTokens; ++t) x[t] = X + int64_t(min(t0 + t, L.T - 1)) * ldx + lane * 8;
         float s[kRouterTokens] = {};
+        int64_t d = 0;
+        if (aligned)
 #pragma unroll 4
-        for (int64_t d = lane * 8; d < L.D; d += 512) {
+            for (; d + 512 <= L.D; d += 512) {
+                float a[8];
+                load8_aligned(r + d, a);
+#pragma unroll
+                for (int t = 0; t < kRouterTokens; ++t) {
+                    float v[8];
+                    load8_aligned(x[t] + d, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[t] = fmaf(v[i], a[i], s[t]);
+                }
+            }
+        for (; d < L.D; d += 512) {
             float a[8];
-            load8(r + d, L.D - d, a);
+            load8(r + d, L.D - d - lane * 8, a);
 #pragma unroll
             for (int t = 0; t < kRouterTokens; ++t) {
-                if (t >= n) continue;
-                float x[8];
-                load8(X + int64_t(t0 + t) * ldx + d, L.D - d, x);
+                float v[8];
+                load8(x[t] + d, L.D - d - lane * 8, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[t] = fmaf(x[i], a[i], s[t]);
+                for (int i = 0; i < 8; ++i) s[t] = fmaf(v[i], a[i], s[t]);
             }
         }
 #pragma unroll
@@ -105,11 +134,21 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, 
     }
 }
 
-// Larger logits first, equal ones by index, NaN last: a 64-bit key.
-__device__ __forceinline__ uint64_t key_of(float v, int e) {
-    uint32_t b = __float_as_uint(v + 0.f);  // -0 as +0
-    b = (b & 0x7fffffffu) > 0x7f800000u ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    return uint64_t(b) << 32 | uint32_t(~e);
+// A key that grows with the logit: 0 stands for none, 1 for NaN, -0 is +0.
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return (b & 0x7fffffffu) > 0x7f800000u ? 1u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+    return __uint_as_float(k == 1u ? 0x7fc00000u : (k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// The largest of a wave's values, uniform.
+__device__ __forceinline__ uint32_t max_of_wave(uint32_t v) {
+    v = max16(v);
+    const uint32_t a = __builtin_amdgcn_readlane(int(v), 0), b = __builtin_amdgcn_readlane(int(v), 16),
+                   c = __builtin_amdgcn_readlane(int(v), 32), d = __builtin_amdgcn_readlane(int(v), 48);
+    return max(max(a, b), max(c, d));
 }
 
 constexpr int kChooseWaves = 16;
@@ -125,32 +164,29 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(Layer L, 
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     if (threadIdx.x < RETRO_MOE_MAX_E) count[threadIdx.x] = 0;
     for (int t = wave; t < L.T; t += kChooseWaves) {
-        uint64_t key[4];
+        uint32_t key[4];
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = 64 * i + lane;
-            v[i] = e < L.E ? L.logits[t * L.E + e] : -__builtin_inff();
-            key[i] = e < L.E ? key_of(v[i], e) : 0;
+            v[i] = e < L.E ? L.logits[t * L.E + e] : 0.f;
+            key[i] = e < L.E ? key_of(v[i]) : 0u;
         }
         float top = 0.f, chosen_sum = 0.f, mine = 0.f;
         for (int j = 0; j < L.k; ++j) {
-            uint64_t best = key[0];
-#pragma unroll
-            for (int i = 1; i < 4; ++i) best = key[i] > best ? key[i] : best;
-#pragma unroll
-            for (int m = 32; m; m >>= 1) {
-                const uint64_t o = __shfl_xor((unsigned long long)best, m);
-                best = o > best ? o : best;
-            }
-            const int e = int(~uint32_t(best));
-            float l = 0.f;
+            // the largest key, at its lowest expert
+            const uint32_t best = max_of_wave(max(max(key[0], key[1]), max(key[2], key[3])));
+            int e = -1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float got = __shfl(v[i], e & 63);
-                if (e >> 6 == i) l = got;
-                if (key[i] == best) key[i] = 0;
+                const uint64_t m = __ballot(key[i] == best);
+                if (e < 0 && m) {
+                    const int at = __ffsll((unsigned long long)m) - 1;
+                    e = 64 * i + at;
+                    if (lane == at) key[i] = 0;
+                }
             }
+            const float l = of_key(best);
             if (j == 0) top = l;
             const float p = expf(l - top);
             chosen_sum += p;
@@ -222,85 +258,87 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(Layer L, 
     for (int i = threadIdx.x; i < n_chosen * L.T; i += kChooseWaves * 64) L.choice[i] = choice[i];
 }
 
-// 32 codes of a row's block (16 bytes) times their scale, as bf16: four
-// operands of 8 elements.
-__device__ __forceinline__ void decode_block(const u32x4& q, uint32_t e, bf16x8 w[4]) {
+// A lane's part of a 256-element step of 16 rows: lane (r, g) holds blocks g and
+// 4 + g of row r and the row's eight scale bytes, so that a wave reads whole
+// 128-byte pieces of the rows.
+struct Step {
+    u32x4 code[2];
+    u32x2 scale;
+};
+
+__device__ __forceinline__ void load_step(Step& s, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                          int64_t row, int64_t steps, int64_t step, int g) {
+    const uint8_t* c = codes + (row * steps + step) * kStepBytes + g * 16;
+    s.code[0] = *reinterpret_cast<const u32x4*>(c);
+    s.code[1] = *reinterpret_cast<const u32x4*>(c + 64);
+    s.scale = *reinterpret_cast<const u32x2*>(scales + (step * rows + row) * kStepScales);
+}
+
+// One of its blocks times its scale, as bf16: four operands of 8 elements.
+__device__ __forceinline__ void decode(const Step& st, int half, int g, bf16x8 w[4]) {
+    const uint32_t e = (st.scale[half] >> (8 * g)) & 0xffu;
     const float s = e == 255u ? __uint_as_float(0x7fc00000u) : scale_value(e);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], s, 0);
-        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], s, 1);
-        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], s, 2);
-        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], s, 3);
+        const uint32_t q = st.code[half][i];
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1);
+        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2);
+        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3);
         w[i] = bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
     }
 }
 
-// Address of block b (32 codes) of a row, and of its scale byte, in a matrix of
-// `rows` rows of `steps` steps.
-__device__ __forceinline__ u32x4 block_codes(const uint8_t* codes, int64_t row, int64_t steps, int64_t b) {
-    return *reinterpret_cast<const u32x4*>(codes + row * steps * kStepBytes + b * 16);
-}
-__device__ __forceinline__ uint32_t block_scale(const uint8_t* scales, int64_t rows, int64_t row, int64_t b) {
-    return scales[(b / 8 * rows + row) * kStepScales + b % 8];
+// 32 elements of a row of x or h, as four operands.
+__device__ __forceinline__ void load_block(bf16x8 v[4], const __bf16* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const bf16x8*>(p + i * 8);
 }
 
 constexpr int kGateWaves = 8;
 
-// 16 features of one chosen expert: rows f0 .. f0 + 15 of gate and up times x of
-// the expert's tokens, 16 tokens at a time. The waves share the 128-element
-// pieces of D, U at a time so that their loads are in flight together; the
-// waves' sums are added in LDS in their order.
-template <int PX, int PH, int U>
-__global__ __launch_bounds__(kGateWaves * 64, 4) void moe_gate_up_kernel(Layer L) {
+// Features of one chosen expert in slabs of 16: rows f0 .. f0 + 15 of gate and up
+// times x of the expert's tokens, 16 tokens at a time. `ks` (1, 2, 4 or 8) waves
+// share a slab, each a part of D; their sums are added in LDS in their order.
+template <int PX, int PH>
+__global__ __launch_bounds__(kGateWaves * 64, 4) void moe_gate_up_kernel(Layer L, int ks) {
     __shared__ float part[kGateWaves][2][16][17];
     if (int(blockIdx.y) >= L.lists[0]) return;
     const int e = L.lists[1 + blockIdx.y * 3], first = L.lists[2 + blockIdx.y * 3], n = L.lists[3 + blockIdx.y * 3];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-    const int r = lane & 15, g = lane >> 4;
+    const int r = lane & 15, g = lane >> 4, slabs = kGateWaves / ks;
     const int64_t rows = int64_t(L.E) * 2 * L.F, Dp = L.steps_d * kStep, Fp = L.steps_f * kStep;
-    const int64_t f0 = int64_t(blockIdx.x) * 16, f = min(f0 + r, L.F - 1);
+    const int64_t g0 = int64_t(blockIdx.x) * slabs * 16, f0 = g0 + wave / ks * 16, f = min(f0 + r, L.F - 1);
     const int64_t row[2] = {int64_t(e) * 2 * L.F + f, int64_t(e) * 2 * L.F + L.F + f};
-    const int pieces = f0 < L.F ? int(L.steps_d) * 2 : 0;  // past F only the zeros that pad h are written
+    // past F only the zeros that pad h are written
+    const int steps = f0 < L.F ? int(L.steps_d) : 0;
     for (int p0 = 0; p0 < n; p0 += 16) {
-        const bool used = p0 + r < n;  // columns past the pairs are computed from what is there and dropped
-        const int pair = L.order[first + (used ? p0 + r : p0)];
-        const __bf16* x = L.xp + int64_t(pair / L.k) * Dp;
+        // columns past the pairs repeat the first and are dropped
+        const int pair = L.order[first + (p0 + r < n ? p0 + r : p0)];
+        const __bf16* x = L.xp + int64_t(pair / L.k) * Dp + g * 32;
         f32x4 acc[2] = {};
-        for (int c0 = wave; c0 < pieces; c0 += kGateWaves * U) {
-            u32x4 q[U][2];
-            uint32_t s[U][2];
-            bf16x8 v[U][PX][4];
+#pragma unroll 2
+        for (int c = wave % ks; c < steps; c += ks) {
+            Step w[2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * kGateWaves;
-                if (c >= pieces) continue;
-                const int64_t b = c * 4 + g;
+            for (int m = 0; m < 2; ++m) load_step(w[m], L.guc, L.gus, rows, row[m], L.steps_d, c, g);
+            bf16x8 v[2][PX][4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    q[u][m] = block_codes(L.guc, row[m], L.steps_d, b);
-                    s[u][m] = block_scale(L.gus, rows, row[m], b);
-                }
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int p = 0; p < PX; ++p)
+                for (int p = 0; p < PX; ++p) load_block(v[b][p], x + int64_t(p) * L.T * Dp + c * kStep + b * 128);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[u][p][i] = *reinterpret_cast<const bf16x8*>(x + int64_t(p) * L.T * Dp + b * 32 + i * 8);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (c0 + u * kGateWaves >= pieces) continue;
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    bf16x8 w[4];
-                    decode_block(q[u][m], s[u][m], w);
+                    bf16x8 o[4];
+                    decode(w[m], b, g, o);
 #pragma unroll
                     for (int p = PX - 1; p >= 0; --p)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], v[u][p][i], acc[m], 0, 0, 0);
+                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[i], v[b][p][i], acc[m], 0, 0, 0);
                 }
-            }
         }
         __syncthreads();  // the last round's sums are read
 #pragma unroll
@@ -308,20 +346,20 @@ __global__ __launch_bounds__(kGateWaves * 64, 4) void moe_gate_up_kernel(Layer L
 #pragma unroll
             for (int i = 0; i < 4; ++i) part[wave][m][4 * g + i][r] = acc[m][i];
         __syncthreads();
-        const int ff = threadIdx.x & 15, c = threadIdx.x >> 4;
-        if (c < 16 && p0 + c < n) {
+        for (int o = threadIdx.x; o < slabs * 256; o += kGateWaves * 64) {
+            const int ff = o % (slabs * 16), c = o / (slabs * 16);
+            if (p0 + c >= n || g0 + ff >= Fp) continue;
             float gate = 0.f, up = 0.f;
-#pragma unroll
-            for (int w = 0; w < kGateWaves; ++w) {
-                gate += part[w][0][ff][c];
-                up += part[w][1][ff][c];
+            for (int w = 0; w < ks; ++w) {
+                gate += part[ff / 16 * ks + w][0][ff % 16][c];
+                up += part[ff / 16 * ks + w][1][ff % 16][c];
             }
             const int pr = L.order[first + p0 + c];
-            const float h = f0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * L.share[pr] : 0.f;
+            const float h = g0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * L.share[pr] : 0.f;
             __bf16 cutp[PH];
             cut<PH>(h, cutp);
 #pragma unroll
-            for (int p = 0; p < PH; ++p) L.hp[(int64_t(p) * L.T * L.k + pr) * Fp + f0 + ff] = cutp[p];
+            for (int p = 0; p < PH; ++p) L.hp[(int64_t(p) * L.T * L.k + pr) * Fp + g0 + ff] = cutp[p];
         }
     }
 }
@@ -329,10 +367,10 @@ __global__ __launch_bounds__(kGateWaves * 64, 4) void moe_gate_up_kernel(Layer L
 // 16 RF outputs of all tokens: y[t] is the sum over the chosen experts of down
 // times share times h of the token's pair with it, zero where it has none, so
 // the experts' rows are one long contraction with the tokens as columns. The
-// (expert, 128-element piece of F) items are cut into gridDim.y equal parts, a
-// part is dealt to the waves, U items at a time; their sums are added in LDS in
-// the order of the waves. One part writes Y, several write their sums.
-template <typename TY, int PH, int TB, int RF, int U, int WAVES>
+// (expert, 256-element step of F) items are cut into gridDim.y equal parts, a
+// part is dealt to the waves; their sums are added in LDS in the order of the
+// waves. One part writes Y, several write their sums.
+template <typename TY, int PH, int TB, int RF, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, TB == 1 ? 4 : 2) void moe_down_kernel(Layer L, TY* __restrict__ Y,
                                                                                int64_t ldy) {
     __shared__ float part[WAVES][16 * TB][16 * RF + 1];
@@ -346,67 +384,42 @@ __global__ __launch_bounds__(WAVES * 64, TB == 1 ? 4 : 2) void moe_down_kernel(L
     int64_t d[RF];
 #pragma unroll
     for (int m = 0; m < RF; ++m) d[m] = min(d0 + 16 * m + r, L.D - 1);
-    const int pieces = int(L.steps_f) * 2;
-    const int64_t items = int64_t(n_chosen) * pieces;
+    const int steps = int(L.steps_f);
+    const int64_t items = int64_t(n_chosen) * steps;
     const int lo = int(items * blockIdx.y / gridDim.y), hi = int(items * (blockIdx.y + 1) / gridDim.y);
     f32x4 acc[RF][TB] = {};
-    for (int i0 = lo + wave; i0 < hi; i0 += WAVES * U) {
-        u32x4 q[U][RF];
-        uint32_t s[U][RF];
-        int pair[U][TB];
-        int64_t b[U];
+#pragma unroll(TB == 1 && PH == 2 ? 2 : 1)
+    for (int item = lo + wave; item < hi; item += WAVES) {
+        const int i = item / steps, c = item - i * steps, e = L.lists[1 + i * 3];
+        Step w[RF];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int item = i0 + u * WAVES;
-            if (item >= hi) continue;
-            const int i = item / pieces, e = L.lists[1 + i * 3];
-            b[u] = (item - i * pieces) * 4 + g;
+        for (int m = 0; m < RF; ++m) load_step(w[m], L.dc, L.ds, rows, int64_t(e) * L.D + d[m], L.steps_f, c, g);
+        const __bf16* h[TB];
+        bool has[TB];
 #pragma unroll
-            for (int m = 0; m < RF; ++m) {
-                const int64_t row = int64_t(e) * L.D + d[m];
-                q[u][m] = block_codes(L.dc, row, L.steps_f, b[u]);
-                s[u][m] = block_scale(L.ds, rows, row, b[u]);
-            }
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                const int token = 16 * t + r, j = token < L.T ? choice[i * L.T + token] : -1;
-                pair[u][t] = j < 0 ? -1 : token * L.k + j;
-            }
+        for (int t = 0; t < TB; ++t) {
+            const int token = 16 * t + r, j = token < L.T ? choice[i * L.T + token] : -1;
+            has[t] = j >= 0;
+            h[t] = L.hp + int64_t(has[t] ? token * L.k + j : 0) * Fp + c * kStep + g * 32;
         }
-        bf16x8 v[U][TB == 1 ? PH : 1][4];
-        auto load_h = [&](int u, int t, int p, bf16x8 (&to)[4]) {
-            const __bf16* h = L.hp + (int64_t(p) * pairs + max(pair[u][t], 0)) * Fp + b[u] * 32;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                to[i] = bf16x8{};
-                if (pair[u][t] >= 0) to[i] = *reinterpret_cast<const bf16x8*>(h + i * 8);
-            }
-        };
-        if constexpr (TB == 1)
+        for (int b = 0; b < 2; ++b) {
+            bf16x8 o[RF][4];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * WAVES < hi)
-#pragma unroll
-                    for (int p = 0; p < PH; ++p) load_h(u, 0, p, v[u][p]);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u * WAVES >= hi) continue;
-            bf16x8 w[RF][4];
-#pragma unroll
-            for (int m = 0; m < RF; ++m) decode_block(q[u][m], s[u][m], w[m]);
+            for (int m = 0; m < RF; ++m) decode(w[m], b, g, o[m]);
 #pragma unroll
             for (int t = 0; t < TB; ++t) {
-                // a block of 16 tokens that none of this expert's are in
-                if (TB > 1 && !__any(pair[u][t] >= 0)) continue;
+                // a block of 16 tokens without one of this expert's
+                if (TB > 1 && !__any(has[t])) continue;
 #pragma unroll
                 for (int p = PH - 1; p >= 0; --p) {
-                    bf16x8(&h)[4] = v[u][TB == 1 ? p : 0];
-                    if (TB > 1) load_h(u, t, p, h);
+                    bf16x8 v[4] = {};
+                    if (has[t]) load_block(v, h[t] + int64_t(p) * pairs * Fp + b * 128);
 #pragma unroll
                     for (int m = 0; m < RF; ++m)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[m][i], h[i], acc[m][t], 0, 0, 0);
+                        for (int q = 0; q < 4; ++q)
+                            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[m][q], v[q], acc[m][t], 0, 0, 0);
                 }
             }
         }
@@ -450,13 +463,20 @@ template <> constexpr int type_of<float>() { return RETRO_F32; }
 template <> constexpr int type_of<_Float16>() { return RETRO_F16; }
 template <> constexpr int type_of<__bf16>() { return RETRO_BF16; }
 
-// Workgroups along the experts of the down kernel: enough for two a CU.
-int down_splits(int64_t T, int64_t D, int64_t F, int64_t E, int64_t k, int rf) {
-    const int64_t slabs = host::cdiv(D, 16 * rf), items = std::min(E, T * k) * steps_of(F) * 2;
-    return int(std::max<int64_t>(1, std::min(host::cdiv(2 * host::kNumCUs, slabs), items / 16)));
+// The down kernel's shape: outputs of a workgroup in sixteens, waves, and parts
+// of the experts' items (workgroups enough for two a CU). With few items, as for
+// single tokens, one part whose 16 waves take an item or a few each.
+struct Down {
+    int rf, waves, splits;
+};
+
+Down down_shape(int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
+    const int64_t items = std::min(E, T * k) * steps_of(F);
+    if (T <= 16 && items <= 64) return {1, 16, 1};
+    const int rf = T <= 16 ? 2 : 4;
+    const int64_t slabs = host::cdiv(D, 16 * rf);
+    return {rf, 8, int(std::max<int64_t>(1, std::min(host::cdiv(2 * host::kNumCUs, slabs), items / 8)))};
 }
-// Outputs (in sixteens) of a workgroup of the down kernel.
-int down_rows(int64_t T) { return T <= 16 ? 2 : 4; }
 
 // The workspace's pieces, each on a 256-byte boundary.
 struct Pieces {
@@ -478,7 +498,7 @@ Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) 
     put(p.choice, chosen * T);
     put(p.xp, x_parts(xtype) * T * steps_of(D) * kStep * 2);
     put(p.hp, h_parts(xtype) * T * k * steps_of(F) * kStep * 2);
-    const int splits = down_splits(T, D, F, E, k, down_rows(T));
+    const int splits = down_shape(T, D, F, E, k).splits;
     put(p.sums, splits > 1 ? splits * T * D * 4 : 0);
     p.all = at;
     return p;
@@ -488,29 +508,36 @@ template <typename TX, typename TR>
 int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t ldr, TX* Y, int64_t ldy,
                  int renormalize, hipStream_t st) {
     constexpr int PX = x_parts(type_of<TX>()), PH = h_parts(type_of<TX>());
-    constexpr int UG = PX == 1 ? 2 : 1, UD = PH == 2 ? 2 : 1;
     const int groups = int(host::cdiv(L.E, kRouterWaves));
     const int64_t cuts = host::cdiv(L.steps_d * kStep, kRouterWaves * 64 * 8);
     const int chosen = std::min(L.E, L.T * L.k);
+    const bool aligned = mx::aligned(X, 16) && mx::aligned(R, 16) && ldx * int64_t(sizeof(TX)) % 16 == 0 &&
+                         ldr * int64_t(sizeof(TR)) % 16 == 0;
     host::clear_last_error();
     moe_router_kernel<TX, TR, PX>
         <<<dim3(uint32_t(groups + cuts), uint32_t(host::cdiv(L.T, kRouterTokens))), dim3(kRouterWaves * 64), 0, st>>>(
-            L, X, ldx, R, ldr, groups);
+            L, X, ldx, R, ldr, groups, aligned);
     moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
-    moe_gate_up_kernel<PX, PH, UG>
-        <<<dim3(uint32_t(L.steps_f * (kStep / 16)), chosen), dim3(kGateWaves * 64), 0, st>>>(L);
-    const int rf = down_rows(L.T), splits = down_splits(L.T, L.D, L.F, L.E, L.k, rf);
-    const dim3 grid(uint32_t(host::cdiv(L.D, 16 * rf)), splits);
+    // waves enough for two workgroups a CU: several share a slab where there are few
+    const int64_t slabs = L.steps_f * (kStep / 16);
+    int ks = 1;
+    while (ks < kGateWaves && host::cdiv(slabs * ks, kGateWaves) * chosen < 2 * host::kNumCUs) ks *= 2;
+    moe_gate_up_kernel<PX, PH>
+        <<<dim3(uint32_t(host::cdiv(slabs * ks, kGateWaves)), chosen), dim3(kGateWaves * 64), 0, st>>>(L, ks);
+    const Down s = down_shape(L.T, L.D, L.F, L.E, L.k);
+    const dim3 grid(uint32_t(host::cdiv(L.D, 16 * s.rf)), s.splits), threads(s.waves * 64);
     const size_t lds = size_t(chosen) * L.T;
-    if (L.T <= 16)
-        moe_down_kernel<TX, PH, 1, 2, UD, 8><<<grid, dim3(512), lds, st>>>(L, Y, ldy);
+    if (s.rf == 1)
+        moe_down_kernel<TX, PH, 1, 1, 16><<<grid, threads, lds, st>>>(L, Y, ldy);
+    else if (L.T <= 16)
+        moe_down_kernel<TX, PH, 1, 2, 8><<<grid, threads, lds, st>>>(L, Y, ldy);
     else if (L.T <= 32)
-        moe_down_kernel<TX, PH, 2, 4, 1, 8><<<grid, dim3(512), lds, st>>>(L, Y, ldy);
+        moe_down_kernel<TX, PH, 2, 4, 8><<<grid, threads, lds, st>>>(L, Y, ldy);
     else
-        moe_down_kernel<TX, PH, 4, 4, 1, 8><<<grid, dim3(512), lds, st>>>(L, Y, ldy);
-    if (splits > 1)
+        moe_down_kernel<TX, PH, 4, 4, 8><<<grid, threads, lds, st>>>(L, Y, ldy);
+    if (s.splits > 1)
         moe_combine_kernel<TX>
-            <<<dim3(uint32_t(host::cdiv(L.D, 256)), L.T), dim3(256), 0, st>>>(L, splits, Y, ldy);
+            <<<dim3(uint32_t(host::cdiv(L.D, 256)), L.T), dim3(256), 0, st>>>(L, s.splits, Y, ldy);
     return host::launch_status();
 }
 

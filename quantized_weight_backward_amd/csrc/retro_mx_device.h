@@ -53,6 +53,16 @@ __device__ __forceinline__ uint32_t to_fp4(uint32_t old, float a, float b, float
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, BYTE);
 }
 
+// The largest of 16 neighbouring lanes' values, in all of them: exchanges in
+// pairs, in fours, and of the halves' mirror images.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xf, 0xf, true)));   // lanes 1 0 3 2
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xf, 0xf, true)));   // lanes 2 3 0 1
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xf, 0xf, true)));  // half rows mirrored
+    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xf, 0xf, true)));  // rows mirrored
+    return v;
+}
+
 // 8 elements of a row, the first `left` of them (zeros past them): one 16-byte
 // load, or two, where the row allows it.
 template <typename TX>

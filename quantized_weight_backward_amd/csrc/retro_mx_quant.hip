@@ -28,16 +28,6 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const TX* __res
         scales[(int64_t(k / kStep) * all_rows + row) * kStepScales + (k % kStep) / 32] = uint8_t(e);
 }
 
-// The largest of 16 neighbouring lanes' values, in all of them: exchanges in
-// pairs, in fours, and of the halves' mirror images.
-__device__ __forceinline__ uint32_t max16(uint32_t v) {
-    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xf, 0xf, true)));   // lanes 1 0 3 2
-    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xf, 0xf, true)));   // lanes 2 3 0 1
-    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xf, 0xf, true)));  // half rows mirrored
-    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xf, 0xf, true)));  // rows mirrored
-    return v;
-}
-
 constexpr int kTileRows = 256, kTileCols = 128;  // a workgroup's part of X
 constexpr int kTileWaves = 8;                    // each 32 rows
 constexpr int kColPitch = kStepBytes + 16, kRowPitch = kTileCols / 2 + 16;
