@@ -31,7 +31,6 @@ struct Layer {
     float* share;    // T x k
     int* lists;      // number of chosen experts, then for each in order of index: expert, first place, pairs
     int16_t* order;  // the pairs, by expert
-    int8_t* choice;  // chosen expert x T: which of the token's choices it is, or -1
     __bf16* xp;      // parts x T x Dp
     __bf16* hp;      // parts x (T * k) x Fp: share times h
     float* sums;     // splits x T x D
@@ -151,19 +150,24 @@ __device__ __forceinline__ uint32_t max_of_wave(uint32_t v) {
     return max(max(a, b), max(c, d));
 }
 
-constexpr int kChooseWaves = 16;
+// The chosen experts and their pairs, in LDS.
+struct Lists {
+    int16_t ids[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];    // expert of each pair
+    float share[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];    // and its share
+    int16_t order[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];  // the pairs by expert
+    int count[RETRO_MOE_MAX_E], place[RETRO_MOE_MAX_E];
+    int entry[3 * RETRO_MOE_MAX_E];  // of each chosen expert: expert, first place, pairs
+    int wave_chosen[4], wave_pairs[4], n_chosen;
+};
 
-// One workgroup. A wave a token at a time, lane l holding experts l, 64 + l,
-// 128 + l, 192 + l; then the lists by expert. Where a pair stands in its
-// expert's list changes no result, so places are taken by atomics in LDS.
-__global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(Layer L, int renormalize) {
-    __shared__ int16_t ids[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];
-    __shared__ int count[RETRO_MOE_MAX_E], rank[RETRO_MOE_MAX_E], place[RETRO_MOE_MAX_E];
-    __shared__ int wave_chosen[4], wave_pairs[4], n_chosen;
-    __shared__ int8_t choice[RETRO_MOE_MAX_E * RETRO_MOE_MAX_T];
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    if (threadIdx.x < RETRO_MOE_MAX_E) count[threadIdx.x] = 0;
-    for (int t = wave; t < L.T; t += kChooseWaves) {
+// Top-k of all tokens by a workgroup of at least 4 waves, a wave a token at a
+// time, lane l holding experts l, 64 + l, 128 + l, 192 + l; then the lists by
+// expert. Where a pair stands in its expert's list changes no result, so places
+// are taken by atomics.
+__device__ __forceinline__ void choose(const Layer& L, int renormalize, Lists& s) {
+    const int waves = blockDim.x / 64, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    for (int e = threadIdx.x; e < RETRO_MOE_MAX_E; e += blockDim.x) s.count[e] = 0;
+    for (int t = wave; t < L.T; t += waves) {
         uint32_t key[4];
         float v[4];
 #pragma unroll
@@ -192,7 +196,7 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(Layer L, 
             chosen_sum += p;
             if (lane == j) {
                 mine = p;
-                ids[t * L.k + j] = int16_t(e);
+                s.ids[t * L.k + j] = int16_t(e);
             }
         }
         float sum = chosen_sum;
@@ -204,58 +208,66 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(Layer L, 
 #pragma unroll
             for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
         }
-        if (lane < L.k) L.share[t * L.k + lane] = mine / sum;
+        if (lane < L.k) s.share[t * L.k + lane] = mine / sum;
     }
     __syncthreads();
-    const int pairs = L.T * L.k, p = threadIdx.x;  // at most a pair a thread
-    if (p < pairs) atomicAdd(&count[ids[p]], 1);
+    const int pairs = L.T * L.k;
+    for (int p = threadIdx.x; p < pairs; p += blockDim.x) atomicAdd(&s.count[s.ids[p]], 1);
     __syncthreads();
     // ranks of the chosen experts, and where their pairs begin
-    int n = 0, before_pairs = 0, before = 0;
-    if (threadIdx.x < RETRO_MOE_MAX_E) {
-        n = count[threadIdx.x];
+    const int e = threadIdx.x;
+    int n = 0, first = 0, rank = 0;
+    if (e < RETRO_MOE_MAX_E) {
+        n = s.count[e];
         const uint64_t m = __ballot(n > 0);
-        before = __popcll(m & ((1ull << lane) - 1));
+        rank = __popcll(m & ((1ull << lane) - 1));
         int run = n;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const int o = __shfl_up(run, d);
             if (lane >= d) run += o;
         }
-        before_pairs = run - n;
+        first = run - n;
         if (lane == 63) {
-            wave_chosen[wave] = __popcll(m);
-            wave_pairs[wave] = run;
+            s.wave_chosen[wave] = __popcll(m);
+            s.wave_pairs[wave] = run;
         }
     }
     __syncthreads();
-    if (threadIdx.x < RETRO_MOE_MAX_E) {
+    if (e < RETRO_MOE_MAX_E) {
         for (int w = 0; w < wave; ++w) {
-            before += wave_chosen[w];
-            before_pairs += wave_pairs[w];
+            rank += s.wave_chosen[w];
+            first += s.wave_pairs[w];
         }
-        rank[threadIdx.x] = before;
-        place[threadIdx.x] = before_pairs;
+        s.place[e] = first;
         if (n > 0) {
-            L.lists[1 + before * 3] = threadIdx.x;
-            L.lists[2 + before * 3] = before_pairs;
-            L.lists[3 + before * 3] = n;
+            s.entry[3 * rank] = e;
+            s.entry[3 * rank + 1] = first;
+            s.entry[3 * rank + 2] = n;
         }
-        if (threadIdx.x == RETRO_MOE_MAX_E - 1) {
-            n_chosen = before + (n > 0);
-            L.lists[0] = n_chosen;
-        }
+        if (e == RETRO_MOE_MAX_E - 1) s.n_chosen = rank + (n > 0);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n_chosen * L.T; i += kChooseWaves * 64) choice[i] = -1;
+    for (int p = threadIdx.x; p < pairs; p += blockDim.x) s.order[atomicAdd(&s.place[s.ids[p]], 1)] = int16_t(p);
     __syncthreads();
-    if (p < pairs) {
-        const int e = ids[p];
-        L.order[atomicAdd(&place[e], 1)] = int16_t(p);
-        choice[rank[e] * L.T + p / L.k] = int8_t(p % L.k);
+}
+
+// The lists for the launches that follow.
+__device__ __forceinline__ void write_lists(const Layer& L, const Lists& s) {
+    if (threadIdx.x == 0) L.lists[0] = s.n_chosen;
+    for (int i = threadIdx.x; i < 3 * s.n_chosen; i += blockDim.x) L.lists[1 + i] = s.entry[i];
+    for (int p = threadIdx.x; p < L.T * L.k; p += blockDim.x) {
+        L.order[p] = s.order[p];
+        L.share[p] = s.share[p];
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n_chosen * L.T; i += kChooseWaves * 64) L.choice[i] = choice[i];
+}
+
+constexpr int kChooseWaves = 16;
+
+__global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(Layer L, int renormalize) {
+    __shared__ Lists lists;
+    choose(L, renormalize, lists);
+    write_lists(L, lists);
 }
 
 // A lane's part of a 256-element step of 16 rows: lane (r, g) holds blocks g and
@@ -274,13 +286,14 @@ __device__ __forceinline__ void load_step(Step& s, const uint8_t* codes, const u
     s.scale = *reinterpret_cast<const u32x2*>(scales + (step * rows + row) * kStepScales);
 }
 
-// One of its blocks times its scale, as bf16: four operands of 8 elements.
-__device__ __forceinline__ void decode(const Step& st, int half, int g, bf16x8 w[4]) {
-    const uint32_t e = (st.scale[half] >> (8 * g)) & 0xffu;
+// A block times the scale byte at the bottom of `scale`, as bf16: four operands
+// of 8 elements.
+__device__ __forceinline__ void decode(const u32x4& code, uint32_t scale, bf16x8 w[4]) {
+    const uint32_t e = scale & 0xffu;
     const float s = e == 255u ? __uint_as_float(0x7fc00000u) : scale_value(e);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t q = st.code[half][i];
+        const uint32_t q = code[i];
         const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0);
         const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1);
         const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2);
@@ -295,67 +308,120 @@ __device__ __forceinline__ void load_block(bf16x8 v[4], const __bf16* p) {
     for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const bf16x8*>(p + i * 8);
 }
 
-constexpr int kGateWaves = 8;
+// use(c) for c = first, first + by, ... below end, each loaded while the one
+// before is used.
+template <typename Loaded, typename Load, typename Use>
+__device__ __forceinline__ void in_pairs(int first, int end, int by, Load&& load, Use&& use) {
+    if (first >= end) return;
+    Loaded a, b;
+    load(a, first);
+    for (int c = first;; c += 2 * by) {
+        if (c + by >= end) {
+            use(a);
+            return;
+        }
+        load(b, c + by);
+        use(a);
+        if (c + 2 * by >= end) {
+            use(b);
+            return;
+        }
+        load(a, c + 2 * by);
+        use(b);
+    }
+}
 
-// Features of one chosen expert in slabs of 16: rows f0 .. f0 + 15 of gate and up
-// times x of the expert's tokens, 16 tokens at a time. `ks` (1, 2, 4 or 8) waves
-// share a slab, each a part of D; their sums are added in LDS in their order.
-template <int PX, int PH>
-__global__ __launch_bounds__(kGateWaves * 64, 4) void moe_gate_up_kernel(Layer L, int ks) {
-    __shared__ float part[kGateWaves][2][16][17];
-    if (int(blockIdx.y) >= L.lists[0]) return;
-    const int e = L.lists[1 + blockIdx.y * 3], first = L.lists[2 + blockIdx.y * 3], n = L.lists[3 + blockIdx.y * 3];
+constexpr int kGateWaves = 4;
+
+// Features of one chosen expert in slabs of 16 SL: their rows of gate and of up
+// times x of the expert's tokens, 16 tokens at a time. `ks` (1, 2 or 4) waves
+// share a slab, each a part of D; their sums are added in LDS in their order. A
+// wave loads a step while it works on the one before. x comes from the caches,
+// which costs a wave as much as weights do: two slabs of 16 halve that.
+//
+// For a token or a few (OWN_LISTS) every workgroup chooses the experts itself,
+// which takes it about a microsecond where a launch of its own takes several.
+template <int PX, int PH, int SL, bool OWN_LISTS>
+__global__ __launch_bounds__(kGateWaves * 64, PX == 1 && SL == 1 ? 3 : 2) void moe_gate_up_kernel(Layer L, int ks,
+                                                                                                  int renormalize) {
+    constexpr int kRows = 16 * SL;
+    __shared__ float part[kGateWaves][2][kRows][17];
+    const int* entry = L.lists + 1 + blockIdx.y * 3;
+    const int16_t* order = L.order;
+    const float* share = L.share;
+    if constexpr (OWN_LISTS) {
+        __shared__ Lists own;
+        choose(L, renormalize, own);
+        if (blockIdx.x == 0 && blockIdx.y == 0) write_lists(L, own);
+        if (int(blockIdx.y) >= own.n_chosen) return;
+        entry = own.entry + blockIdx.y * 3;
+        order = own.order;
+        share = own.share;
+    } else {
+        if (int(blockIdx.y) >= L.lists[0]) return;
+    }
+    const int e = entry[0], first = entry[1], n = entry[2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int r = lane & 15, g = lane >> 4, slabs = kGateWaves / ks;
     const int64_t rows = int64_t(L.E) * 2 * L.F, Dp = L.steps_d * kStep, Fp = L.steps_f * kStep;
-    const int64_t g0 = int64_t(blockIdx.x) * slabs * 16, f0 = g0 + wave / ks * 16, f = min(f0 + r, L.F - 1);
-    const int64_t row[2] = {int64_t(e) * 2 * L.F + f, int64_t(e) * 2 * L.F + L.F + f};
+    const int64_t g0 = int64_t(blockIdx.x) * slabs * kRows, f0 = g0 + wave / ks * kRows;
+    int64_t row[2 * SL];  // gate, then up
+#pragma unroll
+    for (int m = 0; m < 2 * SL; ++m)
+        row[m] = int64_t(e) * 2 * L.F + (m / SL) * L.F + min(f0 + 16 * (m % SL) + r, L.F - 1);
     // past F only the zeros that pad h are written
     const int steps = f0 < L.F ? int(L.steps_d) : 0;
     for (int p0 = 0; p0 < n; p0 += 16) {
-        // columns past the pairs repeat the first and are dropped
-        const int pair = L.order[first + (p0 + r < n ? p0 + r : p0)];
+        // lanes of columns past the pairs load nothing; their sums are dropped
+        const bool used = p0 + r < n;
+        const int pair = order[first + (used ? p0 + r : p0)];
         const __bf16* x = L.xp + int64_t(pair / L.k) * Dp + g * 32;
-        f32x4 acc[2] = {};
-#pragma unroll 2
-        for (int c = wave % ks; c < steps; c += ks) {
-            Step w[2];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) load_step(w[m], L.guc, L.gus, rows, row[m], L.steps_d, c, g);
+        f32x4 acc[2 * SL] = {};
+        struct Loaded {
+            Step w[2 * SL];
             bf16x8 v[2][PX][4];
+        };
+        auto load = [&](Loaded& l, int c) {
+#pragma unroll
+            for (int m = 0; m < 2 * SL; ++m) load_step(l.w[m], L.guc, L.gus, rows, row[m], L.steps_d, c, g);
+            if (used)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int p = 0; p < PX; ++p)
+                        load_block(l.v[b][p], x + int64_t(p) * L.T * Dp + c * kStep + b * 128);
+        };
+        auto use = [&](const Loaded& l) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int p = 0; p < PX; ++p) load_block(v[b][p], x + int64_t(p) * L.T * Dp + c * kStep + b * 128);
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
+                for (int m = 0; m < 2 * SL; ++m) {
                     bf16x8 o[4];
-                    decode(w[m], b, g, o);
+                    decode(l.w[m].code[b], l.w[m].scale[b] >> (8 * g), o);
 #pragma unroll
                     for (int p = PX - 1; p >= 0; --p)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[i], v[b][p][i], acc[m], 0, 0, 0);
+                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[i], l.v[b][p][i], acc[m], 0, 0, 0);
                 }
-        }
+        };
+        in_pairs<Loaded>(wave % ks, steps, ks, load, use);
         __syncthreads();  // the last round's sums are read
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2 * SL; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[wave][m][4 * g + i][r] = acc[m][i];
+            for (int i = 0; i < 4; ++i) part[wave][m / SL][16 * (m % SL) + 4 * g + i][r] = acc[m][i];
         __syncthreads();
-        for (int o = threadIdx.x; o < slabs * 256; o += kGateWaves * 64) {
-            const int ff = o % (slabs * 16), c = o / (slabs * 16);
+        for (int o = threadIdx.x; o < slabs * kRows * 16; o += kGateWaves * 64) {
+            const int ff = o % (slabs * kRows), c = o / (slabs * kRows);
             if (p0 + c >= n || g0 + ff >= Fp) continue;
             float gate = 0.f, up = 0.f;
             for (int w = 0; w < ks; ++w) {
-                gate += part[ff / 16 * ks + w][0][ff % 16][c];
-                up += part[ff / 16 * ks + w][1][ff % 16][c];
+                gate += part[ff / kRows * ks + w][0][ff % kRows][c];
+                up += part[ff / kRows * ks + w][1][ff % kRows][c];
             }
-            const int pr = L.order[first + p0 + c];
-            const float h = g0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * L.share[pr] : 0.f;
+            const int pr = order[first + p0 + c];
+            const float h = g0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * share[pr] : 0.f;
             __bf16 cutp[PH];
             cut<PH>(h, cutp);
 #pragma unroll
@@ -364,79 +430,107 @@ __global__ __launch_bounds__(kGateWaves * 64, 4) void moe_gate_up_kernel(Layer L
     }
 }
 
-// 16 RF outputs of all tokens: y[t] is the sum over the chosen experts of down
-// times share times h of the token's pair with it, zero where it has none, so
-// the experts' rows are one long contraction with the tokens as columns. The
-// (expert, 256-element step of F) items are cut into gridDim.y equal parts, a
-// part is dealt to the waves; their sums are added in LDS in the order of the
-// waves. One part writes Y, several write their sums.
-template <typename TY, int PH, int TB, int RF, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, TB == 1 ? 4 : 2) void moe_down_kernel(Layer L, TY* __restrict__ Y,
-                                                                               int64_t ldy) {
-    __shared__ float part[WAVES][16 * TB][16 * RF + 1];
-    extern __shared__ int8_t choice[];  // chosen expert x T
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-    const int r = lane & 15, g = lane >> 4, n_chosen = L.lists[0], pairs = L.T * L.k;
-    for (int i = threadIdx.x; i < n_chosen * L.T; i += WAVES * 64) choice[i] = L.choice[i];
+// 16 RF outputs of all tokens. The chosen experts' rows, one expert after
+// another, are one list of 128-element pieces, of which every wave of the
+// gridDim.y workgroups of these outputs takes an equal run. Within an expert the
+// columns are its pairs, 16 CT at a time, whose h holds the share; at the end of
+// an expert the wave adds its sums to those of the pairs' tokens in LDS, and at
+// the end of the kernel the waves' are added in their order. One workgroup writes
+// Y, several write their sums.
+template <typename TY, int PH, int CT, int RF, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kernel(Layer L, TY* __restrict__ Y,
+                                                                                   int64_t ldy) {
+    constexpr int kWide = 16 * RF + 4;
+    extern __shared__ __align__(16) float sums[];  // wave x token x kWide, then the lists
+    int* entry = reinterpret_cast<int*>(sums + WAVES * L.T * kWide);
+    const int n_chosen = L.lists[0];
+    int16_t* order = reinterpret_cast<int16_t*>(entry + 3 * min(L.E, L.T * L.k));
+    for (int i = threadIdx.x; i < 3 * n_chosen; i += WAVES * 64) entry[i] = L.lists[1 + i];
+    for (int i = threadIdx.x; i < L.T * L.k; i += WAVES * 64) order[i] = L.order[i];
+    for (int i = threadIdx.x; i < WAVES * L.T * kWide; i += WAVES * 64) sums[i] = 0.f;
     __syncthreads();
-    const int64_t rows = int64_t(L.E) * L.D, Fp = L.steps_f * kStep;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int r = lane & 15, g = lane >> 4;
+    float* mine = sums + wave * L.T * kWide;
+    const int64_t rows = int64_t(L.E) * L.D, Fp = L.steps_f * kStep, part_of_h = int64_t(L.T) * L.k * Fp;
     const int64_t d0 = int64_t(blockIdx.x) * (16 * RF);
-    int64_t d[RF];
+    const int pieces = int(L.steps_f) * 2;
+    const int64_t all = int64_t(n_chosen) * pieces;
+    const int share = blockIdx.y * WAVES + wave, shares = gridDim.y * WAVES;
+    const int64_t lo = all * share / shares, hi = all * (share + 1) / shares;
+    for (int64_t at = lo; at < hi;) {
+        const int i = __builtin_amdgcn_readfirstlane(int(at / pieces)), c0 = int(at - int64_t(i) * pieces);
+        const int c1 = int(min(int64_t(pieces), c0 + hi - at));
+        at += c1 - c0;
+        const int e = __builtin_amdgcn_readfirstlane(entry[3 * i]);
+        const int first = __builtin_amdgcn_readfirstlane(entry[3 * i + 1]);
+        const int n = __builtin_amdgcn_readfirstlane(entry[3 * i + 2]);
+        const uint8_t *code[RF], *scale[RF];
 #pragma unroll
-    for (int m = 0; m < RF; ++m) d[m] = min(d0 + 16 * m + r, L.D - 1);
-    const int steps = int(L.steps_f);
-    const int64_t items = int64_t(n_chosen) * steps;
-    const int lo = int(items * blockIdx.y / gridDim.y), hi = int(items * (blockIdx.y + 1) / gridDim.y);
-    f32x4 acc[RF][TB] = {};
-#pragma unroll(TB == 1 && PH == 2 ? 2 : 1)
-    for (int item = lo + wave; item < hi; item += WAVES) {
-        const int i = item / steps, c = item - i * steps, e = L.lists[1 + i * 3];
-        Step w[RF];
-#pragma unroll
-        for (int m = 0; m < RF; ++m) load_step(w[m], L.dc, L.ds, rows, int64_t(e) * L.D + d[m], L.steps_f, c, g);
-        const __bf16* h[TB];
-        bool has[TB];
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const int token = 16 * t + r, j = token < L.T ? choice[i * L.T + token] : -1;
-            has[t] = j >= 0;
-            h[t] = L.hp + int64_t(has[t] ? token * L.k + j : 0) * Fp + c * kStep + g * 32;
+        for (int m = 0; m < RF; ++m) {
+            const int64_t row = int64_t(e) * L.D + min(d0 + 16 * m + r, L.D - 1);
+            code[m] = L.dc + row * L.steps_f * kStepBytes + g * 16;
+            scale[m] = L.ds + row * kStepScales;
         }
+        for (int p0 = 0; p0 < n; p0 += 16 * CT) {
+            int pair[CT];
+            const __bf16* h[CT];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            bf16x8 o[RF][4];
-#pragma unroll
-            for (int m = 0; m < RF; ++m) decode(w[m], b, g, o[m]);
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                // a block of 16 tokens without one of this expert's
-                if (TB > 1 && !__any(has[t])) continue;
-#pragma unroll
-                for (int p = PH - 1; p >= 0; --p) {
-                    bf16x8 v[4] = {};
-                    if (has[t]) load_block(v, h[t] + int64_t(p) * pairs * Fp + b * 128);
-#pragma unroll
-                    for (int m = 0; m < RF; ++m)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[m][q], v[q], acc[m][t], 0, 0, 0);
-                }
+            for (int t = 0; t < CT; ++t) {
+                pair[t] = order[first + min(p0 + 16 * t + r, n - 1)];
+                h[t] = L.hp + pair[t] * Fp + g * 32;
             }
+            f32x4 acc[RF][CT] = {};
+            struct Loaded {
+                u32x4 code[RF];
+                uint32_t scale[RF];
+                bf16x8 v[CT][PH][4];
+            };
+            auto load = [&](Loaded& l, int c) {
+#pragma unroll
+                for (int m = 0; m < RF; ++m) {
+                    l.code[m] = *reinterpret_cast<const u32x4*>(code[m] + c * 64);
+                    l.scale[m] = *reinterpret_cast<const uint32_t*>(scale[m] + c / 2 * rows * kStepScales + c % 2 * 4);
+                }
+#pragma unroll
+                for (int t = 0; t < CT; ++t)
+#pragma unroll
+                    for (int p = 0; p < PH; ++p) load_block(l.v[t][p], h[t] + p * part_of_h + c * 128);
+            };
+            auto use = [&](const Loaded& l) {
+#pragma unroll
+                for (int m = 0; m < RF; ++m) {
+                    bf16x8 o[4];
+                    decode(l.code[m], l.scale[m] >> (8 * g), o);
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+#pragma unroll
+                        for (int p = PH - 1; p >= 0; --p)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                acc[m][t] =
+                                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[q], l.v[t][p][q], acc[m][t], 0, 0, 0);
+                }
+            };
+            in_pairs<Loaded>(c0, c1, 1, load, use);
+            // a token has an expert once, so no two lanes add to one place
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                if (p0 + 16 * t + r < n)
+#pragma unroll
+                    for (int m = 0; m < RF; ++m) {
+                        f32x4* to = reinterpret_cast<f32x4*>(mine + pair[t] / L.k * kWide + 16 * m + 4 * g);
+                        *to = *to + acc[m][t];
+                    }
         }
     }
-#pragma unroll
-    for (int m = 0; m < RF; ++m)
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[wave][16 * t + r][16 * m + 4 * g + i] = acc[m][t][i];
     __syncthreads();
     for (int o = threadIdx.x; o < L.T * 16 * RF; o += WAVES * 64) {
         const int t = o / (16 * RF), c = o % (16 * RF);
         if (d0 + c >= L.D) continue;
         float y = 0.f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) y += part[w][t][c];
+        for (int w = 0; w < WAVES; ++w) y += sums[(w * L.T + t) * kWide + c];
         if (gridDim.y == 1)
             Y[int64_t(t) * ldy + d0 + c] = from_f32<TY>(y);
         else
@@ -450,8 +544,16 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(Layer L, int splits, T
     const int64_t d = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int t = blockIdx.y;
     if (d >= L.D) return;
+    const float* p = L.sums + int64_t(t) * L.D + d;
+    const int64_t stride = int64_t(L.T) * L.D;
     float y = 0.f;
-    for (int s = 0; s < splits; ++s) y += L.sums[(int64_t(s) * L.T + t) * L.D + d];
+    for (int s = 0; s < splits; s += 8) {  // eight loads in flight
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = s + i < splits ? p[(s + i) * stride] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y += v[i];
+    }
     Y[int64_t(t) * ldy + d] = from_f32<TY>(y);
 }
 
@@ -463,24 +565,32 @@ template <> constexpr int type_of<float>() { return RETRO_F32; }
 template <> constexpr int type_of<_Float16>() { return RETRO_F16; }
 template <> constexpr int type_of<__bf16>() { return RETRO_BF16; }
 
-// The down kernel's shape: outputs of a workgroup in sixteens, waves, and parts
-// of the experts' items (workgroups enough for two a CU). With few items, as for
-// single tokens, one part whose 16 waves take an item or a few each.
+// The down kernel's shape: outputs of a workgroup in sixteens, blocks of 16 pairs
+// at a time, waves, and workgroups that share the pieces.
 struct Down {
-    int rf, waves, splits;
+    int rf, ct, waves, splits;
+    int64_t lds(int64_t T, int64_t E, int64_t k) const {
+        return waves * T * (16 * rf + 4) * 4 + 12 * std::min(E, T * k) + 2 * T * k;
+    }
 };
 
-Down down_shape(int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
-    const int64_t items = std::min(E, T * k) * steps_of(F);
-    if (T <= 16 && items <= 64) return {1, 16, 1};
-    const int rf = T <= 16 ? 2 : 4;
+Down down_shape(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
+    const int64_t items = std::min(E, T * k) * steps_of(F) * 2;
+    // Few pieces, as for single tokens: one workgroup of 16 waves, no parts to add.
+    if (T <= 16 && items <= 128) return {1, 1, 16, 1};
+    // Else one workgroup of 8 waves a CU (that many registers). 32 tokens, 8
+    // experts, D = 4096, F = 14336: 77 us with 64 outputs a workgroup; 104 with 32
+    // and two blocks of pairs, which pays where experts have more than 16 pairs.
+    // F32 (three parts of h) and many tokens (LDS) take 32 outputs too.
+    const bool two = T * k > 12 * E;
+    const int rf = two || xtype == RETRO_F32 || T > 32 ? 2 : 4;
     const int64_t slabs = host::cdiv(D, 16 * rf);
-    return {rf, 8, int(std::max<int64_t>(1, std::min(host::cdiv(2 * host::kNumCUs, slabs), items / 8)))};
+    return {rf, two ? 2 : 1, 8, int(std::max<int64_t>(1, std::min(host::cdiv(host::kNumCUs, slabs), items / 16)))};
 }
 
 // The workspace's pieces, each on a 256-byte boundary.
 struct Pieces {
-    int64_t logits, share, lists, order, choice, xp, hp, sums, all;
+    int64_t logits, share, lists, order, xp, hp, sums, all;
 };
 
 Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
@@ -495,10 +605,9 @@ Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) 
     put(p.share, T * k * 4);
     put(p.lists, (1 + 3 * chosen) * 4);
     put(p.order, T * k * 2);
-    put(p.choice, chosen * T);
     put(p.xp, x_parts(xtype) * T * steps_of(D) * kStep * 2);
     put(p.hp, h_parts(xtype) * T * k * steps_of(F) * kStep * 2);
-    const int splits = down_shape(T, D, F, E, k).splits;
+    const int splits = down_shape(xtype, T, D, F, E, k).splits;
     put(p.sums, splits > 1 ? splits * T * D * 4 : 0);
     p.all = at;
     return p;
@@ -517,24 +626,36 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
     moe_router_kernel<TX, TR, PX>
         <<<dim3(uint32_t(groups + cuts), uint32_t(host::cdiv(L.T, kRouterTokens))), dim3(kRouterWaves * 64), 0, st>>>(
             L, X, ldx, R, ldr, groups, aligned);
-    moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
-    // waves enough for two workgroups a CU: several share a slab where there are few
-    const int64_t slabs = L.steps_f * (kStep / 16);
-    int ks = 1;
-    while (ks < kGateWaves && host::cdiv(slabs * ks, kGateWaves) * chosen < 2 * host::kNumCUs) ks *= 2;
-    moe_gate_up_kernel<PX, PH>
-        <<<dim3(uint32_t(host::cdiv(slabs * ks, kGateWaves)), chosen), dim3(kGateWaves * 64), 0, st>>>(L, ks);
-    const Down s = down_shape(L.T, L.D, L.F, L.E, L.k);
-    const dim3 grid(uint32_t(host::cdiv(L.D, 16 * s.rf)), s.splits), threads(s.waves * 64);
-    const size_t lds = size_t(chosen) * L.T;
-    if (s.rf == 1)
-        moe_down_kernel<TX, PH, 1, 1, 16><<<grid, threads, lds, st>>>(L, Y, ldy);
-    else if (L.T <= 16)
-        moe_down_kernel<TX, PH, 1, 2, 8><<<grid, threads, lds, st>>>(L, Y, ldy);
-    else if (L.T <= 32)
-        moe_down_kernel<TX, PH, 2, 4, 8><<<grid, threads, lds, st>>>(L, Y, ldy);
+    const bool own_lists = L.T <= kGateWaves;
+    if (!own_lists) moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
+    // Slabs of 32 features where that leaves enough of them, and workgroups enough
+    // for four a CU: several waves share a slab where there are few.
+    auto gate_up = [&](auto kernel, int width) {
+        const int64_t slabs = host::cdiv(L.steps_f * kStep, width);
+        int ks = 1;
+        while (ks < kGateWaves && host::cdiv(slabs * ks, kGateWaves) * chosen < 4 * host::kNumCUs) ks *= 2;
+        kernel<<<dim3(uint32_t(host::cdiv(slabs * ks, kGateWaves)), chosen), dim3(kGateWaves * 64), 0, st>>>(
+            L, ks, renormalize);
+    };
+    const bool wide = PX == 1 && L.steps_f * (kStep / 32) * chosen >= 2 * host::kNumCUs;
+    constexpr int SL = PX == 1 ? 2 : 1;
+    if (own_lists)
+        wide ? gate_up(moe_gate_up_kernel<PX, PH, SL, true>, 32) : gate_up(moe_gate_up_kernel<PX, PH, 1, true>, 16);
     else
-        moe_down_kernel<TX, PH, 4, 4, 8><<<grid, threads, lds, st>>>(L, Y, ldy);
+        wide ? gate_up(moe_gate_up_kernel<PX, PH, SL, false>, 32) : gate_up(moe_gate_up_kernel<PX, PH, 1, false>, 16);
+    const Down s = down_shape(type_of<TX>(), L.T, L.D, L.F, L.E, L.k);
+    auto down = [&](auto kernel) {
+        kernel<<<dim3(uint32_t(host::cdiv(L.D, 16 * s.rf)), s.splits), dim3(s.waves * 64),
+                 size_t(s.lds(L.T, L.E, L.k)), st>>>(L, Y, ldy);
+    };
+    if (s.waves == 16)
+        down(moe_down_kernel<TX, PH, 1, 1, 16>);
+    else if (s.ct == 2)
+        down(moe_down_kernel<TX, PH, 2, 2, 8>);
+    else if (s.rf == 2)
+        down(moe_down_kernel<TX, PH, 1, 2, 8>);
+    else
+        down(moe_down_kernel<TX, PH, 1, 4, 8>);
     if (s.splits > 1)
         moe_combine_kernel<TX>
             <<<dim3(uint32_t(host::cdiv(L.D, 256)), L.T), dim3(256), 0, st>>>(L, s.splits, Y, ldy);
@@ -614,7 +735,6 @@ int retro_moe(int xtype, const void* X, int64_t ldx, int rtype, const void* R, i
     L.share = reinterpret_cast<float*>(base + p.share);
     L.lists = reinterpret_cast<int*>(base + p.lists);
     L.order = reinterpret_cast<int16_t*>(base + p.order);
-    L.choice = reinterpret_cast<int8_t*>(base + p.choice);
     L.xp = reinterpret_cast<__bf16*>(base + p.xp);
     L.hp = reinterpret_cast<__bf16*>(base + p.hp);
     L.sums = reinterpret_cast<float*>(base + p.sums);
