@@ -146,29 +146,33 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     // 14.6 against 9.7.
     if (skinny_applies(K, T) && tiles(32, 64) < 128) return RETRO_MX_VARIANT_SKINNY;
     if (!tiles_apply(size, ldy, K, N, T)) return skinny_applies(K, T) ? RETRO_MX_VARIANT_SKINNY : RETRO_MX_VARIANT_SIMPLE;
-    // Time of a round of workgroups over the CUs at K = 4096, in us, with one and
-    // with as many a CU as fit, measured at T x N = 4096 x 14336 and 128 .. 1024 x
-    // 4096; it grows with K alike for all. The last round has as many a CU as it
-    // needs.
+    // Time of a round of workgroups over the CUs, in us: a start and end and a time
+    // for each 256 elements of K, with one workgroup a CU and with as many as fit.
+    // Fitted to T x N x K = 4096 x 14336 x 4096, 4096 x 5120 x 4096, 8192^3, 17408 x
+    // 5120 x 2048 and 64 .. 1024 x 4096 x 4096 and 14336. The last round has as
+    // many a CU as it needs.
     struct Cost {
         int variant, rows_t, rows_n, per_cu;
-        double one, full;
+        double one, one_step, full, full_step;
     };
-    constexpr Cost costs[] = {
-        {RETRO_MX_VARIANT_TILE_256x256, 256, 256, Tile256x256::kPerCU, 34, 34},
-        {RETRO_MX_VARIANT_TILE_128x128, 128, 128, Tile128x128::kPerCU, 15, 22.5},
-        {RETRO_MX_VARIANT_TILE_64x128, 64, 128, Tile64x128::kPerCU, 12, 19},
-        {RETRO_MX_VARIANT_TILE_64x64, 64, 64, Tile64x64::kPerCU, 9.5, 15.5},
-        {RETRO_MX_VARIANT_TILE_64x64_K4, 64, 64, Tile64x64K4::kPerCU, 6.2, 6.2},
-        {RETRO_MX_VARIANT_TILE_32x64_K4, 32, 64, Tile32x64K4::kPerCU, 4.8, 4.8},
+    const double f32 = size == 4 ? 4 : 0;  // twice the bytes to write, with nothing beside
+    const Cost costs[] = {
+        {RETRO_MX_VARIANT_TILE_256x256, 256, 256, Tile256x256::kPerCU, 7 + f32, 1.9, 7 + f32, 1.9},
+        {RETRO_MX_VARIANT_TILE_128x128, 128, 128, Tile128x128::kPerCU, 3, 0.8, 5, 1.07},
+        {RETRO_MX_VARIANT_TILE_64x128, 64, 128, Tile64x128::kPerCU, 2.5, 0.6, 4, 0.95},
+        {RETRO_MX_VARIANT_TILE_64x64, 64, 64, Tile64x64::kPerCU, 2, 0.47, 3.5, 0.75},
+        {RETRO_MX_VARIANT_TILE_64x64_K4, 64, 64, Tile64x64K4::kPerCU, 2.5, 0.3, 2.5, 0.3},
+        {RETRO_MX_VARIANT_TILE_32x64_K4, 32, 64, Tile32x64K4::kPerCU, 2.5, 0.23, 2.5, 0.23},
     };
+    const double steps = double(steps_of(K));
     int best = 0;
     double least = 0;
     for (const Cost& c : costs) {
         const int64_t n = tiles(c.rows_t, c.rows_n), round = int64_t(host::kNumCUs) * c.per_cu;
         const int64_t rest = host::cdiv(n % round, host::kNumCUs);
-        double cost = double(n / round) * c.full;
-        if (rest) cost += c.one + (c.per_cu > 1 ? (c.full - c.one) * double(rest - 1) / (c.per_cu - 1) : 0);
+        const double one = c.one + c.one_step * steps, full = c.full + c.full_step * steps;
+        double cost = double(n / round) * full;
+        if (rest) cost += one + (c.per_cu > 1 ? (full - one) * double(rest - 1) / (c.per_cu - 1) : 0);
         if (!best || cost < least) {
             best = c.variant;
             least = cost;
