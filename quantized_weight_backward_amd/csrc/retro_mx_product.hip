@@ -149,18 +149,19 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     // Time of a round of workgroups over the CUs, in us: a start and end and a time
     // for each 256 elements of K, with one workgroup a CU and with as many as fit.
     // Fitted to T x N x K = 4096 x 14336 x 4096, 4096 x 5120 x 4096, 8192^3, 17408 x
-    // 5120 x 2048 and 64 .. 1024 x 4096 x 4096 and 14336. The last round has as
-    // many a CU as it needs.
+    // 5120 x 2048, 2048 x 5120 x 17408 and 64 .. 1024 x 4096 x 4096 and 14336. The
+    // last round has as many a CU as it needs (or, at one a CU, as many CUs: the
+    // fewer, the higher their clock).
     struct Cost {
         int variant, rows_t, rows_n, per_cu;
         double one, one_step, full, full_step;
     };
     const double f32 = size == 4 ? 4 : 0;  // twice the bytes to write, with nothing beside
     const Cost costs[] = {
-        {RETRO_MX_VARIANT_TILE_256x256, 256, 256, Tile256x256::kPerCU, 7 + f32, 1.9, 7 + f32, 1.9},
+        {RETRO_MX_VARIANT_TILE_256x256, 256, 256, Tile256x256::kPerCU, 7 + f32, 1.4, 7 + f32, 1.9},
         {RETRO_MX_VARIANT_TILE_128x128, 128, 128, Tile128x128::kPerCU, 3, 0.8, 5, 1.07},
         {RETRO_MX_VARIANT_TILE_64x128, 64, 128, Tile64x128::kPerCU, 2.5, 0.6, 4, 0.95},
-        {RETRO_MX_VARIANT_TILE_64x64, 64, 64, Tile64x64::kPerCU, 2, 0.47, 3.5, 0.75},
+        {RETRO_MX_VARIANT_TILE_64x64, 64, 64, Tile64x64::kPerCU, 2, 0.47, 4.5, 0.75},
         {RETRO_MX_VARIANT_TILE_64x64_K4, 64, 64, Tile64x64K4::kPerCU, 2.5, 0.3, 2.5, 0.3},
         {RETRO_MX_VARIANT_TILE_32x64_K4, 32, 64, Tile32x64K4::kPerCU, 2.5, 0.23, 2.5, 0.23},
     };
@@ -172,7 +173,8 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
         const int64_t rest = host::cdiv(n % round, host::kNumCUs);
         const double one = c.one + c.one_step * steps, full = c.full + c.full_step * steps;
         double cost = double(n / round) * full;
-        if (rest) cost += one + (c.per_cu > 1 ? (full - one) * double(rest - 1) / (c.per_cu - 1) : 0);
+        const double filled = c.per_cu > 1 ? double(rest - 1) / (c.per_cu - 1) : double(n % round) / double(round);
+        if (rest) cost += one + (full - one) * filled;
         if (!best || cost < least) {
             best = c.variant;
             least = cost;
