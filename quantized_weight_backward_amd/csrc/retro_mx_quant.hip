@@ -30,13 +30,110 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const TX* __res
 
 constexpr int kTileRows = 256, kTileCols = 128;  // a workgroup's part of X
 constexpr int kTileWaves = 8;                    // each 32 rows
-constexpr int kColPitch = kStepBytes + 16, kRowPitch = kTileCols / 2 + 16;
+constexpr int kColPitch = kStepBytes + 16;
+
+// Two neighbouring elements of a row, at whatever alignment the row has.
+template <typename TX>
+struct __attribute__((packed, aligned(sizeof(TX)))) Pair {
+    TX a, b;
+};
+
+// 32 rows of two columns in a lane. F32 values are held as such, 16-bit ones as
+// loaded, two to a register: magnitudes compare as integers, and the conversions
+// take 16-bit pairs.
+template <typename TX>
+struct Columns {
+    float v[2][32];
+    __device__ __forceinline__ void set(int i, Pair<TX> p) {
+        v[0][i] = p.a;
+        v[1][i] = p.b;
+    }
+    __device__ __forceinline__ void largest(uint32_t m[2]) const {
+        m[0] = m[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            m[0] = max(m[0], abs_bits(v[0][i]));
+            m[1] = max(m[1], abs_bits(v[1][i]));
+        }
+    }
+    // The larger of row i's two magnitudes, in an order that of_row undoes.
+    __device__ __forceinline__ uint32_t row(int i) const { return max(abs_bits(v[0][i]), abs_bits(v[1][i])); }
+    static __device__ __forceinline__ uint32_t of_row(uint32_t m) { return m; }
+    // Codes of rows i and i + 1 of column j, and of row i's two columns, as a byte.
+    template <int BYTE>
+    __device__ __forceinline__ uint32_t down(uint32_t old, int j, int i, float s) const {
+        return to_fp4<BYTE>(old, v[j][i], v[j][i + 1], s);
+    }
+    template <int BYTE>
+    __device__ __forceinline__ uint32_t across(uint32_t old, int i, float s) const {
+        return to_fp4<BYTE>(old, v[0][i], v[1][i], s);
+    }
+};
+
+__device__ __forceinline__ float half_of(uint32_t bits, const __bf16*) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ float half_of(uint32_t bits, const _Float16*) {
+    return float(__builtin_bit_cast(_Float16, uint16_t(bits)));
+}
+template <int BYTE>
+__device__ __forceinline__ uint32_t pair_to_fp4(uint32_t old, uint32_t two, float s, const __bf16*) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2, two), s, BYTE);
+}
+template <int BYTE>
+__device__ __forceinline__ uint32_t pair_to_fp4(uint32_t old, uint32_t two, float s, const _Float16*) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(f16x2, two), s, BYTE);
+}
+
+template <typename TX>
+struct Columns16 {
+    uint32_t x[32];
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    __device__ __forceinline__ void set(int i, Pair<TX> p) { x[i] = __builtin_bit_cast(uint32_t, p); }
+    __device__ __forceinline__ void largest(uint32_t m[2]) const {
+        u16x2 both = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            both = __builtin_elementwise_max(both, __builtin_bit_cast(u16x2, x[i] & 0x7fff7fffu));
+        m[0] = __float_as_uint(half_of(both[0], static_cast<const TX*>(nullptr)));
+        m[1] = __float_as_uint(half_of(both[1], static_cast<const TX*>(nullptr)));
+    }
+    __device__ __forceinline__ uint32_t row(int i) const { return max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu); }
+    static __device__ __forceinline__ uint32_t of_row(uint32_t m) {
+        return __float_as_uint(half_of(m, static_cast<const TX*>(nullptr)));
+    }
+    template <int BYTE>
+    __device__ __forceinline__ uint32_t down(uint32_t old, int j, int i, float s) const {
+        const uint32_t two = __builtin_amdgcn_perm(x[i + 1], x[i], j ? 0x07060302u : 0x05040100u);
+        return pair_to_fp4<BYTE>(old, two, s, static_cast<const TX*>(nullptr));
+    }
+    template <int BYTE>
+    __device__ __forceinline__ uint32_t across(uint32_t old, int i, float s) const {
+        return pair_to_fp4<BYTE>(old, x[i], s, static_cast<const TX*>(nullptr));
+    }
+};
+template <> struct Columns<__bf16> : Columns16<__bf16> {};
+template <> struct Columns<_Float16> : Columns16<_Float16> {};
+
+// Lane I's value of each 16 lanes, in all of them.
+template <int I>
+__device__ __forceinline__ uint32_t from16(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x150 + I, 0xf, 0xf, true));
+}
+
+// Rows 4 G .. 4 G + 3 of `c`, a byte each, and the lanes' scale words of 16 rows.
+template <int G, typename TX>
+__device__ __forceinline__ uint32_t across4(const Columns<TX>& c, uint32_t scales) {
+    constexpr int L = 4 * G % 16;
+    uint32_t w = c.template across<0>(0, 4 * G, __uint_as_float(from16<L>(scales)));
+    w = c.template across<1>(w, 4 * G + 1, __uint_as_float(from16<L + 1>(scales)));
+    w = c.template across<2>(w, 4 * G + 2, __uint_as_float(from16<L + 2>(scales)));
+    return c.template across<3>(w, 4 * G + 3, __uint_as_float(from16<L + 3>(scales)));
+}
 
 // Columns, or columns and rows from one reading of X. A wave takes 32 rows, a
 // lane two neighbouring columns of them: a column's block lies in one lane, a
-// row's in 16 lanes. 256 rows make whole 128-byte steps of the columns' codes,
-// which are gathered in LDS and written as such (and 64-byte pieces of the
-// rows').
+// row's in 16 lanes, of which lane j keeps the scales of rows j and 16 + j. 256
+// rows make whole 128-byte steps of the columns' codes, which are gathered in LDS
+// and written as such (and 64-byte pieces of the rows').
 template <typename TX, bool ROWS>
 __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
     const TX* __restrict__ X, int64_t ldx, int64_t rows, uint32_t cols, uint32_t groups, int64_t tile0,
@@ -44,7 +141,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
     uint8_t* __restrict__ col_codes, uint8_t* __restrict__ col_scales) {
     __shared__ __align__(16) uint8_t by_col[kTileCols * kColPitch];
     __shared__ __align__(16) uint8_t col_e[kTileCols * kStepScales];
-    __shared__ __align__(16) uint8_t by_row[ROWS ? kTileRows * kRowPitch : 16];
+    __shared__ __align__(16) uint32_t by_row[ROWS ? kTileRows / 4 * 64 : 4];  // four rows' bytes a word
     __shared__ __align__(16) uint8_t row_e[ROWS ? kTileRows * 4 : 16];
     const int64_t tile = tile0 + blockIdx.x / groups;  // of 256 rows
     const uint32_t c0 = (blockIdx.x % groups) * kTileCols;
@@ -52,54 +149,60 @@ __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
     const int64_t r0 = tile * kTileRows + wave * 32;
     const uint32_t c = c0 + 2 * lane;
     const int n = int(min(max(rows - r0, int64_t(0)), int64_t(32)));
-    float v[2][32];
+    Columns<TX> v;
     const TX* x = X + r0 * ldx + c;
-    if (c + 1 < cols) {
-        // one load for both columns, at whatever alignment the row has
-        struct __attribute__((packed, aligned(sizeof(TX)))) Pair {
-            TX a, b;
-        };
+    if (n == 32 && c0 + kTileCols <= cols) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            v[0][i] = v[1][i] = 0.f;
-            if (i < n) {
-                const Pair p = *reinterpret_cast<const Pair*>(x + i * ldx);
-                v[0][i] = to_f32(p.a);
-                v[1][i] = to_f32(p.b);
-            }
-        }
+        for (int i = 0; i < 32; ++i) v.set(i, *reinterpret_cast<const Pair<TX>*>(x + i * ldx));
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            v[0][i] = i < n && c < cols ? to_f32(x[i * ldx]) : 0.f;
-            v[1][i] = 0.f;
+            Pair<TX> p = {TX(0.f), TX(0.f)};
+            if (i < n && c < cols) p.a = x[i * ldx];
+            if (i < n && c + 1 < cols) p.b = x[i * ldx + 1];
+            v.set(i, p);
         }
     }
+    uint32_t m[2];
+    v.largest(m);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = max(m, abs_bits(v[j][i]));
-        const uint32_t e = scale_byte(m);
+        const uint32_t e = scale_byte(m[j]);
         const float s = scale_value(e);
         u32x4 q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t w = to_fp4<0>(0, v[j][8 * i], v[j][8 * i + 1], s);
-            w = to_fp4<1>(w, v[j][8 * i + 2], v[j][8 * i + 3], s);
-            w = to_fp4<2>(w, v[j][8 * i + 4], v[j][8 * i + 5], s);
-            q[i] = to_fp4<3>(w, v[j][8 * i + 6], v[j][8 * i + 7], s);
+            uint32_t w = v.template down<0>(0, j, 8 * i, s);
+            w = v.template down<1>(w, j, 8 * i + 2, s);
+            w = v.template down<2>(w, j, 8 * i + 4, s);
+            q[i] = v.template down<3>(w, j, 8 * i + 6, s);
         }
         *reinterpret_cast<u32x4*>(by_col + (2 * lane + j) * kColPitch + wave * 16) = q;
         col_e[(2 * lane + j) * kStepScales + wave] = uint8_t(e);
     }
     if constexpr (ROWS) {
+        uint32_t scales[2];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const uint32_t e = scale_byte(max16(max(abs_bits(v[0][i]), abs_bits(v[1][i]))));
-            by_row[(wave * 32 + i) * kRowPitch + lane] = uint8_t(to_fp4<0>(0, v[0][i], v[1][i], scale_value(e)));
-            if ((lane & 15) == 0) row_e[(wave * 32 + i) * 4 + lane / 16] = uint8_t(e);
+        for (int half = 0; half < 2; ++half) {
+            uint32_t mine = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t of_row = max16(v.row(16 * half + i));
+                mine = (lane & 15) == i ? of_row : mine;
+            }
+            const uint32_t e = scale_byte(Columns<TX>::of_row(mine));
+            scales[half] = __float_as_uint(scale_value(e));
+            row_e[(wave * 32 + 16 * half + (lane & 15)) * 4 + lane / 16] = uint8_t(e);
         }
+        uint32_t* w = by_row + wave * 8 * 64 + lane;
+        w[0 * 64] = across4<0>(v, scales[0]);
+        w[1 * 64] = across4<1>(v, scales[0]);
+        w[2 * 64] = across4<2>(v, scales[0]);
+        w[3 * 64] = across4<3>(v, scales[0]);
+        w[4 * 64] = across4<4>(v, scales[1]);
+        w[5 * 64] = across4<5>(v, scales[1]);
+        w[6 * 64] = across4<6>(v, scales[1]);
+        w[7 * 64] = across4<7>(v, scales[1]);
     }
     __syncthreads();
     for (int o = threadIdx.x; o < kTileCols * 8; o += kTileWaves * 64) {
@@ -113,11 +216,22 @@ __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
             *reinterpret_cast<const u32x2*>(col_e + threadIdx.x * kStepScales);
     if constexpr (ROWS) {
         const int64_t t0 = tile * kTileRows;
-        for (int o = threadIdx.x; o < kTileRows * 4; o += kTileWaves * 64) {
-            const int r = o / 4, part = o % 4;
-            if (t0 + r < rows)
-                *reinterpret_cast<u32x4*>(row_codes + (t0 + r) * row_steps * kStepBytes + c0 / 2 + part * 16) =
-                    *reinterpret_cast<const u32x4*>(by_row + r * kRowPitch + part * 16);
+        for (int o = threadIdx.x; o < kTileRows / 4 * 16; o += kTileWaves * 64) {
+            // words of four lanes, a byte a row: transposed to a word of each row
+            const int four = o / 16, part = o % 16;
+            const u32x4 w = *reinterpret_cast<const u32x4*>(by_row + four * 64 + part * 4);
+            const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);
+            const uint32_t b = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+            const uint32_t d = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+            const uint32_t e = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+            const uint32_t out[4] = {
+                __builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(b, a, 0x07060302u),
+                __builtin_amdgcn_perm(e, d, 0x05040100u), __builtin_amdgcn_perm(e, d, 0x07060302u)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t0 + 4 * four + j < rows)
+                    *reinterpret_cast<uint32_t*>(row_codes + (t0 + 4 * four + j) * row_steps * kStepBytes + c0 / 2 +
+                                                 part * 4) = out[j];
         }
         if (threadIdx.x < kTileRows && t0 + threadIdx.x < rows)
             *reinterpret_cast<uint32_t*>(row_scales + (int64_t(c0 / kStep) * rows + t0 + threadIdx.x) * kStepScales +
