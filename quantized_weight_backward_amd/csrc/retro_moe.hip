@@ -8,7 +8,7 @@
 //   choose   top-k of each token, the list of chosen experts and their pairs
 //   gate_up  a workgroup: 16 features of one chosen expert, all its tokens
 //   down     a workgroup: some outputs of all tokens, over all chosen experts or
-//            a part of them; the parts are added by a last launch (combine)
+//            a part of them; the last of those outputs' workgroups adds the parts
 // Weights are decoded exactly to bf16 (E2M1 times a power of two) and meet x
 // and h on v_mfma_f32_16x16x32_bf16 with F32 sums. x and h are cut into bf16
 // parts that add up to them: one for a BF16 x, two for F16 (11 bits), three for
@@ -29,11 +29,13 @@ struct Layer {
     const uint8_t *guc, *gus, *dc, *ds;
     float* logits;   // T x E
     float* share;    // T x k
-    int* lists;      // number of chosen experts, then for each in order of index: expert, first place, pairs
+    int* lists;      // number of chosen experts, then for each: expert, first place, pairs
     int16_t* order;  // the pairs, by expert
     __bf16* xp;      // parts x T x Dp
     __bf16* hp;      // parts x (T * k) x Fp: share times h
     float* sums;     // splits x T x D
+    unsigned* done;  // workgroups that have written their sums, for each block of outputs
+    int blocks;      // of outputs
 };
 
 // v as bf16 parts that add up to it (up to the last part's rounding). What does
@@ -113,6 +115,11 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, 
         }
         return;
     }
+    // the counters of the down kernel
+    if (blockIdx.y == 0)
+        for (int i = (blockIdx.x - expert_groups) * blockDim.x + threadIdx.x; i < L.blocks;
+             i += (gridDim.x - expert_groups) * blockDim.x)
+            L.done[i] = 0;
     const int64_t Dp = L.steps_d * kStep;
     const int64_t d = (int64_t(blockIdx.x - expert_groups) * (kRouterWaves * 64) + threadIdx.x) * 8;
     if (d >= Dp) return;
@@ -212,6 +219,17 @@ __device__ __forceinline__ void choose(const Layer& L, int renormalize, Lists& s
     }
     __syncthreads();
     const int pairs = L.T * L.k;
+    if (L.T == 1) {  // every choice is an expert of its own
+        if (int(threadIdx.x) < pairs) {
+            s.entry[3 * threadIdx.x] = s.ids[threadIdx.x];
+            s.entry[3 * threadIdx.x + 1] = threadIdx.x;
+            s.entry[3 * threadIdx.x + 2] = 1;
+            s.order[threadIdx.x] = int16_t(threadIdx.x);
+        }
+        if (threadIdx.x == 0) s.n_chosen = pairs;
+        __syncthreads();
+        return;
+    }
     for (int p = threadIdx.x; p < pairs; p += blockDim.x) atomicAdd(&s.count[s.ids[p]], 1);
     __syncthreads();
     // ranks of the chosen experts, and where their pairs begin
@@ -436,16 +454,19 @@ __global__ __launch_bounds__(kGateWaves * 64, PX == 1 && SL == 1 ? 3 : 2) void m
 // columns are its pairs, 16 CT at a time, whose h holds the share; at the end of
 // an expert the wave adds its sums to those of the pairs' tokens in LDS, and at
 // the end of the kernel the waves' are added in their order. One workgroup writes
-// Y, several write their sums.
+// Y; of several, each writes its sums at device scope (they run on different
+// XCDs) and the one that is done last adds them in their order. None waits for
+// another.
 template <typename TY, int PH, int CT, int RF, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kernel(Layer L, TY* __restrict__ Y,
                                                                                    int64_t ldy) {
     constexpr int kWide = 16 * RF + 4;
     extern __shared__ __align__(16) float sums[];  // wave x token x kWide, then the lists
     int* entry = reinterpret_cast<int*>(sums + WAVES * L.T * kWide);
-    const int n_chosen = L.lists[0];
-    int16_t* order = reinterpret_cast<int16_t*>(entry + 3 * min(L.E, L.T * L.k));
-    for (int i = threadIdx.x; i < 3 * n_chosen; i += WAVES * 64) entry[i] = L.lists[1 + i];
+    const int n_chosen = L.lists[0], most = min(L.E, L.T * L.k);
+    int16_t* order = reinterpret_cast<int16_t*>(entry + 3 * most);
+    // all that may be there: what lies past the chosen ones is not used
+    for (int i = threadIdx.x; i < 3 * most; i += WAVES * 64) entry[i] = L.lists[1 + i];
     for (int i = threadIdx.x; i < L.T * L.k; i += WAVES * 64) order[i] = L.order[i];
     for (int i = threadIdx.x; i < WAVES * L.T * kWide; i += WAVES * 64) sums[i] = 0.f;
     __syncthreads();
@@ -534,27 +555,37 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kern
         if (gridDim.y == 1)
             Y[int64_t(t) * ldy + d0 + c] = from_f32<TY>(y);
         else
-            L.sums[(int64_t(blockIdx.y) * L.T + t) * L.D + d0 + c] = y;
+            __hip_atomic_store(L.sums + (int64_t(blockIdx.y) * L.T + t) * L.D + d0 + c, y, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
     }
-}
-
-// The parts of the down product, added in their order.
-template <typename TY>
-__global__ __launch_bounds__(256) void moe_combine_kernel(Layer L, int splits, TY* __restrict__ Y, int64_t ldy) {
-    const int64_t d = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    const int t = blockIdx.y;
-    if (d >= L.D) return;
-    const float* p = L.sums + int64_t(t) * L.D + d;
+    if (gridDim.y == 1) return;
+    // this workgroup's sums are complete at device scope before its count
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        entry[0] = __hip_atomic_fetch_add(L.done + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                   gridDim.y - 1;
+    __syncthreads();
+    if (!entry[0]) return;
+    const int splits = gridDim.y;
     const int64_t stride = int64_t(L.T) * L.D;
-    float y = 0.f;
-    for (int s = 0; s < splits; s += 8) {  // eight loads in flight
-        float v[8];
+    for (int o = threadIdx.x; o < L.T * 16 * RF; o += WAVES * 64) {
+        const int t = o / (16 * RF), c = o % (16 * RF);
+        if (d0 + c >= L.D) continue;
+        const float* p = L.sums + int64_t(t) * L.D + d0 + c;
+        float y = 0.f;
+        for (int i = 0; i < splits; i += 8) {  // eight loads in flight
+            float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = s + i < splits ? p[(s + i) * stride] : 0.f;
+            for (int j = 0; j < 8; ++j)
+                v[j] = i + j < splits
+                           ? __hip_atomic_load(p + (i + j) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                           : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y += v[i];
+            for (int j = 0; j < 8; ++j) y += v[j];
+        }
+        Y[int64_t(t) * ldy + d0 + c] = from_f32<TY>(y);
     }
-    Y[int64_t(t) * ldy + d] = from_f32<TY>(y);
 }
 
 // bf16 parts of x and h for a type of x.
@@ -569,6 +600,7 @@ template <> constexpr int type_of<__bf16>() { return RETRO_BF16; }
 // at a time, waves, and workgroups that share the pieces.
 struct Down {
     int rf, ct, waves, splits;
+    int64_t blocks(int64_t D) const { return host::cdiv(D, 16 * rf); }
     int64_t lds(int64_t T, int64_t E, int64_t k) const {
         return waves * T * (16 * rf + 4) * 4 + 12 * std::min(E, T * k) + 2 * T * k;
     }
@@ -590,7 +622,7 @@ Down down_shape(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k
 
 // The workspace's pieces, each on a 256-byte boundary.
 struct Pieces {
-    int64_t logits, share, lists, order, xp, hp, sums, all;
+    int64_t logits, share, lists, order, xp, hp, sums, done, all;
 };
 
 Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
@@ -607,8 +639,9 @@ Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) 
     put(p.order, T * k * 2);
     put(p.xp, x_parts(xtype) * T * steps_of(D) * kStep * 2);
     put(p.hp, h_parts(xtype) * T * k * steps_of(F) * kStep * 2);
-    const int splits = down_shape(xtype, T, D, F, E, k).splits;
-    put(p.sums, splits > 1 ? splits * T * D * 4 : 0);
+    const Down s = down_shape(xtype, T, D, F, E, k);
+    put(p.sums, s.splits > 1 ? s.splits * T * D * 4 : 0);
+    put(p.done, s.splits > 1 ? s.blocks(D) * 4 : 0);
     p.all = at;
     return p;
 }
@@ -645,7 +678,7 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
         wide ? gate_up(moe_gate_up_kernel<PX, PH, SL, false>, 32) : gate_up(moe_gate_up_kernel<PX, PH, 1, false>, 16);
     const Down s = down_shape(type_of<TX>(), L.T, L.D, L.F, L.E, L.k);
     auto down = [&](auto kernel) {
-        kernel<<<dim3(uint32_t(host::cdiv(L.D, 16 * s.rf)), s.splits), dim3(s.waves * 64),
+        kernel<<<dim3(uint32_t(s.blocks(L.D)), s.splits), dim3(s.waves * 64),
                  size_t(s.lds(L.T, L.E, L.k)), st>>>(L, Y, ldy);
     };
     if (s.waves == 16)
@@ -656,9 +689,6 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
         down(moe_down_kernel<TX, PH, 1, 2, 8>);
     else
         down(moe_down_kernel<TX, PH, 1, 4, 8>);
-    if (s.splits > 1)
-        moe_combine_kernel<TX>
-            <<<dim3(uint32_t(host::cdiv(L.D, 256)), L.T), dim3(256), 0, st>>>(L, s.splits, Y, ldy);
     return host::launch_status();
 }
 
@@ -738,6 +768,9 @@ int retro_moe(int xtype, const void* X, int64_t ldx, int rtype, const void* R, i
     L.xp = reinterpret_cast<__bf16*>(base + p.xp);
     L.hp = reinterpret_cast<__bf16*>(base + p.hp);
     L.sums = reinterpret_cast<float*>(base + p.sums);
+    L.done = reinterpret_cast<unsigned*>(base + p.done);
+    const Down shape = down_shape(xtype, T, D, F, E, top_k);
+    L.blocks = shape.splits > 1 ? int(shape.blocks(D)) : 0;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_float(xtype, [&](auto* tag) {
         using TX = std::remove_pointer_t<decltype(tag)>;
