@@ -1511,11 +1511,16 @@ template <int TYPE>
 __global__ __launch_bounds__(256) void dequant_kernel(DequantArgs args) {
     const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
     if (gid >= args.groups) return;
-    const int n = (int)(gid / args.gpr);
+    // a 32-bit division wherever the groups' number allows it
+    const int n = args.groups >> 32 ? (int)(gid / args.gpr) : (int)((uint32_t)gid / (uint32_t)args.gpr);
     const int k = 4 * (int)(gid - (long long)n * args.gpr);
     float e[4];
     skinny_load4<TYPE>(args.W + (long long)n * args.pitch, k, args.K, args.wide, e);
     float* o = args.out + (long long)n * args.K + k;
+    if (args.wide) {  // whole groups, on 16-byte boundaries of the 16-byte aligned output
+        *reinterpret_cast<f32x4*>(o) = f32x4{e[0], e[1], e[2], e[3]};
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (k + i < args.K) o[i] = e[i];
