@@ -53,11 +53,23 @@ __device__ __forceinline__ uint32_t to_fp4(uint32_t old, float a, float b, float
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, BYTE);
 }
 
+// The value of the lane whose number differs in one bit.
+template <int BIT>
+__device__ __forceinline__ uint32_t swap_lanes(uint32_t v) {
+    if constexpr (BIT == 1) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xf, 0xf, true));  // 1 0 3 2
+    if constexpr (BIT == 2) return uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xf, 0xf, true));  // 2 3 0 1
+    if constexpr (BIT == 4) {
+        // eights mirrored, then each four mirrored back
+        const int m = __builtin_amdgcn_mov_dpp(int(v), 0x141, 0xf, 0xf, true);
+        return uint32_t(__builtin_amdgcn_mov_dpp(m, 0x1B, 0xf, 0xf, true));
+    }
+}
+
 // The largest of 16 neighbouring lanes' values, in all of them: exchanges in
 // pairs, in fours, and of the halves' mirror images.
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
-    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xf, 0xf, true)));   // lanes 1 0 3 2
-    v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xf, 0xf, true)));   // lanes 2 3 0 1
+    v = max(v, swap_lanes<1>(v));
+    v = max(v, swap_lanes<2>(v));
     v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x141, 0xf, 0xf, true)));  // half rows mirrored
     v = max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x140, 0xf, 0xf, true)));  // rows mirrored
     return v;
@@ -88,8 +100,8 @@ __device__ __forceinline__ uint32_t quantize8(const float v[8], uint32_t& e) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-    m = max(m, uint32_t(__shfl_xor(int(m), 1)));
-    m = max(m, uint32_t(__shfl_xor(int(m), 2)));
+    m = max(m, swap_lanes<1>(m));
+    m = max(m, swap_lanes<2>(m));
     e = scale_byte(m);
     const float s = scale_value(e);
     uint32_t q = to_fp4<0>(0, v[0], v[1], s);

@@ -274,8 +274,9 @@ __global__ __launch_bounds__(kThreads) void quantize_mxfp4_kernel(const TX* __re
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) m = max(m, abs_bits(v[i]));
-#pragma unroll
-    for (int d = 1; d < kLanes; d *= 2) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    m = max(m, swap_lanes<1>(m));
+    if (kLanes > 2) m = max(m, swap_lanes<2>(m));
+    if (kLanes > 4) m = max(m, swap_lanes<4>(m));
     const uint32_t e = scale_byte(m), lane = at % kLanes;
     const float s = scale_value(e);
     uint8_t* w = W + (int64_t(row) * (units / kLanes) + at / kLanes) * 17;
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void quantize_mxfp4_kernel(const TX* __re
         mine = to_fp4<1>(mine, v[i + 1], 0.f, s);
         mine = to_fp4<2>(mine, v[i + 2], 0.f, s);
         mine = to_fp4<3>(mine, v[i + 3], 0.f, s);
-        const uint32_t other = uint32_t(__shfl_xor(int(mine), kLanes / 2));
+        const uint32_t other = swap_lanes<kLanes / 2>(mine);
         if (lane < kLanes / 2)
             reinterpret_cast<AnyWord*>(w + 1 + lane * PER + i)->w = mine | other << 4;
     }
@@ -332,8 +333,9 @@ __global__ __launch_bounds__(kThreads) void quantize_nvfp4_kernel(const TX* __re
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) m = max(m, abs_bits(v[i]));
-#pragma unroll
-    for (int d = 1; d < kLanes; d *= 2) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    m = max(m, swap_lanes<1>(m));
+    if (kLanes > 2) m = max(m, swap_lanes<2>(m));
+    if (kLanes > 4) m = max(m, swap_lanes<4>(m));
     const uint32_t e = e4m3_scale(m), lane = at % kLanes, sub = at / kLanes;
     const float S = __builtin_amdgcn_cvt_f32_fp8(int(e), 0);
     uint8_t* w = W + (int64_t(row) * (units / (4 * kLanes)) + sub / 4) * 36;
@@ -344,7 +346,7 @@ __global__ __launch_bounds__(kThreads) void quantize_nvfp4_kernel(const TX* __re
     for (int i = 0; i < PER; i += 4) {
         const uint32_t mine = nvfp4_code(v[i], S) | nvfp4_code(v[i + 1], S) << 8 | nvfp4_code(v[i + 2], S) << 16 |
                               nvfp4_code(v[i + 3], S) << 24;
-        const uint32_t other = uint32_t(__shfl_xor(int(mine), kLanes / 2));
+        const uint32_t other = swap_lanes<kLanes / 2>(mine);
         if (lane < kLanes / 2) d[i / 4] = mine | other << 4;
     }
 }
