@@ -38,14 +38,16 @@ struct Layer {
     int blocks;      // of outputs
 };
 
-// v as bf16 parts that add up to it (up to the last part's rounding). What does
-// not fit is left whole in the first part: inf - inf would be NaN.
+// v as bf16 parts that add up to it (up to the last part's rounding). An infinity
+// or NaN is left whole in the first part (inf - inf would be NaN), and a value
+// that would round up to an infinity is cut short.
 template <int P>
 __device__ __forceinline__ void cut(float v, __bf16 part[P]) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        part[i] = __bf16(v);
-        const float got = float(part[i]);
+        float got = float(__bf16(v));
+        if (abs_bits(got) == 0x7f800000u) got = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+        part[i] = __bf16(got);
         v = abs_bits(got) < 0x7f800000u ? v - got : 0.f;
     }
 }
@@ -167,55 +169,72 @@ struct Lists {
     int wave_chosen[4], wave_pairs[4], n_chosen;
 };
 
+// Top-k of one token by a wave, lane l holding experts l, 64 + l, ... below 64 WORDS.
+template <int WORDS>
+__device__ __forceinline__ void choose_token(const Layer& L, int t, int renormalize, Lists& s) {
+    const int lane = threadIdx.x % 64;
+    uint32_t key[WORDS];
+    float v[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        const int e = 64 * i + lane;
+        v[i] = e < L.E ? L.logits[t * L.E + e] : 0.f;
+        key[i] = e < L.E ? key_of(v[i]) : 0u;
+    }
+    uint32_t mine = 0, top = 0;  // lane j: the key of choice j
+    int expert = 0;
+    for (int j = 0; j < L.k; ++j) {
+        // the largest key, at its lowest expert
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < WORDS; ++i) best = max(best, key[i]);
+        best = max_of_wave(best);
+        if (j == 0) top = best;
+        int e = -1;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            const uint64_t m = __ballot(key[i] == best);
+            if (e < 0 && m) {
+                const int at = __ffsll((unsigned long long)m) - 1;
+                e = 64 * i + at;
+                if (lane == at) key[i] = 0;
+            }
+        }
+        if (lane == j) {
+            mine = best;
+            expert = e;
+        }
+    }
+    const float first = of_key(top);
+    const float p = lane < L.k ? expf(of_key(mine) - first) : 0.f;
+    float sum = p;
+    if (!renormalize) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            if (64 * i + lane < L.E) sum += expf(v[i] - first);
+    }
+#pragma unroll
+    for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+    if (lane < L.k) {
+        s.ids[t * L.k + lane] = int16_t(expert);
+        s.share[t * L.k + lane] = p / sum;
+    }
+}
+
 // Top-k of all tokens by a workgroup of at least 4 waves, a wave a token at a
-// time, lane l holding experts l, 64 + l, 128 + l, 192 + l; then the lists by
-// expert. Where a pair stands in its expert's list changes no result, so places
-// are taken by atomics.
+// time; then the lists by expert. Where a pair stands in its expert's list
+// changes no result, so places are taken by atomics.
 __device__ __forceinline__ void choose(const Layer& L, int renormalize, Lists& s) {
     const int waves = blockDim.x / 64, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     for (int e = threadIdx.x; e < RETRO_MOE_MAX_E; e += blockDim.x) s.count[e] = 0;
     for (int t = wave; t < L.T; t += waves) {
-        uint32_t key[4];
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 64 * i + lane;
-            v[i] = e < L.E ? L.logits[t * L.E + e] : 0.f;
-            key[i] = e < L.E ? key_of(v[i]) : 0u;
-        }
-        float top = 0.f, chosen_sum = 0.f, mine = 0.f;
-        for (int j = 0; j < L.k; ++j) {
-            // the largest key, at its lowest expert
-            const uint32_t best = max_of_wave(max(max(key[0], key[1]), max(key[2], key[3])));
-            int e = -1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint64_t m = __ballot(key[i] == best);
-                if (e < 0 && m) {
-                    const int at = __ffsll((unsigned long long)m) - 1;
-                    e = 64 * i + at;
-                    if (lane == at) key[i] = 0;
-                }
-            }
-            const float l = of_key(best);
-            if (j == 0) top = l;
-            const float p = expf(l - top);
-            chosen_sum += p;
-            if (lane == j) {
-                mine = p;
-                s.ids[t * L.k + j] = int16_t(e);
-            }
-        }
-        float sum = chosen_sum;
-        if (!renormalize) {
-            sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (64 * i + lane < L.E) sum += expf(v[i] - top);
-#pragma unroll
-            for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
-        }
-        if (lane < L.k) s.share[t * L.k + lane] = mine / sum;
+        if (L.E <= 64)
+            choose_token<1>(L, t, renormalize, s);
+        else if (L.E <= 128)
+            choose_token<2>(L, t, renormalize, s);
+        else
+            choose_token<4>(L, t, renormalize, s);
     }
     __syncthreads();
     const int pairs = L.T * L.k;

@@ -121,8 +121,9 @@ int launch_skinny(const Args& p, TY* Y) {
 }
 
 // A linear layer quantises x in the product's own kernel where that is few
-// elements a workgroup: 8 a thread at the limit.
-constexpr int64_t kFusedElements = 32768;
+// elements a workgroup. N = 14336, K = 4096: 12.5 us for 4 rows, 17.3 for 8, against
+// 14.7 in two launches.
+constexpr int64_t kFusedElements = 16384;
 bool fuse_linear(int64_t K, int64_t T) {
     return T <= 16 && T * steps_of(K) * kStep <= kFusedElements;
 }
