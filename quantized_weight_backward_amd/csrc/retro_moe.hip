@@ -14,6 +14,14 @@
 // parts that add up to them: one for a BF16 x, two for F16 (11 bits), three for
 // F32 (24 bits); h, which is computed in F32, into two (16 bits, below a BF16
 // or F16 result's own rounding) or three.
+//
+// Measured (BF16; router, choose, gate_up, down): 1 token, 4 of 32 experts, D =
+// 2048, F = 1024: 16.5 us (3, in gate_up, 7.5, 7: launches and the latencies of
+// each, 13 MB of weights are 2.6 us). 16 tokens, 8 of 64 experts, F = 1000: 65 us
+// (4.7, 5.0, 32, 24) for 176 MB, 2.7 TB/s. 32 tokens, 2 of 8 experts, D = 4096, F =
+// 14336: 216 us (4.8, 5.6, 117, 93) for 749 MB, 3.5 TB/s: gate_up reads at 4.3
+// TB/s, near what a plain read of its weights takes (96 us); down is bound by h,
+// of which a wave reads two bytes for each of its weights' (56 us without).
 #include "retro_mx_device.h"
 #include "retro_mx_host.h"
 
@@ -53,7 +61,6 @@ __device__ __forceinline__ void cut(float v, __bf16 part[P]) {
 }
 
 constexpr int kRouterWaves = 4;
-constexpr int kRouterTokens = 4;  // a wave
 
 // 8 elements on a 16-byte boundary.
 template <typename T>
@@ -68,22 +75,22 @@ __device__ __forceinline__ void load8_aligned(const T* x, float v[8]) {
     }
 }
 
-// logits: a wave one expert and a few tokens, 8 elements a lane at a time; whole
+// logits: a wave one expert and TOKENS tokens, 8 elements a lane at a time; whole
 // steps of 512 elements without branches where all rows are `aligned` to 16
 // bytes. Workgroups past the experts cut x.
-template <typename TX, typename TR, int PX>
+template <typename TX, typename TR, int PX, int TOKENS>
 __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, const TX* __restrict__ X, int64_t ldx,
                                                                        const TR* __restrict__ R, int64_t ldr,
                                                                        int expert_groups, bool aligned) {
-    const int lane = threadIdx.x % 64, t0 = blockIdx.y * kRouterTokens, n = min(kRouterTokens, L.T - t0);
+    const int lane = threadIdx.x % 64, t0 = blockIdx.y * TOKENS, n = min(TOKENS, L.T - t0);
     if (int(blockIdx.x) < expert_groups) {
         const int e = blockIdx.x * kRouterWaves + threadIdx.x / 64;
         if (e >= L.E) return;
         const TR* r = R + int64_t(e) * ldr + lane * 8;
-        const TX* x[kRouterTokens];
+        const TX* x[TOKENS];
 #pragma unroll
-        for (int t = 0; t < kRouterTokens; ++t) x[t] = X + int64_t(min(t0 + t, L.T - 1)) * ldx + lane * 8;
-        float s[kRouterTokens] = {};
+        for (int t = 0; t < TOKENS; ++t) x[t] = X + int64_t(min(t0 + t, L.T - 1)) * ldx + lane * 8;
+        float s[TOKENS] = {};
         int64_t d = 0;
         if (aligned)
 #pragma unroll 4
@@ -91,7 +98,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, 
                 float a[8];
                 load8_aligned(r + d, a);
 #pragma unroll
-                for (int t = 0; t < kRouterTokens; ++t) {
+                for (int t = 0; t < TOKENS; ++t) {
                     float v[8];
                     load8_aligned(x[t] + d, v);
 #pragma unroll
@@ -102,7 +109,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, 
             float a[8];
             load8(r + d, L.D - d - lane * 8, a);
 #pragma unroll
-            for (int t = 0; t < kRouterTokens; ++t) {
+            for (int t = 0; t < TOKENS; ++t) {
                 float v[8];
                 load8(x[t] + d, L.D - d - lane * 8, v);
 #pragma unroll
@@ -110,7 +117,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, 
             }
         }
 #pragma unroll
-        for (int t = 0; t < kRouterTokens; ++t) {
+        for (int t = 0; t < TOKENS; ++t) {
 #pragma unroll
             for (int m = 32; m; m >>= 1) s[t] += __shfl_xor(s[t], m);
             if (lane == 0 && t < n) L.logits[(t0 + t) * L.E + e] = s[t];
@@ -675,9 +682,16 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
     const bool aligned = mx::aligned(X, 16) && mx::aligned(R, 16) && ldx * int64_t(sizeof(TX)) % 16 == 0 &&
                          ldr * int64_t(sizeof(TR)) % 16 == 0;
     host::clear_last_error();
-    moe_router_kernel<TX, TR, PX>
-        <<<dim3(uint32_t(groups + cuts), uint32_t(host::cdiv(L.T, kRouterTokens))), dim3(kRouterWaves * 64), 0, st>>>(
+    // a token a wave while that leaves CUs to fill (32 tokens, 8 experts, D = 4096: 4.8
+    // us against 8.4 with four), else four, which read R a fourth as often
+    auto router = [&](auto kernel, int tokens) {
+        kernel<<<dim3(uint32_t(groups + cuts), uint32_t(host::cdiv(L.T, tokens))), dim3(kRouterWaves * 64), 0, st>>>(
             L, X, ldx, R, ldr, groups, aligned);
+    };
+    if (L.E * L.T <= 8 * host::kNumCUs)
+        router(moe_router_kernel<TX, TR, PX, 1>, 1);
+    else
+        router(moe_router_kernel<TX, TR, PX, 4>, 4);
     const bool own_lists = L.T <= kGateWaves;
     if (!own_lists) moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
     // Slabs of 32 features where that leaves enough of them, and workgroups enough

@@ -9,8 +9,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// All of these read X once and write 17 bytes for 32 elements, with a few integer
+// operations and half a conversion instruction an element: memory bounds them.
+
 // Rows: a thread takes 8 elements of a row, four neighbouring threads share a
-// block of 32 and exchange its largest magnitude.
+// block of 32 and exchange its largest magnitude. 4096 x 14336 BF16: 28 us, 5.3
+// TB/s; 16 x 14336: 4 us, a launch.
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const TX* __restrict__ X, int64_t ldx, uint32_t rows,
                                                                  int64_t all_rows, uint32_t K, uint32_t units,
@@ -133,7 +137,8 @@ __device__ __forceinline__ uint32_t across4(const Columns<TX>& c, uint32_t scale
 // lane two neighbouring columns of them: a column's block lies in one lane, a
 // row's in 16 lanes, of which lane j keeps the scales of rows j and 16 + j. 256
 // rows make whole 128-byte steps of the columns' codes, which are gathered in LDS
-// and written as such (and 64-byte pieces of the rows').
+// and written as such (and 64-byte pieces of the rows'). 2048 x 17408 BF16: columns
+// 15.6 us (5.8 TB/s), both 21.7 us (5.0 TB/s; two readings take 34).
 template <typename TX, bool ROWS>
 __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
     const TX* __restrict__ X, int64_t ldx, int64_t rows, uint32_t cols, uint32_t groups, int64_t tile0,
@@ -261,7 +266,7 @@ struct __attribute__((packed)) AnyWord {
 
 // Packed MXFP4 blocks: a lane takes 16 bytes of X, 8 (F32) or 4 lanes a block.
 // A lane of the first half of a block has the low nibbles of its bytes, the lane
-// half a block on their high ones.
+// half a block on their high ones. 17408 x 5120 F32: 74 us, 5.5 TB/s.
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void quantize_mxfp4_kernel(const TX* __restrict__ X, int64_t ldx, uint32_t rows,
                                                                   uint32_t units, uint8_t* __restrict__ W) {
@@ -320,7 +325,8 @@ __device__ __forceinline__ uint32_t nvfp4_code(float v, float S) {
 }
 
 // Packed NVFP4 blocks: a lane takes 16 bytes of X, 4 (F32) or 2 lanes a
-// sub-block of 16, nibbles as above.
+// sub-block of 16, nibbles as above. 17408 x 5120 F32: 92 us, 4.4 TB/s (the exact
+// comparisons keep the vector units busy as long as memory takes).
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void quantize_nvfp4_kernel(const TX* __restrict__ X, int64_t ldx, uint32_t rows,
                                                                   uint32_t units, uint8_t* __restrict__ W) {
@@ -351,7 +357,8 @@ __global__ __launch_bounds__(kThreads) void quantize_nvfp4_kernel(const TX* __re
     }
 }
 
-// Values of a microscaled matrix: a thread 8 elements of a row.
+// Values of a microscaled matrix: a thread 8 elements of a row. 4096 x 14336 to
+// BF16: 26 us, 5.7 TB/s.
 template <typename TY>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales, uint32_t rows,

@@ -1,5 +1,17 @@
 // retro_mx_tile.h - the tiled product of two microscaled matrices: operand
 // tiles copied to LDS while the matrix cores work on the tiles before them.
+//
+// What bounds the 256 x 256 tile (eight waves of 128 x 64, the choice for large
+// products): power. On random operands the scaled products alone run at 5.8 PFLOP/s
+// at a clock of 1.5 GHz, on zeros at 8.2. 8192^3 takes 270 us (4.1 PFLOP/s); with
+// nothing but its products and barriers 203 to 220, its LDS reads alone 121 and
+// its copies alone 152 (the three share the clock, and LDS: of its 128 bytes a
+// cycle the reads take 75%, the copies 25% at the products' full rate). Four waves of
+// 128 x 128 read a third less but hide less: 297 us as scheduled by the compiler,
+// 273 with the reads and copies placed among the products by hand, and 8% slower than
+// eight waves at K = 4096. Stages of 128 elements, three or four deep, copy 64
+// bytes of a row at a time: 201 us for the copies instead of 152.
+// 4096 x 14336 x 4096: 147 us (3.3 PFLOP/s), three and a half rounds of tiles.
 #pragma once
 
 #include <type_traits>
