@@ -75,16 +75,21 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
     return v;
 }
 
-// 8 elements of a row, the first `left` of them (zeros past them): one 16-byte
-// load, or two, where the row allows it.
+// 16 bytes of elements at whatever alignment they have: memory accesses take any.
+template <typename TX>
+struct Wide {
+    static constexpr int kPer = 16 / sizeof(TX);
+    typedef TX vec __attribute__((ext_vector_type(16 / sizeof(TX)), aligned(sizeof(TX))));
+};
+
+// 8 elements of a row, the first `left` of them (zeros past them).
 template <typename TX>
 __device__ __forceinline__ void load8(const TX* x, int64_t left, float v[8]) {
-    typedef TX vec __attribute__((ext_vector_type(16 / sizeof(TX))));
-    constexpr int kPer = 16 / sizeof(TX);
-    if (left >= 8 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0) {
+    constexpr int kPer = Wide<TX>::kPer;
+    if (left >= 8) {
 #pragma unroll
         for (int j = 0; j < 8 / kPer; ++j) {
-            const vec w = reinterpret_cast<const vec*>(x)[j];
+            const auto w = reinterpret_cast<const typename Wide<TX>::vec*>(x)[j];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) v[j * kPer + i] = to_f32(w[i]);
         }

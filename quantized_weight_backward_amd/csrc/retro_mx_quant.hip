@@ -245,18 +245,12 @@ __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
     }
 }
 
-// PER neighbouring elements of a row, a 16-byte load where the row allows it.
+// 16 bytes of neighbouring elements of a row.
 template <typename TX, int PER>
 __device__ __forceinline__ void load_few(const TX* x, float v[PER]) {
-    typedef TX vec __attribute__((ext_vector_type(PER)));
-    if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0) {
-        const vec w = *reinterpret_cast<const vec*>(x);
+    const auto w = *reinterpret_cast<const typename Wide<TX>::vec*>(x);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = to_f32(w[i]);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = to_f32(x[i]);
+    for (int i = 0; i < PER; ++i) v[i] = to_f32(w[i]);
 }
 
 // Words at any byte address.
@@ -377,15 +371,14 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
     v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
     v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
     TY* y = Y + int64_t(row) * ldy + k;
-    constexpr int kPer = 16 / sizeof(TY);
-    typedef TY vec __attribute__((ext_vector_type(kPer)));
-    if (k + 8 <= K && (reinterpret_cast<uintptr_t>(y) & 15u) == 0) {
+    constexpr int kPer = Wide<TY>::kPer;
+    if (k + 8 <= K) {
 #pragma unroll
         for (int j = 0; j < 8 / kPer; ++j) {
-            vec o;
+            typename Wide<TY>::vec o;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) o[i] = from_f32<TY>(v[(j * kPer + i) / 2][i % 2] * s);
-            reinterpret_cast<vec*>(y)[j] = o;
+            reinterpret_cast<typename Wide<TY>::vec*>(y)[j] = o;
         }
         return;
     }

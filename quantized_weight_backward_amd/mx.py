@@ -15,6 +15,8 @@ the operands' device); outputs and scratch it allocates belong to that stream.
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import (BF16, E_SHAPE, E_TYPE, F16, F32, MXFP4, TYPES, _check, _current_device, _device_tensor, _raw_stream, lib,
@@ -83,6 +85,17 @@ def _given(out, rows, cols, dtype, like):
         raise ValueError(f"out must be {dtype} of shape {(rows, cols)}")
     _one_device(like, out)
     return ld
+
+
+# sizes of shapes that come again and again
+@functools.lru_cache(maxsize=1024)
+def _linear_workspace(xtype: int, K: int, N: int, T: int) -> int:
+    return lib.retro_mx_linear_workspace_size(xtype, K, N, T)
+
+
+@functools.lru_cache(maxsize=1024)
+def _moe_workspace(xtype: int, T: int, D: int, F: int, E: int, top_k: int) -> int:
+    return lib.retro_moe_workspace_size(xtype, T, D, F, E, top_k)
 
 
 class MXMatrix:
@@ -289,7 +302,7 @@ def mx_linear(x, w: MXMatrix, out=None, stream=None):
         out, ld = torch.empty((T, N), dtype=x.dtype, device=x.device), N
     else:
         ld = _given(out, T, N, x.dtype, x)
-    need = lib.retro_mx_linear_workspace_size(xtype, K, N, T)
+    need = _linear_workspace(xtype, K, N, T)
     ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
     _check(lib.retro_mx_linear(xtype, x.data_ptr(), ldx, w._code_ptr, w._scale_ptr, out.data_ptr(), ld, K, N, T,
                                None if ws is None else ws.data_ptr(), need, _handle()))
@@ -343,7 +356,7 @@ def mx_moe(x, router, gate_up: MXMatrix, down: MXMatrix, top_k: int, renormalize
         out, ld = torch.empty((T, D), dtype=x.dtype, device=x.device), D
     else:
         ld = _given(out, T, D, x.dtype, x)
-    need = lib.retro_moe_workspace_size(xtype, T, D, F, E, top_k)
+    need = _moe_workspace(xtype, T, D, F, E, top_k)
     if need < 0:
         _check(need)
     ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
