@@ -6,22 +6,22 @@
 // Launches:
 //   router   logits, and x in bf16 parts with zeros up to whole 256-element steps
 //   choose   top-k of each token, the list of chosen experts and their pairs
-//   gate_up  a workgroup: 16 features of one chosen expert, all its tokens
+//   gate_up  a workgroup: some features of one chosen expert, 16 of its tokens
 //   down     a workgroup: some outputs of all tokens, over all chosen experts or
-//            a part of them; the last of those outputs' workgroups adds the parts
+//            a part of them
+//   join     adds the parts
 // Weights are decoded exactly to bf16 (E2M1 times a power of two) and meet x
 // and h on v_mfma_f32_16x16x32_bf16 with F32 sums. x and h are cut into bf16
 // parts that add up to them: one for a BF16 x, two for F16 (11 bits), three for
 // F32 (24 bits); h, which is computed in F32, into two (16 bits, below a BF16
 // or F16 result's own rounding) or three.
 //
-// Measured (BF16; router, choose, gate_up, down): 1 token, 4 of 32 experts, D =
-// 2048, F = 1024: 16.5 us (3, in gate_up, 7.5, 7: launches and the latencies of
-// each, 13 MB of weights are 2.6 us). 16 tokens, 8 of 64 experts, F = 1000: 65 us
-// (4.7, 5.0, 32, 24) for 176 MB, 2.7 TB/s. 32 tokens, 2 of 8 experts, D = 4096, F =
-// 14336: 216 us (4.8, 5.6, 117, 93) for 749 MB, 3.5 TB/s: gate_up reads at 4.3
-// TB/s, near what a plain read of its weights takes (96 us); down is bound by h,
-// of which a wave reads two bytes for each of its weights' (56 us without).
+// Measured (BF16; router, choose, gate_up, down, join): 1 token, 4 of 32 experts, D
+// = 2048, F = 1024: 16.5 us (3, in gate_up, 7.5, 7, none: launches and the
+// latencies of each, 13 MB of weights are 2.6 us). 16 tokens, 8 of 64 experts, F =
+// 1000: 63 us (4.7, 5.1, 30, 20, 4.7) for 185 MB, 2.9 TB/s. 32 tokens, 2 of 8
+// experts, D = 4096, F = 14336: 185 us (5.2, 6.2, 112, 64, 5.1) for 749 MB, 4.05
+// TB/s; gate_up reads at 4.5 TB/s and down at 3.9, where a plain read reaches 5.2.
 #include "retro_mx_device.h"
 #include "retro_mx_host.h"
 
@@ -37,13 +37,11 @@ struct Layer {
     const uint8_t *guc, *gus, *dc, *ds;
     float* logits;   // T x E
     float* share;    // T x k
-    int* lists;      // number of chosen experts, then for each: expert, first place, pairs
+    int* lists;      // number of tiles (up to 16 pairs of an expert), then of each: expert, first place, pairs
     int16_t* order;  // the pairs, by expert
     __bf16* xp;      // parts x T x Dp
     __bf16* hp;      // parts x (T * k) x Fp: share times h
     float* sums;     // splits x T x D
-    unsigned* done;  // workgroups that have written their sums, for each block of outputs
-    int blocks;      // of outputs
 };
 
 // v as bf16 parts that add up to it (up to the last part's rounding). An infinity
@@ -124,11 +122,6 @@ __global__ __launch_bounds__(kRouterWaves * 64) void moe_router_kernel(Layer L, 
         }
         return;
     }
-    // the counters of the down kernel
-    if (blockIdx.y == 0)
-        for (int i = (blockIdx.x - expert_groups) * blockDim.x + threadIdx.x; i < L.blocks;
-             i += (gridDim.x - expert_groups) * blockDim.x)
-            L.done[i] = 0;
     const int64_t Dp = L.steps_d * kStep;
     const int64_t d = (int64_t(blockIdx.x - expert_groups) * (kRouterWaves * 64) + threadIdx.x) * 8;
     if (d >= Dp) return;
@@ -166,14 +159,22 @@ __device__ __forceinline__ uint32_t max_of_wave(uint32_t v) {
     return max(max(a, b), max(c, d));
 }
 
+// Tiles of T tokens' pairs: each chosen expert's in sixteens.
+constexpr int kMaxTiles = RETRO_MOE_MAX_E + RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K / 16;
+__host__ __device__ inline int most_tiles(int64_t T, int64_t E, int64_t k) {
+    const int64_t pairs = T * k, chosen = pairs < E ? pairs : E;
+    return int(chosen + pairs / 16);
+}
+
 // The chosen experts and their pairs, in LDS.
 struct Lists {
     int16_t ids[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];    // expert of each pair
     float share[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];    // and its share
     int16_t order[RETRO_MOE_MAX_T * RETRO_MOE_MAX_TOP_K];  // the pairs by expert
-    int count[RETRO_MOE_MAX_E], place[RETRO_MOE_MAX_E];
-    int entry[3 * RETRO_MOE_MAX_E];  // of each chosen expert: expert, first place, pairs
-    int wave_chosen[4], wave_pairs[4], n_chosen;
+    unsigned long long tokens[RETRO_MOE_MAX_E];  // of each expert, a bit each
+    int place[RETRO_MOE_MAX_E];
+    int entry[3 * kMaxTiles];  // of each tile: expert, first place, pairs
+    int wave_tiles[4], wave_pairs[4], n_tiles;
 };
 
 // Top-k of one token by a wave, lane l holding experts l, 64 + l, ... below 64 WORDS.
@@ -230,11 +231,11 @@ __device__ __forceinline__ void choose_token(const Layer& L, int t, int renormal
 }
 
 // Top-k of all tokens by a workgroup of at least 4 waves, a wave a token at a
-// time; then the lists by expert. Where a pair stands in its expert's list
-// changes no result, so places are taken by atomics.
+// time; then the lists by expert, an expert's pairs in the order of their tokens
+// (which tile a pair is in decides the order of its sums).
 __device__ __forceinline__ void choose(const Layer& L, int renormalize, Lists& s) {
     const int waves = blockDim.x / 64, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    for (int e = threadIdx.x; e < RETRO_MOE_MAX_E; e += blockDim.x) s.count[e] = 0;
+    for (int e = threadIdx.x; e < RETRO_MOE_MAX_E; e += blockDim.x) s.tokens[e] = 0;
     for (int t = wave; t < L.T; t += waves) {
         if (L.E <= 64)
             choose_token<1>(L, t, renormalize, s);
@@ -252,54 +253,59 @@ __device__ __forceinline__ void choose(const Layer& L, int renormalize, Lists& s
             s.entry[3 * threadIdx.x + 2] = 1;
             s.order[threadIdx.x] = int16_t(threadIdx.x);
         }
-        if (threadIdx.x == 0) s.n_chosen = pairs;
+        if (threadIdx.x == 0) s.n_tiles = pairs;
         __syncthreads();
         return;
     }
-    for (int p = threadIdx.x; p < pairs; p += blockDim.x) atomicAdd(&s.count[s.ids[p]], 1);
+    for (int p = threadIdx.x; p < pairs; p += blockDim.x) atomicOr(&s.tokens[s.ids[p]], 1ull << (p / L.k));
     __syncthreads();
-    // ranks of the chosen experts, and where their pairs begin
+    // where each expert's tiles and pairs begin
     const int e = threadIdx.x;
-    int n = 0, first = 0, rank = 0;
+    int n = 0, first = 0, tile = 0;
     if (e < RETRO_MOE_MAX_E) {
-        n = s.count[e];
-        const uint64_t m = __ballot(n > 0);
-        rank = __popcll(m & ((1ull << lane) - 1));
-        int run = n;
+        n = __popcll(s.tokens[e]);
+        int run_pairs = n, run_tiles = (n + 15) / 16;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(run, d);
-            if (lane >= d) run += o;
+            const int p = __shfl_up(run_pairs, d), q = __shfl_up(run_tiles, d);
+            if (lane >= d) {
+                run_pairs += p;
+                run_tiles += q;
+            }
         }
-        first = run - n;
+        first = run_pairs - n;
+        tile = run_tiles - (n + 15) / 16;
         if (lane == 63) {
-            s.wave_chosen[wave] = __popcll(m);
-            s.wave_pairs[wave] = run;
+            s.wave_pairs[wave] = run_pairs;
+            s.wave_tiles[wave] = run_tiles;
         }
     }
     __syncthreads();
     if (e < RETRO_MOE_MAX_E) {
         for (int w = 0; w < wave; ++w) {
-            rank += s.wave_chosen[w];
             first += s.wave_pairs[w];
+            tile += s.wave_tiles[w];
         }
         s.place[e] = first;
-        if (n > 0) {
-            s.entry[3 * rank] = e;
-            s.entry[3 * rank + 1] = first;
-            s.entry[3 * rank + 2] = n;
+        for (int i = 0; i < n; i += 16, ++tile) {
+            s.entry[3 * tile] = e;
+            s.entry[3 * tile + 1] = first + i;
+            s.entry[3 * tile + 2] = min(16, n - i);
         }
-        if (e == RETRO_MOE_MAX_E - 1) s.n_chosen = rank + (n > 0);
+        if (e == RETRO_MOE_MAX_E - 1) s.n_tiles = tile;
     }
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += blockDim.x) s.order[atomicAdd(&s.place[s.ids[p]], 1)] = int16_t(p);
+    for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
+        const int id = s.ids[p];
+        s.order[s.place[id] + __popcll(s.tokens[id] & ((1ull << (p / L.k)) - 1))] = int16_t(p);
+    }
     __syncthreads();
 }
 
 // The lists for the launches that follow.
 __device__ __forceinline__ void write_lists(const Layer& L, const Lists& s) {
-    if (threadIdx.x == 0) L.lists[0] = s.n_chosen;
-    for (int i = threadIdx.x; i < 3 * s.n_chosen; i += blockDim.x) L.lists[1 + i] = s.entry[i];
+    if (threadIdx.x == 0) L.lists[0] = s.n_tiles;
+    for (int i = threadIdx.x; i < 3 * s.n_tiles; i += blockDim.x) L.lists[1 + i] = s.entry[i];
     for (int p = threadIdx.x; p < L.T * L.k; p += blockDim.x) {
         L.order[p] = s.order[p];
         L.share[p] = s.share[p];
@@ -377,19 +383,17 @@ __device__ __forceinline__ void in_pairs(int first, int end, int by, Load&& load
 
 constexpr int kGateWaves = 4;
 
-// Features of one chosen expert in slabs of 16 SL: their rows of gate and of up
-// times x of the expert's tokens, 16 tokens at a time. `ks` (1, 2 or 4) waves
-// share a slab, each a part of D; their sums are added in LDS in their order. A
-// wave loads a step while it works on the one before. x comes from the caches,
-// which costs a wave as much as weights do: two slabs of 16 halve that.
+// Features of one chosen expert in slabs of 16: their rows of gate and of up times
+// x of a tile of its tokens. `ks` (1, 2 or 4) waves share a slab, each a part of D;
+// their sums are added in LDS in their order. A wave loads a step while it works
+// on the one before.
 //
 // For a token or a few (OWN_LISTS) every workgroup chooses the experts itself,
 // which takes it about a microsecond where a launch of its own takes several.
-template <int PX, int PH, int SL, bool OWN_LISTS>
-__global__ __launch_bounds__(kGateWaves * 64, PX == 1 && SL == 1 ? 3 : 2) void moe_gate_up_kernel(Layer L, int ks,
-                                                                                                  int renormalize) {
-    constexpr int kRows = 16 * SL;
-    __shared__ float part[kGateWaves][2][kRows][17];
+template <int PX, int PH, bool OWN_LISTS>
+__global__ __launch_bounds__(kGateWaves * 64, PX == 1 ? 3 : 2) void moe_gate_up_kernel(Layer L, int ks,
+                                                                                       int renormalize) {
+    __shared__ float part[kGateWaves][2][16][17];
     const int* entry = L.lists + 1 + blockIdx.y * 3;
     const int16_t* order = L.order;
     const float* share = L.share;
@@ -397,7 +401,7 @@ __global__ __launch_bounds__(kGateWaves * 64, PX == 1 && SL == 1 ? 3 : 2) void m
         __shared__ Lists own;
         choose(L, renormalize, own);
         if (blockIdx.x == 0 && blockIdx.y == 0) write_lists(L, own);
-        if (int(blockIdx.y) >= own.n_chosen) return;
+        if (int(blockIdx.y) >= own.n_tiles) return;
         entry = own.entry + blockIdx.y * 3;
         order = own.order;
         share = own.share;
@@ -408,88 +412,284 @@ __global__ __launch_bounds__(kGateWaves * 64, PX == 1 && SL == 1 ? 3 : 2) void m
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int r = lane & 15, g = lane >> 4, slabs = kGateWaves / ks;
     const int64_t rows = int64_t(L.E) * 2 * L.F, Dp = L.steps_d * kStep, Fp = L.steps_f * kStep;
-    const int64_t g0 = int64_t(blockIdx.x) * slabs * kRows, f0 = g0 + wave / ks * kRows;
-    int64_t row[2 * SL];  // gate, then up
-#pragma unroll
-    for (int m = 0; m < 2 * SL; ++m)
-        row[m] = int64_t(e) * 2 * L.F + (m / SL) * L.F + min(f0 + 16 * (m % SL) + r, L.F - 1);
+    const int64_t g0 = int64_t(blockIdx.x) * slabs * 16, f0 = g0 + wave / ks * 16;
+    const int64_t row = int64_t(e) * 2 * L.F + min(f0 + r, L.F - 1);  // of gate; F further on of up
     // past F only the zeros that pad h are written
     const int steps = f0 < L.F ? int(L.steps_d) : 0;
-    for (int p0 = 0; p0 < n; p0 += 16) {
-        // lanes of columns past the pairs load nothing; their sums are dropped
-        const bool used = p0 + r < n;
-        const int pair = order[first + (used ? p0 + r : p0)];
-        const __bf16* x = L.xp + int64_t(pair / L.k) * Dp + g * 32;
-        f32x4 acc[2 * SL] = {};
-        struct Loaded {
-            Step w[2 * SL];
-            bf16x8 v[2][PX][4];
-        };
-        auto load = [&](Loaded& l, int c) {
+    // lanes of columns past the pairs load nothing; their sums are dropped
+    const bool used = r < n;
+    const int pair = order[first + (used ? r : 0)];
+    const __bf16* x = L.xp + int64_t(pair / L.k) * Dp + g * 32;
+    f32x4 acc[2] = {};
+    struct Loaded {
+        Step w[2];
+        bf16x8 v[2][PX][4];
+    };
+    auto load = [&](Loaded& l, int c) {
 #pragma unroll
-            for (int m = 0; m < 2 * SL; ++m) load_step(l.w[m], L.guc, L.gus, rows, row[m], L.steps_d, c, g);
-            if (used)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int p = 0; p < PX; ++p)
-                        load_block(l.v[b][p], x + int64_t(p) * L.T * Dp + c * kStep + b * 128);
-        };
-        auto use = [&](const Loaded& l) {
+        for (int m = 0; m < 2; ++m) load_step(l.w[m], L.guc, L.gus, rows, row + m * L.F, L.steps_d, c, g);
+        if (used)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int m = 0; m < 2 * SL; ++m) {
-                    bf16x8 o[4];
-                    decode(l.w[m].code[b], l.w[m].scale[b] >> (8 * g), o);
+                for (int p = 0; p < PX; ++p)
+                    load_block(l.v[b][p], x + int64_t(p) * L.T * Dp + c * kStep + b * 128);
+    };
+    auto use = [&](const Loaded& l) {
 #pragma unroll
-                    for (int p = PX - 1; p >= 0; --p)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[i], l.v[b][p][i], acc[m], 0, 0, 0);
-                }
-        };
-        in_pairs<Loaded>(wave % ks, steps, ks, load, use);
-        __syncthreads();  // the last round's sums are read
+            for (int m = 0; m < 2; ++m) {
+                bf16x8 o[4];
+                decode(l.w[m].code[b], l.w[m].scale[b] >> (8 * g), o);
 #pragma unroll
-        for (int m = 0; m < 2 * SL; ++m)
+                for (int p = PX - 1; p >= 0; --p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[wave][m / SL][16 * (m % SL) + 4 * g + i][r] = acc[m][i];
-        __syncthreads();
-        for (int o = threadIdx.x; o < slabs * kRows * 16; o += kGateWaves * 64) {
-            const int ff = o % (slabs * kRows), c = o / (slabs * kRows);
-            if (p0 + c >= n || g0 + ff >= Fp) continue;
-            float gate = 0.f, up = 0.f;
-            for (int w = 0; w < ks; ++w) {
-                gate += part[ff / kRows * ks + w][0][ff % kRows][c];
-                up += part[ff / kRows * ks + w][1][ff % kRows][c];
+                    for (int i = 0; i < 4; ++i)
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[i], l.v[b][p][i], acc[m], 0, 0, 0);
             }
-            const int pr = order[first + p0 + c];
-            const float h = g0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * share[pr] : 0.f;
-            __bf16 cutp[PH];
-            cut<PH>(h, cutp);
+    };
+    in_pairs<Loaded>(wave % ks, steps, ks, load, use);
 #pragma unroll
-            for (int p = 0; p < PH; ++p) L.hp[(int64_t(p) * L.T * L.k + pr) * Fp + g0 + ff] = cutp[p];
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[wave][m][4 * g + i][r] = acc[m][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < slabs * 256; o += kGateWaves * 64) {
+        const int ff = o % (slabs * 16), c = o / (slabs * 16);
+        if (c >= n || g0 + ff >= Fp) continue;
+        float gate = 0.f, up = 0.f;
+        for (int w = 0; w < ks; ++w) {
+            gate += part[ff / 16 * ks + w][0][ff % 16][c];
+            up += part[ff / 16 * ks + w][1][ff % 16][c];
         }
+        const int pr = order[first + c];
+        const float h = g0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * share[pr] : 0.f;
+        __bf16 cutp[PH];
+        cut<PH>(h, cutp);
+#pragma unroll
+        for (int p = 0; p < PH; ++p) L.hp[(int64_t(p) * L.T * L.k + pr) * Fp + g0 + ff] = cutp[p];
     }
 }
 
-// 16 RF outputs of all tokens. The chosen experts' rows, one expert after
-// another, are one list of 128-element pieces, of which every wave of the
-// gridDim.y workgroups of these outputs takes an equal run. Within an expert the
-// columns are its pairs, 16 CT at a time, whose h holds the share; at the end of
-// an expert the wave adds its sums to those of the pairs' tokens in LDS, and at
-// the end of the kernel the waves' are added in their order. One workgroup writes
-// Y; of several, each writes its sums at device scope (they run on different
-// XCDs) and the one that is done last adds them in their order. None waits for
-// another.
-template <typename TY, int PH, int CT, int RF, int WAVES>
+// 16 (or 4) bytes a lane from offset at + `more` (uniform) of the `bytes` at p into
+// LDS, lane after lane.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, uint32_t(min(bytes, int64_t(0xffffffffu))),
+                                             0x00020000);
+}
+__device__ __forceinline__ void copy16(uint8_t* lds, const void* p, int64_t bytes, uint32_t at, uint32_t more) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(p, bytes), lds, 16, at, more, 0, 0);
+}
+__device__ __forceinline__ void copy4(uint8_t* lds, const void* p, int64_t bytes, uint32_t at, uint32_t more) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(p, bytes), lds, 4, at, more, 0, 0);
+}
+
+// All but a wave's last N copies into LDS have landed, its reads are done, and
+// so for every wave.
+template <int N>
+__device__ __forceinline__ void stage_ready() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70);  // vmcnt(N) lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// For larger layers a workgroup of eight waves multiplies 256 rows of weights with
+// a tile through a ring of stages in LDS, each a piece of 128 elements: rows,
+// their scales, and the tile's x or h. Read straight into the operands' lanes each
+// 16 bytes are a cache access of their own (a lane holds another row than its
+// neighbour); those accesses, two for x or h and one for the rows, were what
+// bound it (the address units were busy 86% to 90% of the time). Copies of 64 or
+// 256 contiguous bytes take one for each 64, and x or h is copied once for all
+// waves. Stage rows 0 .. 127 and 128 .. 255 are two ranges of rows; a wave
+// multiplies 16 of each. Rows of 64 bytes lie permuted by XOR with (row / 4) % 4,
+// x's or h's of 256 bytes by XOR with the row, so that neighbouring lanes' reads
+// meet all banks.
+constexpr int kRingWaves = 8, kRingRows = 256;
+
+template <int P>
+struct Ring {
+    static constexpr int kIn = kRingRows * 64, kScales = kIn + P * 4096, kBytes = kScales + kRingRows * 4;
+    static constexpr int kCopiesOfIn = (P * 4 + kRingWaves - 1) / kRingWaves;
+    static constexpr int kCopies = 2 + kCopiesOfIn + 1;  // of a wave, a piece
+
+    const uint8_t *codes, *scales;
+    const __bf16* in;  // P x `in_rows` x `in_pitch` elements
+    int64_t rows, second;  // of the matrix; between the two ranges
+    uint32_t pitch, part;  // bytes of a row of codes, of a part of `in`
+    int wave, lane;
+    int last0, last1;  // the ranges' last rows: past them they are copied again
+    uint32_t code_at[2], scale_at, in_at[kCopiesOfIn];
+
+    // n0 and n1: rows that there are in the two ranges (one at least in the first)
+    __device__ __forceinline__ Ring(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t second, int n0,
+                                    int n1, int64_t steps, const __bf16* in, int64_t in_rows)
+        : codes(codes), scales(scales), in(in), rows(rows), second(n1 > 0 ? second : 0),
+          pitch(uint32_t(steps) * kStepBytes), part(uint32_t(in_rows * steps * (kStep * 2))) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        lane = threadIdx.x % 64;
+        last0 = min(n0, 128) - 1;
+        last1 = n1 > 0 ? min(n1, 128) - 1 : last0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            code_at[j] = min(wave * 16 + lane / 4, j ? last1 : last0) * pitch + ((lane % 4) ^ (lane / 16)) * 16;
+        scale_at = min(wave % 2 * 64 + lane, scale_range() ? last1 : last0) * kStepScales;
+    }
+
+    // A wave copies a quarter of the scales: the range it is of.
+    __device__ __forceinline__ int scale_range() const { return wave / 2 % 2; }
+
+    // Row `at(i)` of `in` is the tile's row i, i < 16.
+    template <typename At>
+    __device__ __forceinline__ void set_tile(At&& at) {
+#pragma unroll
+        for (int j = 0; j < kCopiesOfIn; ++j) {
+            const int row = (j * kRingWaves + wave) % (P * 4) % 4 * 4 + lane / 16;
+            in_at[j] = uint32_t(at(row)) * (pitch * 4) + ((lane % 16) ^ row) * 16;
+        }
+    }
+
+    // Piece c of rows row0 and on.
+    __device__ __forceinline__ void copy(uint8_t* stage, int64_t row0, int c) const {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            copy16(stage + (j * 128 + wave * 16) * 64, codes + (row0 + j * second) * pitch,
+                   int64_t((j ? last1 : last0) + 1) * pitch, code_at[j], c * 64);
+#pragma unroll
+        for (int j = 0; j < kCopiesOfIn; ++j) {
+            const int at = (j * kRingWaves + wave) % (P * 4);
+            copy16(stage + kIn + at * 1024, in, int64_t(P) * part, in_at[j], at / 4 * part + c * 256);
+        }
+        copy4(stage + kScales + wave % 4 * 256,
+              scales + (c / 2 * rows + row0 + (scale_range() ? second : 0)) * kStepScales,
+              int64_t((scale_range() ? last1 : last0) + 1) * kStepScales, scale_at, c % 2 * 4);
+    }
+
+    // acc[m] += the wave's 16 rows of range m times the tile.
+    __device__ __forceinline__ void multiply(const uint8_t* stage, f32x4 acc[2]) const {
+        const int r = lane & 15, g = lane >> 4;
+        bf16x8 v[P][4];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[p][i] =
+                    *reinterpret_cast<const bf16x8*>(stage + kIn + p * 4096 + r * 256 + (((g * 4 + i) ^ r) * 16));
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int row = m * 128 + wave * 16 + r;
+            const u32x4 q = *reinterpret_cast<const u32x4*>(stage + row * 64 + ((g ^ ((r >> 2) & 3)) * 16));
+            bf16x8 o[4];
+            decode(q, stage[kScales + row * 4 + g], o);
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[i], v[p][i], acc[m], 0, 0, 0);
+        }
+    }
+};
+
+// `pieces` pieces through the stages l: copy(stage) takes the next piece, the last
+// again past the end, and use(stage) the next that was copied. Whole rounds
+// without a way out in between: so the compiler sees that a stage was refilled
+// S - 1 steps ago, and waits for no later copy.
+template <int S, int COPIES, typename Copy, typename Use>
+__device__ __forceinline__ void through_ring(uint8_t* l0, uint8_t* l1, uint8_t* l2, uint8_t* l3, int pieces,
+                                             Copy&& copy, Use&& use) {
+    auto step = [&](const uint8_t* cur, uint8_t* refill) {
+        stage_ready<(S - 2) * COPIES>();
+        copy(refill);
+        use(cur);
+    };
+    copy(l0);
+    copy(l1);
+    if constexpr (S > 3) copy(l2);
+    for (; pieces >= S; pieces -= S) {
+        step(l0, S > 3 ? l3 : l2);
+        step(l1, l0);
+        step(l2, l1);
+        if constexpr (S > 3) step(l3, l2);
+    }
+    if (pieces > 0) step(l0, S > 3 ? l3 : l2);
+    if (pieces > 1) step(l1, l0);
+    if (S > 3 && pieces > 2) step(l2, l1);
+    stage_ready<0>();
+}
+
+// 128 features of one tile through the ring: their rows of gate are its first
+// range, of up its second.
+template <int PX, int PH, bool OWN_LISTS>
+__global__ __launch_bounds__(kRingWaves * 64, PX < 3 ? 4 : 2) void moe_gate_up_ring_kernel(Layer L, int renormalize) {
+    using R = Ring<PX>;
+    __shared__ __align__(1024) uint8_t l0[R::kBytes], l1[R::kBytes], l2[R::kBytes];
+    const int* entry = L.lists + 1 + blockIdx.y * 3;
+    const int16_t* order = L.order;
+    const float* share = L.share;
+    if constexpr (OWN_LISTS) {
+        __shared__ Lists own;
+        choose(L, renormalize, own);
+        if (blockIdx.x == 0 && blockIdx.y == 0) write_lists(L, own);
+        if (int(blockIdx.y) >= own.n_tiles) return;
+        entry = own.entry + blockIdx.y * 3;
+        order = own.order;
+        share = own.share;
+    } else {
+        if (int(blockIdx.y) >= L.lists[0]) return;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(entry[0]), first = __builtin_amdgcn_readfirstlane(entry[1]);
+    const int n = __builtin_amdgcn_readfirstlane(entry[2]);
+    const int64_t f0 = int64_t(blockIdx.x) * 128, Fp = L.steps_f * kStep;
+    f32x4 acc[2] = {};
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), r = threadIdx.x & 15, g = threadIdx.x / 16 % 4;
+    if (f0 < L.F) {  // past F only the zeros that pad h are written
+        const int there = int(min(int64_t(128), L.F - f0));
+        R ring(L.guc, L.gus, int64_t(L.E) * 2 * L.F, L.F, there, there, L.steps_d, L.xp, L.T);
+        ring.set_tile([&](int i) { return order[first + min(i, n - 1)] / L.k; });
+        const int64_t row0 = int64_t(e) * 2 * L.F + f0;
+        const int pieces = int(L.steps_d) * 2;
+        int next = 0;
+        through_ring<3, R::kCopies>(
+            l0, l1, l2, nullptr, pieces,
+            [&](uint8_t* stage) {
+                ring.copy(stage, row0, next);
+                next = min(next + 1, pieces - 1);
+            },
+            [&](const uint8_t* stage) { ring.multiply(stage, acc); });
+    }
+    if (r >= n) return;
+    const int pair = order[first + r];
+    const float by = share[pair];
+    const int64_t f = f0 + wave * 16 + 4 * g;
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    bf16x4 out[PH];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float gate = acc[0][i], h = f + i < L.F ? gate / (1.f + expf(-gate)) * acc[1][i] * by : 0.f;
+        __bf16 part[PH];
+        cut<PH>(h, part);
+#pragma unroll
+        for (int p = 0; p < PH; ++p) out[p][i] = part[p];
+    }
+#pragma unroll
+    for (int p = 0; p < PH; ++p)
+        *reinterpret_cast<bf16x4*>(L.hp + (int64_t(p) * L.T * L.k + pair) * Fp + f) = out[p];
+}
+
+// 16 RF outputs of all tokens. The tiles' rows, one tile after another, are one
+// list of 128-element pieces, of which every wave of the gridDim.y workgroups of
+// these outputs takes an equal run. Within a tile the columns are its pairs, whose
+// h holds the share; at its end the wave adds its sums to those of the pairs'
+// tokens in LDS, and at the end of the kernel the waves' are added in their order.
+// One workgroup writes Y; the sums of several are added by the join.
+template <typename TY, int PH, int RF, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kernel(Layer L, TY* __restrict__ Y,
                                                                                    int64_t ldy) {
     constexpr int kWide = 16 * RF + 4;
     extern __shared__ __align__(16) float sums[];  // wave x token x kWide, then the lists
     int* entry = reinterpret_cast<int*>(sums + WAVES * L.T * kWide);
-    const int n_chosen = L.lists[0], most = min(L.E, L.T * L.k);
+    const int n_tiles = L.lists[0], most = most_tiles(L.T, L.E, L.k);
     int16_t* order = reinterpret_cast<int16_t*>(entry + 3 * most);
     // all that may be there: what lies past the chosen ones is not used
     for (int i = threadIdx.x; i < 3 * most; i += WAVES * 64) entry[i] = L.lists[1 + i];
@@ -502,7 +702,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kern
     const int64_t rows = int64_t(L.E) * L.D, Fp = L.steps_f * kStep, part_of_h = int64_t(L.T) * L.k * Fp;
     const int64_t d0 = int64_t(blockIdx.x) * (16 * RF);
     const int pieces = int(L.steps_f) * 2;
-    const int64_t all = int64_t(n_chosen) * pieces;
+    const int64_t all = int64_t(n_tiles) * pieces;
     const int share = blockIdx.y * WAVES + wave, shares = gridDim.y * WAVES;
     const int64_t lo = all * share / shares, hi = all * (share + 1) / shares;
     for (int64_t at = lo; at < hi;) {
@@ -519,57 +719,43 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kern
             code[m] = L.dc + row * L.steps_f * kStepBytes + g * 16;
             scale[m] = L.ds + row * kStepScales;
         }
-        for (int p0 = 0; p0 < n; p0 += 16 * CT) {
-            int pair[CT];
-            const __bf16* h[CT];
+        const int pair = order[first + min(r, n - 1)];
+        const __bf16* h = L.hp + pair * Fp + g * 32;
+        f32x4 acc[RF] = {};
+        struct Loaded {
+            u32x4 code[RF];
+            uint32_t scale[RF];
+            bf16x8 v[PH][4];
+        };
+        auto load = [&](Loaded& l, int c) {
 #pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                pair[t] = order[first + min(p0 + 16 * t + r, n - 1)];
-                h[t] = L.hp + pair[t] * Fp + g * 32;
+            for (int m = 0; m < RF; ++m) {
+                l.code[m] = *reinterpret_cast<const u32x4*>(code[m] + c * 64);
+                l.scale[m] = *reinterpret_cast<const uint32_t*>(scale[m] + c / 2 * rows * kStepScales + c % 2 * 4);
             }
-            f32x4 acc[RF][CT] = {};
-            struct Loaded {
-                u32x4 code[RF];
-                uint32_t scale[RF];
-                bf16x8 v[CT][PH][4];
-            };
-            auto load = [&](Loaded& l, int c) {
 #pragma unroll
-                for (int m = 0; m < RF; ++m) {
-                    l.code[m] = *reinterpret_cast<const u32x4*>(code[m] + c * 64);
-                    l.scale[m] = *reinterpret_cast<const uint32_t*>(scale[m] + c / 2 * rows * kStepScales + c % 2 * 4);
-                }
+            for (int p = 0; p < PH; ++p) load_block(l.v[p], h + p * part_of_h + c * 128);
+        };
+        auto use = [&](const Loaded& l) {
 #pragma unroll
-                for (int t = 0; t < CT; ++t)
+            for (int m = 0; m < RF; ++m) {
+                bf16x8 o[4];
+                decode(l.code[m], l.scale[m] >> (8 * g), o);
 #pragma unroll
-                    for (int p = 0; p < PH; ++p) load_block(l.v[t][p], h[t] + p * part_of_h + c * 128);
-            };
-            auto use = [&](const Loaded& l) {
+                for (int p = PH - 1; p >= 0; --p)
 #pragma unroll
-                for (int m = 0; m < RF; ++m) {
-                    bf16x8 o[4];
-                    decode(l.code[m], l.scale[m] >> (8 * g), o);
+                    for (int q = 0; q < 4; ++q)
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[q], l.v[p][q], acc[m], 0, 0, 0);
+            }
+        };
+        in_pairs<Loaded>(c0, c1, 1, load, use);
+        // a token has an expert once, so no two lanes add to one place
+        if (r < n)
 #pragma unroll
-                    for (int t = 0; t < CT; ++t)
-#pragma unroll
-                        for (int p = PH - 1; p >= 0; --p)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                acc[m][t] =
-                                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[q], l.v[t][p][q], acc[m][t], 0, 0, 0);
-                }
-            };
-            in_pairs<Loaded>(c0, c1, 1, load, use);
-            // a token has an expert once, so no two lanes add to one place
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-                if (p0 + 16 * t + r < n)
-#pragma unroll
-                    for (int m = 0; m < RF; ++m) {
-                        f32x4* to = reinterpret_cast<f32x4*>(mine + pair[t] / L.k * kWide + 16 * m + 4 * g);
-                        *to = *to + acc[m][t];
-                    }
-        }
+            for (int m = 0; m < RF; ++m) {
+                f32x4* to = reinterpret_cast<f32x4*>(mine + pair / L.k * kWide + 16 * m + 4 * g);
+                *to = *to + acc[m];
+            }
     }
     __syncthreads();
     for (int o = threadIdx.x; o < L.T * 16 * RF; o += WAVES * 64) {
@@ -581,37 +767,100 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kern
         if (gridDim.y == 1)
             Y[int64_t(t) * ldy + d0 + c] = from_f32<TY>(y);
         else
-            __hip_atomic_store(L.sums + (int64_t(blockIdx.y) * L.T + t) * L.D + d0 + c, y, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
+            L.sums[(int64_t(blockIdx.y) * L.T + t) * L.D + d0 + c] = y;
     }
-    if (gridDim.y == 1) return;
-    // this workgroup's sums are complete at device scope before its count
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// The same product through the ring, 256 outputs a workgroup, whose waves take
+// its run of pieces together.
+template <typename TY, int PH, int S>
+__global__ __launch_bounds__(kRingWaves * 64, 2) void moe_down_ring_kernel(Layer L, TY* __restrict__ Y, int64_t ldy) {
+    using R = Ring<PH>;
+    constexpr int kWide = 32 + 4;
+    __shared__ __align__(1024) uint8_t l0[R::kBytes], l1[R::kBytes], l2[R::kBytes], l3[S > 3 ? R::kBytes : 16];
+    extern __shared__ __align__(16) float sums[];  // wave x token x kWide, then the lists
+    int* entry = reinterpret_cast<int*>(sums + kRingWaves * L.T * kWide);
+    const int n_tiles = L.lists[0], most = most_tiles(L.T, L.E, L.k);
+    int16_t* order = reinterpret_cast<int16_t*>(entry + 3 * most);
+    for (int i = threadIdx.x; i < 3 * most; i += kRingWaves * 64) entry[i] = L.lists[1 + i];
+    for (int i = threadIdx.x; i < L.T * L.k; i += kRingWaves * 64) order[i] = L.order[i];
+    for (int i = threadIdx.x; i < kRingWaves * L.T * kWide; i += kRingWaves * 64) sums[i] = 0.f;
     __syncthreads();
-    if (threadIdx.x == 0)
-        entry[0] = __hip_atomic_fetch_add(L.done + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                   gridDim.y - 1;
-    __syncthreads();
-    if (!entry[0]) return;
-    const int splits = gridDim.y;
-    const int64_t stride = int64_t(L.T) * L.D;
-    for (int o = threadIdx.x; o < L.T * 16 * RF; o += WAVES * 64) {
-        const int t = o / (16 * RF), c = o % (16 * RF);
-        if (d0 + c >= L.D) continue;
-        const float* p = L.sums + int64_t(t) * L.D + d0 + c;
-        float y = 0.f;
-        for (int i = 0; i < splits; i += 8) {  // eight loads in flight
-            float v[8];
+    const int64_t d0 = int64_t(blockIdx.x) * kRingRows;
+    const int pieces = int(L.steps_f) * 2;
+    const int64_t all = int64_t(n_tiles) * pieces;
+    const int lo = int(all * blockIdx.y / gridDim.y), hi = int(all * (blockIdx.y + 1) / gridDim.y);
+    const int there = int(min(int64_t(kRingRows), L.D - d0));
+    R ring(L.dc, L.ds, int64_t(L.E) * L.D, 128, there, there - 128, L.steps_f, L.hp, int64_t(L.T) * L.k);
+    const int r = ring.lane & 15, g = ring.lane >> 4;
+    float* mine = sums + ring.wave * L.T * kWide;
+    if (lo < hi) {
+        int tile = lo / pieces, column = lo % pieces, copied = lo;  // the next copy's piece
+        int64_t row0 = 0;
+        auto start_tile = [&]() {
+            const int e = __builtin_amdgcn_readfirstlane(entry[3 * tile]);
+            const int first = __builtin_amdgcn_readfirstlane(entry[3 * tile + 1]);
+            const int n = __builtin_amdgcn_readfirstlane(entry[3 * tile + 2]);
+            row0 = int64_t(e) * L.D + d0;
+            ring.set_tile([&](int i) { return order[first + min(i, n - 1)]; });
+        };
+        start_tile();
+        f32x4 acc[2] = {};
+        int used = tile, left = min(pieces - column, hi - lo), more = hi - lo;  // of the tile in use, of all
+        through_ring<S, R::kCopies>(
+            l0, l1, l2, l3, hi - lo,
+            [&](uint8_t* stage) {
+                ring.copy(stage, row0, column);
+                if (++copied < hi && ++column == pieces) {
+                    column = 0;
+                    ++tile;
+                    start_tile();
+                }
+            },
+            [&](const uint8_t* stage) {
+                ring.multiply(stage, acc);
+                --more;
+                if (--left) return;
+                // the end of a tile, or of the run
+                const int first = entry[3 * used + 1], n = entry[3 * used + 2];
+                if (r < n) {
+                    float* to = mine + order[first + r] / L.k * kWide + 4 * g;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = i + j < splits
-                           ? __hip_atomic_load(p + (i + j) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                           : 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y += v[j];
-        }
-        Y[int64_t(t) * ldy + d0 + c] = from_f32<TY>(y);
+                    for (int m = 0; m < 2; ++m) {
+                        f32x4* at = reinterpret_cast<f32x4*>(to + 16 * m);
+                        *at = *at + acc[m];
+                    }
+                }
+                acc[0] = acc[1] = f32x4{};
+                ++used;
+                left = min(pieces, more);
+            });
     }
+    // a wave's own sums: 16 outputs of each range
+    for (int o = ring.lane; o < L.T * 32; o += 64) {
+        const int t = o / 32, c = o % 32;
+        const int64_t d = d0 + c / 16 * 128 + ring.wave * 16 + c % 16;
+        if (d >= L.D) continue;
+        const float y = mine[t * kWide + c];
+        if (gridDim.y == 1)
+            Y[int64_t(t) * ldy + d] = from_f32<TY>(y);
+        else
+            L.sums[(int64_t(blockIdx.y) * L.T + t) * L.D + d] = y;
+    }
+}
+
+constexpr int kJoinThreads = 256;
+
+// The workgroups' sums, in their order: an output a thread, 16 loads in flight.
+template <typename TY>
+__global__ __launch_bounds__(kJoinThreads) void moe_join_kernel(Layer L, TY* __restrict__ Y, int64_t ldy, int splits) {
+    const int64_t d = int64_t(blockIdx.x) * kJoinThreads + threadIdx.x, stride = int64_t(L.T) * L.D;
+    if (d >= L.D) return;
+    const float* p = L.sums + int64_t(blockIdx.y) * L.D + d;
+    float y = 0.f;
+#pragma unroll 16
+    for (int i = 0; i < splits; ++i) y += p[i * stride];
+    Y[int64_t(blockIdx.y) * ldy + d] = from_f32<TY>(y);
 }
 
 // bf16 parts of x and h for a type of x.
@@ -622,33 +871,34 @@ template <> constexpr int type_of<float>() { return RETRO_F32; }
 template <> constexpr int type_of<_Float16>() { return RETRO_F16; }
 template <> constexpr int type_of<__bf16>() { return RETRO_BF16; }
 
-// The down kernel's shape: outputs of a workgroup in sixteens, blocks of 16 pairs
-// at a time, waves, and workgroups that share the pieces.
+// The down kernel's shape: outputs of a workgroup, waves, and workgroups that
+// share the pieces.
 struct Down {
-    int rf, ct, waves, splits;
-    int64_t blocks(int64_t D) const { return host::cdiv(D, 16 * rf); }
+    bool ring;
+    int rows, waves, splits;
+    int64_t blocks(int64_t D) const { return host::cdiv(D, rows); }
     int64_t lds(int64_t T, int64_t E, int64_t k) const {
-        return waves * T * (16 * rf + 4) * 4 + 12 * std::min(E, T * k) + 2 * T * k;
+        const int64_t wide = ring ? 32 + 4 : rows + 4;
+        return waves * T * wide * 4 + 12 * most_tiles(T, E, k) + 2 * T * k;
     }
 };
 
 Down down_shape(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
     const int64_t items = std::min(E, T * k) * steps_of(F) * 2;
     // Few pieces, as for single tokens: one workgroup of 16 waves, no parts to add.
-    if (T <= 16 && items <= 128) return {1, 1, 16, 1};
-    // Else one workgroup of 8 waves a CU (that many registers). 32 tokens, 8
-    // experts, D = 4096, F = 14336: 77 us with 64 outputs a workgroup; 104 with 32
-    // and two blocks of pairs, which pays where experts have more than 16 pairs.
-    // F32 (three parts of h) and many tokens (LDS) take 32 outputs too.
-    const bool two = T * k > 12 * E;
-    const int rf = two || xtype == RETRO_F32 || T > 32 ? 2 : 4;
-    const int64_t slabs = host::cdiv(D, 16 * rf);
-    return {rf, two ? 2 : 1, 8, int(std::max<int64_t>(1, std::min(host::cdiv(host::kNumCUs, slabs), items / 16)))};
+    if (T <= 16 && items <= 128) return {false, 16, 16, 1};
+    // The staged kernel addresses h with 32 bits, and holds four or (many tokens)
+    // three stages beside the tokens' sums.
+    const int parts = h_parts(xtype);
+    const bool fits = parts * T * k * steps_of(F) * 512 < (int64_t(1) << 32) && (parts < 3 || T <= 32);
+    const int rows = fits ? kRingRows : 32;
+    const int64_t slabs = host::cdiv(D, rows);
+    return {fits, rows, 8, int(std::max<int64_t>(1, std::min(host::cdiv(host::kNumCUs, slabs), items / 16)))};
 }
 
 // The workspace's pieces, each on a 256-byte boundary.
 struct Pieces {
-    int64_t logits, share, lists, order, xp, hp, sums, done, all;
+    int64_t logits, share, lists, order, xp, hp, sums, all;
 };
 
 Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
@@ -658,16 +908,14 @@ Pieces pieces(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) 
         where = at;
         at += host::cdiv(bytes, 256) * 256;
     };
-    const int64_t chosen = std::min(E, T * k);
     put(p.logits, T * E * 4);
     put(p.share, T * k * 4);
-    put(p.lists, (1 + 3 * chosen) * 4);
+    put(p.lists, (1 + 3 * most_tiles(T, E, k)) * 4);
     put(p.order, T * k * 2);
     put(p.xp, x_parts(xtype) * T * steps_of(D) * kStep * 2);
     put(p.hp, h_parts(xtype) * T * k * steps_of(F) * kStep * 2);
     const Down s = down_shape(xtype, T, D, F, E, k);
     put(p.sums, s.splits > 1 ? s.splits * T * D * 4 : 0);
-    put(p.done, s.splits > 1 ? s.blocks(D) * 4 : 0);
     p.all = at;
     return p;
 }
@@ -678,7 +926,7 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
     constexpr int PX = x_parts(type_of<TX>()), PH = h_parts(type_of<TX>());
     const int groups = int(host::cdiv(L.E, kRouterWaves));
     const int64_t cuts = host::cdiv(L.steps_d * kStep, kRouterWaves * 64 * 8);
-    const int chosen = std::min(L.E, L.T * L.k);
+    const int tiles = most_tiles(L.T, L.E, L.k);
     const bool aligned = mx::aligned(X, 16) && mx::aligned(R, 16) && ldx * int64_t(sizeof(TX)) % 16 == 0 &&
                          ldr * int64_t(sizeof(TR)) % 16 == 0;
     host::clear_last_error();
@@ -694,34 +942,43 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
         router(moe_router_kernel<TX, TR, PX, 4>, 4);
     const bool own_lists = L.T <= kGateWaves;
     if (!own_lists) moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
-    // Slabs of 32 features where that leaves enough of them, and workgroups enough
-    // for four a CU: several waves share a slab where there are few.
-    auto gate_up = [&](auto kernel, int width) {
-        const int64_t slabs = host::cdiv(L.steps_f * kStep, width);
+    // 128 features a workgroup through the ring where that makes half a workgroup a
+    // CU (1 token, 2 of 8 experts, D = 4096, F = 14336, 224 of them: 48 us against 54
+    // for the layer; 64 tokens, 8 of 64, D = 2048, F = 1024: 78 against 86; at F =
+    // 4096 and one token, 64 of them, 34 against 25). Else workgroups enough for
+    // four a CU, several waves sharing a slab where there are few.
+    const int64_t slabs128 = L.steps_f * 2;
+    if (slabs128 * tiles >= host::kNumCUs / 2) {
+        auto gate_up = [&](void (*kernel)(Layer, int)) {
+            kernel<<<dim3(uint32_t(slabs128), tiles), dim3(kRingWaves * 64), 0, st>>>(L, renormalize);
+        };
+        own_lists ? gate_up(moe_gate_up_ring_kernel<PX, PH, true>) : gate_up(moe_gate_up_ring_kernel<PX, PH, false>);
+    } else {
+        const int64_t slabs = L.steps_f * (kStep / 16);
         int ks = 1;
-        while (ks < kGateWaves && host::cdiv(slabs * ks, kGateWaves) * chosen < 4 * host::kNumCUs) ks *= 2;
-        kernel<<<dim3(uint32_t(host::cdiv(slabs * ks, kGateWaves)), chosen), dim3(kGateWaves * 64), 0, st>>>(
-            L, ks, renormalize);
-    };
-    const bool wide = PX == 1 && L.steps_f * (kStep / 32) * chosen >= 2 * host::kNumCUs;
-    constexpr int SL = PX == 1 ? 2 : 1;
-    if (own_lists)
-        wide ? gate_up(moe_gate_up_kernel<PX, PH, SL, true>, 32) : gate_up(moe_gate_up_kernel<PX, PH, 1, true>, 16);
-    else
-        wide ? gate_up(moe_gate_up_kernel<PX, PH, SL, false>, 32) : gate_up(moe_gate_up_kernel<PX, PH, 1, false>, 16);
+        while (ks < kGateWaves && host::cdiv(slabs * ks, kGateWaves) * tiles < 4 * host::kNumCUs) ks *= 2;
+        auto gate_up = [&](void (*kernel)(Layer, int, int)) {
+            kernel<<<dim3(uint32_t(host::cdiv(slabs * ks, kGateWaves)), tiles), dim3(kGateWaves * 64), 0, st>>>(
+                L, ks, renormalize);
+        };
+        own_lists ? gate_up(moe_gate_up_kernel<PX, PH, true>) : gate_up(moe_gate_up_kernel<PX, PH, false>);
+    }
     const Down s = down_shape(type_of<TX>(), L.T, L.D, L.F, L.E, L.k);
-    auto down = [&](auto kernel) {
+    auto down = [&](void (*kernel)(Layer, TX*, int64_t)) {
         kernel<<<dim3(uint32_t(s.blocks(L.D)), s.splits), dim3(s.waves * 64),
                  size_t(s.lds(L.T, L.E, L.k)), st>>>(L, Y, ldy);
     };
     if (s.waves == 16)
-        down(moe_down_kernel<TX, PH, 1, 1, 16>);
-    else if (s.ct == 2)
-        down(moe_down_kernel<TX, PH, 2, 2, 8>);
-    else if (s.rf == 2)
-        down(moe_down_kernel<TX, PH, 1, 2, 8>);
-    else
-        down(moe_down_kernel<TX, PH, 1, 4, 8>);
+        down(moe_down_kernel<TX, PH, 1, 16>);
+    else if (!s.ring)
+        down(moe_down_kernel<TX, PH, 2, 8>);
+    else if (L.T <= 32)
+        down(moe_down_ring_kernel<TX, PH, 4>);
+    else if constexpr (PH < 3)
+        down(moe_down_ring_kernel<TX, PH, 3>);
+    if (s.splits > 1)
+        moe_join_kernel<<<dim3(uint32_t(host::cdiv(L.D, kJoinThreads)), L.T), dim3(kJoinThreads), 0, st>>>(L, Y, ldy,
+                                                                                                        s.splits);
     return host::launch_status();
 }
 
@@ -801,9 +1058,6 @@ int retro_moe(int xtype, const void* X, int64_t ldx, int rtype, const void* R, i
     L.xp = reinterpret_cast<__bf16*>(base + p.xp);
     L.hp = reinterpret_cast<__bf16*>(base + p.hp);
     L.sums = reinterpret_cast<float*>(base + p.sums);
-    L.done = reinterpret_cast<unsigned*>(base + p.done);
-    const Down shape = down_shape(xtype, T, D, F, E, top_k);
-    L.blocks = shape.splits > 1 ? int(shape.blocks(D)) : 0;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_float(xtype, [&](auto* tag) {
         using TX = std::remove_pointer_t<decltype(tag)>;

@@ -52,6 +52,41 @@ def test_layer(q, dtype, case, renormalize):
     check(y, *ref.moe(x, router, gu[2], dn[2], k, renormalize), dtype)
 
 
+# Layers large enough for workgroups to share the down product's rows: outputs that
+# end in the first and in the second half of a workgroup's, few pieces and many,
+# experts with more than 16 tokens, all three types' stages.
+LARGE = [(2, 520, 9000, 4, 2), (16, 300, 2000, 8, 4), (17, 390, 2000, 8, 4), (33, 1, 3000, 4, 2), (40, 96, 2000, 2, 2),
+         (16, 96, 3000, 16, 4), (64, 257, 1100, 8, 8), (5, 1030, 5000, 3, 2), (32, 130, 4200, 2, 1)]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=NAME.get)
+def test_large_layer(q, dtype, case):
+    T, D, F, E, k = case
+    x, router, *planes = layer(T, D, F, E, dtype, seed=T + D)
+    gu, dn = on_gpu(q, planes[0], D), on_gpu(q, planes[1], F)
+    out = torch.full((T, D + 3), float("nan"), dtype=dtype, device="cuda")
+    y = q.mx_moe(x.cuda(), router.cuda(), gu, dn, k, out=out[:, :D])
+    assert out[:, D:].isnan().all()
+    again = [q.mx_moe(x.cuda(), router.cuda(), gu, dn, k) for _ in range(5)]
+    assert all(torch.equal(a, y) for a in again)
+    check(y, *ref.moe(x, router, planes[0][2], planes[1][2], k, True), dtype)
+
+
+@pytest.mark.parametrize("shape", [(3, 64, 32, 4, 2), (20, 130, 2000, 6, 3)], ids=str)
+def test_the_largest_finite_x(q, shape):
+    """x whose BF16 rounding is an infinity, with weights small enough for finite
+    products."""
+    T, D, F, E, k = shape
+    x, router, gu, dn = layer(T, D, F, E, torch.float32, 6)
+    x[:, ::7] = torch.finfo(torch.float32).max * torch.sign(x[:, ::7])
+    router = router * 2.0 ** -120
+    gu = (gu[0], (gu[1].int() - 112).clamp(min=0).to(torch.uint8), gu[2] * 2.0 ** -112)
+    y = q.mx_moe(x.cuda(), router.cuda(), on_gpu(q, gu, D), on_gpu(q, dn, F), k)
+    assert torch.isfinite(y).all()
+    check(y, *ref.moe(x, router, gu[2], dn[2], k, True), torch.float32)
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=NAME.get)
 def test_router_of_x_type_and_strided_views(q, dtype):
     T, D, F, E, k = 6, 130, 70, 9, 3
