@@ -51,7 +51,7 @@ struct Tile {
 // moves 8 rows of 128 bytes. The 16-byte blocks of row r land in LDS permuted by
 // XOR with (r / 2) % 8, so that the 16 lanes of a read of one block from
 // neighbouring rows meet all banks once. Rows past the matrix read as zeros (the
-// buffer's bound).
+// buffer's bound, against which the lane's offset is checked: the row is in it).
 template <class Z>
 __device__ __forceinline__ void copy_step(__amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b, uint8_t* lds,
                                           uint32_t pitch, uint32_t step, int wave, int lane) {
@@ -63,8 +63,7 @@ __device__ __forceinline__ void copy_step(__amdgpu_buffer_rsrc_t a, __amdgpu_buf
         const uint32_t row = at - (of_a ? 0 : Z::kRowsT);
         const uint32_t swz = ((row + r) >> 1) & 7;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? a : b, lds + at * kStepBytes, 16,
-                                                 r * pitch + ((slot ^ swz) * 16), row * pitch + step * kStepBytes, 0,
-                                                 0);
+                                                 (row + r) * pitch + ((slot ^ swz) * 16), step * kStepBytes, 0, 0);
     }
 }
 
