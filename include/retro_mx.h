@@ -109,7 +109,8 @@ enum {
     RETRO_MX_VARIANT_TILE_64x64 = 5,
     RETRO_MX_VARIANT_SKINNY = 6,
     RETRO_MX_VARIANT_TILE_64x64_K4 = 7,
-    RETRO_MX_VARIANT_TILE_32x64_K4 = 8
+    RETRO_MX_VARIANT_TILE_32x64_K4 = 8,
+    RETRO_MX_VARIANT_TILE_256x192 = 9
 };
 
 /* retro_mx_mul_mat with a forced kernel; RETRO_E_VARIANT when it does not take

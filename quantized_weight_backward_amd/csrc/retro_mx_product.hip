@@ -61,6 +61,7 @@ __global__ __launch_bounds__(64) void product_simple_kernel(const uint8_t* __res
 }
 
 using Tile256x256 = Tile<2, 4, 4, 2>;
+using Tile256x192 = Tile<4, 2, 2, 3>;
 using Tile128x128 = Tile<2, 2, 2, 2>;
 using Tile64x128 = Tile<2, 2, 1, 2>;
 using Tile64x64 = Tile<2, 2, 1, 1>;
@@ -151,8 +152,10 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     // for each 256 elements of K, with one workgroup a CU and with as many as fit.
     // Fitted to T x N x K = 4096 x 14336 x 4096, 4096 x 5120 x 4096, 8192^3, 17408 x
     // 5120 x 2048, 2048 x 5120 x 17408 and 64 .. 1024 x 4096 x 4096 and 14336. The
-    // last round has as many a CU as it needs (or, at one a CU, as many CUs: the
-    // fewer, the higher their clock).
+    // last round has as many a CU as it needs, of which the first cost least beside
+    // one another (512 x 4096 x 4096: two of four a CU 12.0 us, one 11.0, four 19.1),
+    // or, at one a CU, as many CUs (the fewer, the higher their clock): 2048 x 5120 x 17408 takes 97 us as 216 tiles of
+    // 256 x 192 and 112 as 160 of 256 x 256, 8192^3 309 and 276.
     struct Cost {
         int variant, rows_t, rows_n, per_cu;
         double one, one_step, full, full_step;
@@ -160,9 +163,10 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     const double f32 = size == 4 ? 4 : 0;  // twice the bytes to write, with nothing beside
     const Cost costs[] = {
         {RETRO_MX_VARIANT_TILE_256x256, 256, 256, Tile256x256::kPerCU, 7 + f32, 1.4, 7 + f32, 1.9},
+        {RETRO_MX_VARIANT_TILE_256x192, 256, 192, Tile256x192::kPerCU, 3 + f32, 1.1, 5 + f32, 1.55},
         {RETRO_MX_VARIANT_TILE_128x128, 128, 128, Tile128x128::kPerCU, 3, 0.8, 5, 1.07},
         {RETRO_MX_VARIANT_TILE_64x128, 64, 128, Tile64x128::kPerCU, 2.5, 0.6, 4, 0.95},
-        {RETRO_MX_VARIANT_TILE_64x64, 64, 64, Tile64x64::kPerCU, 2, 0.47, 4.5, 0.75},
+        {RETRO_MX_VARIANT_TILE_64x64, 64, 64, Tile64x64::kPerCU, 2, 0.47, 4.5, 0.92},
         {RETRO_MX_VARIANT_TILE_64x64_K4, 64, 64, Tile64x64K4::kPerCU, 2.5, 0.3, 2.5, 0.3},
         {RETRO_MX_VARIANT_TILE_32x64_K4, 32, 64, Tile32x64K4::kPerCU, 2.5, 0.23, 2.5, 0.23},
     };
@@ -174,7 +178,8 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
         const int64_t rest = host::cdiv(n % round, host::kNumCUs);
         const double one = c.one + c.one_step * steps, full = c.full + c.full_step * steps;
         double cost = double(n / round) * full;
-        const double filled = c.per_cu > 1 ? double(rest - 1) / (c.per_cu - 1) : double(n % round) / double(round);
+        const double of = c.per_cu > 1 ? double(rest - 1) / (c.per_cu - 1) : 1;
+        const double filled = c.per_cu > 1 ? of * of : double(n % round) / double(round);
         if (rest) cost += one + (full - one) * filled;
         if (!best || cost < least) {
             best = c.variant;
@@ -191,6 +196,7 @@ bool product_applies(int variant, int size, int64_t ldy, int64_t K, int64_t N, i
         case RETRO_MX_VARIANT_AUTO:
         case RETRO_MX_VARIANT_SIMPLE: return true;
         case RETRO_MX_VARIANT_TILE_256x256:
+        case RETRO_MX_VARIANT_TILE_256x192:
         case RETRO_MX_VARIANT_TILE_64x128:
         case RETRO_MX_VARIANT_TILE_128x128:
         case RETRO_MX_VARIANT_TILE_64x64:
@@ -211,6 +217,7 @@ int launch_product(int variant, int ytype, const void* ac, const void* as, const
         TY* y = static_cast<TY*>(Y);
         switch (variant) {
             case RETRO_MX_VARIANT_TILE_256x256: return launch_tile<Tile256x256>(p, y);
+            case RETRO_MX_VARIANT_TILE_256x192: return launch_tile<Tile256x192>(p, y);
             case RETRO_MX_VARIANT_TILE_64x128: return launch_tile<Tile64x128>(p, y);
             case RETRO_MX_VARIANT_TILE_128x128: return launch_tile<Tile128x128>(p, y);
             case RETRO_MX_VARIANT_TILE_64x64: return launch_tile<Tile64x64>(p, y);

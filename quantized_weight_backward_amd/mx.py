@@ -24,11 +24,13 @@ from . import (BF16, E_SHAPE, E_TYPE, F16, F32, MXFP4, TYPES, _check, _current_d
 
 _FLOAT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 MX_VARIANT_AUTO, MX_VARIANT_SIMPLE, MX_VARIANT_TILE_256x256, MX_VARIANT_TILE_128x128, MX_VARIANT_TILE_64x128, \
-    MX_VARIANT_TILE_64x64, MX_VARIANT_SKINNY, MX_VARIANT_TILE_64x64_K4, MX_VARIANT_TILE_32x64_K4 = range(9)
+    MX_VARIANT_TILE_64x64, MX_VARIANT_SKINNY, MX_VARIANT_TILE_64x64_K4, MX_VARIANT_TILE_32x64_K4, \
+    MX_VARIANT_TILE_256x192 = range(10)
 MX_VARIANT_NAMES = {MX_VARIANT_SIMPLE: "simple", MX_VARIANT_TILE_256x256: "tile_256x256",
                     MX_VARIANT_TILE_128x128: "tile_128x128", MX_VARIANT_TILE_64x128: "tile_64x128",
                     MX_VARIANT_TILE_64x64: "tile_64x64", MX_VARIANT_SKINNY: "skinny",
-                    MX_VARIANT_TILE_64x64_K4: "tile_64x64_k4", MX_VARIANT_TILE_32x64_K4: "tile_32x64_k4"}
+                    MX_VARIANT_TILE_64x64_K4: "tile_64x64_k4", MX_VARIANT_TILE_32x64_K4: "tile_32x64_k4",
+                    MX_VARIANT_TILE_256x192: "tile_256x192"}
 
 
 def _elsewhere(t, stream) -> bool:
