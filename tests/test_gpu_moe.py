@@ -56,7 +56,8 @@ def test_layer(q, dtype, case, renormalize):
 # end in the first and in the second half of a workgroup's, few pieces and many,
 # experts with more than 16 tokens, all three types' stages.
 LARGE = [(2, 520, 9000, 4, 2), (16, 300, 2000, 8, 4), (17, 390, 2000, 8, 4), (33, 1, 3000, 4, 2), (40, 96, 2000, 2, 2),
-         (16, 96, 3000, 16, 4), (64, 257, 1100, 8, 8), (5, 1030, 5000, 3, 2), (32, 130, 4200, 2, 1)]
+         (16, 96, 3000, 16, 4), (64, 257, 1100, 8, 8), (5, 1030, 5000, 3, 2), (32, 130, 4200, 2, 1),
+         (32, 40, 300, 256, 16), (64, 40, 300, 256, 16)]
 
 
 @pytest.mark.parametrize("case", LARGE, ids=str)
@@ -71,6 +72,19 @@ def test_large_layer(q, dtype, case):
     again = [q.mx_moe(x.cuda(), router.cuda(), gu, dn, k) for _ in range(5)]
     assert all(torch.equal(a, y) for a in again)
     check(y, *ref.moe(x, router, planes[0][2], planes[1][2], k, True), dtype)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=NAME.get)
+def test_a_token_that_is_not_finite_in_a_large_layer(q, dtype, bad):
+    """The other columns of its tiles, which are multiplied beside it, are untouched."""
+    T, D, F, E, k = 20, 390, 2000, 3, 2
+    x, router, gu, dn = layer(T, D, F, E, dtype, 8)
+    x[7, 100] = bad
+    y = q.mx_moe(x.cuda(), router.cuda(), on_gpu(q, gu, D), on_gpu(q, dn, F), k)
+    assert not torch.isfinite(y[7]).any()
+    good = [t for t in range(T) if t != 7]
+    check(y[good], *ref.moe(x[good], router, gu[2], dn[2], k, True), dtype)
 
 
 @pytest.mark.parametrize("shape", [(3, 64, 32, 4, 2), (20, 130, 2000, 6, 3)], ids=str)
