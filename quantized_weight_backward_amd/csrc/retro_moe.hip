@@ -19,9 +19,9 @@
 // Measured (BF16; router, choose, gate_up, down, join): 1 token, 4 of 32 experts, D
 // = 2048, F = 1024: 16.5 us (3, in gate_up, 7.5, 7, none: launches and the
 // latencies of each, 13 MB of weights are 2.6 us). 16 tokens, 8 of 64 experts, F =
-// 1000: 63 us (4.7, 5.1, 30, 20, 4.7) for 185 MB, 2.9 TB/s. 32 tokens, 2 of 8
-// experts, D = 4096, F = 14336: 185 us (5.2, 6.2, 112, 64, 5.1) for 749 MB, 4.05
-// TB/s; gate_up reads at 4.5 TB/s and down at 3.9, where a plain read reaches 5.2.
+// 1000: 61 us (4.9, 5.0, 31, 20, 4.8) for 185 MB, 3.0 TB/s. 32 tokens, 2 of 8
+// experts, D = 4096, F = 14336: 173 us (5.3, 6.8, 107, 67, 5.4) for 749 MB, 4.3
+// TB/s; gate_up reads at 4.7 TB/s and down at 3.8, where a plain read reaches 5.2.
 #include "retro_mx_device.h"
 #include "retro_mx_host.h"
 
@@ -495,25 +495,24 @@ __device__ __forceinline__ void stage_ready() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// For larger layers a workgroup of eight waves multiplies 256 rows of weights with
-// a tile through a ring of stages in LDS, each a piece of 128 elements: rows,
+// For larger layers a workgroup of WAVES waves multiplies 32 WAVES rows of weights
+// with a tile through a ring of stages in LDS, each a piece of 128 elements: rows,
 // their scales, and the tile's x or h. Read straight into the operands' lanes each
 // 16 bytes are a cache access of their own (a lane holds another row than its
 // neighbour): 38 to 40 accesses a load instruction, of which x or h had two for
 // each of the rows'. A copy of 64 or 256 contiguous bytes takes one for each 64, 15
 // to 16 an instruction, and x or h is copied once for all waves. 32 tokens, 2 of 8
 // experts, D = 4096, F = 14336: down 36 to 8 million accesses, 93 to 64 us; gate_up
-// 48 to 16 million, 117 to 112 us, its bytes at 4.5 TB/s.
-// waves. Stage rows 0 .. 127 and 128 .. 255 are two ranges of rows; a wave
-// multiplies 16 of each. Rows of 64 bytes lie permuted by XOR with (row / 4) % 4,
+// 48 to 16 million, 117 to 107 us, its bytes at 4.7 TB/s.
+// waves. The two halves of a stage's rows are two ranges of the matrix's; a
+// wave multiplies 16 of each. Rows of 64 bytes lie permuted by XOR with (row / 4) % 4,
 // x's or h's of 256 bytes by XOR with the row, so that neighbouring lanes' reads
 // meet all banks.
-constexpr int kRingWaves = 8, kRingRows = 256;
-
-template <int P>
+template <int P, int WAVES>
 struct Ring {
-    static constexpr int kIn = kRingRows * 64, kScales = kIn + P * 4096, kBytes = kScales + kRingRows * 4;
-    static constexpr int kCopiesOfIn = (P * 4 + kRingWaves - 1) / kRingWaves;
+    static constexpr int kRange = 16 * WAVES, kRows = 2 * kRange;
+    static constexpr int kIn = kRows * 64, kScales = kIn + P * 4096, kBytes = kScales + kRows * 4;
+    static constexpr int kCopiesOfIn = (P * 4 + WAVES - 1) / WAVES;
     static constexpr int kCopies = 2 + kCopiesOfIn + 1;  // of a wave, a piece
 
     const uint8_t *codes, *scales;
@@ -531,23 +530,24 @@ struct Ring {
           pitch(uint32_t(steps) * kStepBytes), part(uint32_t(in_rows * steps * (kStep * 2))) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
         lane = threadIdx.x % 64;
-        last0 = min(n0, 128) - 1;
-        last1 = n1 > 0 ? min(n1, 128) - 1 : last0;
+        last0 = min(n0, kRange) - 1;
+        last1 = n1 > 0 ? min(n1, kRange) - 1 : last0;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             code_at[j] = min(wave * 16 + lane / 4, j ? last1 : last0) * pitch + ((lane % 4) ^ (lane / 16)) * 16;
-        scale_at = min(wave % 2 * 64 + lane, scale_range() ? last1 : last0) * kStepScales;
+        scale_at = min(scale_copy() % (WAVES / 4) * 64 + lane, scale_range() ? last1 : last0) * kStepScales;
     }
 
-    // A wave copies a quarter of the scales: the range it is of.
-    __device__ __forceinline__ int scale_range() const { return wave / 2 % 2; }
+    // A wave copies 64 rows' scales (two waves the same): which, and of which range.
+    __device__ __forceinline__ int scale_copy() const { return wave % (WAVES / 2); }
+    __device__ __forceinline__ int scale_range() const { return scale_copy() / (WAVES / 4); }
 
     // Row `at(i)` of `in` is the tile's row i, i < 16.
     template <typename At>
     __device__ __forceinline__ void set_tile(At&& at) {
 #pragma unroll
         for (int j = 0; j < kCopiesOfIn; ++j) {
-            const int row = (j * kRingWaves + wave) % (P * 4) % 4 * 4 + lane / 16;
+            const int row = (j * WAVES + wave) % (P * 4) % 4 * 4 + lane / 16;
             in_at[j] = uint32_t(at(row)) * (pitch * 4) + ((lane % 16) ^ row) * 16;
         }
     }
@@ -556,14 +556,14 @@ struct Ring {
     __device__ __forceinline__ void copy(uint8_t* stage, int64_t row0, int c) const {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            copy16(stage + (j * 128 + wave * 16) * 64, codes + (row0 + j * second) * pitch,
+            copy16(stage + (j * kRange + wave * 16) * 64, codes + (row0 + j * second) * pitch,
                    int64_t((j ? last1 : last0) + 1) * pitch, code_at[j], c * 64);
 #pragma unroll
         for (int j = 0; j < kCopiesOfIn; ++j) {
-            const int at = (j * kRingWaves + wave) % (P * 4);
+            const int at = (j * WAVES + wave) % (P * 4);
             copy16(stage + kIn + at * 1024, in, int64_t(P) * part, in_at[j], at / 4 * part + c * 256);
         }
-        copy4(stage + kScales + wave % 4 * 256,
+        copy4(stage + kScales + scale_copy() * 256,
               scales + (c / 2 * rows + row0 + (scale_range() ? second : 0)) * kStepScales,
               int64_t((scale_range() ? last1 : last0) + 1) * kStepScales, scale_at, c % 2 * 4);
     }
@@ -580,7 +580,7 @@ struct Ring {
                     *reinterpret_cast<const bf16x8*>(stage + kIn + p * 4096 + r * 256 + (((g * 4 + i) ^ r) * 16));
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            const int row = m * 128 + wave * 16 + r;
+            const int row = m * kRange + wave * 16 + r;
             const u32x4 q = *reinterpret_cast<const u32x4*>(stage + row * 64 + ((g ^ ((r >> 2) & 3)) * 16));
             bf16x8 o[4];
             decode(q, stage[kScales + row * 4 + g], o);
@@ -620,12 +620,14 @@ __device__ __forceinline__ void through_ring(uint8_t* l0, uint8_t* l1, uint8_t* 
     stage_ready<0>();
 }
 
-// 128 features of one tile through the ring: their rows of gate are its first
+constexpr int kRingWavesUp = 4;
+
+// 64 features of one tile through the ring: their rows of gate are its first
 // range, of up its second.
 template <int PX, int PH, bool OWN_LISTS>
-__global__ __launch_bounds__(kRingWaves * 64, PX < 3 ? 4 : 2) void moe_gate_up_ring_kernel(Layer L, int renormalize) {
-    using R = Ring<PX>;
-    __shared__ __align__(1024) uint8_t l0[R::kBytes], l1[R::kBytes], l2[R::kBytes];
+__global__ __launch_bounds__(kRingWavesUp * 64, PX < 3 ? 3 : 2) void moe_gate_up_ring_kernel(Layer L, int renormalize) {
+    using R = Ring<PX, kRingWavesUp>;
+    __shared__ __align__(256) uint8_t l0[R::kBytes], l1[R::kBytes], l2[R::kBytes];
     const int* entry = L.lists + 1 + blockIdx.y * 3;
     const int16_t* order = L.order;
     const float* share = L.share;
@@ -642,11 +644,11 @@ __global__ __launch_bounds__(kRingWaves * 64, PX < 3 ? 4 : 2) void moe_gate_up_r
     }
     const int e = __builtin_amdgcn_readfirstlane(entry[0]), first = __builtin_amdgcn_readfirstlane(entry[1]);
     const int n = __builtin_amdgcn_readfirstlane(entry[2]);
-    const int64_t f0 = int64_t(blockIdx.x) * 128, Fp = L.steps_f * kStep;
+    const int64_t f0 = int64_t(blockIdx.x) * R::kRange, Fp = L.steps_f * kStep;
     f32x4 acc[2] = {};
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), r = threadIdx.x & 15, g = threadIdx.x / 16 % 4;
     if (f0 < L.F) {  // past F only the zeros that pad h are written
-        const int there = int(min(int64_t(128), L.F - f0));
+        const int there = int(min(int64_t(R::kRange), L.F - f0));
         R ring(L.guc, L.gus, int64_t(L.E) * 2 * L.F, L.F, there, there, L.steps_d, L.xp, L.T);
         ring.set_tile([&](int i) { return order[first + min(i, n - 1)] / L.k; });
         const int64_t row0 = int64_t(e) * 2 * L.F + f0;
@@ -775,11 +777,14 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) void moe_down_kern
 
 // The same product through the ring, 256 outputs a workgroup, whose waves take
 // its run of pieces together.
+constexpr int kRingWaves = 8, kRingRows = 256;
+
 template <typename TY, int PH, int S>
 __global__ __launch_bounds__(kRingWaves * 64, 2) void moe_down_ring_kernel(Layer L, TY* __restrict__ Y, int64_t ldy) {
-    using R = Ring<PH>;
+    using R = Ring<PH, kRingWaves>;
+    static_assert(R::kRows == kRingRows, "outputs of a workgroup");
     constexpr int kWide = 32 + 4;
-    __shared__ __align__(1024) uint8_t l0[R::kBytes], l1[R::kBytes], l2[R::kBytes], l3[S > 3 ? R::kBytes : 16];
+    __shared__ __align__(256) uint8_t l0[R::kBytes], l1[R::kBytes], l2[R::kBytes], l3[S > 3 ? R::kBytes : 16];
     extern __shared__ __align__(16) float sums[];  // wave x token x kWide, then the lists
     int* entry = reinterpret_cast<int*>(sums + kRingWaves * L.T * kWide);
     const int n_tiles = L.lists[0], most = most_tiles(L.T, L.E, L.k);
@@ -793,7 +798,7 @@ __global__ __launch_bounds__(kRingWaves * 64, 2) void moe_down_ring_kernel(Layer
     const int64_t all = int64_t(n_tiles) * pieces;
     const int lo = int(all * blockIdx.y / gridDim.y), hi = int(all * (blockIdx.y + 1) / gridDim.y);
     const int there = int(min(int64_t(kRingRows), L.D - d0));
-    R ring(L.dc, L.ds, int64_t(L.E) * L.D, 128, there, there - 128, L.steps_f, L.hp, int64_t(L.T) * L.k);
+    R ring(L.dc, L.ds, int64_t(L.E) * L.D, R::kRange, there, there - R::kRange, L.steps_f, L.hp, int64_t(L.T) * L.k);
     const int r = ring.lane & 15, g = ring.lane >> 4;
     float* mine = sums + ring.wave * L.T * kWide;
     if (lo < hi) {
@@ -841,7 +846,7 @@ __global__ __launch_bounds__(kRingWaves * 64, 2) void moe_down_ring_kernel(Layer
     // a wave's own sums: 16 outputs of each range
     for (int o = ring.lane; o < L.T * 32; o += 64) {
         const int t = o / 32, c = o % 32;
-        const int64_t d = d0 + c / 16 * 128 + ring.wave * 16 + c % 16;
+        const int64_t d = d0 + c / 16 * R::kRange + ring.wave * 16 + c % 16;
         if (d >= L.D) continue;
         const float y = mine[t * kWide + c];
         if (gridDim.y == 1)
@@ -887,15 +892,20 @@ struct Down {
 
 Down down_shape(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
     const int64_t items = std::min(E, T * k) * steps_of(F) * 2;
-    // Few pieces, as for single tokens: one workgroup of 16 waves, no parts to add.
-    if (T <= 16 && items <= 128) return {false, 16, 16, 1};
+    // Few pieces, as for single tokens: one workgroup of 16 waves, no parts to add
+    // (1 token, 4 of 32 experts, D = 2048, F = 1024, 32 pieces: the layer in 16.4 us
+    // against 18.8; 2 of 8, D = 4096, F = 4096, 64: 24.7 against 25.9; 8 of 64, F = 2048,
+    // 128: 31.5 against 27.1).
+    if (T <= 16 && items <= 64) return {false, 16, 16, 1};
     // The staged kernel addresses h with 32 bits, and holds four or (many tokens)
     // three stages beside the tokens' sums.
     const int parts = h_parts(xtype);
     const bool fits = parts * T * k * steps_of(F) * 512 < (int64_t(1) << 32) && (parts < 3 || T <= 32);
     const int rows = fits ? kRingRows : 32;
+    // as many workgroups as CUs, each at least four pieces (sixteen: 1 token, 4 of 16
+    // experts, D = 2048, F = 5120 in 37.7 us instead of 29.9)
     const int64_t slabs = host::cdiv(D, rows);
-    return {fits, rows, 8, int(std::max<int64_t>(1, std::min(host::cdiv(host::kNumCUs, slabs), items / 16)))};
+    return {fits, rows, 8, int(std::max<int64_t>(1, std::min(host::cdiv(host::kNumCUs, slabs), items / 4)))};
 }
 
 // The workspace's pieces, each on a 256-byte boundary.
@@ -944,15 +954,15 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
         router(moe_router_kernel<TX, TR, PX, 4>, 4);
     const bool own_lists = L.T <= kGateWaves;
     if (!own_lists) moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
-    // 128 features a workgroup through the ring where that makes half a workgroup a
-    // CU (1 token, 2 of 8 experts, D = 4096, F = 14336, 224 of them: 48 us against 54
-    // for the layer; 64 tokens, 8 of 64, D = 2048, F = 1024: 78 against 86; at F =
-    // 4096 and one token, 64 of them, 34 against 25). Else workgroups enough for
-    // four a CU, several waves sharing a slab where there are few.
-    const int64_t slabs128 = L.steps_f * 2;
-    if (slabs128 * tiles >= host::kNumCUs / 2) {
+    // 64 features a workgroup through the ring where that makes one a CU (1 token, 2
+    // of 8 experts, D = 4096, F = 8192, 256 of them: 44 us against 46 for the layer; F =
+    // 14336: 50 against 55; F = 4096, 128: 30 against 25; 32 tokens, F = 14336: 177
+    // against 208, with 128 features 182). Else workgroups enough for four a CU,
+    // several waves sharing a slab where there are few.
+    const int64_t ring_slabs = L.steps_f * (kStep / (16 * kRingWavesUp));
+    if (ring_slabs * tiles >= host::kNumCUs) {
         auto gate_up = [&](void (*kernel)(Layer, int)) {
-            kernel<<<dim3(uint32_t(slabs128), tiles), dim3(kRingWaves * 64), 0, st>>>(L, renormalize);
+            kernel<<<dim3(uint32_t(ring_slabs), tiles), dim3(kRingWavesUp * 64), 0, st>>>(L, renormalize);
         };
         own_lists ? gate_up(moe_gate_up_ring_kernel<PX, PH, true>) : gate_up(moe_gate_up_ring_kernel<PX, PH, false>);
     } else {
