@@ -110,44 +110,58 @@ class MXMatrix:
     in the layout of include/retro_mx.h (codes past K are zero).
     """
 
-    __slots__ = ("_codes", "_scales", "_both", "K", "rows", "_code_ptr", "_scale_ptr")
+    __slots__ = ("_codes", "_scales", "_both", "K", "rows")
 
     def __init__(self, codes, scales, K: int):
+        self._codes, self._scales, self._both, self.K, self.rows = codes, scales, None, K, None
+        self._validate()
+
+    def _validate(self):
+        """Refuses given arrays that are not (or, having got other storage or
+        sizes since, no longer are) a matrix of this size."""
+        codes, scales, steps = self._codes, self._scales, self._steps
         _device_tensor(codes, "codes")
         _device_tensor(scales, "scales")
-        steps = -(-K // 256)
         shape = codes.shape
         if codes.dtype is not torch.uint8 or len(shape) != 2 or shape[1] != steps * 128:
-            raise ValueError(f"codes must be uint8 [rows, {steps * 128}] for K = {K}")
+            raise ValueError(f"codes must be uint8 [rows, {steps * 128}] for K = {self.K}")
+        if self.rows is None:
+            self.rows = shape[0]
+        elif shape[0] != self.rows:
+            raise ValueError(f"codes has {shape[0]} rows, the matrix had {self.rows}")
         if scales.dtype is not torch.uint8 or scales.shape != (steps, shape[0], 8):
             raise ValueError(f"scales must be uint8 [{steps}, {shape[0]}, 8]")
         _one_device(codes, scales)
-        self._codes, self._scales, self._both, self.K, self.rows = codes, scales, None, K, shape[0]
-        self._code_ptr, self._scale_ptr = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
     def _new(cls, rows: int, K: int, like):
         """Both arrays in one allocation on like's device and the current stream."""
         m = cls.__new__(cls)
-        steps = -(-K // 256)
         m._codes = m._scales = None
-        m._both = torch.empty(rows * steps * 136, dtype=torch.uint8, device=like.device)
+        m._both = torch.empty(rows * -(-K // 256) * 136, dtype=torch.uint8, device=like.device)
         m.K, m.rows = K, rows
-        m._code_ptr = m._both.data_ptr()
-        m._scale_ptr = m._code_ptr + rows * steps * 128
         return m
 
+    def _planes(self):
+        """The arrays' addresses now: a caller's tensors may get other storage
+        between two calls."""
+        if self._both is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        at = self._both.data_ptr()
+        return at, at + self.rows * -(-self.K // 256) * 128
+
+    # of a matrix made here, views made anew: what is done to one is not done to the matrix
     @property
     def codes(self):
-        if self._codes is None:
-            self._codes = self._both[:self.rows * self._steps * 128].view(self.rows, self._steps * 128)
-        return self._codes
+        if self._both is None:
+            return self._codes
+        return self._both[:self.rows * self._steps * 128].view(self.rows, self._steps * 128)
 
     @property
     def scales(self):
-        if self._scales is None:
-            self._scales = self._both[self.rows * self._steps * 128:].view(self._steps, self.rows, 8)
-        return self._scales
+        if self._both is None:
+            return self._scales
+        return self._both[self.rows * self._steps * 128:].view(self._steps, self.rows, 8)
 
     @property
     def _steps(self):
@@ -168,6 +182,8 @@ class MXMatrix:
 def _matrix(m, name):
     if not isinstance(m, MXMatrix):
         raise ValueError(f"{name} must be an MXMatrix")
+    if m._both is None:
+        m._validate()
 
 
 def quantize(wtype: int, x, out=None, stream=None):
@@ -205,10 +221,10 @@ def mx_quantize(x, axis: int = 1, stream=None) -> MXMatrix:
     T, K = x.shape
     if axis == 0:
         m = MXMatrix._new(K, T, x)
-        _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, None, None, m._code_ptr, m._scale_ptr, _handle()))
+        _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, None, None, *m._planes(), _handle()))
     else:
         m = MXMatrix._new(T, K, x)
-        _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, m._code_ptr, m._scale_ptr, None, None, _handle()))
+        _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, *m._planes(), None, None, _handle()))
     return m
 
 
@@ -220,8 +236,7 @@ def mx_quantize_both(x, stream=None) -> tuple[MXMatrix, MXMatrix]:
             return mx_quantize_both(x)
     T, K = x.shape
     r, c = MXMatrix._new(T, K, x), MXMatrix._new(K, T, x)
-    _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, r._code_ptr, r._scale_ptr, c._code_ptr, c._scale_ptr,
-                                 _handle()))
+    _check(lib.retro_mx_quantize(xtype, x.data_ptr(), ldx, T, K, *r._planes(), *c._planes(), _handle()))
     return r, c
 
 
@@ -239,7 +254,7 @@ def mx_dequantize(m: MXMatrix, dtype=torch.float32, out=None, stream=None):
         out = torch.empty((rows, ld), dtype=dtype, device=m.device)
     else:
         ld = _given(out, rows, ld, dtype, m)
-    _check(lib.retro_mx_dequantize(ytype, m._code_ptr, m._scale_ptr, out.data_ptr(), ld, m.K, rows, _handle()))
+    _check(lib.retro_mx_dequantize(ytype, *m._planes(), out.data_ptr(), ld, m.K, rows, _handle()))
     return out
 
 
@@ -255,7 +270,7 @@ def mx_from_blocks(W, K: int, N: int, stream=None) -> MXMatrix:
         with _on(W, stream):
             return mx_from_blocks(W, K, N)
     m = MXMatrix._new(N, K, W)
-    _check(lib.retro_mx_from_blocks(W.data_ptr(), m._code_ptr, m._scale_ptr, K, N, _handle()))
+    _check(lib.retro_mx_from_blocks(W.data_ptr(), *m._planes(), K, N, _handle()))
     return m
 
 
@@ -282,8 +297,8 @@ def mx_mul_mat(a: MXMatrix, b: MXMatrix, dtype=torch.float32, out=None, variant:
         out, ld = torch.empty((T, N), dtype=dtype, device=a.device), N
     else:
         ld = _given(out, T, N, dtype, a)
-    _check(lib.retro_mx_mul_mat_variant(variant, ytype, a._code_ptr, a._scale_ptr, b._code_ptr, b._scale_ptr,
-                                        out.data_ptr(), ld, a.K, N, T, _handle()))
+    _check(lib.retro_mx_mul_mat_variant(variant, ytype, *a._planes(), *b._planes(), out.data_ptr(), ld, a.K, N, T,
+                                        _handle()))
     return out
 
 
@@ -306,7 +321,7 @@ def mx_linear(x, w: MXMatrix, out=None, stream=None):
         ld = _given(out, T, N, x.dtype, x)
     need = _linear_workspace(xtype, K, N, T)
     ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
-    _check(lib.retro_mx_linear(xtype, x.data_ptr(), ldx, w._code_ptr, w._scale_ptr, out.data_ptr(), ld, K, N, T,
+    _check(lib.retro_mx_linear(xtype, x.data_ptr(), ldx, *w._planes(), out.data_ptr(), ld, K, N, T,
                                None if ws is None else ws.data_ptr(), need, _handle()))
     return out
 
@@ -362,7 +377,7 @@ def mx_moe(x, router, gate_up: MXMatrix, down: MXMatrix, top_k: int, renormalize
     if need < 0:
         _check(need)
     ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    _check(lib.retro_moe(xtype, x.data_ptr(), ldx, rtype, router.data_ptr(), ldr, gate_up._code_ptr,
-                         gate_up._scale_ptr, down._code_ptr, down._scale_ptr, out.data_ptr(), ld, T, D, F, E, top_k,
-                         int(bool(renormalize)), None if ws is None else ws.data_ptr(), need, _handle()))
+    _check(lib.retro_moe(xtype, x.data_ptr(), ldx, rtype, router.data_ptr(), ldr, *gate_up._planes(),
+                         *down._planes(), out.data_ptr(), ld, T, D, F, E, top_k, int(bool(renormalize)),
+                         None if ws is None else ws.data_ptr(), need, _handle()))
     return out

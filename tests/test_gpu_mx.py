@@ -368,3 +368,19 @@ def test_offsets_past_32_bits(q):
     bound = ref.product_bound(a[2], b[2], K, 2.0 ** -8)[at % 64]
     assert ((y[-64:, -64:].cpu().double() - want).abs() <= bound).all()
     assert torch.equal(y[:64, :64], y[64 * 1000:64 * 1001, 64 * 600:64 * 601])
+
+
+def test_a_matrix_follows_its_arrays(q):
+    """Planes that get other storage: the products are those of the new bytes,
+    and planes that went to the host are refused."""
+    T, N, K = 20, 50, 300
+    x = values(T, K, torch.bfloat16, 1).cuda()
+    old, new = (q.mx_quantize(values(N, K, torch.float32, s).cuda()) for s in (2, 3))
+    codes, scales = old.codes.clone(), old.scales.clone()
+    m = q.MXMatrix(codes, scales, K)
+    assert torch.equal(q.mx_linear(x, m), q.mx_linear(x, old))
+    codes.data, scales.data = new.codes.clone(), new.scales.clone()
+    assert torch.equal(q.mx_linear(x, m), q.mx_linear(x, new))
+    codes.data = codes.data.cpu()
+    with pytest.raises(ValueError):
+        q.mx_linear(x, m)
