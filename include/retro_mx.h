@@ -33,7 +33,8 @@
  * Execution and errors are those of retro_out_prod.h: asynchronous on the
  * stream, no allocation, no CPU fallback, negative codes, all checks made on
  * the host before any launch. An empty output returns RETRO_OK and touches
- * nothing. Sizes: every dimension below 2^31 and every array below 2^62 bytes.
+ * nothing. Sizes: every dimension below 2^31 and every array below 2^62 bytes;
+ * the products also need ceil(T / 32) * ceil(N / 32) below 2^30 (RETRO_E_SHAPE).
  */
 #ifndef RETRO_MX_H
 #define RETRO_MX_H
@@ -92,8 +93,9 @@ int retro_mx_mul_mat(int ytype, const void *a_codes, const void *a_scales, const
  * Kernels of the product, for tests and benchmarks (retro_mx_mul_mat chooses
  * one by shape):
  *   RETRO_MX_VARIANT_SIMPLE   a wave a 32 x 32 tile, operands from memory; any
- *                             shape, and the only one for sizes whose offsets
- *                             pass 32 bits within a tile
+ *                             shape, and the only one for T > 32 where offsets
+ *                             pass 32 bits within a tile or the tiles' threads
+ *                             2^32
  *   RETRO_MX_VARIANT_TILE_*   rows of A x rows of B a workgroup, staged in LDS;
  *                             _K4: four groups of waves take K's steps in turn
  *                             and add their sums

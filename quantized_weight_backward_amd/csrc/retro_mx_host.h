@@ -2,14 +2,30 @@
 // retro_mx.h. No device code.
 #pragma once
 
+#include <algorithm>
+
 #include "retro_host.h"
 #include "retro_mx.h"
 
 namespace retro {
 namespace mx {
 
-// Workgroups of one launch; larger work is cut into several launches.
-constexpr int64_t kMaxBlocks = int64_t(1) << 23;
+// Workgroups (of at most 512 threads) of one launch, whose threads have to stay
+// below 2^32; larger work is cut into several launches.
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
+
+// f(first, blocks) for each launch of `blocks` workgroups.
+template <typename F>
+int in_block_ranges(int64_t blocks, F&& f) {
+    for (int64_t b = 0; b < blocks; b += kMaxBlocks) {
+        host::clear_last_error();
+        f(b, uint32_t(std::min(kMaxBlocks, blocks - b)));
+        const int rc = host::launch_status();
+        if (rc != RETRO_OK) return rc;
+    }
+    return RETRO_OK;
+}
 
 inline int float_bytes(int type) {
     return type == RETRO_F32 ? 4 : type == RETRO_F16 || type == RETRO_BF16 ? 2 : 0;

@@ -24,9 +24,9 @@ __global__ __launch_bounds__(64) void product_simple_kernel(const uint8_t* __res
                                                             const uint8_t* __restrict__ bc,
                                                             const uint8_t* __restrict__ bs, TY* __restrict__ Y,
                                                             int64_t ldy, int64_t steps, int64_t N, int64_t T,
-                                                            uint32_t tiles_n) {
+                                                            int64_t tiles_n, int64_t tile0) {
     const int lane = threadIdx.x, r = lane & 31, h = lane >> 5;
-    const int64_t t0 = int64_t(blockIdx.x / tiles_n) * 32, n0 = int64_t(blockIdx.x % tiles_n) * 32;
+    const int64_t tile = tile0 + blockIdx.x, t0 = tile / tiles_n * 32, n0 = tile % tiles_n * 32;
     const int64_t ra = min(t0 + r, T - 1), rb = min(n0 + r, N - 1);
     const uint8_t* pa = ac + ra * steps * kStepBytes + h * 64;
     const uint8_t* pb = bc + rb * steps * kStepBytes + h * 64;
@@ -77,10 +77,10 @@ struct Args {
 template <typename TY>
 int launch_simple(const Args& p, TY* Y) {
     const int64_t tiles_n = host::cdiv(p.N, 32), tiles_t = host::cdiv(p.T, 32);
-    host::clear_last_error();
-    product_simple_kernel<TY><<<dim3(uint32_t(tiles_n * tiles_t)), dim3(64), 0, p.st>>>(
-        p.ac, p.as, p.bc, p.bs, Y, p.ldy, steps_of(p.K), p.N, p.T, uint32_t(tiles_n));
-    return host::launch_status();
+    return in_block_ranges(tiles_n * tiles_t, [&](int64_t first, uint32_t blocks) {
+        product_simple_kernel<TY><<<dim3(blocks), dim3(64), 0, p.st>>>(p.ac, p.as, p.bc, p.bs, Y, p.ldy, steps_of(p.K),
+                                                                       p.N, p.T, tiles_n, first);
+    });
 }
 
 template <class Z, typename TY>
@@ -93,6 +93,12 @@ int launch_tile(const Args& p, TY* Y) {
         p.ac, p.as, p.bc, p.bs, Y, p.ldy, uint32_t(steps_of(p.K)), p.N, p.T, uint32_t(tiles_n), uint32_t(tiles_t),
         uint32_t(group));
     return host::launch_status();
+}
+
+// Whether all of a tile kernel's workgroups fit one launch.
+template <class Z>
+bool one_launch(int64_t N, int64_t T) {
+    return host::cdiv(T, Z::kRowsT) * host::cdiv(N, Z::kRowsN) <= kMaxThreads / Z::kThreads;
 }
 
 // The tiles address 256 rows of codes, all rows' scales of a step and five rows
@@ -109,11 +115,10 @@ bool skinny_applies(int64_t K, int64_t T) { return K > 0 && T <= kSkinnyMaxT; }
 
 template <int TB, int U, typename TY>
 int launch_skinny_blocks(const Args& p, TY* Y) {
-    host::clear_last_error();
-    product_skinny_kernel<TY, TB, U>
-        <<<dim3(uint32_t(host::cdiv(p.N, kSkinnyRows))), dim3(kSkinnyWaves * 64), 0, p.st>>>(
-            p.ac, p.as, p.bc, p.bs, Y, p.ldy, int(steps_of(p.K)), p.N, int(p.T));
-    return host::launch_status();
+    return in_block_ranges(host::cdiv(p.N, kSkinnyRows), [&](int64_t first, uint32_t blocks) {
+        product_skinny_kernel<TY, TB, U><<<dim3(blocks), dim3(kSkinnyWaves * 64), 0, p.st>>>(
+            p.ac, p.as, p.bc, p.bs, Y, p.ldy, int(steps_of(p.K)), p.N, int(p.T), uint32_t(first));
+    });
 }
 
 template <typename TY>
@@ -131,13 +136,12 @@ bool fuse_linear(int64_t K, int64_t T) {
 
 template <typename TX>
 int launch_linear_skinny(const Args& p, const TX* X, int64_t ldx, TX* Y) {
-    host::clear_last_error();
     const int64_t steps = steps_of(p.K);
-    linear_skinny_kernel<TX, 4>
-        <<<dim3(uint32_t(host::cdiv(p.N, kSkinnyRows))), dim3(kSkinnyWaves * 64),
-           size_t(p.T * steps * (kStepBytes + kStepScales)), p.st>>>(X, ldx, p.bc, p.bs, Y, p.ldy, int(p.K),
-                                                                     int(steps), p.N, int(p.T));
-    return host::launch_status();
+    return in_block_ranges(host::cdiv(p.N, kSkinnyRows), [&](int64_t first, uint32_t blocks) {
+        linear_skinny_kernel<TX, 4>
+            <<<dim3(blocks), dim3(kSkinnyWaves * 64), size_t(p.T * steps * (kStepBytes + kStepScales)), p.st>>>(
+                X, ldx, p.bc, p.bs, Y, p.ldy, int(p.K), int(steps), p.N, int(p.T), uint32_t(first));
+    });
 }
 
 int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
@@ -147,7 +151,6 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     // tiles; N = 14336, K = 4096: 10.8 against 9.2. T = 32: 13.8 against 15.6 and
     // 14.6 against 9.7.
     if (skinny_applies(K, T) && tiles(32, 64) < 128) return RETRO_MX_VARIANT_SKINNY;
-    if (!tiles_apply(size, ldy, K, N, T)) return skinny_applies(K, T) ? RETRO_MX_VARIANT_SKINNY : RETRO_MX_VARIANT_SIMPLE;
     // Time of a round of workgroups over the CUs, in us: a start and end and a time
     // for each 256 elements of K, with one workgroup a CU and with as many as fit.
     // Fitted to T x N x K = 4096 x 14336 x 4096, 4096 x 5120 x 4096, 8192^3, 17408 x
@@ -174,6 +177,7 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     int best = 0;
     double least = 0;
     for (const Cost& c : costs) {
+        if (!product_applies(c.variant, size, ldy, K, N, T)) continue;
         const int64_t n = tiles(c.rows_t, c.rows_n), round = int64_t(host::kNumCUs) * c.per_cu;
         const int64_t rest = host::cdiv(n % round, host::kNumCUs);
         const double one = c.one + c.one_step * steps, full = c.full + c.full_step * steps;
@@ -186,7 +190,7 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
             least = cost;
         }
     }
-    return best;
+    return best ? best : skinny_applies(K, T) ? RETRO_MX_VARIANT_SKINNY : RETRO_MX_VARIANT_SIMPLE;
 }
 
 }  // namespace
@@ -195,13 +199,13 @@ bool product_applies(int variant, int size, int64_t ldy, int64_t K, int64_t N, i
     switch (variant) {
         case RETRO_MX_VARIANT_AUTO:
         case RETRO_MX_VARIANT_SIMPLE: return true;
-        case RETRO_MX_VARIANT_TILE_256x256:
-        case RETRO_MX_VARIANT_TILE_256x192:
-        case RETRO_MX_VARIANT_TILE_64x128:
-        case RETRO_MX_VARIANT_TILE_128x128:
-        case RETRO_MX_VARIANT_TILE_64x64:
-        case RETRO_MX_VARIANT_TILE_64x64_K4:
-        case RETRO_MX_VARIANT_TILE_32x64_K4: return tiles_apply(size, ldy, K, N, T);
+        case RETRO_MX_VARIANT_TILE_256x256: return tiles_apply(size, ldy, K, N, T) && one_launch<Tile256x256>(N, T);
+        case RETRO_MX_VARIANT_TILE_256x192: return tiles_apply(size, ldy, K, N, T) && one_launch<Tile256x192>(N, T);
+        case RETRO_MX_VARIANT_TILE_64x128: return tiles_apply(size, ldy, K, N, T) && one_launch<Tile64x128>(N, T);
+        case RETRO_MX_VARIANT_TILE_128x128: return tiles_apply(size, ldy, K, N, T) && one_launch<Tile128x128>(N, T);
+        case RETRO_MX_VARIANT_TILE_64x64: return tiles_apply(size, ldy, K, N, T) && one_launch<Tile64x64>(N, T);
+        case RETRO_MX_VARIANT_TILE_64x64_K4: return tiles_apply(size, ldy, K, N, T) && one_launch<Tile64x64K4>(N, T);
+        case RETRO_MX_VARIANT_TILE_32x64_K4: return tiles_apply(size, ldy, K, N, T) && one_launch<Tile32x64K4>(N, T);
         case RETRO_MX_VARIANT_SKINNY: return skinny_applies(K, T);
         default: return false;
     }
@@ -237,15 +241,19 @@ using namespace retro::mx;
 
 namespace {
 
-// The shape and operand checks of both products. The grid of 32 x 32 tiles
-// bounds T * N.
+// Sizes that both products take: fewer than 2^30 tiles of 32 x 32 in Y.
+bool product_dims(int64_t K, int64_t N, int64_t T) {
+    return dim_ok(K) && dim_ok(N) && dim_ok(T) && host::cdiv(N, 32) * host::cdiv(T, 32) < host::kGridLimit;
+}
+
+// The shape and operand checks of both products.
 int check_product(int ytype, const void* bc, const void* bs, const void* Y, int64_t ldy, int64_t K, int64_t N,
                   int64_t T, int64_t& y_bytes) {
     const int size = float_bytes(ytype);
     if (!size) return RETRO_E_TYPE;
-    if (!dim_ok(K) || !dim_ok(N) || !dim_ok(T)) return RETRO_E_SHAPE;
+    if (!product_dims(K, N, T)) return RETRO_E_SHAPE;
     y_bytes = span_bytes(T, N, ldy, size);
-    if (y_bytes < 0 || host::cdiv(N, 32) * host::cdiv(T, 32) >= host::kGridLimit) return RETRO_E_SHAPE;
+    if (y_bytes < 0) return RETRO_E_SHAPE;
     if (N == 0 || T == 0) return RETRO_OK;
     if (!Y || (K && (!bc || !bs))) return RETRO_E_NULL;
     if (!aligned(bc, 16) || !aligned(bs, 16) || !aligned(Y, size)) return RETRO_E_ALIGN;
@@ -272,7 +280,7 @@ int retro_mx_mul_mat(int ytype, const void* a_codes, const void* a_scales, const
 int retro_mx_mul_mat_choice(int ytype, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     const int size = float_bytes(ytype);
     if (!size) return RETRO_E_TYPE;
-    if (!dim_ok(K) || !dim_ok(N) || !dim_ok(T) || span_bytes(T, N, ldy, size) < 0) return RETRO_E_SHAPE;
+    if (!product_dims(K, N, T) || span_bytes(T, N, ldy, size) < 0) return RETRO_E_SHAPE;
     return choose(size, ldy, K, N, T);
 }
 
@@ -292,7 +300,7 @@ int retro_mx_mul_mat_variant(int variant, int ytype, const void* a_codes, const 
 
 int64_t retro_mx_linear_workspace_size(int xtype, int64_t K, int64_t N, int64_t T) {
     if (!float_bytes(xtype)) return RETRO_E_TYPE;
-    if (!dim_ok(K) || !dim_ok(N) || !dim_ok(T)) return RETRO_E_SHAPE;
+    if (!product_dims(K, N, T)) return RETRO_E_SHAPE;
     return N == 0 || fuse_linear(K, T) ? 0 : linear_workspace(K, T);
 }
 

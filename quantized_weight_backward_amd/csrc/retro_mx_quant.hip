@@ -141,7 +141,7 @@ __device__ __forceinline__ uint32_t across4(const Columns<TX>& c, uint32_t scale
 // 15.6 us (5.8 TB/s), both 21.7 us (5.0 TB/s; two readings take 34).
 template <typename TX, bool ROWS>
 __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
-    const TX* __restrict__ X, int64_t ldx, int64_t rows, uint32_t cols, uint32_t groups, int64_t tile0,
+    const TX* __restrict__ X, int64_t ldx, int64_t rows, uint32_t cols, uint32_t groups, int64_t tile0, uint32_t col0,
     uint32_t row_steps, uint32_t col_steps, uint8_t* __restrict__ row_codes, uint8_t* __restrict__ row_scales,
     uint8_t* __restrict__ col_codes, uint8_t* __restrict__ col_scales) {
     __shared__ __align__(16) uint8_t by_col[kTileCols * kColPitch];
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 4) void quantize_tile_kernel(
     __shared__ __align__(16) uint32_t by_row[ROWS ? kTileRows / 4 * 64 : 4];  // four rows' bytes a word
     __shared__ __align__(16) uint8_t row_e[ROWS ? kTileRows * 4 : 16];
     const int64_t tile = tile0 + blockIdx.x / groups;  // of 256 rows
-    const uint32_t c0 = (blockIdx.x % groups) * kTileCols;
+    const uint32_t c0 = col0 + (blockIdx.x % groups) * kTileCols;
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const int64_t r0 = tile * kTileRows + wave * 32;
     const uint32_t c = c0 + 2 * lane;
@@ -430,16 +430,18 @@ template <bool ROWS, typename TX>
 int launch_tiles(const TX* X, int64_t ldx, int64_t rows, int64_t cols, uint8_t* row_codes, uint8_t* row_scales,
                  uint8_t* col_codes, uint8_t* col_scales, hipStream_t st) {
     // with rows wanted the columns' padding is written too
-    const int64_t tiles = steps_of(rows), groups = ROWS ? steps_of(cols) * 2 : host::cdiv(cols, kTileCols);
-    const int64_t most = std::max<int64_t>(1, kMaxBlocks / groups);
-    for (int64_t b = 0; b < tiles; b += most) {
-        const int64_t n = std::min(most, tiles - b);
-        host::clear_last_error();
-        quantize_tile_kernel<TX, ROWS><<<dim3(uint32_t(n * groups)), dim3(kTileWaves * 64), 0, st>>>(
-            X, ldx, rows, uint32_t(cols), uint32_t(groups), b, uint32_t(steps_of(cols)), uint32_t(tiles), row_codes,
-            row_scales, col_codes, col_scales);
-        const int rc = host::launch_status();
-        if (rc != RETRO_OK) return rc;
+    const int64_t tiles = steps_of(rows), all = ROWS ? steps_of(cols) * 2 : host::cdiv(cols, kTileCols);
+    for (int64_t g = 0; g < all; g += kMaxBlocks) {
+        const int64_t groups = std::min(all - g, kMaxBlocks), most = kMaxBlocks / groups;
+        for (int64_t b = 0; b < tiles; b += most) {
+            const int64_t n = std::min(most, tiles - b);
+            host::clear_last_error();
+            quantize_tile_kernel<TX, ROWS><<<dim3(uint32_t(n * groups)), dim3(kTileWaves * 64), 0, st>>>(
+                X, ldx, rows, uint32_t(cols), uint32_t(groups), b, uint32_t(g * kTileCols), uint32_t(steps_of(cols)),
+                uint32_t(tiles), row_codes, row_scales, col_codes, col_scales);
+            const int rc = host::launch_status();
+            if (rc != RETRO_OK) return rc;
+        }
     }
     return RETRO_OK;
 }

@@ -33,15 +33,17 @@ __device__ __forceinline__ void load_rows(StepRows& s, const uint8_t* codes, con
 // 16 rows of B times up to 16 TB rows of A, the steps of K dealt to the waves in
 // turn (U at a time, so that 2 U loads of B a lane are in flight); the waves'
 // sums are added in LDS in the order of the waves. The reading of B bounds it:
-// T = 16, N = 4096, K = 14336 in 10.0 us, 3.1 TB/s with the launch.
+// T = 16, N = 4096, K = 14336 in 10.0 us, 3.1 TB/s with the launch. `first` is the
+// launch's first workgroup of all.
 template <typename TY, int TB, int U>
 __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void product_skinny_kernel(
     const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as, const uint8_t* __restrict__ bc,
-    const uint8_t* __restrict__ bs, TY* __restrict__ Y, int64_t ldy, int steps, int64_t N, int T) {
+    const uint8_t* __restrict__ bs, TY* __restrict__ Y, int64_t ldy, int steps, int64_t N, int T,
+    uint32_t first) {
     __shared__ float part[kSkinnyWaves][TB * 16][kSkinnyRows + 4];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int r = lane & 15, q = lane >> 4;
-    const int64_t n0 = int64_t(blockIdx.x) * kSkinnyRows, n = min(n0 + r, N - 1);
+    const int64_t n0 = int64_t(first + blockIdx.x) * kSkinnyRows, n = min(n0 + r, N - 1);
     const uint8_t* b_row = bc + n * steps * kStepBytes;
     const uint8_t* a_row[TB];
     int t[TB];
@@ -93,13 +95,13 @@ __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void product_skinny_kernel(
 template <typename TX, int U>
 __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void linear_skinny_kernel(
     const TX* __restrict__ X, int64_t ldx, const uint8_t* __restrict__ bc, const uint8_t* __restrict__ bs,
-    TX* __restrict__ Y, int64_t ldy, int K, int steps, int64_t N, int T) {
+    TX* __restrict__ Y, int64_t ldy, int K, int steps, int64_t N, int T, uint32_t first) {
     __shared__ float part[kSkinnyWaves][16][kSkinnyRows + 4];
     extern __shared__ __align__(16) uint8_t x_codes[];  // T x steps x 128, then the scales, T x steps x 8
     uint8_t* x_scales = x_codes + T * steps * kStepBytes;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int r = lane & 15, q = lane >> 4;
-    const int64_t n0 = int64_t(blockIdx.x) * kSkinnyRows, n = min(n0 + r, N - 1);
+    const int64_t n0 = int64_t(first + blockIdx.x) * kSkinnyRows, n = min(n0 + r, N - 1);
     const uint8_t* b_row = bc + n * steps * kStepBytes;
     StepRows b[U];
     auto load_b = [&](int s0) {

@@ -384,3 +384,74 @@ def test_a_matrix_follows_its_arrays(q):
     codes.data = codes.data.cpu()
     with pytest.raises(ValueError):
         q.mx_linear(x, m)
+
+
+def room(gigabytes):
+    """Skips where other tenants of the card leave less."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes * 1e9:
+        pytest.skip(f"needs {gigabytes} GB of device memory")
+
+
+def test_more_rows_of_b_than_one_launch_takes(q):
+    """2^27 + 37 rows of B are 2^23 + 3 workgroups of 512 threads: the linear
+    call's own kernel and the skinny product take them in several launches."""
+    room(40)
+    N, K = (1 << 27) + 37, 40
+    b = ref.random_planes(gen(2), 96, K)
+    codes = torch.zeros((N, 128), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((1, N, 8), dtype=torch.uint8, device="cuda")
+    starts = [0, (1 << 26) - 48, N - 96]  # the ends of the launches among them
+    for at in starts:
+        codes[at:at + 96] = b[0].cuda()
+        scales[:, at:at + 96] = b[1].cuda()
+    B = q.MXMatrix(codes, scales, K)
+    x = values(2, K, torch.bfloat16, 3)
+    A = ref.quantized(x)
+    want, bound = A @ b[2].T, ref.product_bound(A, b[2], K, ref.OUT_ULP[torch.bfloat16])
+    for y in (q.mx_linear(x.cuda(), B), q.mx_mul_mat(q.mx_quantize(x.cuda()), B, torch.bfloat16,
+                                                      variant=q.mx.MX_VARIANT_SKINNY)):
+        for at in starts:
+            assert ((y[:, at:at + 96].cpu().double() - want).abs() <= bound).all(), at
+        assert not y[:, 200:1 << 20].any()  # the zero rows between
+
+
+def test_more_tiles_than_one_launch_takes(q):
+    """2^26 + 2^13 tiles of a wave each in the simple kernel, Y of 137 GB."""
+    room(150)
+    T, N, K = (1 << 18) + 32, 1 << 18, 40
+    a, b = ref.random_planes(gen(1), 96, K), ref.random_planes(gen(2), 96, K)
+
+    def matrix(planes, rows):
+        codes = torch.zeros((rows, 128), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros((1, rows, 8), dtype=torch.uint8, device="cuda")
+        codes[:96], codes[-96:] = planes[0].cuda(), planes[0].cuda()
+        scales[:, :96], scales[:, -96:] = planes[1].cuda(), planes[1].cuda()
+        return q.MXMatrix(codes, scales, K)
+
+    y = q.mx_mul_mat(matrix(a, T), matrix(b, N), torch.bfloat16, variant=q.mx.MX_VARIANT_SIMPLE)
+    want, bound = a[2] @ b[2].T, ref.product_bound(a[2], b[2], K, ref.OUT_ULP[torch.bfloat16])
+    for t in (0, T - 96):
+        for n in (0, N - 96):
+            assert ((y[t:t + 96, n:n + 96].cpu().double() - want).abs() <= bound).all(), (t, n)
+    assert not y[T // 2:T // 2 + 64].any()
+    del y
+    torch.cuda.empty_cache()
+
+
+def test_more_columns_than_one_launch_takes(q):
+    """The columns of a 2 x (2^30 + 300) tensor: 2^23 + 3 workgroups of 512
+    threads, codes of 137 GB."""
+    room(165)
+    cols = (1 << 30) + 300
+    x = torch.zeros((2, cols), dtype=torch.bfloat16, device="cuda")
+    tail = values(2, 600, torch.bfloat16, 5)  # both sides of a launches' border
+    x[:, -600:] = tail.cuda()
+    x[:, :600] = tail.cuda()
+    m = q.mx_quantize(x, axis=0)
+    for at in (0, cols - 600):
+        part = q.MXMatrix(m.codes[at:at + 600].contiguous(), m.scales[:, at:at + 600].contiguous(), 2)
+        check_planes(part, *ref.mx_encode(tail.T), 2, at)
+    assert not m.codes[1 << 20:1 << 21].any()
+    del x, m
+    torch.cuda.empty_cache()

@@ -154,3 +154,21 @@ def test_the_binding_refuses_host_tensors_and_wrong_arguments():
                  lambda: q.mx_linear_backward(x, x, x), lambda: q.mx_moe(x, x, x, x, 1)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_sizes_past_one_launch():
+    """A launch takes fewer than 2^32 threads: tiles that need more are refused
+    or passed over, and all calls agree on the sizes they take."""
+    T, N = 1 << 19, 1 << 20  # 2^23 workgroups of 512 threads and 256 x 256 outputs
+    args = (q.F32, addr(1), addr(2), addr(3), addr(4), addr(5), N, 256, N, T, None)
+    for variant, name in q.MX_VARIANT_NAMES.items():
+        if name.startswith("tile"):
+            assert q.lib.retro_mx_mul_mat_variant(variant, *args) == q.E_VARIANT, name
+    assert q.MX_VARIANT_NAMES[q.mx_mul_mat_choice(256, N, T)] == "simple"
+    assert q.MX_VARIANT_NAMES[q.mx_mul_mat_choice(256, (1 << 31) - 1, 32)] == "skinny"
+    assert q.MX_VARIANT_NAMES[q.mx_mul_mat_choice(256, N // 2, T)].startswith("tile")
+    most = (1 << 31) - 1
+    assert product(T=most, N=most, ldy=most) == q.E_SHAPE
+    assert linear(T=most, N=most, ldy=most) == q.E_SHAPE
+    assert q.lib.retro_mx_mul_mat_choice(q.F32, most, 300, most, most) == q.E_SHAPE
+    assert q.lib.retro_mx_linear_workspace_size(q.F32, 300, most, most) == q.E_SHAPE
