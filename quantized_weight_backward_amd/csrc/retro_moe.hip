@@ -383,16 +383,14 @@ __device__ __forceinline__ void in_pairs(int first, int end, int by, Load&& load
 
 constexpr int kGateWaves = 4;
 
-// Features of one chosen expert in slabs of 16: their rows of gate and of up times
-// x of a tile of its tokens. `ks` (1, 2 or 4) waves share a slab, each a part of D;
-// their sums are added in LDS in their order. A wave loads a step while it works
-// on the one before.
+// 16 features of one chosen expert: their rows of gate and of up times x of a tile
+// of its tokens. D's steps are dealt to the waves in turn, whose sums are added in
+// LDS in their order. A wave loads a step while it works on the one before.
 //
 // For a token or a few (OWN_LISTS) every workgroup chooses the experts itself,
 // which takes it about a microsecond where a launch of its own takes several.
 template <int PX, int PH, bool OWN_LISTS>
-__global__ __launch_bounds__(kGateWaves * 64, PX == 1 ? 3 : 2) void moe_gate_up_kernel(Layer L, int ks,
-                                                                                       int renormalize) {
+__global__ __launch_bounds__(kGateWaves * 64, PX == 1 ? 3 : 2) void moe_gate_up_kernel(Layer L, int renormalize) {
     __shared__ float part[kGateWaves][2][16][17];
     const int* entry = L.lists + 1 + blockIdx.y * 3;
     const int16_t* order = L.order;
@@ -410,9 +408,9 @@ __global__ __launch_bounds__(kGateWaves * 64, PX == 1 ? 3 : 2) void moe_gate_up_
     }
     const int e = entry[0], first = entry[1], n = entry[2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-    const int r = lane & 15, g = lane >> 4, slabs = kGateWaves / ks;
+    const int r = lane & 15, g = lane >> 4;
     const int64_t rows = int64_t(L.E) * 2 * L.F, Dp = L.steps_d * kStep, Fp = L.steps_f * kStep;
-    const int64_t g0 = int64_t(blockIdx.x) * slabs * 16, f0 = g0 + wave / ks * 16;
+    const int64_t f0 = int64_t(blockIdx.x) * 16;
     const int64_t row = int64_t(e) * 2 * L.F + min(f0 + r, L.F - 1);  // of gate; F further on of up
     // past F only the zeros that pad h are written
     const int steps = f0 < L.F ? int(L.steps_d) : 0;
@@ -449,27 +447,27 @@ __global__ __launch_bounds__(kGateWaves * 64, PX == 1 ? 3 : 2) void moe_gate_up_
                         acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o[i], l.v[b][p][i], acc[m], 0, 0, 0);
             }
     };
-    in_pairs<Loaded>(wave % ks, steps, ks, load, use);
+    in_pairs<Loaded>(wave, steps, kGateWaves, load, use);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) part[wave][m][4 * g + i][r] = acc[m][i];
     __syncthreads();
-    for (int o = threadIdx.x; o < slabs * 256; o += kGateWaves * 64) {
-        const int ff = o % (slabs * 16), c = o / (slabs * 16);
-        if (c >= n || g0 + ff >= Fp) continue;
-        float gate = 0.f, up = 0.f;
-        for (int w = 0; w < ks; ++w) {
-            gate += part[ff / 16 * ks + w][0][ff % 16][c];
-            up += part[ff / 16 * ks + w][1][ff % 16][c];
-        }
-        const int pr = order[first + c];
-        const float h = g0 + ff < L.F ? gate / (1.f + expf(-gate)) * up * share[pr] : 0.f;
-        __bf16 cutp[PH];
-        cut<PH>(h, cutp);
+    static_assert(kGateWaves * 64 == 16 * 16, "an output a thread");
+    const int f = threadIdx.x % 16, c = threadIdx.x / 16;
+    if (c >= n) return;
+    float gate = 0.f, up = 0.f;
 #pragma unroll
-        for (int p = 0; p < PH; ++p) L.hp[(int64_t(p) * L.T * L.k + pr) * Fp + g0 + ff] = cutp[p];
+    for (int w = 0; w < kGateWaves; ++w) {
+        gate += part[w][0][f][c];
+        up += part[w][1][f][c];
     }
+    const int pr = order[first + c];
+    const float h = f0 + f < L.F ? gate / (1.f + expf(-gate)) * up * share[pr] : 0.f;
+    __bf16 cutp[PH];
+    cut<PH>(h, cutp);
+#pragma unroll
+    for (int p = 0; p < PH; ++p) L.hp[(int64_t(p) * L.T * L.k + pr) * Fp + f0 + f] = cutp[p];
 }
 
 // 16 (or 4) bytes a lane from offset at + `more` (uniform) of the `bytes` at p into
@@ -957,8 +955,7 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
     // 64 features a workgroup through the ring where that makes one a CU (1 token, 2
     // of 8 experts, D = 4096, F = 8192, 256 of them: 44 us against 46 for the layer; F =
     // 14336: 50 against 55; F = 4096, 128: 30 against 25; 32 tokens, F = 14336: 177
-    // against 208, with 128 features 182). Else workgroups enough for four a CU,
-    // several waves sharing a slab where there are few.
+    // against 208, with 128 features 182). Else 16, four times as many workgroups.
     const int64_t ring_slabs = L.steps_f * (kStep / (16 * kRingWavesUp));
     if (ring_slabs * tiles >= host::kNumCUs) {
         auto gate_up = [&](void (*kernel)(Layer, int)) {
@@ -966,12 +963,8 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
         };
         own_lists ? gate_up(moe_gate_up_ring_kernel<PX, PH, true>) : gate_up(moe_gate_up_ring_kernel<PX, PH, false>);
     } else {
-        const int64_t slabs = L.steps_f * (kStep / 16);
-        int ks = 1;
-        while (ks < kGateWaves && host::cdiv(slabs * ks, kGateWaves) * tiles < 4 * host::kNumCUs) ks *= 2;
-        auto gate_up = [&](void (*kernel)(Layer, int, int)) {
-            kernel<<<dim3(uint32_t(host::cdiv(slabs * ks, kGateWaves)), tiles), dim3(kGateWaves * 64), 0, st>>>(
-                L, ks, renormalize);
+        auto gate_up = [&](void (*kernel)(Layer, int)) {
+            kernel<<<dim3(uint32_t(L.steps_f * (kStep / 16)), tiles), dim3(kGateWaves * 64), 0, st>>>(L, renormalize);
         };
         own_lists ? gate_up(moe_gate_up_kernel<PX, PH, true>) : gate_up(moe_gate_up_kernel<PX, PH, false>);
     }
