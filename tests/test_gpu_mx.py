@@ -455,3 +455,51 @@ def test_more_columns_than_one_launch_takes(q):
     assert not m.codes[1 << 20:1 << 21].any()
     del x, m
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("TNK", PRODUCTS, ids=str)
+def test_which_kernels_take_a_product(q, TNK):
+    """Every tile and the simple kernel take all of these, the skinny one up to 32 rows."""
+    T, N, K = TNK
+    a, b = ref.random_planes(gen(T), T, K), ref.random_planes(gen(N + 1), N, K)
+    A, B = q.MXMatrix(a[0].cuda(), a[1].cuda(), K), q.MXMatrix(b[0].cuda(), b[1].cuda(), K)
+    for variant, name in q.MX_VARIANT_NAMES.items():
+        if name == "skinny" and T > 32:
+            with pytest.raises(q.RetroError) as refused:
+                q.mx_mul_mat(A, B, variant=variant)
+            assert refused.value.code == q.E_VARIANT
+        else:
+            assert q.mx_mul_mat(A, B, variant=variant).shape == (T, N), name
+
+
+# Several tile rows and columns of every size, with remainders; 12, 9 and 2 steps
+# of K, whole and ragged; no row like another.
+MANY_TILES = [(1100, 1300, 2900), (700, 2100, 2304), (1537, 450, 300)]
+TILED = ["simple", "tile_256x256", "tile_256x192", "tile_128x128", "tile_64x128", "tile_64x64", "tile_64x64_k4",
+         "tile_32x64_k4"]
+
+
+@pytest.mark.parametrize("kernel", TILED)
+@pytest.mark.parametrize("TNK", MANY_TILES, ids=str)
+def test_products_of_many_tiles(q, TNK, kernel):
+    T, N, K = TNK
+    a, b = ref.random_planes(gen(T), T, K), ref.random_planes(gen(N + 1), N, K)
+    A, B = q.MXMatrix(a[0].cuda(), a[1].cuda(), K), q.MXMatrix(b[0].cuda(), b[1].cuda(), K)
+    want, size = a[2] @ b[2].T, a[2].abs() @ b[2].abs().T
+    variant = next(v for v, name in q.MX_VARIANT_NAMES.items() if name == kernel)
+    for dtype in FLOATS:
+        out = torch.full((T, N + 5), float("nan"), dtype=dtype, device="cuda")
+        y = q.mx_mul_mat(A, B, dtype, out=out[:, :N], variant=variant)
+        assert out[:, N:].isnan().all()
+        bound = -(-K // 64) * 2.0 ** -22 * size + ref.OUT_ULP[dtype] * want.abs() + 2.0 ** -149
+        assert ((y.cpu().double() - want).abs() <= bound).all(), dtype
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 1500, 2900), (16, 700, 4100), (17, 1100, 2304), (32, 533, 5000)])
+def test_skinny_products_of_many_steps(q, T, N, K):
+    a, b = ref.random_planes(gen(T), T, K), ref.random_planes(gen(N + 1), N, K)
+    A, B = q.MXMatrix(a[0].cuda(), a[1].cuda(), K), q.MXMatrix(b[0].cuda(), b[1].cuda(), K)
+    for dtype in FLOATS:
+        y = q.mx_mul_mat(A, B, dtype, variant=q.mx.MX_VARIANT_SKINNY)
+        bound = ref.product_bound(a[2], b[2], K, ref.OUT_ULP[dtype])
+        assert ((y.cpu().double() - a[2] @ b[2].T).abs() <= bound).all(), dtype

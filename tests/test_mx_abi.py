@@ -172,3 +172,14 @@ def test_sizes_past_one_launch():
     assert linear(T=most, N=most, ldy=most) == q.E_SHAPE
     assert q.lib.retro_mx_mul_mat_choice(q.F32, most, 300, most, most) == q.E_SHAPE
     assert q.lib.retro_mx_linear_workspace_size(q.F32, 300, most, most) == q.E_SHAPE
+
+
+@pytest.mark.parametrize("dtype,T,N,K,name", [
+    (torch.bfloat16, 4096, 14336, 4096, "tile_256x256"), (torch.float32, 8192, 8192, 8192, "tile_256x256"),
+    (torch.bfloat16, 2048, 5120, 17408, "tile_256x192"), (torch.float32, 17408, 5120, 2048, "tile_128x128"),
+    (torch.bfloat16, 512, 14336, 4096, "tile_128x128"), (torch.bfloat16, 1024, 4096, 4096, "tile_64x128"),
+    (torch.bfloat16, 512, 4096, 4096, "tile_64x64"), (torch.bfloat16, 256, 4096, 14336, "tile_64x64_k4"),
+    (torch.float16, 333, 1000, 1500, "tile_32x64_k4"), (torch.bfloat16, 32, 14336, 4096, "tile_32x64_k4"),
+    (torch.bfloat16, 16, 4096, 14336, "skinny"), (torch.bfloat16, 64, 4096, 1 << 30, "simple")])
+def test_kernels_chosen(dtype, T, N, K, name):
+    assert q.MX_VARIANT_NAMES[q.mx_mul_mat_choice(K, N, T, dtype)] == name
