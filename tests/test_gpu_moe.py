@@ -188,3 +188,22 @@ def test_a_captured_layer_replays_like_eager_calls(q):
         torch.cuda.synchronize()
         got = y.clone()
         assert torch.equal(got, q.mx_moe(x, *args)), i
+
+
+# Batches whose router takes four tokens a wave (more than 2048 logits): whole
+# 512-element steps and a ragged end, all tokens and a last few.
+ROUTED = [(33, 1032, 64, 128, 4), (64, 2048, 40, 64, 8), (62, 520, 33, 40, 3), (43, 1537, 48, 64, 2)]
+
+
+@pytest.mark.parametrize("router_of_x", [False, True])
+@pytest.mark.parametrize("case", ROUTED, ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=NAME.get)
+def test_router_of_many_tokens(q, dtype, case, router_of_x):
+    T, D, F, E, k = case
+    x, router, gu, dn = layer(T, D, F, E, dtype, T + D, router_dtype=dtype if router_of_x else torch.float32)
+    planes = on_gpu(q, gu, D), on_gpu(q, dn, F)
+    want = ref.moe(x, router, gu[2], dn[2], k, True)
+    check(q.mx_moe(x.cuda(), router.cuda(), *planes, k), *want, dtype)
+    wide = torch.full((T, D + 3), float("nan"), dtype=dtype, device="cuda")  # rows off the 16-byte boundaries
+    wide[:, 1:1 + D] = x.cuda()
+    check(q.mx_moe(wide[:, 1:1 + D], router.cuda(), *planes, k), *want, dtype)
