@@ -41,7 +41,11 @@ def _elsewhere(t, stream) -> bool:
 def _on(t, stream):
     """t's device, and `stream` or its current stream, as torch's current ones:
     what a call allocates belongs to the stream that it runs on."""
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(t.device)
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError("stream must be of the operands' device")
+    return torch.cuda.stream(stream)
 
 
 # the current device, and its current stream's handle

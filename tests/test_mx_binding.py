@@ -1,6 +1,8 @@
 """What the binding of the microscaled operators passes to the library, with a
 recorder in the library's place: needs no GPU."""
 
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -80,3 +82,12 @@ def test_a_view_of_a_made_matrix_is_the_caller_s_own(recorder):
     c.data, s.data = planes(5, 320)
     q.mx_dequantize(m)
     assert recorder.calls[-1][1][1:3] == at == (m.codes.data_ptr(), m.scales.data_ptr())
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Under such a stream the call would go back to the operands' device and
+    run on that device's current stream instead."""
+    monkeypatch.setattr(mx, "_device_tensor", lambda t, name: t)
+    W = torch.zeros(5 * q.row_bytes(q.MXFP4, 320), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="stream"):
+        q.mx_from_blocks(W, 320, 5, stream=SimpleNamespace(device=torch.device("cuda", 1)))
