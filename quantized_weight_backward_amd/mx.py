@@ -280,7 +280,10 @@ def mx_from_blocks(W, K: int, N: int, stream=None) -> MXMatrix:
 
 def mx_mul_mat_choice(K: int, N: int, T: int, dtype=torch.float32) -> int:
     """The kernel mx_mul_mat runs for a contiguous T x N result (a key of MX_VARIANT_NAMES)."""
-    return int(lib.retro_mx_mul_mat_choice(_FLOAT[dtype], int(N), int(K), int(N), int(T)))
+    ytype = _FLOAT.get(dtype)
+    if ytype is None:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    return int(lib.retro_mx_mul_mat_choice(ytype, int(N), int(K), int(N), int(T)))
 
 
 def mx_mul_mat(a: MXMatrix, b: MXMatrix, dtype=torch.float32, out=None, variant: int = MX_VARIANT_AUTO, stream=None):

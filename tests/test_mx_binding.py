@@ -91,3 +91,11 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     W = torch.zeros(5 * q.row_bytes(q.MXFP4, 320), dtype=torch.uint8)
     with pytest.raises(ValueError, match="stream"):
         q.mx_from_blocks(W, 320, 5, stream=SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+def test_a_result_of_another_type_is_refused(recorder):
+    m = q.MXMatrix(*planes(5, 300), 300)
+    for call in (lambda: q.mx_mul_mat_choice(300, 5, 5, torch.float64), lambda: q.mx_mul_mat(m, m, torch.float64),
+                 lambda: q.mx_dequantize(m, torch.int32)):
+        with pytest.raises(ValueError, match="dtype"):
+            call()
