@@ -13,9 +13,11 @@
  * e2m1(q) * 2^(e - 127). Quantising a block with largest magnitude amax:
  *     e    = clamp(floor(log2(amax)) - 2 + 127, 0, 254), 0 when amax = 0
  *     q[i] = x[i] * 2^(127 - e) rounded to the nearest E2M1 value, a tie to
- *            the even code, magnitudes above 6 to 6
- * A block that holds an infinity or a NaN gets e = 255: all of it is NaN.
- * These are exact statements: every call below returns those bytes.
+ *            the even code, magnitudes above 6 to 6; the sign bit is x[i]'s, also
+ *            of what rounds to zero
+ * A block that holds an infinity or a NaN gets e = 255: all of it is NaN, and its
+ * codes are unspecified. These are exact statements: every call below returns
+ * those bytes.
  *
  * A microscaled matrix of `rows` x K is two arrays, with C = ceil(K / 256):
  *   codes   rows x C x 128 bytes: element 2i of a row in the low nibble of its
@@ -55,9 +57,10 @@ int64_t retro_mx_scale_bytes(int64_t rows, int64_t K);
  * the blocks of X[n][0..K). type RETRO_MXFP4 (the rule above, K % 32 == 0) or
  * RETRO_NVFP4 (K % 64 == 0): per 16 elements the E4M3 scale S nearest to
  * amax / 6 (ties to even, at most 448) and each x[i] / S rounded to the nearest
- * E2M1 value (ties to the even code, at most 6); S = 0 gives zero codes; an
- * infinity or a NaN gives S = NaN. The inverse of retro_dequantize up to the
- * rounding. xtype is X's type, ldx its row stride in elements.
+ * E2M1 value (ties to the even code, at most 6, the sign bit x[i]'s); S = 0 gives
+ * zeros with x's signs; an infinity or a NaN gives S = NaN (byte 0x7f) and
+ * unspecified codes. The inverse of retro_dequantize up to the rounding. xtype is
+ * X's type, ldx its row stride in elements.
  */
 int retro_quantize(int type, int xtype, const void *X, int64_t ldx, void *W, int64_t K, int64_t N, void *stream);
 
@@ -82,9 +85,13 @@ int retro_mx_from_blocks(const void *W, void *codes, void *scales, int64_t K, in
 
 /*
  * Y[t][n] = sum_k A[t][k] B[n][k] for t < T, n < N: A a T x K and B an N x K
- * microscaled matrix, Y of ytype with rows ldy elements apart. The products of
- * a block pair are exact; the sum over blocks is taken in F32 and rounded to
- * ytype once. K == 0 writes zeros.
+ * microscaled matrix, Y of ytype with rows ldy elements apart. The sum of a block
+ * pair's products is exact; the sum over blocks is taken in F32 and rounded to
+ * ytype (to nearest) once. The matrix cores add two or four blocks' sums to an F32
+ * accumulator at a time, not always to the nearest F32 (1 + 1.5 * 2^-24 gives 1
+ * or 1 + 2^-23, by which of the two came first): before the rounding to ytype
+ * the error is at most ceil(K / 64) * 2^-22 * sum_k |A[t][k] B[n][k]| (or 2^-149).
+ * K == 0 writes zeros.
  */
 int retro_mx_mul_mat(int ytype, const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales,
                      void *Y, int64_t ldy, int64_t K, int64_t N, int64_t T, void *stream);
@@ -147,11 +154,12 @@ int64_t retro_mx_linear_workspace_size(int xtype, int64_t K, int64_t N, int64_t 
  * x and y are T x D of xtype with rows ldx and ldy elements apart; R is E x D of
  * rtype (RETRO_F32 or xtype) with contiguous rows ldr elements apart; gate_up is
  * a microscaled matrix of E * 2F rows x D (an expert's F gate rows, then its F
- * up rows), down one of E * D rows x F. x and h enter the products unrounded to
- * fewer bits than their type needs (bf16 parts: one for a BF16 x, two for F16,
- * three for F32 and h likewise, at least two), the sums are F32. Not-a-number
- * logits sort below every number.
- * 1 <= top_k <= min(E, RETRO_MOE_MAX_TOP_K), E <= RETRO_MOE_MAX_E, D and F >= 1
+ * up rows), down one of E * D rows x F. x enters the products as it is, in bf16
+ * parts that add up to it. h, computed in F32 and times its p, is rounded to two
+ * bf16 parts (16 bits) for BF16 and F16, whose own rounding to 8 and 11 bits y
+ * takes at the end, and to three (24 bits) for F32. The sums are F32.
+ * Not-a-number logits sort below every number.
+ * 1 <= top_k <= min(E, RETRO_MOE_MAX_TOP_K), E <= RETRO_MOE_MAX_E, 1 <= D, F < 2^22
  * (RETRO_E_SHAPE otherwise). workspace: retro_moe_workspace_size bytes, 16-byte
  * aligned, overlapping no operand (RETRO_E_WORKSPACE otherwise); it needs no
  * initial value and holds nothing between calls.

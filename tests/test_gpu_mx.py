@@ -503,3 +503,27 @@ def test_skinny_products_of_many_steps(q, T, N, K):
         y = q.mx_mul_mat(A, B, dtype, variant=q.mx.MX_VARIANT_SKINNY)
         bound = ref.product_bound(a[2], b[2], K, ref.OUT_ULP[dtype])
         assert ((y.cpu().double() - a[2] @ b[2].T).abs() <= bound).all(), dtype
+
+
+@pytest.mark.parametrize("kernel", TILED + ["skinny"])
+def test_sums_keep_what_f32_holds(q, kernel):
+    """1 + 2^-j from two blocks is exact up to F32's last place, whichever comes
+    first and whether or not one instruction takes both; beyond it the result is
+    one of the two neighbours."""
+    K, last = 512, list(range(16, 28))
+    variant = next(v for v, name in q.MX_VARIANT_NAMES.items() if name == kernel)
+
+    def matrix(rows):  # each row's list of (block, scale byte): the value 1 times the scale at its first element
+        codes, scales = torch.zeros((len(rows), 256), dtype=torch.uint8), torch.full((2, len(rows), 8), 127,
+                                                                                   dtype=torch.uint8)
+        for r, row in enumerate(rows):
+            for block, e in row:
+                codes[r, block * 16] = 2
+                scales[block // 8, r, block % 8] = e
+        return q.MXMatrix(codes.cuda(), scales.cuda(), K)
+
+    for one, small in [(0, 1), (1, 0), (0, 4), (4, 0), (0, 2), (0, 8), (8, 0), (3, 15), (15, 3)]:
+        A = matrix([[(one, 127), (small, 127 - j)] for j in last])
+        y = q.mx_mul_mat(A, matrix([[(one, 127), (small, 127)]]), variant=variant)[:, 0].cpu().double()
+        for j, v in zip(last, y.tolist()):
+            assert v == 1 + 2.0 ** -j if j < 24 else v in (1.0, 1 + 2.0 ** -23), (one, small, j)

@@ -183,3 +183,10 @@ def test_sizes_past_one_launch():
     (torch.bfloat16, 16, 4096, 14336, "skinny"), (torch.bfloat16, 64, 4096, 1 << 30, "simple")])
 def test_kernels_chosen(dtype, T, N, K, name):
     assert q.MX_VARIANT_NAMES[q.mx_mul_mat_choice(K, N, T, dtype)] == name
+
+
+def test_the_largest_layers():
+    most = (1 << 22) - 1
+    assert q.lib.retro_moe_workspace_size(q.BF16, 1, most, most, 4, 2) > 0
+    assert q.lib.retro_moe_workspace_size(q.BF16, 1, most + 1, 40, 4, 2) == q.E_SHAPE
+    assert q.lib.retro_moe_workspace_size(q.BF16, 1, 40, most + 1, 4, 2) == q.E_SHAPE
