@@ -11,6 +11,9 @@
 
 Every call runs asynchronously on `stream` (default: torch's current stream of
 the operands' device); outputs and scratch it allocates belong to that stream.
+None is recorded for autograd: results require no gradient, also where an
+operand does. mx_linear's gradients come from mx_linear_backward; mx_moe, for
+serving, has none.
 """
 
 from __future__ import annotations

@@ -527,3 +527,17 @@ def test_sums_keep_what_f32_holds(q, kernel):
         y = q.mx_mul_mat(A, matrix([[(one, 127), (small, 127)]]), variant=variant)[:, 0].cpu().double()
         for j, v in zip(last, y.tolist()):
             assert v == 1 + 2.0 ** -j if j < 24 else v in (1.0, 1 + 2.0 ** -23), (one, small, j)
+
+
+def test_results_require_no_gradient(q):
+    """The calls are outside autograd, whatever their operands: gradients come from mx_linear_backward."""
+    x = values(4, 64, torch.float32, 1).cuda().requires_grad_()
+    w = values(8, 64, torch.float32, 2).cuda().requires_grad_()
+    wr, wt = q.mx_quantize_both(w)
+    dx, dw = q.mx_linear_backward(torch.ones((4, 8), device="cuda"), x, wt)
+    results = [q.mx_linear(x, wr), dx, dw, q.mx_dequantize(wr),
+               q.mx_moe(x, w, q.mx_quantize(torch.ones((8 * 2 * 32, 64), device="cuda")),
+                        q.mx_quantize(torch.ones((8 * 64, 32), device="cuda")), 2)]
+    assert not any(t.requires_grad for t in results)
+    with pytest.raises(RuntimeError):
+        results[0].sum().backward()
