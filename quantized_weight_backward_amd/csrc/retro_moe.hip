@@ -11,17 +11,23 @@
 //            a part of them
 //   join     adds the parts
 // Weights are decoded exactly to bf16 (E2M1 times a power of two) and meet x
-// and h on v_mfma_f32_16x16x32_bf16 with F32 sums. x and h are cut into bf16
-// parts that add up to them: one for a BF16 x, two for F16 (11 bits), three for
-// F32 (24 bits); h, which is computed in F32, into two (16 bits, below a BF16
-// or F16 result's own rounding) or three.
+// and h on v_mfma_f32_16x16x32_bf16 with F32 sums. x is cut into bf16 parts that
+// add up to it: one for a BF16 x, two for F16 (11 bits), three for F32 (24 bits).
+// h, which is computed in F32, is rounded to three parts for F32 and to two (16
+// bits) for BF16 and F16, which round y to 8 or 11 bits: with three the error
+// against 64 bits is the same to four digits (1.6e-3 of y in BF16; 0.1 to 0.2% of
+// its last bits differ from those of an F32 h, 0.3% with two), and the layers below
+// take 21.6, 66 and 190 us instead of 16.6, 63 and 179.
 //
-// Measured (BF16; router, choose, gate_up, down, join): 1 token, 4 of 32 experts, D
-// = 2048, F = 1024: 16.5 us (3, in gate_up, 7.5, 7, none: launches and the
-// latencies of each, 13 MB of weights are 2.6 us). 16 tokens, 8 of 64 experts, F =
-// 1000: 61 us (4.9, 5.0, 31, 20, 4.8) for 185 MB, 3.0 TB/s. 32 tokens, 2 of 8
-// experts, D = 4096, F = 14336: 173 us (5.3, 6.8, 107, 67, 5.4) for 749 MB, 4.3
-// TB/s; gate_up reads at 4.7 TB/s and down at 3.8, where a plain read reaches 5.2.
+// Measured (BF16; calls one after another from a graph, weights in turn past the
+// caches; in brackets router, choose, gate_up, down and join traced one launch at
+// a time, which takes longer: they do not add up to the call): 1 token, 4 of 32
+// experts, D = 2048, F = 1024: 16.2 us (3.0, in gate_up, 6.9, 6.9, none: launches and
+// the latencies of each, 13 MB of weights are 2.6 us). 16 tokens, 8 of 64 experts, F =
+// 1000: 63 us (4.0, 4.6, 32, 20, 4.8) for 185 MB, 2.9 TB/s. 32 tokens, 2 of 8
+// experts, D = 4096, F = 14336: 172 to 180 us (5.3, 6.7, 106, 66, 5.4) for 749 MB, 4.2
+// to 4.4 TB/s, where a plain read reaches 5.2; traced, gate_up reads at 4.7 and down
+// at 3.8.
 #include "retro_mx_device.h"
 #include "retro_mx_host.h"
 
@@ -501,9 +507,9 @@ __device__ __forceinline__ void stage_ready() {
 // each of the rows'. A copy of 64 or 256 contiguous bytes takes one for each 64, 15
 // to 16 an instruction, and x or h is copied once for all waves. 32 tokens, 2 of 8
 // experts, D = 4096, F = 14336: down 36 to 8 million accesses, 93 to 64 us; gate_up
-// 48 to 16 million, 117 to 107 us, its bytes at 4.7 TB/s.
-// waves. The two halves of a stage's rows are two ranges of the matrix's; a
-// wave multiplies 16 of each. Rows of 64 bytes lie permuted by XOR with (row / 4) % 4,
+// 48 to 16 million, 117 to 107 us, its bytes at 4.7 TB/s (traced).
+// The two halves of a stage's rows are two ranges of the matrix's; a wave
+// multiplies 16 of each. Rows of 64 bytes lie permuted by XOR with (row / 4) % 4,
 // x's or h's of 256 bytes by XOR with the row, so that neighbouring lanes' reads
 // meet all banks.
 template <int P, int WAVES>
@@ -896,7 +902,8 @@ Down down_shape(int xtype, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k
     // 128: 31.5 against 27.1).
     if (T <= 16 && items <= 64) return {false, 16, 16, 1};
     // The staged kernel addresses h with 32 bits, and holds four or (many tokens)
-    // three stages beside the tokens' sums.
+    // three stages beside the tokens' sums; those of F32 fit up to 32 tokens (2 of 8,
+    // D = 4096, F = 14336: the layer in 217 us with 32 and 272 with 33).
     const int parts = h_parts(xtype);
     const bool fits = parts * T * k * steps_of(F) * 512 < (int64_t(1) << 32) && (parts < 3 || T <= 32);
     const int rows = fits ? kRingRows : 32;
@@ -954,8 +961,9 @@ int launch_layer(const Layer& L, const TX* X, int64_t ldx, const TR* R, int64_t 
     if (!own_lists) moe_choose_kernel<<<dim3(1), dim3(kChooseWaves * 64), 0, st>>>(L, renormalize);
     // 64 features a workgroup through the ring where that makes one a CU (1 token, 2
     // of 8 experts, D = 4096, F = 8192, 256 of them: 44 us against 46 for the layer; F =
-    // 14336: 50 against 55; F = 4096, 128: 30 against 25; 32 tokens, F = 14336: 177
-    // against 208, with 128 features 182). Else 16, four times as many workgroups.
+    // 14336: 50 against 55; F = 4096, 128: 30 against 25, all with one set of weights, part
+    // of which the last cache holds; 32 tokens, F = 14336: 177 against 208, with 128
+    // features 182). Else 16, four times as many workgroups.
     const int64_t ring_slabs = L.steps_f * (kStep / (16 * kRingWavesUp));
     if (ring_slabs * tiles >= host::kNumCUs) {
         auto gate_up = [&](void (*kernel)(Layer, int)) {

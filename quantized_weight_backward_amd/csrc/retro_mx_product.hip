@@ -157,8 +157,9 @@ int choose(int size, int64_t ldy, int64_t K, int64_t N, int64_t T) {
     // 5120 x 2048, 2048 x 5120 x 17408 and 64 .. 1024 x 4096 x 4096 and 14336. The
     // last round has as many a CU as it needs, of which the first cost least beside
     // one another (512 x 4096 x 4096: two of four a CU 12.0 us, one 11.0, four 19.1),
-    // or, at one a CU, as many CUs (the fewer, the higher their clock): 2048 x 5120 x 17408 takes 97 us as 216 tiles of
-    // 256 x 192 and 112 as 160 of 256 x 256, 8192^3 309 and 276.
+    // or, at one a CU, as many CUs (the fewer, the higher their clock): 2048 x 5120 x
+    // 17408 takes 97 us as 216 tiles of 256 x 192 and 112 as 160 of 256 x 256, 8192^3
+    // 309 and 276.
     struct Cost {
         int variant, rows_t, rows_n, per_cu;
         double one, one_step, full, full_step;
@@ -284,8 +285,9 @@ int retro_mx_mul_mat_choice(int ytype, int64_t ldy, int64_t K, int64_t N, int64_
     return choose(size, ldy, K, N, T);
 }
 
-int retro_mx_mul_mat_variant(int variant, int ytype, const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,
-                             void* Y, int64_t ldy, int64_t K, int64_t N, int64_t T, void* stream) {
+int retro_mx_mul_mat_variant(int variant, int ytype, const void* a_codes, const void* a_scales, const void* b_codes,
+                             const void* b_scales, void* Y, int64_t ldy, int64_t K, int64_t N, int64_t T,
+                             void* stream) {
     int64_t yb = 0;
     const int rc = check_product(ytype, b_codes, b_scales, Y, ldy, K, N, T, yb);
     if (rc != RETRO_OK || N == 0 || T == 0) return rc;

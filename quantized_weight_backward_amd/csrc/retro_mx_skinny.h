@@ -33,7 +33,7 @@ __device__ __forceinline__ void load_rows(StepRows& s, const uint8_t* codes, con
 // 16 rows of B times up to 16 TB rows of A, the steps of K dealt to the waves in
 // turn (U at a time, so that 2 U loads of B a lane are in flight); the waves'
 // sums are added in LDS in the order of the waves. The reading of B bounds it:
-// T = 16, N = 4096, K = 14336 in 10.0 us, 3.1 TB/s with the launch. `first` is the
+// T = 16, N = 4096, K = 14336 in 10.5 us traced, 3.0 TB/s. `first` is the
 // launch's first workgroup of all.
 template <typename TY, int TB, int U>
 __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void product_skinny_kernel(
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void product_skinny_kernel(
 // The same for T rows of A given as floats: the workgroup quantises them into
 // LDS first (retro_mx_quantize's rule), while its first loads of B are on their
 // way. For few elements only, since every workgroup does it. T = 1, N = 14336,
-// K = 4096 in 8.8 us, 3.5 TB/s of B with the launch (6.1 us at a copy's rate).
+// K = 4096 in 9.0 us, 3.5 TB/s of B with the launch (8.0 traced, 6.1 at a copy's rate).
 template <typename TX, int U>
 __global__ __launch_bounds__(kSkinnyWaves * 64, 4) void linear_skinny_kernel(
     const TX* __restrict__ X, int64_t ldx, const uint8_t* __restrict__ bc, const uint8_t* __restrict__ bs,

@@ -11,7 +11,8 @@
 // 273 with the reads and copies placed among the products by hand, and 8% slower than
 // eight waves at K = 4096. Stages of 128 elements, three or four deep, copy 64
 // bytes of a row at a time: 201 us for the copies instead of 152.
-// 4096 x 14336 x 4096: 147 us (3.3 PFLOP/s), three and a half rounds of tiles.
+// 4096 x 14336 x 4096: 144 to 155 us (3.1 to 3.3 PFLOP/s) in calls one after another,
+// 172 traced one launch at a time; three and a half rounds of tiles.
 #pragma once
 
 #include <type_traits>
