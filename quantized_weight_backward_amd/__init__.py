@@ -70,7 +70,7 @@ VARIANT_NAMES = {
 LIB_PATH = _build.LIB_PATH
 
 # The exported symbols, as declared in include/retro_out_prod.h,
-# include/retro_mx.h and include/retro_probe.h.
+# include/retro_mx.h, include/retro_vocab.h and include/retro_probe.h.
 EXPORTS = ("retro_out_prod", "retro_out_prod_variant", "retro_out_prod_strided", "retro_out_prod_strided_variant",
            "retro_dequantize", "retro_out_prod_supported", "retro_out_prod_choice", "retro_out_prod_variant_applies",
            "retro_out_prod_strided_variant_applies", "retro_out_prod_batched", "retro_out_prod_batched_variant",
@@ -85,6 +85,9 @@ EXPORTS = ("retro_out_prod", "retro_out_prod_variant", "retro_out_prod_strided",
            "retro_mx_dequantize", "retro_mx_from_blocks", "retro_mx_mul_mat", "retro_mx_mul_mat_variant",
            "retro_mx_mul_mat_choice", "retro_mx_linear",
            "retro_mx_linear_workspace_size", "retro_moe", "retro_moe_workspace_size",
+           "retro_embedding", "retro_embedding_backward", "retro_embedding_backward_workspace_size",
+           "retro_cross_entropy", "retro_cross_entropy_workspace_size", "retro_cross_entropy_backward",
+           "retro_cross_entropy_backward_workspace_size",
            "retro_probe_sink_floats", "retro_probe_mfma", "retro_probe_mfma_valu", "retro_probe_copy")
 
 PROBE_MFMA_F32 = 0
@@ -188,6 +191,22 @@ def _load() -> ctypes.CDLL:
                               i64, vp]
     lib.retro_moe_workspace_size.restype = i64
     lib.retro_moe_workspace_size.argtypes = [i32, i64, i64, i64, i64, i64]
+    f32 = ctypes.c_float
+    lib.retro_embedding.restype = i32
+    lib.retro_embedding.argtypes = [i32, vp, i64, i32, vp, f32, i32, vp, i64, i64, i64, i64, vp]
+    lib.retro_embedding_backward.restype = i32
+    lib.retro_embedding_backward.argtypes = [i32, vp, i32, vp, i64, f32, i32, vp, i64, i32, i64, i64, i64, vp, i64, vp]
+    lib.retro_embedding_backward_workspace_size.restype = i64
+    lib.retro_embedding_backward_workspace_size.argtypes = [i64, i64, i64]
+    lib.retro_cross_entropy.restype = i32
+    lib.retro_cross_entropy.argtypes = [i32, vp, i64, i32, vp, i64, i32, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+    lib.retro_cross_entropy_workspace_size.restype = i64
+    lib.retro_cross_entropy_workspace_size.argtypes = [i32, i64, i32, i64, i64, i64]
+    lib.retro_cross_entropy_backward.restype = i32
+    lib.retro_cross_entropy_backward.argtypes = [i32, vp, i64, i32, vp, i64, i32, vp, vp, vp, vp, i64, vp, i64, i64,
+                                                 i64, i64, vp, i64, vp]
+    lib.retro_cross_entropy_backward_workspace_size.restype = i64
+    lib.retro_cross_entropy_backward_workspace_size.argtypes = [i32, i64, i32, i32, i64, i64, i64]
     lib.retro_probe_sink_floats.restype = i64
     lib.retro_probe_sink_floats.argtypes = []
     lib.retro_probe_mfma.restype = i32
@@ -669,3 +688,4 @@ def dequantize(wtype: int, W, K: int, N: int, out=None, stream=None):
 
 from .mx import (MX_VARIANT_NAMES, MXMatrix, mx_dequantize, mx_from_blocks, mx_linear, mx_linear_backward, mx_moe,  # noqa: E402
                  mx_mul_mat, mx_mul_mat_choice, mx_quantize, mx_quantize_both, quantize)
+from .vocab import cross_entropy, cross_entropy_backward, embedding, embedding_backward  # noqa: E402

@@ -3,8 +3,9 @@
 The kernels of each weight type are compiled into an object of their own
 (retro_unit.hip with -DRETRO_UNIT_TYPE=<type id>) and the C ABI into another
 (retro_api.hip), the measured-ceiling probes into a third (retro_probe.hip),
-the microscaled 4-bit operators and the expert layer into one each; the
-objects are built in parallel and linked into one shared library.
+the microscaled 4-bit operators, the expert layer and the operators over a
+vocabulary into some of their own; the objects are built in parallel and linked
+into one shared library.
 """
 
 from __future__ import annotations
@@ -25,6 +26,8 @@ UNIT_SOURCE = os.path.join(CSRC, "retro_unit.hip")
 PROBE_SOURCE = os.path.join(CSRC, "retro_probe.hip")
 # the microscaled 4-bit operators and the expert layer (include/retro_mx.h)
 MX_SOURCES = {name: os.path.join(CSRC, f"{name}.hip") for name in ("retro_mx_quant", "retro_mx_product", "retro_moe")}
+# the operators over a vocabulary (include/retro_vocab.h)
+VOCAB_SOURCES = {name: os.path.join(CSRC, f"{name}.hip") for name in ("retro_ce", "retro_embed")}
 # GGUF ids of the weight types, one kernel object each
 UNIT_TYPES = {"f32": 0, "f16": 1, "q4_0": 2, "q4_1": 3, "q5_0": 6, "q5_1": 7, "q8_0": 8, "q2_k": 10, "q3_k": 11,
               "q4_k": 12, "q5_k": 13, "q6_k": 14, "bf16": 30, "mxfp4": 39,
@@ -51,7 +54,7 @@ def hipcc() -> str:
 
 def _jobs() -> int:
     limit = int(os.environ.get("MAX_JOBS", "16") or 16)
-    return max(1, min(limit, os.cpu_count() or 1, len(UNIT_TYPES) + 2 + len(MX_SOURCES)))
+    return max(1, min(limit, os.cpu_count() or 1, len(UNIT_TYPES) + 2 + len(MX_SOURCES) + len(VOCAB_SOURCES)))
 
 
 def _run(cmd: list[str]) -> str:
@@ -68,7 +71,7 @@ def build(verbose: bool = False) -> str:
     base = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c"]
     jobs = [(os.path.join(OBJ_DIR, "retro_api.o"), [API_SOURCE]),
             (os.path.join(OBJ_DIR, "retro_probe.o"), [PROBE_SOURCE])]
-    jobs += [(os.path.join(OBJ_DIR, f"{name}.o"), [src]) for name, src in MX_SOURCES.items()]
+    jobs += [(os.path.join(OBJ_DIR, f"{name}.o"), [src]) for name, src in {**MX_SOURCES, **VOCAB_SOURCES}.items()]
     for name, tid in UNIT_TYPES.items():
         jobs.append((os.path.join(OBJ_DIR, f"retro_unit_{name}.o"), [f"-DRETRO_UNIT_TYPE={tid}", UNIT_SOURCE]))
     with ThreadPoolExecutor(max_workers=_jobs()) as pool:

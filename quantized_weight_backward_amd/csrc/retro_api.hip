@@ -812,6 +812,12 @@ int mul_mat_impl(int variant, int type, const void* W, const float* X, float* Y,
 
 }  // namespace
 
+namespace retro {
+namespace vocab {
+int row_alignment(int type) { return int(block_alignment(type)); }
+}  // namespace vocab
+}  // namespace retro
+
 extern "C" {
 
 int retro_mul_mat(int type, const void* W, const float* X, float* Y, int64_t K, int64_t N, int64_t T,
@@ -1093,4 +1099,3 @@ const char* retro_strerror(int code) {
 }
 
 }  // extern "C"
-

@@ -1,0 +1,347 @@
+// retro_ce_kernel.h - the matrix products of the cross entropy over a
+// vocabulary: C[i][j] = sum_k A[i][k] B[j][k] of 16-bit rows, with what becomes
+// of C done in the registers that hold it, so that no logits are kept.
+//
+//   kStats  A rows of the head, B tokens: per 32 BT rows of the head and token the
+//           largest logit and the sum of exp(l - largest), and the target's logit
+//   kProb   the same logits again: d = exp(l - lse) - [target], written as 16-bit
+//           operands of the gradients' products: rows of tokens, and of the head
+//           times dloss
+//   kSum    C itself, in F32 (added to what is there) or rounded to the result's type
+//
+// Tokens are the columns of a matrix-core block: a lane then holds 16 rows of the
+// head of one token, whose maximum and sum need one exchange, with the other half
+// of the wave.
+#pragma once
+
+#include <type_traits>
+
+#include "retro_vocab_device.h"
+
+namespace retro {
+namespace ce {
+
+using mx::f32x16;
+using mx::i32x4;
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+enum Kind { kStats, kProb, kSum };
+
+constexpr int kStepBytes = 128;  // 64 elements of a row
+
+__device__ __forceinline__ f32x16 mfma(__bf16, const i32x4& a, const i32x4& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(_Float16, const i32x4& a, const i32x4& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+// exp(x) for x <= 0 or so: the product with log2 e in two parts, since the error of
+// one would be as large as x.
+__device__ __forceinline__ float exp_of(float x) {
+    constexpr float kLog2e = 1.44269504088896340736f, kRest = 1.92596299112661746887e-8f;
+    const float t = x * kLog2e;
+    const float r = fmaf(x, kRest, fmaf(x, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return t > -126.f ? fmaf(e * 0.693147180559945f, r, e) : e;
+}
+
+// Rows of 16-bit elements in one or two parts.
+struct Operand {
+    const uint8_t* p;
+    int64_t pitch;  // bytes of a row
+    int64_t plane;  // bytes from the first part to the second
+    int64_t rows;
+};
+
+struct Args {
+    Operand a, b;
+    uint32_t steps;       // of 64 elements in a row
+    uint32_t pairs;       // products of parts: (1, 1), or the first two or three of `order`
+    uint32_t order;       // part of A in bit 2p, part of B in bit 2p + 1 of product p
+    uint32_t tiles_a, tiles_b, group, splits;
+    // kStats, kProb: token factors and targets
+    const float* factor;   // what a token's sums are multiplied with (NULL: 1)
+    const uint32_t* top;   // and, with factor, W's scale
+    const void* targets;
+    bool wide_targets;
+    int64_t N, n0;         // rows of the head in all, and before A's first
+    // kStats
+    float2* part;          // [runs of 32 BT rows][T]
+    int64_t part0;         // first run
+    float* at_target;      // [T]
+    // kProb
+    const float* lse;
+    const float* weight;   // a token's factor in `across` (NULL: no `across`); 0 where it is not learnt from
+    float by;              // factor of `along`
+    uint16_t *along, *across;            // rows of tokens; rows of the head
+    int64_t along_pitch, along_plane;    // elements
+    int64_t across_pitch, across_plane;
+    // kSum
+    void* out;
+    int64_t ldo, split_stride;           // elements
+    const float* out_factor;             // (NULL: 1)
+    int64_t cols;                        // of C that are written
+};
+
+// Workgroup of WA x WB waves, each BA x BB blocks of 32 x 32.
+template <int WA_, int WB_, int BA_, int BB_>
+struct Tile {
+    static constexpr int WA = WA_, WB = WB_, BA = BA_, BB = BB_;
+    static constexpr int kWaves = WA * WB;
+    static constexpr int kRowsA = 32 * WA * BA, kRowsB = 32 * WB * BB;
+    static constexpr int kBytes = (kRowsA + kRowsB) * kStepBytes;  // LDS of one step
+    static constexpr int kCopies = kBytes / (1024 * kWaves);       // 1 KB copies a wave and step
+    static constexpr int kFit = 160 * 1024 / (2 * kBytes), kPerCU = kFit < 4 ? kFit : 4;
+    static constexpr int kThreads = kWaves * 64;
+    static constexpr int kPerSimd = kWaves * kPerCU / 4 < 8 ? (kWaves * kPerCU + 3) / 4 : 8;
+    static_assert(kRowsA * kStepBytes % (1024 * kWaves) == 0 && kRowsB * kStepBytes % (1024 * kWaves) == 0,
+                  "a copy lies in one operand");
+};
+
+// One step's tiles from memory into LDS, without registers: a wave's copy moves 8
+// rows of 128 bytes. The 16-byte pieces of row r land permuted by XOR with
+// (r / 2) % 8, so that the 16 lanes of a read of one piece from neighbouring rows
+// meet all banks once. Rows past the operand read as zeros (the buffer's bound).
+template <class Z>
+__device__ __forceinline__ void copy_step(__amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b, uint8_t* lds,
+                                          uint32_t pitch_a, uint32_t pitch_b, uint32_t at_k, int wave, int lane) {
+    const uint32_t r = lane >> 3, slot = lane & 7;
+#pragma unroll
+    for (int i = 0; i < Z::kCopies; ++i) {
+        const int at = (i * Z::kWaves + wave) * 8;  // first row of this copy
+        const bool of_a = i * Z::kWaves * 8 < Z::kRowsA;
+        const uint32_t row = at - (of_a ? 0 : Z::kRowsA);
+        const uint32_t swz = ((row + r) >> 1) & 7;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? a : b, lds + at * kStepBytes, 16,
+                                                 (row + r) * (of_a ? pitch_a : pitch_b) + ((slot ^ swz) * 16), at_k, 0,
+                                                 0);
+    }
+}
+
+// Every wave's copies into LDS have landed, its reads are done, and every wave is
+// here. A wave's counters cover its own work only, so the wait comes before the
+// barrier.
+__device__ __forceinline__ void copies_done_for_all() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <typename E, class Z, Kind KIND, typename TO, int PARTS>
+__global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const Args g) {
+    constexpr int WB = Z::WB, BA = Z::BA, BB = Z::BB;
+    __shared__ __align__(1024) uint8_t lds0[Z::kBytes];
+    __shared__ __align__(1024) uint8_t lds1[Z::kBytes];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int r = lane & 31, h = lane >> 5, wa = wave / WB, wb = wave % WB;
+
+    // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous range of
+    // tiles, in groups of `group` tiles of B by all of A, so that the workgroups
+    // that share its L2 at one time form a block of tiles.
+    const uint32_t tiles = g.tiles_a * g.tiles_b, all = tiles * g.splits, per = all / 8, more = all % 8;
+    const uint32_t x = blockIdx.x % 8;
+    uint32_t id = x * per + min(x, more) + blockIdx.x / 8;
+    const uint32_t split = id / tiles;
+    id -= split * tiles;
+    const uint32_t gr = id / (g.group * g.tiles_a), in = id - gr * g.group * g.tiles_a;
+    const uint32_t high = min(g.group, g.tiles_b - gr * g.group);
+    const int64_t b0 = int64_t(gr * g.group + in % high) * Z::kRowsB, a0 = int64_t(in / high) * Z::kRowsA;
+
+    const uint32_t pitch_a = uint32_t(g.a.pitch), pitch_b = uint32_t(g.b.pitch);
+    const uint8_t *base_of_a = g.a.p + a0 * g.a.pitch, *base_of_b = g.b.p + b0 * g.b.pitch;
+    const uint32_t bytes_a = uint32_t(min(int64_t(Z::kRowsA), g.a.rows - a0) * g.a.pitch);
+    const uint32_t bytes_b = uint32_t(min(int64_t(Z::kRowsB), g.b.rows - b0) * g.b.pitch);
+    // Steps of this split; step s is k = s % steps of product s / steps.
+    const uint32_t total = g.steps * g.pairs;
+    const uint32_t begin = uint32_t(uint64_t(total) * split / g.splits);
+    const uint32_t end = uint32_t(uint64_t(total) * (split + 1) / g.splits);
+    auto copy = [&](uint8_t* lds, uint32_t s) {
+        const uint32_t p = (s >= g.steps) + (s >= 2 * g.steps), k = s - p * g.steps;
+        const bool second_a = (g.order >> (2 * p)) & 1, second_b = (g.order >> (2 * p + 1)) & 1;
+        copy_step<Z>(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base_of_a + (second_a ? g.a.plane : 0)), 0,
+                                                       bytes_a, 0x00020000),
+                     __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base_of_b + (second_b ? g.b.plane : 0)), 0,
+                                                       bytes_b, 0x00020000),
+                     lds, pitch_a, pitch_b, k * kStepBytes, wave, lane);
+    };
+
+    // LDS offsets of the lane's pieces of its first rows
+    uint32_t off[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) off[s] = r * kStepBytes + (((4 * h + s) ^ ((r >> 1) & 7)) * 16);
+    const uint32_t base_a = wa * BA * 32 * kStepBytes, base_b = (Z::kRowsA + wb * BB * 32) * kStepBytes;
+    i32x4 fa[2][BA], fb[2][BB];
+    auto read = [&](const uint8_t* lds, int s, i32x4 (&a)[BA], i32x4 (&b)[BB]) {
+#pragma unroll
+        for (int i = 0; i < BA; ++i) a[i] = *reinterpret_cast<const i32x4*>(lds + base_a + off[s] + i * 32 * kStepBytes);
+#pragma unroll
+        for (int i = 0; i < BB; ++i) b[i] = *reinterpret_cast<const i32x4*>(lds + base_b + off[s] + i * 32 * kStepBytes);
+    };
+    f32x16 acc[BA][BB] = {};
+
+    // One step from `cur` (its copies done, piece 0 in registers): the reads of
+    // piece s + 1 are issued ahead of piece s's products; before the last piece's,
+    // everyone has read all of cur and the next step's copies are in `nxt`, so cur is
+    // refilled with the step after that. Past the last step the last one is copied
+    // again, so that the loop has no branches.
+    auto run = [&](uint8_t* cur, const uint8_t* nxt, uint32_t s) {
+        auto block = [&](auto which) {
+            constexpr int B = decltype(which)::value % 2;
+#pragma unroll
+            for (int i = 0; i < BA; ++i)
+#pragma unroll
+                for (int j = 0; j < BB; ++j) acc[i][j] = mfma(E(), fa[B][i], fb[B][j], acc[i][j]);
+        };
+        read(cur, 1, fa[1], fb[1]);
+        __builtin_amdgcn_sched_barrier(0);
+        block(std::integral_constant<int, 0>{});
+        read(cur, 2, fa[0], fb[0]);
+        __builtin_amdgcn_sched_barrier(0);
+        block(std::integral_constant<int, 1>{});
+        read(cur, 3, fa[1], fb[1]);
+        __builtin_amdgcn_sched_barrier(0);
+        block(std::integral_constant<int, 2>{});
+        copies_done_for_all();
+        read(nxt, 0, fa[0], fb[0]);
+        copy(cur, min(s + 2, end - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        block(std::integral_constant<int, 3>{});
+    };
+    if (begin < end) {
+        copy(lds0, begin);
+        copies_done_for_all();
+        copy(lds1, min(begin + 1, end - 1));
+        read(lds0, 0, fa[0], fb[0]);
+        uint32_t s = begin;
+        for (; s + 2 <= end; s += 2) {
+            run(lds0, lds1, s);
+            run(lds1, lds0, s + 1);
+        }
+        if (s < end) run(lds0, lds1, s);
+        copies_done_for_all();  // the copies past the end are done before LDS is given up
+    }
+
+    // Element v of a block: row (v / 4) * 8 + 4 h + v % 4 of A, row r of B.
+    const int64_t aw = a0 + wa * BA * 32 + 4 * h, bw = b0 + wb * BB * 32 + r;
+    if constexpr (KIND == kSum) {
+        TO* out = static_cast<TO*>(g.out) + split * g.split_stride;
+        const float f = g.out_factor ? *g.out_factor : 1.f;
+#pragma unroll
+        for (int i = 0; i < BA; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int64_t row = aw + i * 32 + (v / 4) * 8 + v % 4;
+                if (row >= g.a.rows) continue;
+#pragma unroll
+                for (int j = 0; j < BB; ++j) {
+                    const int64_t col = bw + j * 32;
+                    if (col >= g.cols) continue;
+                    TO* to = out + row * g.ldo + col;
+                    const float c = g.out_factor ? acc[i][j][v] * f : acc[i][j][v];
+                    if constexpr (PARTS)  // of kSum: add
+                        *to = mx::from_f32<TO>(mx::to_f32(*to) + c);
+                    else
+                        __builtin_nontemporal_store(mx::from_f32<TO>(c), to);
+                }
+            }
+        return;
+    }
+
+    const float by_top = g.factor ? vocab::unscale_of(*g.top) : 1.f;
+#pragma unroll
+    for (int j = 0; j < BB; ++j) {
+        const int64_t t = bw + j * 32;
+        if constexpr (KIND == kProb) {
+            // the padding of the head's rows past the last token is zeros
+            if (t >= g.b.rows && g.across && t < g.across_pitch)
+#pragma unroll
+                for (int i = 0; i < BA; ++i)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        const int64_t row = aw + i * 32 + (v / 4) * 8 + v % 4;
+                        if (row >= g.a.rows) continue;
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            g.across[part * g.across_plane + row * g.across_pitch + t] = 0;
+                    }
+        }
+        if (t >= g.b.rows) continue;  // both halves of the wave alike
+        if (g.factor) {
+            const float f = g.factor[t];
+#pragma unroll
+            for (int i = 0; i < BA; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = acc[i][j][v] * f * by_top;
+        }
+        // the target as a row of this lane's, were it one
+        const int64_t target = int64_t(vocab::token_at(g.targets, g.wide_targets, t, g.N)) - g.n0 - aw;
+        if constexpr (KIND == kStats) {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < BA; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int at = i * 32 + (v / 4) * 8 + v % 4;
+                    if (aw + at >= g.a.rows) acc[i][j][v] = -__builtin_inff();
+                    top = fmaxf(top, acc[i][j][v]);
+                    if (target == at) g.at_target[t] = acc[i][j][v];
+                }
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float from = top == -__builtin_inff() ? 0.f : top;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < BA; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) sum += exp_of(acc[i][j][v] - from);
+            sum += __shfl_xor(sum, 32);
+            if (h == 0) g.part[(g.part0 + (a0 / 32 + wa * BA) / BA) * g.b.rows + t] = make_float2(top, sum);
+        } else {
+            const float lse = g.lse[t];
+            const bool learnt = vocab::token_at(g.targets, g.wide_targets, t, g.N) >= 0;
+            const float weight = g.weight ? g.weight[t] : 0.f;
+#pragma unroll
+            for (int i = 0; i < BA; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int at = i * 32 + q * 8;
+                    float d[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        d[v] = exp_of(acc[i][j][q * 4 + v] - lse) - (target == at + v ? 1.f : 0.f);
+                        if (!learnt || aw + at + v >= g.a.rows) d[v] = 0.f;
+                    }
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+                        if (!g.along) break;
+                        u16x4 w;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            float p = d[v] * g.by;
+                            if (part) p = vocab::rest_of<E>(p);
+                            w[v] = __builtin_bit_cast(uint16_t, E(p));
+                        }
+                        // the padding past the head's last row is written too
+                        if (aw + at < g.along_pitch)
+                            *reinterpret_cast<u16x4*>(g.along + part * g.along_plane + t * g.along_pitch + aw + at) = w;
+                    }
+                    if (!g.across) continue;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        if (aw + at + v >= g.a.rows) continue;
+                        uint16_t* to = g.across + (aw + at + v) * g.across_pitch + t;
+                        const float p = learnt ? d[v] * weight : 0.f;
+                        *to = __builtin_bit_cast(uint16_t, E(p));
+                        if constexpr (PARTS == 2) to[g.across_plane] = __builtin_bit_cast(uint16_t, E(vocab::rest_of<E>(p)));
+                    }
+                }
+        }
+    }
+}
+
+}  // namespace ce
+}  // namespace retro

@@ -1,0 +1,500 @@
+// retro_embed.hip - embedding lookup and its gradient (retro_vocab.h).
+#include <algorithm>
+
+#include "retro_vocab_device.h"
+#include "retro_vocab_host.h"
+
+namespace retro {
+namespace vocab {
+namespace {
+
+using host::cdiv;
+using mx::Span;
+
+// The gradient. Tokens are sorted by id, stably, so that the tokens of an id lie side
+// by side in rising order: a radix sort from the low digit up, of `bits` bits a pass.
+// An id that is none sorts last, as N. The sorted list is cut into runs of 64; an id
+// whose tokens lie in several runs has the sum of each run's part made first, by
+// workgroups of their own, so that a frequent id is not one workgroup's work.
+
+constexpr int kMaxBits = 9, kMaxDigits = 1 << kMaxBits;
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSmallT = 8192;      // sorted by one workgroup in LDS
+constexpr int kBlockItems = 2048;  // of a workgroup of a larger sort's pass
+constexpr int kBlockThreads = 256, kBlockWaves = kBlockThreads / 64;
+constexpr int kRun = 64;
+
+// Passes and bits of each for keys 0 .. N.
+struct Radix {
+    int passes, bits;
+};
+Radix radix_of(int64_t N) {
+    int bits = 1;
+    while ((N >> bits) > 0) ++bits;
+    const int passes = int(cdiv(bits, kMaxBits));
+    return {passes, int(cdiv(bits, passes))};
+}
+
+__device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t t, int64_t N) {
+    const int id = token_at(ids, wide, t, N);
+    return id < 0 ? uint32_t(N) : uint32_t(id);
+}
+
+// What the wave's lanes wrote to LDS before is what they read after.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The lane's place among the lanes of its wave that have its digit (live lanes only),
+// and their number. All lanes of the wave are here.
+__device__ __forceinline__ uint32_t match(uint32_t digit, int bits, bool live, uint32_t& count) {
+    uint64_t same = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (digit >> b) & 1;
+        const uint64_t ones = __ballot(one);
+        same &= one ? ones : ~ones;
+    }
+    count = uint32_t(__popcll(same));
+    return uint32_t(__popcll(same & ((uint64_t(1) << (threadIdx.x % 64)) - 1)));
+}
+
+// Exclusive sums over `n` (at most the workgroup's threads) values, one a thread.
+template <int THREADS>
+__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* waves) {
+    uint32_t in = v;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t below = __shfl_up(in, d);
+        if (int(threadIdx.x % 64) >= d) in += below;
+    }
+    if (threadIdx.x % 64 == 63) waves[threadIdx.x / 64] = in;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < THREADS / 64; ++w) before += w < int(threadIdx.x / 64) ? waves[w] : 0;
+    __syncthreads();
+    return before + in - v;
+}
+
+// Up to kSmallT tokens: all passes in one workgroup. Wave w takes items w * per ..,
+// 64 at a time, and keeps a count a digit: an item's place is its digit's first, the
+// counts of the waves before, its wave's count so far, and the lanes before it.
+__global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __restrict__ ids, bool wide, int64_t N,
+                                                                 int T, int passes, int bits, uint32_t* __restrict__ keys,
+                                                                 uint32_t* __restrict__ order) {
+    constexpr int kPer = kSmallT / kSortThreads;
+    __shared__ uint32_t key[kSmallT];
+    __shared__ uint16_t from[kSmallT];
+    __shared__ uint16_t count[kSortWaves][kMaxDigits];
+    __shared__ uint32_t waves[kSortWaves];
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, rounds = (T + kSortThreads - 1) / kSortThreads;
+    uint32_t k[kPer], at[kPer], place[kPer];
+    auto item = [&](int i) { return (wave * rounds + i) * 64 + lane; };
+    for (int i = 0; i < kPer; ++i) {
+        const bool live = i < rounds && item(i) < T;
+        k[i] = live ? key_of(ids, wide, item(i), N) : 0;
+        at[i] = uint32_t(item(i));
+    }
+    for (int p = 0; p < passes; ++p) {
+        for (int d = threadIdx.x; d < kSortWaves * kMaxDigits; d += kSortThreads) (&count[0][0])[d] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (i >= rounds) break;
+            const bool live = item(i) < T;
+            const uint32_t digit = (k[i] >> (p * bits)) & ((1u << bits) - 1);
+            uint32_t same;
+            const uint32_t mine = match(digit, bits, live, same);
+            const uint32_t before = count[wave][digit];
+            place[i] = before + mine;
+            wave_fence();
+            if (live && mine == 0) count[wave][digit] = uint16_t(before + same);
+            wave_fence();
+        }
+        __syncthreads();
+        // counts become the places of each wave's first item of a digit
+        uint32_t all = 0;
+        if (threadIdx.x < kMaxDigits)
+            for (int w = 0; w < kSortWaves; ++w) all += count[w][threadIdx.x];
+        uint32_t first = scan<kSortThreads>(all, waves);
+        if (threadIdx.x < kMaxDigits)
+            for (int w = 0; w < kSortWaves; ++w) {
+                const uint32_t n = count[w][threadIdx.x];
+                count[w][threadIdx.x] = uint16_t(first);
+                first += n;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (i >= rounds || item(i) >= T) break;
+            const uint32_t to = count[wave][(k[i] >> (p * bits)) & ((1u << bits) - 1)] + place[i];
+            key[to] = k[i];
+            from[to] = uint16_t(at[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (i >= rounds || item(i) >= T) break;
+            k[i] = key[item(i)];
+            at[i] = from[item(i)];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (i >= rounds || item(i) >= T) break;
+        keys[item(i)] = k[i];
+        order[item(i)] = at[i];
+    }
+}
+
+// A pass of a larger sort: a workgroup kBlockItems items, a wave a quarter of them in
+// rows of 64. With `totals` NULL the digits of each workgroup are counted, into
+// counts[digit][workgroup]; then counts holds the items of the digit in workgroups
+// before, totals the digits' numbers, and the items are moved.
+__global__ __launch_bounds__(kBlockThreads) void sort_pass_kernel(
+    const void* __restrict__ ids, bool wide, int64_t N, const uint32_t* __restrict__ keys_in,
+    const uint32_t* __restrict__ order_in, int64_t T, int shift, int bits, uint32_t* __restrict__ counts,
+    const uint32_t* __restrict__ totals, uint32_t* __restrict__ keys, uint32_t* __restrict__ order) {
+    constexpr int kRounds = kBlockItems / kBlockThreads;
+    __shared__ uint32_t count[kBlockWaves][kMaxDigits];
+    __shared__ uint32_t waves[kBlockWaves];
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, digits = 1 << bits;
+    const int64_t first = int64_t(blockIdx.x) * kBlockItems + wave * (kBlockItems / kBlockWaves) + lane;
+    for (int d = threadIdx.x; d < kBlockWaves * kMaxDigits; d += kBlockThreads) (&count[0][0])[d] = 0;
+    __syncthreads();
+    uint32_t k[kRounds], place[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int64_t t = first + i * 64;
+        const bool live = t < T;
+        k[i] = !live ? 0 : keys_in ? keys_in[t] : key_of(ids, wide, t, N);
+        const uint32_t digit = (k[i] >> shift) & (digits - 1);
+        uint32_t same;
+        const uint32_t mine = match(digit, bits, live, same);
+        const uint32_t before = count[wave][digit];
+        place[i] = before + mine;
+        wave_fence();
+        if (live && mine == 0) count[wave][digit] = before + same;
+        wave_fence();
+    }
+    __syncthreads();
+    if (!totals) {
+        for (int d = threadIdx.x; d < digits; d += kBlockThreads) {
+            uint32_t all = 0;
+            for (int w = 0; w < kBlockWaves; ++w) all += count[w][d];
+            counts[int64_t(d) * gridDim.x + blockIdx.x] = all;
+        }
+        return;
+    }
+    uint32_t before = 0;  // of the digits below
+    for (int d0 = 0; d0 < digits; d0 += kBlockThreads) {
+        const int d = d0 + threadIdx.x;
+        const uint32_t n = d < digits ? totals[d] : 0, below = scan<kBlockThreads>(n, waves);
+        if (d < digits) {
+            uint32_t to = before + below + counts[int64_t(d) * gridDim.x + blockIdx.x];
+            for (int w = 0; w < kBlockWaves; ++w) {
+                const uint32_t of = count[w][d];
+                count[w][d] = to;
+                to += of;
+            }
+        }
+        __shared__ uint32_t last;
+        if (threadIdx.x == kBlockThreads - 1) last = below + n;
+        __syncthreads();
+        before += last;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int64_t t = first + i * 64;
+        if (t >= T) break;
+        const uint32_t to = count[wave][(k[i] >> shift) & (digits - 1)] + place[i];
+        keys[to] = k[i];
+        order[to] = order_in ? order_in[t] : uint32_t(t);
+    }
+}
+
+// counts of one digit (a workgroup each): those of the workgroups before, and their sum.
+__global__ __launch_bounds__(256) void sort_scan_kernel(uint32_t* __restrict__ counts, uint32_t blocks,
+                                                        uint32_t* __restrict__ totals) {
+    __shared__ uint32_t waves[4], last;
+    uint32_t* c = counts + int64_t(blockIdx.x) * blocks;
+    uint32_t before = 0;
+    for (uint32_t b0 = 0; b0 < blocks; b0 += 256) {
+        const uint32_t b = b0 + threadIdx.x, n = b < blocks ? c[b] : 0, below = scan<256>(n, waves);
+        if (b < blocks) c[b] = before + below;
+        if (threadIdx.x == 255) last = below + n;
+        __syncthreads();
+        before += last;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) totals[blockIdx.x] = before;
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(uint2* p, int64_t n) {
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) p[i] = make_uint2(0, 0);
+}
+
+// span[id] = the id's first place in the sorted list and the place after its last.
+__global__ __launch_bounds__(256) void spans_kernel(const uint32_t* __restrict__ keys, int64_t T, int64_t N,
+                                                    uint2* __restrict__ span) {
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= T) return;
+    const uint32_t k = keys[i];
+    if (k >= N) return;
+    if (i == 0 || keys[i - 1] != k) span[k].x = uint32_t(i);
+    if (i + 1 == T || keys[i + 1] != k) span[k].y = uint32_t(i) + 1;
+}
+
+// The sum of dY's rows order[i] for begin <= i < end, in that order.
+template <typename TY>
+__device__ __forceinline__ void sum_rows(const TY* __restrict__ dY, int64_t ldy, int64_t left,
+                                         const uint32_t* __restrict__ order, uint32_t begin, uint32_t end, float e[8]) {
+    uint32_t i = begin;
+    for (; i + 4 <= end; i += 4) {
+        float v[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx::load8(dY + int64_t(order[i + j]) * ldy, left, v[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) e[c] += v[j][c];
+    }
+    for (; i < end; ++i) {
+        float v[8];
+        mx::load8(dY + int64_t(order[i]) * ldy, left, v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) e[c] += v[c];
+    }
+}
+
+// Sums of the parts of ids whose tokens lie in several runs: of run c, slot 2c holds
+// the part that begins with the run, slot 2c + 1 one that begins inside it. A thread
+// 8 columns of a run.
+template <typename TY>
+__global__ __launch_bounds__(256) void parts_kernel(const TY* __restrict__ dY, int64_t ldy, int64_t K, int64_t T,
+                                                    int64_t N, const uint32_t* __restrict__ keys,
+                                                    const uint32_t* __restrict__ order, float* __restrict__ parts,
+                                                    uint32_t per, int64_t first_block) {
+    const int64_t at = (first_block + blockIdx.x) * 256 + threadIdx.x;
+    const int64_t c = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
+    const uint32_t begin = uint32_t(c * kRun);
+    if (begin >= T) return;
+    const int64_t k = (at - c * per) * 8, pitch = int64_t(per) * 8;
+    const uint32_t end = uint32_t(min(T, int64_t(begin) + kRun));
+    const uint32_t head = keys[begin], tail = keys[end - 1];
+    const bool from_before = begin > 0 && keys[begin - 1] == head, goes_on = end < T && keys[end] == tail;
+    auto put = [&](int slot, uint32_t b, uint32_t e) {
+        float v[8] = {};
+        sum_rows(dY + k, ldy, K - k, order, b, e, v);
+        store8(parts + (2 * c + slot) * pitch + k, 8, v);
+    };
+    if (head < N && (from_before || (goes_on && head == tail))) {
+        uint32_t e = begin + 1;
+        while (e < end && keys[e] == head) ++e;
+        put(0, begin, e);
+    }
+    if (goes_on && tail < N && head != tail) {
+        uint32_t b = end - 1;
+        while (keys[b - 1] == tail) --b;
+        put(1, b, end);
+    }
+}
+
+// Rows of dW from their tokens. A thread 8 columns of a row: of every row (each is
+// written), or, when adding, of the row of every place in the sorted list where an id
+// begins.
+template <typename TY, typename TW, bool ADD>
+__global__ __launch_bounds__(256) void rows_kernel(const TY* __restrict__ dY, int64_t ldy, float scale,
+                                                   TW* __restrict__ dW, int64_t ldw, int64_t K, int64_t T, int64_t N,
+                                                   const uint32_t* __restrict__ keys, const uint32_t* __restrict__ order,
+                                                   const uint2* __restrict__ span, const float* __restrict__ parts,
+                                                   uint32_t per, int64_t first_block) {
+    const int64_t at = (first_block + blockIdx.x) * 256 + threadIdx.x;
+    int64_t row = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
+    const int64_t k = (at - row * per) * 8, pitch = int64_t(per) * 8;
+    if (row >= (ADD ? T : N)) return;
+    if constexpr (ADD) {
+        const uint32_t key = keys[row];
+        if (key >= N || (row > 0 && keys[row - 1] == key)) return;
+        row = key;
+    }
+    const uint2 s = span[row];
+    float e[8] = {};
+    const uint32_t c0 = s.x / kRun, c1 = s.y == 0 ? c0 : (s.y - 1) / kRun;
+    if (c0 == c1) {
+        sum_rows(dY + k, ldy, K - k, order, s.x, s.y, e);
+    } else {
+        for (uint32_t c = c0; c <= c1; ++c) {
+            float v[8];
+            mx::load8(parts + (2 * int64_t(c) + (c == c0 && s.x % kRun ? 1 : 0)) * pitch + k, 8, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] += v[i];
+        }
+    }
+    TW* to = dW + row * ldw + k;
+    if (s.x != s.y)  // a row of no token is zeros whatever the scale
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] *= scale;
+    if constexpr (ADD) {
+        float old[8];
+        mx::load8(to, K - k, old);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] += old[i];
+    }
+    store8(to, K - k, e);
+}
+
+struct Plan {
+    Radix radix;
+    int64_t keys[2], order[2], counts, totals, span, parts, bytes;
+    int64_t blocks;
+};
+
+Plan plan_of(int64_t K, int64_t N, int64_t T) {
+    Plan p = {};
+    p.radix = radix_of(N);
+    p.blocks = cdiv(T, kBlockItems);
+    auto take = [&](int64_t bytes) {
+        const int64_t here = p.bytes;
+        p.bytes += cdiv(bytes, 256) * 256;
+        return here;
+    };
+    for (int i = 0; i < (T > kSmallT ? 2 : 1); ++i) {
+        p.keys[i] = take(4 * T);
+        p.order[i] = take(4 * T);
+    }
+    if (T > kSmallT) {
+        p.counts = take(4 * p.blocks << p.radix.bits);
+        p.totals = take(4 << p.radix.bits);
+    }
+    p.span = take(8 * N);
+    p.parts = take(4 * 2 * cdiv(T, kRun) * cdiv(K, 8) * 8);
+    return p;
+}
+
+#define RETRO_TRY(e)                     \
+    do {                                 \
+        const int rc_ = (e);             \
+        if (rc_ != RETRO_OK) return rc_; \
+    } while (0)
+
+// Sorted keys and tokens end in plane `out` of the workspace.
+int sort(const Plan& p, const void* ids, bool wide, int64_t N, int64_t T, uint8_t* ws, int& out, hipStream_t st) {
+    auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
+    out = 0;
+    host::clear_last_error();
+    if (T <= kSmallT) {
+        sort_small_kernel<<<dim3(1), dim3(kSortThreads), 0, st>>>(ids, wide, N, int(T), p.radix.passes, p.radix.bits,
+                                                                 words(p.keys[0]), words(p.order[0]));
+        return host::launch_status();
+    }
+    const dim3 grid(uint32_t(p.blocks)), threads(kBlockThreads);
+    for (int i = 0; i < p.radix.passes; ++i) {
+        const uint32_t *keys_in = i ? words(p.keys[out]) : nullptr, *order_in = i ? words(p.order[out]) : nullptr;
+        const int to = i ? 1 - out : 0, shift = i * p.radix.bits;
+        uint32_t *counts = words(p.counts), *totals = words(p.totals);
+        sort_pass_kernel<<<grid, threads, 0, st>>>(ids, wide, N, keys_in, order_in, T, shift, p.radix.bits, counts,
+                                                   nullptr, nullptr, nullptr);
+        sort_scan_kernel<<<dim3(1u << p.radix.bits), dim3(256), 0, st>>>(counts, uint32_t(p.blocks), totals);
+        sort_pass_kernel<<<grid, threads, 0, st>>>(ids, wide, N, keys_in, order_in, T, shift, p.radix.bits, counts,
+                                                   totals, words(p.keys[to]), words(p.order[to]));
+        out = to;
+    }
+    return host::launch_status();
+}
+
+constexpr int64_t kMaxK = int64_t(1) << 22, kMaxT = int64_t(1) << 28;
+
+int id_bytes(int type) { return type == RETRO_I32 ? 4 : type == RETRO_I64 ? 8 : 0; }
+
+}  // namespace
+}  // namespace vocab
+}  // namespace retro
+
+using namespace retro;
+using namespace retro::vocab;
+
+extern "C" {
+
+int retro_embedding(int type, const void* W, int64_t ldw, int idtype, const void* ids, float scale, int ytype, void* Y,
+                    int64_t ldy, int64_t K, int64_t N, int64_t T, void* stream) {
+    host::Geometry geo;
+    const int size = mx::float_bytes(ytype), idsize = id_bytes(idtype);
+    if (!host::geometry(type, geo) || !size || !idsize) return RETRO_E_TYPE;
+    if (K < 0 || K >= kMaxK || K % geo.block || !mx::dim_ok(N) || !mx::dim_ok(T)) return RETRO_E_SHAPE;
+    const int64_t row = host::row_bytes_of(type, K), yb = mx::span_bytes(T, K, ldy, size);
+    if (yb < 0 || ldw < row || (N > 1 && ldw > (host::kByteLimit - row) / (N - 1))) return RETRO_E_SHAPE;
+    if (T == 0 || K == 0) return RETRO_OK;
+    if (!ids || !Y || (N > 0 && !W)) return RETRO_E_NULL;
+    if (!mx::aligned(W, 16) || !mx::aligned(Y, size) || !mx::aligned(ids, idsize) || ldw % row_alignment(type))
+        return RETRO_E_ALIGN;
+    const Span y{Y, yb};
+    if (mx::overlap(y, {W, N > 0 ? (N - 1) * ldw + row : 0}) || mx::overlap(y, {ids, T * idsize})) return RETRO_E_ALIAS;
+    const EmbedArgs a{static_cast<const uint8_t*>(W), ldw, ids, idtype == RETRO_I64, Y, ldy, scale, K, N, T};
+    return with_type(type, [&](auto t) { return launch_embed<decltype(t)::value>(ytype, a, static_cast<hipStream_t>(stream)); });
+}
+
+int64_t retro_embedding_backward_workspace_size(int64_t K, int64_t N, int64_t T) {
+    if (K < 0 || K >= kMaxK || !mx::dim_ok(N) || T < 0 || T >= kMaxT) return RETRO_E_SHAPE;
+    return K == 0 || N == 0 ? 0 : plan_of(K, N, T).bytes;
+}
+
+int retro_embedding_backward(int idtype, const void* ids, int ytype, const void* dY, int64_t ldy, float scale, int wtype,
+                             void* dW, int64_t ldw, int accumulate, int64_t K, int64_t N, int64_t T, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    const int ys = mx::float_bytes(ytype), wsize = mx::float_bytes(wtype), idsize = id_bytes(idtype);
+    if (!ys || !wsize || !idsize) return RETRO_E_TYPE;
+    const int64_t need = retro_embedding_backward_workspace_size(K, N, T);
+    if (need < 0) return int(need);
+    const int64_t yb = mx::span_bytes(T, K, ldy, ys), wb = mx::span_bytes(N, K, ldw, wsize);
+    if (yb < 0 || wb < 0) return RETRO_E_SHAPE;
+    if (N == 0 || K == 0 || (T == 0 && accumulate)) return RETRO_OK;
+    if (!dW || (T > 0 && (!ids || !dY))) return RETRO_E_NULL;
+    if (!mx::aligned(dW, wsize) || !mx::aligned(dY, ys) || !mx::aligned(ids, idsize)) return RETRO_E_ALIGN;
+    const Span w{dW, wb}, y{dY, yb}, i{ids, T * idsize}, s{workspace, need};
+    if (mx::overlap(w, y) || mx::overlap(w, i)) return RETRO_E_ALIAS;
+    if (!workspace || workspace_bytes < need || !mx::aligned(workspace, 16) || mx::overlap(s, w) || mx::overlap(s, y) ||
+        mx::overlap(s, i))
+        return RETRO_E_WORKSPACE;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const Plan p = plan_of(K, N, T);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint2* span = reinterpret_cast<uint2*>(ws + p.span);
+    float* parts = reinterpret_cast<float*>(ws + p.parts);
+    if (!accumulate)
+        RETRO_TRY(mx::in_block_ranges(cdiv(N, 256), [&](int64_t first, uint32_t blocks) {
+            clear_kernel<<<dim3(blocks), dim3(256), 0, st>>>(span + first * 256, N - first * 256);
+        }));
+    int out = 0;
+    if (T > 0) {
+        RETRO_TRY(sort(p, ids, idtype == RETRO_I64, N, T, ws, out, st));
+        host::clear_last_error();
+        spans_kernel<<<dim3(uint32_t(cdiv(T, 256))), dim3(256), 0, st>>>(
+            reinterpret_cast<uint32_t*>(ws + p.keys[out]), T, N, span);
+        RETRO_TRY(host::launch_status());
+    }
+    const uint32_t *keys = reinterpret_cast<uint32_t*>(ws + p.keys[out]),
+                   *order = reinterpret_cast<uint32_t*>(ws + p.order[out]);
+    const uint32_t per = uint32_t(cdiv(K, 8));
+    return mx::with_float(ytype, [&](auto* ytag) {
+        using TY = std::remove_pointer_t<decltype(ytag)>;
+        const TY* dy = static_cast<const TY*>(dY);
+        if (T > kRun)  // fewer lie in one run
+            RETRO_TRY(mx::in_block_ranges(cdiv(cdiv(T, kRun) * per, 256), [&](int64_t first, uint32_t blocks) {
+                parts_kernel<TY><<<dim3(blocks), dim3(256), 0, st>>>(dy, ldy, K, T, N, keys, order, parts, per, first);
+            }));
+        return mx::with_float(wtype, [&](auto* wtag) {
+            using TW = std::remove_pointer_t<decltype(wtag)>;
+            return mx::in_block_ranges(cdiv((accumulate ? T : N) * per, 256), [&](int64_t first, uint32_t blocks) {
+                auto kernel = accumulate ? rows_kernel<TY, TW, true> : rows_kernel<TY, TW, false>;
+                kernel<<<dim3(blocks), dim3(256), 0, st>>>(dy, ldy, scale, static_cast<TW*>(dW), ldw, K, T, N, keys,
+                                                           order, span, parts, per, first);
+            });
+        });
+    });
+}
+
+}  // extern "C"

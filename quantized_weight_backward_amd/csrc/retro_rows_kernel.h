@@ -1,0 +1,92 @@
+// retro_rows_kernel.h - kernels over rows of one weight type: embedding lookup,
+// and the rows of a table as 16-bit planes for the matrix cores.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "retro_kernels.h"
+#include "retro_vocab_device.h"
+
+namespace retro {
+namespace vocab {
+
+// Elements k .. k + 7 of a row, zeros past K (k a multiple of 8).
+template <int TYPE>
+__device__ __forceinline__ void row8(const uint8_t* row, int k, int K, int wide, float e[8]) {
+    float a[4], b[4];
+    skinny_load4<TYPE>(row, k, K, wide, a);
+    if (k + 4 < K || Format<TYPE>::kBlock == 1)  // packed rows end with a block
+        skinny_load4<TYPE>(row, k + 4, K, wide, b);
+    else
+        b[0] = b[1] = b[2] = b[3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        e[i] = a[i];
+        e[4 + i] = b[i];
+    }
+}
+
+// y[t] = scale * W[ids[t]]: a thread 8 elements. Nothing but the memory bounds it.
+template <int TYPE, typename TY, typename TI>
+__global__ __launch_bounds__(256) void embed_kernel(const uint8_t* __restrict__ W, int64_t ldw,
+                                                    const TI* __restrict__ ids, TY* __restrict__ Y, int64_t ldy,
+                                                    float scale, int K, int64_t N, int64_t T, int wide, uint32_t per,
+                                                    int64_t first) {
+    const int64_t at = (first + blockIdx.x) * 256 + threadIdx.x;
+    const int64_t t = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
+    if (t >= T) return;
+    const int k = int(at - t * per) * 8;
+    const int64_t id = ids[t];
+    float e[8] = {};
+    if (id >= 0 && id < N) {
+        row8<TYPE>(W + id * ldw, k, K, wide, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] *= scale;
+    }
+    store8(Y + t * ldy + k, K - k, e);
+}
+
+// Rows as planes (PlaneArgs): a thread 8 elements of a row.
+template <int TYPE, int PARTS>
+__global__ __launch_bounds__(256) void planes_kernel(const uint8_t* __restrict__ W, int64_t ldw, int64_t rows, int K,
+                                                     uint16_t* __restrict__ out, int64_t plane,
+                                                     const uint32_t* __restrict__ top, int wide, uint32_t per,
+                                                     int64_t first) {
+    const int64_t at = (first + blockIdx.x) * 256 + threadIdx.x;
+    const int64_t r = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
+    if (r >= rows) return;
+    const int k = int(at - r * per) * 8;
+    float e[8] = {};
+    if (k < K) row8<TYPE>(W + r * ldw, k, K, wide, e);
+    uint16_t* to = out + r * (int64_t(per) * 8) + k;
+    if constexpr (PARTS == 0) {
+        typedef typename std::conditional<TYPE == kBF16, __bf16, _Float16>::type E;
+        store_part<E>(to, e);
+    } else {
+        const float s = scale_of(*top);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] *= s;
+        store_parts<_Float16, PARTS>(to, plane, e);
+    }
+}
+
+// The largest magnitude's bits of a table, NaN above all.
+template <int TYPE>
+__global__ __launch_bounds__(256) void top_kernel(const uint8_t* __restrict__ W, int64_t ldw, int64_t rows, int K,
+                                                  uint32_t* __restrict__ top, int wide, uint32_t per) {
+    uint32_t m = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (uint32_t g = threadIdx.x; g < per; g += 256) {
+            float e[8];
+            row8<TYPE>(W + r * ldw, int(g) * 8, K, wide, e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[i]) & 0x7fffffffu);
+        }
+    m = wave_max(m);
+    // a maximum is the same in whatever order
+    if (threadIdx.x % 64 == 0 && m) atomicMax(top, m);
+}
+
+}  // namespace vocab
+}  // namespace retro

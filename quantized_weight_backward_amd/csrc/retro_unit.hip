@@ -8,7 +8,9 @@
 #include "retro_host.h"
 #include "retro_kernels.h"
 #include "retro_mm_kernel.h"
+#include "retro_rows_kernel.h"
 #include "retro_split_kernel.h"
+#include "retro_vocab_host.h"
 #include "retro_ws_kernel.h"
 
 #ifndef RETRO_UNIT_TYPE
@@ -391,5 +393,56 @@ template int launch_mul_mat<RETRO_UNIT_TYPE>(int, const void*, const float*, flo
 template int launch_dequant<RETRO_UNIT_TYPE>(const void*, float*, int64_t, int64_t, hipStream_t);
 
 }  // namespace host
-}  // namespace retro
 
+namespace vocab {
+namespace {
+
+// Rows of 16-byte aligned floats in fours, or packed rows.
+int wide_rows(int type, int64_t ldw, int64_t K) { return K % 4 == 0 && (type > RETRO_F16 && type != RETRO_BF16 ? true : ldw % 16 == 0); }
+
+template <typename TY, typename TI>
+int launch_embed_as(const EmbedArgs& a, hipStream_t st) {
+    const uint32_t per = uint32_t(host::cdiv(a.K, 8));
+    return mx::in_block_ranges(host::cdiv(a.T * per, 256), [&](int64_t first, uint32_t blocks) {
+        embed_kernel<RETRO_UNIT_TYPE, TY, TI><<<dim3(blocks), dim3(256), 0, st>>>(
+            a.W, a.ldw, static_cast<const TI*>(a.ids), static_cast<TY*>(a.Y), a.ldy, a.scale, int(a.K), a.N, a.T,
+            wide_rows(RETRO_UNIT_TYPE, a.ldw, a.K), per, first);
+    });
+}
+
+}  // namespace
+
+template <int TYPE>
+int launch_embed(int ytype, const EmbedArgs& a, hipStream_t st) {
+    return mx::with_float(ytype, [&](auto* tag) {
+        using TY = std::remove_pointer_t<decltype(tag)>;
+        return a.wide_ids ? launch_embed_as<TY, int64_t>(a, st) : launch_embed_as<TY, int32_t>(a, st);
+    });
+}
+
+template <int TYPE>
+int launch_planes(const PlaneArgs& a, hipStream_t st) {
+    const uint32_t per = uint32_t(padded(a.K) / 8);
+    const int wide = wide_rows(TYPE, a.ldw, a.K);
+    return mx::in_block_ranges(host::cdiv(a.rows * per, 256), [&](int64_t first, uint32_t blocks) {
+        auto kernel = a.parts == 2 ? planes_kernel<TYPE, 2> : planes_kernel<TYPE, 1>;
+        if constexpr (TYPE == RETRO_F16 || TYPE == RETRO_BF16)
+            if (a.parts == 0) kernel = planes_kernel<TYPE, 0>;
+        kernel<<<dim3(blocks), dim3(256), 0, st>>>(a.W, a.ldw, a.rows, int(a.K), a.out, a.plane, a.top, wide, per, first);
+    });
+}
+
+template <int TYPE>
+int launch_top(const uint8_t* W, int64_t ldw, int64_t rows, int64_t K, uint32_t* top, hipStream_t st) {
+    host::clear_last_error();
+    top_kernel<TYPE><<<dim3(uint32_t(std::min<int64_t>(rows, 2048))), dim3(256), 0, st>>>(
+        W, ldw, rows, int(K), top, wide_rows(TYPE, ldw, K), uint32_t(host::cdiv(K, 8)));
+    return host::launch_status();
+}
+
+template int launch_embed<RETRO_UNIT_TYPE>(int, const EmbedArgs&, hipStream_t);
+template int launch_planes<RETRO_UNIT_TYPE>(const PlaneArgs&, hipStream_t);
+template int launch_top<RETRO_UNIT_TYPE>(const uint8_t*, int64_t, int64_t, int64_t, uint32_t*, hipStream_t);
+
+}  // namespace vocab
+}  // namespace retro
