@@ -91,15 +91,17 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* __restri
 
 // ---------------------------------------------------------------- what follows the products
 
-// lse and loss from the runs' largest logits and sums, in the runs' order. 8 tokens
-// a workgroup, 32 threads each.
+// lse and loss from the runs' largest logits and sums, joined in an order that the
+// sizes alone give. TT tokens a workgroup, 256 / TT threads each, four runs in flight.
+template <int TT>
 __global__ __launch_bounds__(256) void combine_kernel(const float2* __restrict__ part, int64_t runs, int64_t T,
                                                       const void* __restrict__ targets, bool wide_targets, int64_t N,
                                                       const float* __restrict__ at_target, float* __restrict__ loss,
                                                       float* __restrict__ lse) {
-    __shared__ float2 held[32][8];
-    const int tt = threadIdx.x % 8, p = threadIdx.x / 8;
-    const int64_t t = int64_t(blockIdx.x) * 8 + tt;
+    constexpr int kPer = 256 / TT;
+    __shared__ float2 held[kPer][TT];
+    const int tt = threadIdx.x % TT, p = threadIdx.x / TT;
+    const int64_t t = int64_t(blockIdx.x) * TT + tt;
     const float none = -__builtin_inff();
     float top = none, sum = 0.f;
     auto join = [&](float2 v) {
@@ -108,11 +110,20 @@ __global__ __launch_bounds__(256) void combine_kernel(const float2* __restrict__
         top = m;
     };
     if (t < T)
-        for (int64_t i = p; i < runs; i += 32) join(part[i * T + t]);
-    held[p][tt] = make_float2(top, sum);
-    __syncthreads();
+        for (int64_t i = p; i < runs; i += 4 * kPer) {
+            float2 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = i + j * kPer < runs ? part[(i + j * kPer) * T + t] : make_float2(none, 0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) join(v[j]);
+        }
+    for (int d = kPer / 2; d > 0; d /= 2) {
+        held[p][tt] = make_float2(top, sum);
+        __syncthreads();
+        if (p < d) join(held[p + d][tt]);
+        __syncthreads();
+    }
     if (p || t >= T) return;
-    for (int i = 1; i < 32; ++i) join(held[i][tt]);
     const float l = sum == 0.f ? top : top + logf(sum);
     lse[t] = l;
     loss[t] = vocab::token_at(targets, wide_targets, t, N) >= 0 ? l - at_target[t] : 0.f;
@@ -268,6 +279,14 @@ int parts_of(int type) {
     return type == RETRO_F16 || type == RETRO_BF16 || type == RETRO_MXFP4 || type == RETRO_NVFP4 ? 1 : 2;
 }
 
+// And in the gradients of a BF16 x, where one part of 11 bits leaves the result's 8 as
+// they are: what the logits lose by it is an eighth of what x's own rounding put into
+// them. Two parts double both products: 2048 x 131072 x 4096 through Q8_0 7.6 ms
+// against 3.9. An F32 dW takes its parts in full.
+int grad_parts_of(int type, int xtype, bool weight_grad) {
+    return xtype == RETRO_BF16 && !(weight_grad && type == RETRO_F32) ? 1 : parts_of(type);
+}
+
 // Both operands in one 16-bit type, which the matrix cores take as they are.
 bool is_narrow(int type, int xtype) { return type == xtype && type != RETRO_F32; }
 
@@ -291,9 +310,9 @@ int64_t piece_rows(int64_t N, int64_t most) {
 }
 // planes of at most 2^27 elements
 int64_t plane_piece(int64_t K, int64_t N) { return piece_rows(N, std::min<int64_t>((1 << 27) / vocab::padded(K), 32768)); }
-// d of at most 2^26 elements a plane, where that leaves 4096 rows for the sums over them
+// d of at most 2^27 elements a plane, where that leaves 4096 rows for the sums over them
 int64_t grad_piece(int64_t K, int64_t N, int64_t T) {
-    return std::min(plane_piece(K, N), piece_rows(N, std::max<int64_t>((1 << 26) / std::max<int64_t>(T, 1), 4096)));
+    return std::min(plane_piece(K, N), piece_rows(N, std::max<int64_t>((1 << 27) / std::max<int64_t>(T, 1), 4096)));
 }
 int64_t few_piece(int64_t N, int64_t T) { return piece_rows(N, (1 << 24) / std::max<int64_t>(T, 1)); }
 
@@ -406,7 +425,7 @@ Backward backward_plan(int type, int64_t ldw, int xtype, bool weight_grad, bool 
     }
     const bool narrow = is_narrow(type, xtype), direct = is_direct(type, xtype, ldw, K);
     const int64_t Kp = vocab::padded(K), Tp = vocab::padded(T);
-    const int px = narrow ? 1 : parts_of(xtype), pw = narrow ? 1 : parts_of(type);
+    const int px = narrow ? 1 : parts_of(xtype), pw = narrow ? 1 : grad_parts_of(type, xtype, weight_grad);
     const int pd = xtype == RETRO_F32 || (weight_grad && type == RETRO_F32) ? 2 : 1;
     p.piece = grad_piece(K, N, T);
     p.x = b.take(plane_bytes(px, T, Kp));
@@ -502,7 +521,8 @@ int transpose(const void* in, int64_t pitch, int64_t rows, int64_t cols, void* o
 }
 
 // Rows n0 .. n0 + rows of the head as an operand: in place, or as planes.
-int head_rows(const Call& c, int64_t n0, int64_t rows, int64_t piece, uint8_t* planes, const uint32_t* top, Operand& o) {
+int head_rows(const Call& c, int64_t n0, int64_t rows, int64_t piece, int parts, uint8_t* planes, const uint32_t* top,
+              Operand& o) {
     if (is_direct(c.type, c.xtype, c.ldw, c.K)) {
         o = {c.W + n0 * c.ldw, c.ldw, 0, rows};
         return RETRO_OK;
@@ -510,7 +530,7 @@ int head_rows(const Call& c, int64_t n0, int64_t rows, int64_t piece, uint8_t* p
     const int64_t pitch = vocab::padded(c.K);
     o = {planes, pitch * 2, piece * pitch * 2, rows};
     vocab::PlaneArgs a{c.W + n0 * c.ldw,  c.ldw, rows, c.K, reinterpret_cast<uint16_t*>(planes), piece * pitch, top,
-                       is_narrow(c.type, c.xtype) ? 0 : parts_of(c.type)};
+                       is_narrow(c.type, c.xtype) ? 0 : parts};
     return vocab::with_type(c.type, [&](auto type) { return vocab::launch_planes<decltype(type)::value>(a, c.st); });
 }
 
@@ -585,15 +605,17 @@ int forward(const Call& c, float* loss, float* lse, uint8_t* ws) {
         g.at_target = at_target;
         for (g.n0 = 0; g.n0 < c.N; g.n0 += p.piece) {
             const int64_t rows = std::min(p.piece, c.N - g.n0);
-            RETRO_TRY(head_rows(c, g.n0, rows, p.piece, ws + p.planes, top, g.a));
+            RETRO_TRY(head_rows(c, g.n0, rows, p.piece, parts_of(c.type), ws + p.planes, top, g.a));
             g.part0 = runs;
             RETRO_TRY(with_element(c, [&](auto e) { return launch_logits<decltype(e), kStats, 1>(g, c.st); }));
             runs += logits_runs(rows, c.T);
         }
     }
     host::clear_last_error();
-    combine_kernel<<<dim3(uint32_t(cdiv(c.T, 8))), dim3(256), 0, c.st>>>(part, runs, c.T, c.targets, c.wide_targets, c.N,
-                                                                       at_target, loss, lse);
+    // neighbouring tokens' runs lie side by side: eight together where there are workgroups enough
+    auto combine = c.T > 512 ? combine_kernel<8> : combine_kernel<1>;
+    combine<<<dim3(uint32_t(cdiv(c.T, c.T > 512 ? 8 : 1))), dim3(256), 0, c.st>>>(
+        part, runs, c.T, c.targets, c.wide_targets, c.N, at_target, loss, lse);
     return host::launch_status();
 }
 
@@ -637,7 +659,7 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
     float* factor = narrow ? nullptr : reinterpret_cast<float*>(ws + p.factor);
     uint32_t* top = narrow ? nullptr : reinterpret_cast<uint32_t*>(ws + p.top);
     float *weight = reinterpret_cast<float*>(ws + p.weight), *unscale = reinterpret_cast<float*>(ws + p.unscale);
-    const int px = narrow ? 1 : parts_of(c.xtype), pw = narrow ? 1 : parts_of(c.type);
+    const int px = narrow ? 1 : parts_of(c.xtype), pw = narrow ? 1 : grad_parts_of(c.type, c.xtype, dW != nullptr);
     const int pd = c.xtype == RETRO_F32 || (dW && c.type == RETRO_F32) ? 2 : 1;
     const int64_t Kp = vocab::padded(c.K), Tp = vocab::padded(c.T);
     if (!narrow) RETRO_TRY(head_top(c, top));
@@ -670,13 +692,15 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
     g.across = dW ? reinterpret_cast<uint16_t*>(ws + p.across) : nullptr;
     for (g.n0 = 0; g.n0 < c.N; g.n0 += p.piece) {
         const int64_t rows = std::min(p.piece, c.N - g.n0), rows_p = vocab::padded(rows);
-        RETRO_TRY(head_rows(c, g.n0, rows, p.piece, ws + p.planes, top, g.a));
+        RETRO_TRY(head_rows(c, g.n0, rows, p.piece, pw, ws + p.planes, top, g.a));
         g.along_pitch = rows_p;
         g.along_plane = c.T * rows_p;
         g.across_pitch = Tp;
         g.across_plane = rows * Tp;
         RETRO_TRY(with_element(c, [&](auto e) {
-            return pd == 2 ? launch_logits<decltype(e), kProb, 2>(g, c.st) : launch_logits<decltype(e), kProb, 1>(g, c.st);
+            if constexpr (std::is_same<decltype(e), _Float16>::value)
+                if (pd == 2) return launch_logits<_Float16, kProb, 2>(g, c.st);
+            return launch_logits<decltype(e), kProb, 1>(g, c.st);
         }));
         if (dX) {
             // W^T of the piece, then sums[t][k] (+)= sum_n d[t][n] W[n][k]

@@ -24,6 +24,7 @@ namespace ce {
 using mx::f32x16;
 using mx::i32x4;
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -132,6 +133,31 @@ __device__ __forceinline__ void copies_done_for_all() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// What the wave's lanes wrote to LDS before is what they read after.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The parts of v as element `at` of w.
+template <typename E, int PARTS>
+__device__ __forceinline__ void put_parts(float v, int at, u16x4 (&w)[PARTS]) {
+    w[0][at] = __builtin_bit_cast(uint16_t, E(v));
+    if constexpr (PARTS == 2) w[1][at] = __builtin_bit_cast(uint16_t, E(vocab::rest_of<E>(v)));
+}
+
+// 8 elements to a place of any alignment of which `left` lie in the row.
+__device__ __forceinline__ void put8(uint16_t* to, int64_t left, const u16x8& w) {
+    typedef uint16_t any __attribute__((ext_vector_type(8), aligned(2)));
+    if (left >= 8) {
+        *reinterpret_cast<any*>(to) = w;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) to[i] = w[i];
+}
+
 template <typename E, class Z, Kind KIND, typename TO, int PARTS>
 __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const Args g) {
     constexpr int WB = Z::WB, BA = Z::BA, BB = Z::BB;
@@ -227,67 +253,85 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
     }
 
     // Element v of a block: row (v / 4) * 8 + 4 h + v % 4 of A, row r of B.
-    const int64_t aw = a0 + wa * BA * 32 + 4 * h, bw = b0 + wb * BB * 32 + r;
+    const int64_t aw = a0 + wa * BA * 32, bw = b0 + wb * BB * 32;
+    // The wave's own part of LDS, in which 16-bit results change places so that a lane
+    // stores 16 bytes of a row and a row's lanes whole lines.
+    constexpr int kStage = Z::kBytes / ((Z::kWaves + 1) / 2);
+    uint16_t* stage = reinterpret_cast<uint16_t*>((wave % 2 ? lds1 : lds0) + wave / 2 * kStage);
     if constexpr (KIND == kSum) {
         TO* out = static_cast<TO*>(g.out) + split * g.split_stride;
         const float f = g.out_factor ? *g.out_factor : 1.f;
+        if constexpr (sizeof(TO) == 2) {
+            constexpr int kPitch = BB * 32 + 8;
+            static_assert(32 * kPitch * 2 <= kStage, "a block row fits");
 #pragma unroll
-        for (int i = 0; i < BA; ++i)
+            for (int i = 0; i < BA; ++i) {
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int64_t row = aw + i * 32 + (v / 4) * 8 + v % 4;
-                if (row >= g.a.rows) continue;
+                for (int v = 0; v < 16; ++v)
 #pragma unroll
-                for (int j = 0; j < BB; ++j) {
-                    const int64_t col = bw + j * 32;
-                    if (col >= g.cols) continue;
-                    TO* to = out + row * g.ldo + col;
-                    const float c = g.out_factor ? acc[i][j][v] * f : acc[i][j][v];
-                    if constexpr (PARTS)  // of kSum: add
-                        *to = mx::from_f32<TO>(mx::to_f32(*to) + c);
-                    else
-                        __builtin_nontemporal_store(mx::from_f32<TO>(c), to);
+                    for (int j = 0; j < BB; ++j)
+                        stage[((v / 4) * 8 + 4 * h + v % 4) * kPitch + j * 32 + r] =
+                            __builtin_bit_cast(uint16_t, mx::from_f32<TO>(g.out_factor ? acc[i][j][v] * f : acc[i][j][v]));
+                wave_fence();
+                constexpr int kLanes = BB * 4, kRows = 64 / kLanes;  // lanes of a row, rows a store
+#pragma unroll
+                for (int p = 0; p < 32 / kRows; ++p) {
+                    const int at = p * kRows + lane / kLanes, col = lane % kLanes * 8;
+                    const u16x8 w = *reinterpret_cast<const u16x8*>(stage + at * kPitch + col);
+                    const int64_t row = aw + i * 32 + at, left = g.cols - (bw + col);
+                    if (row < g.a.rows) put8(reinterpret_cast<uint16_t*>(out + row * g.ldo + bw + col), left, w);
                 }
+                wave_fence();
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < BA; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int64_t row = aw + i * 32 + (v / 4) * 8 + 4 * h + v % 4;
+                    if (row >= g.a.rows) continue;
+#pragma unroll
+                    for (int j = 0; j < BB; ++j) {
+                        const int64_t col = bw + j * 32 + r;
+                        if (col >= g.cols) continue;
+                        TO* to = out + row * g.ldo + col;
+                        const float c = g.out_factor ? acc[i][j][v] * f : acc[i][j][v];
+                        if constexpr (PARTS)  // of kSum: add
+                            *to = *to + c;
+                        else
+                            *to = c;
+                    }
+                }
+        }
         return;
     }
 
     const float by_top = g.factor ? vocab::unscale_of(*g.top) : 1.f;
+    auto scaled = [&](int j, int64_t t) {
+        if (!g.factor || t >= g.b.rows) return;
+        const float f = g.factor[t];
 #pragma unroll
-    for (int j = 0; j < BB; ++j) {
-        const int64_t t = bw + j * 32;
-        if constexpr (KIND == kProb) {
-            // the padding of the head's rows past the last token is zeros
-            if (t >= g.b.rows && g.across && t < g.across_pitch)
+        for (int i = 0; i < BA; ++i)
 #pragma unroll
-                for (int i = 0; i < BA; ++i)
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = acc[i][j][v] * f * by_top;
+    };
+    // the target as a row of this lane's, were it one
+    auto target_of = [&](int token) { return int64_t(token) - g.n0 - aw - 4 * h; };
+
+    if constexpr (KIND == kStats) {
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int64_t row = aw + i * 32 + (v / 4) * 8 + v % 4;
-                        if (row >= g.a.rows) continue;
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part)
-                            g.across[part * g.across_plane + row * g.across_pitch + t] = 0;
-                    }
-        }
-        if (t >= g.b.rows) continue;  // both halves of the wave alike
-        if (g.factor) {
-            const float f = g.factor[t];
-#pragma unroll
-            for (int i = 0; i < BA; ++i)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = acc[i][j][v] * f * by_top;
-        }
-        // the target as a row of this lane's, were it one
-        const int64_t target = int64_t(vocab::token_at(g.targets, g.wide_targets, t, g.N)) - g.n0 - aw;
-        if constexpr (KIND == kStats) {
+        for (int j = 0; j < BB; ++j) {
+            const int64_t t = bw + j * 32 + r;
+            if (t >= g.b.rows) continue;  // both halves of the wave alike
+            scaled(j, t);
+            const int64_t target = target_of(vocab::token_at(g.targets, g.wide_targets, t, g.N));
             float top = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < BA; ++i)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int at = i * 32 + (v / 4) * 8 + v % 4;
-                    if (aw + at >= g.a.rows) acc[i][j][v] = -__builtin_inff();
+                    if (aw + 4 * h + at >= g.a.rows) acc[i][j][v] = -__builtin_inff();
                     top = fmaxf(top, acc[i][j][v]);
                     if (target == at) g.at_target[t] = acc[i][j][v];
                 }
@@ -300,45 +344,94 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
                 for (int v = 0; v < 16; ++v) sum += exp_of(acc[i][j][v] - from);
             sum += __shfl_xor(sum, 32);
             if (h == 0) g.part[(g.part0 + (a0 / 32 + wa * BA) / BA) * g.b.rows + t] = make_float2(top, sum);
-        } else {
-            const float lse = g.lse[t];
-            const bool learnt = vocab::token_at(g.targets, g.wide_targets, t, g.N) >= 0;
-            const float weight = g.weight ? g.weight[t] : 0.f;
+        }
+    }
+    if constexpr (KIND == kProb) {
+        float weight[BB];
+        bool learnt[BB];
+#pragma unroll
+        for (int j = 0; j < BB; ++j) {
+            // logits become d; the padding past the last token and the last row is zeros
+            const int64_t t = bw + j * 32 + r;
+            const int token = t < g.b.rows ? vocab::token_at(g.targets, g.wide_targets, t, g.N) : -1;
+            learnt[j] = token >= 0;
+            weight[j] = learnt[j] && g.weight ? g.weight[t] : 0.f;
+            const float lse = learnt[j] ? g.lse[t] : 0.f;
+            const int64_t target = target_of(token);
+            scaled(j, t);
 #pragma unroll
             for (int i = 0; i < BA; ++i)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int at = i * 32 + q * 8;
-                    float d[4];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        d[v] = exp_of(acc[i][j][q * 4 + v] - lse) - (target == at + v ? 1.f : 0.f);
-                        if (!learnt || aw + at + v >= g.a.rows) d[v] = 0.f;
-                    }
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part) {
-                        if (!g.along) break;
-                        u16x4 w;
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            float p = d[v] * g.by;
-                            if (part) p = vocab::rest_of<E>(p);
-                            w[v] = __builtin_bit_cast(uint16_t, E(p));
-                        }
-                        // the padding past the head's last row is written too
-                        if (aw + at < g.along_pitch)
-                            *reinterpret_cast<u16x4*>(g.along + part * g.along_plane + t * g.along_pitch + aw + at) = w;
-                    }
-                    if (!g.across) continue;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        if (aw + at + v >= g.a.rows) continue;
-                        uint16_t* to = g.across + (aw + at + v) * g.across_pitch + t;
-                        const float p = learnt ? d[v] * weight : 0.f;
-                        *to = __builtin_bit_cast(uint16_t, E(p));
-                        if constexpr (PARTS == 2) to[g.across_plane] = __builtin_bit_cast(uint16_t, E(vocab::rest_of<E>(p)));
-                    }
+                for (int v = 0; v < 16; ++v) {
+                    const int at = i * 32 + (v / 4) * 8 + v % 4;
+                    const float d = exp_of(acc[i][j][v] - lse) - (target == at ? 1.f : 0.f);
+                    acc[i][j][v] = learnt[j] && aw + 4 * h + at < g.a.rows ? d : 0.f;
                 }
+        }
+        if (g.along) {
+            // rows of tokens: a lane has four neighbouring elements of its token's row
+            constexpr int kBlocks = PARTS == 2 && BA > 1 ? BA / 2 : BA;  // of 32 rows of the head at a time
+            constexpr int kPitch = kBlocks * 32 + 8, kLanes = kBlocks * 4, kRows = 64 / kLanes, kPlane = 32 * kPitch;
+            static_assert(PARTS * kPlane * 2 <= kStage, "32 tokens' rows fit");
+#pragma unroll
+            for (int j = 0; j < BB; ++j)
+#pragma unroll
+                for (int i0 = 0; i0 < BA; i0 += kBlocks) {
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            u16x4 w[PARTS];
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) put_parts<E, PARTS>(acc[i0 + i][j][q * 4 + v] * g.by, v, w);
+#pragma unroll
+                            for (int part = 0; part < PARTS; ++part)
+                                *reinterpret_cast<u16x4*>(stage + part * kPlane + r * kPitch + i * 32 + q * 8 + 4 * h) =
+                                    w[part];
+                        }
+                    wave_fence();
+#pragma unroll
+                    for (int p = 0; p < 32 / kRows; ++p) {
+                        const int at = p * kRows + lane / kLanes, col = lane % kLanes * 8;
+                        const int64_t t = bw + j * 32 + at, row = aw + i0 * 32 + col;
+                        // rows are whole 64s
+                        if (t < g.b.rows && row < g.along_pitch)
+#pragma unroll
+                            for (int part = 0; part < PARTS; ++part)
+                                *reinterpret_cast<u16x8*>(g.along + part * g.along_plane + t * g.along_pitch + row) =
+                                    *reinterpret_cast<const u16x8*>(stage + part * kPlane + at * kPitch + col);
+                    }
+                    wave_fence();
+                }
+        }
+        if (g.across) {
+            constexpr int kPitch = BB * 32 + 8, kLanes = BB * 4, kRows = 64 / kLanes, kPlane = 32 * kPitch;
+            static_assert(PARTS * kPlane * 2 <= kStage, "32 rows of the head fit");
+#pragma unroll
+            for (int i = 0; i < BA; ++i) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+#pragma unroll
+                    for (int j = 0; j < BB; ++j) {
+                        u16x4 w[PARTS];
+                        put_parts<E, PARTS>(learnt[j] ? acc[i][j][v] * weight[j] : 0.f, 0, w);
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            stage[part * kPlane + ((v / 4) * 8 + 4 * h + v % 4) * kPitch + j * 32 + r] = w[part][0];
+                    }
+                wave_fence();
+#pragma unroll
+                for (int p = 0; p < 32 / kRows; ++p) {
+                    const int at = p * kRows + lane / kLanes, col = lane % kLanes * 8;
+                    const int64_t row = aw + i * 32 + at;
+                    if (row < g.a.rows && bw + col < g.across_pitch)
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            *reinterpret_cast<u16x8*>(g.across + part * g.across_plane + row * g.across_pitch + bw + col) =
+                                *reinterpret_cast<const u16x8*>(stage + part * kPlane + at * kPitch + col);
+                }
+                wave_fence();
+            }
         }
     }
 }

@@ -16,6 +16,10 @@ using mx::Span;
 // An id that is none sorts last, as N. The sorted list is cut into runs of 64; an id
 // whose tokens lie in several runs has the sum of each run's part made first, by
 // workgroups of their own, so that a frequent id is not one workgroup's work.
+//
+// What bounds it is the table's rows being written. With many more rows than tokens
+// all of them are cleared beside the sort, in the same launches, and only the rows of
+// tokens are then written from their sums; else each row looks its tokens up.
 
 constexpr int kMaxBits = 9, kMaxDigits = 1 << kMaxBits;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
@@ -44,6 +48,25 @@ __device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t t
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// Zeros over rows of `row` bytes `pitch` apart, 16 bytes a step, the steps begin ..
+// end of them all dealt to `workers` threads. A row is whole 2s.
+struct Fill {
+    uint8_t* p;
+    int64_t pitch, row, per, begin, end;  // per: steps of a row
+};
+__device__ __forceinline__ void fill(const Fill& f, int64_t worker, int64_t workers) {
+    typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
+    for (int64_t at = f.begin + worker; at < f.end; at += workers) {
+        const int64_t r = f.per >= f.end ? 0 : at / f.per, b = (at - r * f.per) * 16;
+        uint8_t* to = f.p + r * f.pitch + b;
+        if (b + 16 <= f.row) {
+            *reinterpret_cast<words*>(to) = words{0, 0, 0, 0};
+        } else {
+            for (int64_t i = 0; i < f.row - b; i += 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
+        }
+    }
 }
 
 // The lane's place among the lanes of its wave that have its digit (live lanes only),
@@ -76,12 +99,16 @@ __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* waves) {
     return before + in - v;
 }
 
-// Up to kSmallT tokens: all passes in one workgroup. Wave w takes items w * per ..,
+// Up to kSmallT tokens: all passes in one workgroup, the other workgroups fill. Wave w takes items w * per ..,
 // 64 at a time, and keeps a count a digit: an item's place is its digit's first, the
 // counts of the waves before, its wave's count so far, and the lanes before it.
 __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __restrict__ ids, bool wide, int64_t N,
                                                                  int T, int passes, int bits, uint32_t* __restrict__ keys,
-                                                                 uint32_t* __restrict__ order) {
+                                                                 uint32_t* __restrict__ order, Fill f) {
+    if (blockIdx.x > 0) {
+        fill(f, int64_t(blockIdx.x - 1) * kSortThreads + threadIdx.x, int64_t(gridDim.x - 1) * kSortThreads);
+        return;
+    }
     constexpr int kPer = kSmallT / kSortThreads;
     __shared__ uint32_t key[kSmallT];
     __shared__ uint16_t from[kSmallT];
@@ -149,13 +176,18 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __
 }
 
 // A pass of a larger sort: a workgroup kBlockItems items, a wave a quarter of them in
-// rows of 64. With `totals` NULL the digits of each workgroup are counted, into
+// rows of 64; the workgroups past `blocks` fill. With `totals` NULL the digits of each workgroup are counted, into
 // counts[digit][workgroup]; then counts holds the items of the digit in workgroups
 // before, totals the digits' numbers, and the items are moved.
 __global__ __launch_bounds__(kBlockThreads) void sort_pass_kernel(
     const void* __restrict__ ids, bool wide, int64_t N, const uint32_t* __restrict__ keys_in,
-    const uint32_t* __restrict__ order_in, int64_t T, int shift, int bits, uint32_t* __restrict__ counts,
-    const uint32_t* __restrict__ totals, uint32_t* __restrict__ keys, uint32_t* __restrict__ order) {
+    const uint32_t* __restrict__ order_in, int64_t T, int shift, int bits, uint32_t blocks,
+    uint32_t* __restrict__ counts, const uint32_t* __restrict__ totals, uint32_t* __restrict__ keys,
+    uint32_t* __restrict__ order, Fill f) {
+    if (blockIdx.x >= blocks) {
+        fill(f, int64_t(blockIdx.x - blocks) * kBlockThreads + threadIdx.x, int64_t(gridDim.x - blocks) * kBlockThreads);
+        return;
+    }
     constexpr int kRounds = kBlockItems / kBlockThreads;
     __shared__ uint32_t count[kBlockWaves][kMaxDigits];
     __shared__ uint32_t waves[kBlockWaves];
@@ -183,7 +215,7 @@ __global__ __launch_bounds__(kBlockThreads) void sort_pass_kernel(
         for (int d = threadIdx.x; d < digits; d += kBlockThreads) {
             uint32_t all = 0;
             for (int w = 0; w < kBlockWaves; ++w) all += count[w][d];
-            counts[int64_t(d) * gridDim.x + blockIdx.x] = all;
+            counts[int64_t(d) * blocks + blockIdx.x] = all;
         }
         return;
     }
@@ -192,7 +224,7 @@ __global__ __launch_bounds__(kBlockThreads) void sort_pass_kernel(
         const int d = d0 + threadIdx.x;
         const uint32_t n = d < digits ? totals[d] : 0, below = scan<kBlockThreads>(n, waves);
         if (d < digits) {
-            uint32_t to = before + below + counts[int64_t(d) * gridDim.x + blockIdx.x];
+            uint32_t to = before + below + counts[int64_t(d) * blocks + blockIdx.x];
             for (int w = 0; w < kBlockWaves; ++w) {
                 const uint32_t of = count[w][d];
                 count[w][d] = to;
@@ -232,41 +264,42 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(uint32_t* __restrict__ c
     if (threadIdx.x == 0) totals[blockIdx.x] = before;
 }
 
-__global__ __launch_bounds__(256) void clear_kernel(uint2* p, int64_t n) {
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) p[i] = make_uint2(0, 0);
+// The first place at or after `from` whose key is `key` or above (list of T keys).
+__device__ __forceinline__ uint32_t first_of(const uint32_t* __restrict__ keys, uint32_t from, uint32_t T, uint32_t key) {
+    uint32_t low = from, high = T;
+    while (low < high) {
+        const uint32_t mid = low + (high - low) / 2;
+        if (keys[mid] < key)
+            low = mid + 1;
+        else
+            high = mid;
+    }
+    return low;
 }
 
-// span[id] = the id's first place in the sorted list and the place after its last.
-__global__ __launch_bounds__(256) void spans_kernel(const uint32_t* __restrict__ keys, int64_t T, int64_t N,
-                                                    uint2* __restrict__ span) {
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= T) return;
-    const uint32_t k = keys[i];
-    if (k >= N) return;
-    if (i == 0 || keys[i - 1] != k) span[k].x = uint32_t(i);
-    if (i + 1 == T || keys[i + 1] != k) span[k].y = uint32_t(i) + 1;
+// The place after the last of the keys that are as at `from`: most have few, so the
+// steps double until they pass it.
+__device__ __forceinline__ uint32_t end_of(const uint32_t* __restrict__ keys, uint32_t from, uint32_t T) {
+    const uint32_t key = keys[from];
+    uint32_t step = 1;
+    while (step < T - from && keys[from + step] == key) step *= 2;
+    return first_of(keys, from + step / 2, min(T, from + step), key + 1);
 }
 
 // The sum of dY's rows order[i] for begin <= i < end, in that order.
 template <typename TY>
 __device__ __forceinline__ void sum_rows(const TY* __restrict__ dY, int64_t ldy, int64_t left,
                                          const uint32_t* __restrict__ order, uint32_t begin, uint32_t end, float e[8]) {
-    uint32_t i = begin;
-    for (; i + 4 <= end; i += 4) {
-        float v[4][8];
+    // eight rows in flight; what is past the end is the last row again, not added
+    for (uint32_t i = begin; i < end; i += 8) {
+        float v[8][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx::load8(dY + int64_t(order[i + j]) * ldy, left, v[j]);
+        for (int j = 0; j < 8; ++j) mx::load8(dY + int64_t(order[min(i + j, end - 1)]) * ldy, left, v[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 8; ++j)
+            if (i + j < end)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) e[c] += v[j][c];
-    }
-    for (; i < end; ++i) {
-        float v[8];
-        mx::load8(dY + int64_t(order[i]) * ldy, left, v);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) e[c] += v[c];
+                for (int c = 0; c < 8; ++c) e[c] += v[j][c];
     }
 }
 
@@ -291,54 +324,54 @@ __global__ __launch_bounds__(256) void parts_kernel(const TY* __restrict__ dY, i
         sum_rows(dY + k, ldy, K - k, order, b, e, v);
         store8(parts + (2 * c + slot) * pitch + k, 8, v);
     };
-    if (head < N && (from_before || (goes_on && head == tail))) {
-        uint32_t e = begin + 1;
-        while (e < end && keys[e] == head) ++e;
-        put(0, begin, e);
-    }
-    if (goes_on && tail < N && head != tail) {
-        uint32_t b = end - 1;
-        while (keys[b - 1] == tail) --b;
-        put(1, b, end);
-    }
+    if (head < N && (from_before || (goes_on && head == tail))) put(0, begin, first_of(keys, begin, end, head + 1));
+    if (goes_on && tail < N && head != tail) put(1, first_of(keys, begin, end, tail), end);
 }
 
-// Rows of dW from their tokens. A thread 8 columns of a row: of every row (each is
-// written), or, when adding, of the row of every place in the sorted list where an id
-// begins.
-template <typename TY, typename TW, bool ADD>
+// Rows of dW from their tokens. A thread 8 columns: of every row (kAll), or of the
+// row of each place in the sorted list where an id begins (kHeads: written, kAdd: added).
+enum Rows { kAll, kHeads, kAdd };
+template <typename TY, typename TW, Rows ROWS>
 __global__ __launch_bounds__(256) void rows_kernel(const TY* __restrict__ dY, int64_t ldy, float scale,
-                                                   TW* __restrict__ dW, int64_t ldw, int64_t K, int64_t T, int64_t N,
+                                                   TW* __restrict__ dW, int64_t ldw, int64_t K, uint32_t T, int64_t N,
                                                    const uint32_t* __restrict__ keys, const uint32_t* __restrict__ order,
-                                                   const uint2* __restrict__ span, const float* __restrict__ parts,
-                                                   uint32_t per, int64_t first_block) {
+                                                   const float* __restrict__ parts, uint32_t per, int64_t first_block) {
     const int64_t at = (first_block + blockIdx.x) * 256 + threadIdx.x;
     int64_t row = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
     const int64_t k = (at - row * per) * 8, pitch = int64_t(per) * 8;
-    if (row >= (ADD ? T : N)) return;
-    if constexpr (ADD) {
-        const uint32_t key = keys[row];
-        if (key >= N || (row > 0 && keys[row - 1] == key)) return;
-        row = key;
-    }
-    const uint2 s = span[row];
-    float e[8] = {};
-    const uint32_t c0 = s.x / kRun, c1 = s.y == 0 ? c0 : (s.y - 1) / kRun;
-    if (c0 == c1) {
-        sum_rows(dY + k, ldy, K - k, order, s.x, s.y, e);
+    if (row >= (ROWS == kAll ? N : int64_t(T))) return;
+    uint32_t begin = uint32_t(row), end;
+    if constexpr (ROWS == kAll) {
+        begin = first_of(keys, 0, T, uint32_t(row));
+        end = begin < T && keys[begin] == row ? end_of(keys, begin, T) : begin;
     } else {
-        for (uint32_t c = c0; c <= c1; ++c) {
-            float v[8];
-            mx::load8(parts + (2 * int64_t(c) + (c == c0 && s.x % kRun ? 1 : 0)) * pitch + k, 8, v);
+        row = keys[begin];
+        if (row >= N || (begin > 0 && keys[begin - 1] == row)) return;
+        end = end_of(keys, begin, T);
+    }
+    float e[8] = {};
+    const uint32_t c0 = begin / kRun, c1 = end == begin ? c0 : (end - 1) / kRun;
+    if (c0 == c1) {
+        sum_rows(dY + k, ldy, K - k, order, begin, end, e);
+    } else {
+        const float* from = parts + 2 * int64_t(c0) * pitch + k;
+        mx::load8(from + (begin % kRun ? pitch : 0), 8, e);
+        for (uint32_t c = 1; c <= c1 - c0; c += 4) {
+            float v[4][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] += v[i];
+            for (int j = 0; j < 4; ++j) mx::load8(from + 2 * int64_t(min(c + j, c1 - c0)) * pitch, 8, v[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j <= c1 - c0)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[i] += v[j][i];
         }
     }
     TW* to = dW + row * ldw + k;
-    if (s.x != s.y)  // a row of no token is zeros whatever the scale
+    if (begin != end)  // a row of no token is zeros whatever the scale
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] *= scale;
-    if constexpr (ADD) {
+    if constexpr (ROWS == kAdd) {
         float old[8];
         mx::load8(to, K - k, old);
 #pragma unroll
@@ -347,9 +380,13 @@ __global__ __launch_bounds__(256) void rows_kernel(const TY* __restrict__ dY, in
     store8(to, K - k, e);
 }
 
+// Whether all rows are cleared beside the sort and then those of tokens written: where
+// more than half of them are of no token.
+bool clears(int64_t N, int64_t T) { return 2 * T < N; }
+
 struct Plan {
     Radix radix;
-    int64_t keys[2], order[2], counts, totals, span, parts, bytes;
+    int64_t keys[2], order[2], counts, totals, parts, bytes;
     int64_t blocks;
 };
 
@@ -370,7 +407,6 @@ Plan plan_of(int64_t K, int64_t N, int64_t T) {
         p.counts = take(4 * p.blocks << p.radix.bits);
         p.totals = take(4 << p.radix.bits);
     }
-    p.span = take(8 * N);
     p.parts = take(4 * 2 * cdiv(T, kRun) * cdiv(K, 8) * 8);
     return p;
 }
@@ -381,26 +417,36 @@ Plan plan_of(int64_t K, int64_t N, int64_t T) {
         if (rc_ != RETRO_OK) return rc_; \
     } while (0)
 
-// Sorted keys and tokens end in plane `out` of the workspace.
-int sort(const Plan& p, const void* ids, bool wide, int64_t N, int64_t T, uint8_t* ws, int& out, hipStream_t st) {
+// Sorted keys and tokens end in plane `out` of the workspace; `f`, where it has
+// steps, is filled in shares beside the sort's launches.
+int sort(const Plan& p, const void* ids, bool wide, int64_t N, int64_t T, uint8_t* ws, int& out, Fill f, hipStream_t st) {
     auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
+    // eight waves a SIMD's worth of workgroups, or fewer where each has little to do
+    auto fillers = [](const Fill& f, int threads) {
+        return uint32_t(std::min<int64_t>(cdiv(f.end - f.begin, 4 * threads), host::kNumCUs * 2048 / threads));
+    };
     out = 0;
     host::clear_last_error();
     if (T <= kSmallT) {
-        sort_small_kernel<<<dim3(1), dim3(kSortThreads), 0, st>>>(ids, wide, N, int(T), p.radix.passes, p.radix.bits,
-                                                                 words(p.keys[0]), words(p.order[0]));
+        sort_small_kernel<<<dim3(1 + fillers(f, kSortThreads)), dim3(kSortThreads), 0, st>>>(
+            ids, wide, N, int(T), p.radix.passes, p.radix.bits, words(p.keys[0]), words(p.order[0]), f);
         return host::launch_status();
     }
-    const dim3 grid(uint32_t(p.blocks)), threads(kBlockThreads);
+    const uint32_t blocks = uint32_t(p.blocks);
+    const int64_t steps = f.end, shares = 2 * p.radix.passes;
     for (int i = 0; i < p.radix.passes; ++i) {
         const uint32_t *keys_in = i ? words(p.keys[out]) : nullptr, *order_in = i ? words(p.order[out]) : nullptr;
         const int to = i ? 1 - out : 0, shift = i * p.radix.bits;
         uint32_t *counts = words(p.counts), *totals = words(p.totals);
-        sort_pass_kernel<<<grid, threads, 0, st>>>(ids, wide, N, keys_in, order_in, T, shift, p.radix.bits, counts,
-                                                   nullptr, nullptr, nullptr);
-        sort_scan_kernel<<<dim3(1u << p.radix.bits), dim3(256), 0, st>>>(counts, uint32_t(p.blocks), totals);
-        sort_pass_kernel<<<grid, threads, 0, st>>>(ids, wide, N, keys_in, order_in, T, shift, p.radix.bits, counts,
-                                                   totals, words(p.keys[to]), words(p.order[to]));
+        auto pass = [&](int share, const uint32_t* of, uint32_t* keys, uint32_t* order) {
+            f.begin = steps * share / shares;
+            f.end = steps * (share + 1) / shares;
+            sort_pass_kernel<<<dim3(blocks + fillers(f, kBlockThreads)), dim3(kBlockThreads), 0, st>>>(
+                ids, wide, N, keys_in, order_in, T, shift, p.radix.bits, blocks, counts, of, keys, order, f);
+        };
+        pass(2 * i, nullptr, nullptr, nullptr);
+        sort_scan_kernel<<<dim3(1u << p.radix.bits), dim3(256), 0, st>>>(counts, blocks, totals);
+        pass(2 * i + 1, totals, words(p.keys[to]), words(p.order[to]));
         out = to;
     }
     return host::launch_status();
@@ -456,26 +502,30 @@ int retro_embedding_backward(int idtype, const void* ids, int ytype, const void*
     if (!mx::aligned(dW, wsize) || !mx::aligned(dY, ys) || !mx::aligned(ids, idsize)) return RETRO_E_ALIGN;
     const Span w{dW, wb}, y{dY, yb}, i{ids, T * idsize}, s{workspace, need};
     if (mx::overlap(w, y) || mx::overlap(w, i)) return RETRO_E_ALIAS;
-    if (!workspace || workspace_bytes < need || !mx::aligned(workspace, 16) || mx::overlap(s, w) || mx::overlap(s, y) ||
-        mx::overlap(s, i))
+    if (need && (!workspace || workspace_bytes < need || !mx::aligned(workspace, 16) || mx::overlap(s, w) ||
+                 mx::overlap(s, y) || mx::overlap(s, i)))
         return RETRO_E_WORKSPACE;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const Plan p = plan_of(K, N, T);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    uint2* span = reinterpret_cast<uint2*>(ws + p.span);
     float* parts = reinterpret_cast<float*>(ws + p.parts);
-    if (!accumulate)
-        RETRO_TRY(mx::in_block_ranges(cdiv(N, 256), [&](int64_t first, uint32_t blocks) {
-            clear_kernel<<<dim3(blocks), dim3(256), 0, st>>>(span + first * 256, N - first * 256);
-        }));
     int out = 0;
-    if (T > 0) {
-        RETRO_TRY(sort(p, ids, idtype == RETRO_I64, N, T, ws, out, st));
-        host::clear_last_error();
-        spans_kernel<<<dim3(uint32_t(cdiv(T, 256))), dim3(256), 0, st>>>(
-            reinterpret_cast<uint32_t*>(ws + p.keys[out]), T, N, span);
-        RETRO_TRY(host::launch_status());
+    const bool cleared = !accumulate && clears(N, T);
+    Fill f = {};
+    if (cleared) {
+        f.p = static_cast<uint8_t*>(dW);
+        f.pitch = ldw * wsize;
+        f.row = K * wsize;
+        int64_t rows = N;
+        if (f.pitch == f.row) {  // one long row
+            f.row *= N;
+            rows = 1;
+        }
+        f.per = cdiv(f.row, 16);
+        f.end = rows * f.per;
     }
+    RETRO_TRY(sort(p, ids, idtype == RETRO_I64, N, T, ws, out, f, st));
+    if (T == 0 && cleared) return RETRO_OK;
     const uint32_t *keys = reinterpret_cast<uint32_t*>(ws + p.keys[out]),
                    *order = reinterpret_cast<uint32_t*>(ws + p.order[out]);
     const uint32_t per = uint32_t(cdiv(K, 8));
@@ -488,10 +538,11 @@ int retro_embedding_backward(int idtype, const void* ids, int ytype, const void*
             }));
         return mx::with_float(wtype, [&](auto* wtag) {
             using TW = std::remove_pointer_t<decltype(wtag)>;
-            return mx::in_block_ranges(cdiv((accumulate ? T : N) * per, 256), [&](int64_t first, uint32_t blocks) {
-                auto kernel = accumulate ? rows_kernel<TY, TW, true> : rows_kernel<TY, TW, false>;
-                kernel<<<dim3(blocks), dim3(256), 0, st>>>(dy, ldy, scale, static_cast<TW*>(dW), ldw, K, T, N, keys,
-                                                           order, span, parts, per, first);
+            const bool all = !accumulate && !cleared;
+            return mx::in_block_ranges(cdiv((all ? N : T) * per, 256), [&](int64_t first, uint32_t blocks) {
+                auto kernel = all ? rows_kernel<TY, TW, kAll> : accumulate ? rows_kernel<TY, TW, kAdd> : rows_kernel<TY, TW, kHeads>;
+                kernel<<<dim3(blocks), dim3(256), 0, st>>>(dy, ldy, scale, static_cast<TW*>(dW), ldw, K, uint32_t(T), N,
+                                                           keys, order, parts, per, first);
             });
         });
     });

@@ -119,5 +119,5 @@ def test_workspace_sizes():
     assert f(q.BF16, 8192, q.BF16, 4096, 131072, 4096) < 1 << 27
     assert f(q.BF16, 128, q.BF16, 64, 100, 0) == 0 and b(q.BF16, 128, q.BF16, 1, 64, 0, 5) == 0
     assert b(q.Q8_0, 68, q.BF16, 1, 64, 10, 5) == q.E_TYPE and f(q.BF16, 2, q.BF16, 64, 10, 5) == q.E_SHAPE
-    assert e(64, 10, 0) > 0 and e(0, 10, 5) == 0 and e(64, 0, 5) == 0 and e(-1, 1, 1) == q.E_SHAPE
+    assert e(64, 10, 0) == 0 and e(64, 10, 1) > 0 and e(0, 10, 5) == 0 and e(64, 0, 5) == 0 and e(-1, 1, 1) == q.E_SHAPE
     assert e(4096, 131072, 16384) < 1 << 24

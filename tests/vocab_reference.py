@@ -40,9 +40,10 @@ def loss_error(w, x, lse):
     return 2 * logit_error(w, x).amax(1) + (128 + 32 + 16) * 2.0 ** -24 + 2.0 ** -20 + lse.abs() * 2.0 ** -22
 
 
-def gradients(w, x, targets, dloss, part_error, dtype_x, dtype_w):
+def gradients(w, x, targets, dloss, part_error, dtype_x, dtype_w, head_error=0.0):
     """((dx, its bound), (dw, its bound)). part_error is the relative rounding of d in
-    the products; d's own error is that of exp: two logits' and lse's."""
+    the products, head_error that of the head's values in logits and products; d's own
+    error is that of exp: two logits' and lse's."""
     loss, lse, learnt, l = cross_entropy(w, x, targets)
     p = torch.exp(l - lse[:, None])
     d = p.clone()
@@ -50,7 +51,9 @@ def gradients(w, x, targets, dloss, part_error, dtype_x, dtype_w):
     d[t, targets[t]] -= 1
     g = torch.where(learnt, dloss.double(), 0.0)[:, None]
     d = torch.where(learnt[:, None], d, 0.0)
-    off = logit_error(w, x) + loss_error(w, x, lse)[:, None] + 2.0 ** -20
+    off = logit_error(w, x) + loss_error(w, x, lse)[:, None] + 2.0 ** -20 + head_error * (x.abs() @ w.abs().T)
+    # exp(off) - 1, at most twice off while that is below 1
+    off = torch.where(off < 1, 2 * off, torch.exp(off))
     # 2^-39: the smallest steps of F16 under the scale of 2^14
     ed = p * off + 2.0 ** -23 * d.abs() + part_error * d.abs() + 2.0 ** -38
     ed = torch.where(learnt[:, None], ed, 0.0)
@@ -58,7 +61,7 @@ def gradients(w, x, targets, dloss, part_error, dtype_x, dtype_w):
     N, T = w.shape[0], x.shape[0]
     dx, dw = g * (d @ w), (g * d).T @ x
     sums = 3 * 2.0 ** -22
-    bx = g.abs() * (ed @ w.abs() + ((N / 16 + 64) * STEP + sums) * (d.abs() @ w.abs()) + 2.0 ** -38 * w.abs().max() * d.abs().sum(1, keepdim=True))
+    bx = g.abs() * (ed @ w.abs() + ((N / 16 + 64) * STEP + sums + head_error) * (d.abs() @ w.abs()) + 2.0 ** -38 * w.abs().max() * d.abs().sum(1, keepdim=True))
     top = g.abs().max() * x.abs().max()
     bw = (g.abs() * ed).T @ x.abs() + ((T / 16 + 64) * STEP + sums) * ((g * d).abs().T @ x.abs()) + 2.0 ** -38 * top * T
     tiny_x, tiny_w = torch.finfo(dtype_x).smallest_normal, torch.finfo(dtype_w).smallest_normal
