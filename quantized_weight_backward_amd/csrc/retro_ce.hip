@@ -254,10 +254,11 @@ __global__ __launch_bounds__(256) void run_prob_kernel(float* __restrict__ l, in
 
 using Big = Tile<2, 4, 4, 2>;     // 256 x 256
 using Mid = Tile<2, 2, 2, 2>;     // 128 x 128
-using Rows64 = Tile<4, 1, 1, 2>;  // 128 rows of A by 64 of B
-using Rows32 = Tile<4, 1, 1, 1>;
-using Cols64 = Tile<1, 4, 2, 1>;  // 64 rows of A by 128 of B
-using Cols32 = Tile<1, 4, 1, 1>;
+using Rows64 = Tile<4, 1, 1, 2, 3>;   // 128 rows of A by 64 of B
+using Half64 = Tile<2, 1, 1, 2, 4>;   // 64 by 64
+using Rows32 = Tile<4, 1, 1, 1, 4>;   // 128 by 32
+using Cols64 = Tile<1, 4, 2, 1, 3>;   // 64 rows of A by 128 of B
+using Cols32 = Tile<1, 4, 1, 1, 4>;
 
 struct Call {
     int type, xtype;
@@ -316,6 +317,10 @@ int64_t grad_piece(int64_t K, int64_t N, int64_t T) {
 }
 int64_t few_piece(int64_t N, int64_t T) { return piece_rows(N, (1 << 24) / std::max<int64_t>(T, 1)); }
 
+// Elements between rows along a piece of the head: 128 bytes more than its whole steps,
+// so that neighbouring rows do not lie a power of two apart and on one memory channel.
+int64_t grad_pitch(int64_t rows) { return vocab::padded(rows) + vocab::kStepK; }
+
 // Parts of the workspace, each on a 256-byte boundary.
 struct Bump {
     int64_t at = 0;
@@ -329,23 +334,42 @@ struct Bump {
 template <class Z>
 int64_t runs_of(int64_t rows) { return cdiv(rows, Z::kRowsA) * Z::WA; }
 
-// Rows of tokens, rows of the head by how many: 256 x 256 tiles where they leave few
-// CUs idle.
-enum Shape { kBig, kMid, kSmall64, kSmall32 };
+// Tile of a number of the head's rows and of tokens: 256 x 256 where they leave few CUs
+// idle.
+enum Shape { kBig, kMid, kSmall64, kHalf64, kSmall32 };
 Shape shape_of(int64_t rows, int64_t tokens) {
     if (tokens <= 32) return kSmall32;
-    if (tokens <= 64) return kSmall64;
+    if (tokens <= 64) return cdiv(rows, 128) >= 2 * host::kNumCUs ? kSmall64 : kHalf64;
     if (tokens <= 128) return kMid;
     return cdiv(rows, 256) * cdiv(tokens, 256) >= 128 ? kBig : kMid;
 }
 
-int64_t logits_runs(int64_t rows, int64_t tokens) {
-    switch (shape_of(rows, tokens)) {
+// Rows of the head in whole rounds of 256 x 256 tiles over the CUs, where what is left
+// would fill less than half of another: it goes to smaller tiles in a launch of its
+// own. 50001 x 2048 and 1021 tokens: 784 tiles, three rounds and 16.
+int64_t rows_of_rounds(int64_t rows, int64_t tokens) {
+    if (shape_of(rows, tokens) != kBig) return rows;
+    const int64_t across = cdiv(tokens, 256), tiles = cdiv(rows, 256) * across, over = tiles % host::kNumCUs;
+    if (tiles < host::kNumCUs || over == 0 || over >= host::kNumCUs / 2) return rows;
+    const int64_t most = (tiles - over) / across * 256;
+    return most ? most : rows;
+}
+Shape shape_of_rest(int64_t rows, int64_t tokens) {
+    return cdiv(rows, 128) * cdiv(tokens, 128) >= host::kNumCUs ? kMid : kHalf64;
+}
+
+int64_t runs_in(Shape shape, int64_t rows) {
+    switch (shape) {
         case kBig: return runs_of<Big>(rows);
         case kMid: return runs_of<Mid>(rows);
         case kSmall64: return runs_of<Rows64>(rows);
+        case kHalf64: return runs_of<Half64>(rows);
         default: return runs_of<Rows32>(rows);
     }
+}
+int64_t logits_runs(int64_t rows, int64_t tokens) {
+    const int64_t most = rows_of_rounds(rows, tokens), rest = rows - most;
+    return runs_in(shape_of(rows, tokens), most) + (rest ? runs_in(shape_of_rest(rest, tokens), rest) : 0);
 }
 
 struct Forward {
@@ -439,8 +463,8 @@ Backward backward_plan(int type, int64_t ldw, int xtype, bool weight_grad, bool 
         p.across = b.take(plane_bytes(pd, p.piece, Tp));
     }
     if (x_grad) {
-        p.planes_t = b.take(plane_bytes(pw, K, p.piece));
-        p.along = b.take(plane_bytes(pd, T, p.piece));
+        p.planes_t = b.take(plane_bytes(pw, K, grad_pitch(p.piece)));
+        p.along = b.take(plane_bytes(pd, T, grad_pitch(p.piece)));
         sum_plan(K, T, p.piece / vocab::kStepK, p);
         p.sums = b.take(4 * p.splits * T * K);
     }
@@ -469,14 +493,39 @@ int launch(Args g, hipStream_t st) {
 }
 
 template <typename E, Kind KIND, int PARTS>
-int launch_logits(const Args& g, hipStream_t st) {
-    // the padding of `across`, to whole 64s of tokens, lies in the tiles
-    switch (shape_of(g.a.rows, g.across ? std::max<int64_t>(g.b.rows, 33) : g.b.rows)) {
+int launch_shape(Shape shape, const Args& g, hipStream_t st) {
+    switch (shape) {
         case kBig: return launch<E, Big, KIND, float, PARTS>(g, st);
         case kMid: return launch<E, Mid, KIND, float, PARTS>(g, st);
         case kSmall64: return launch<E, Rows64, KIND, float, PARTS>(g, st);
+        case kHalf64: return launch<E, Half64, KIND, float, PARTS>(g, st);
         default: return launch<E, Rows32, KIND, float, PARTS>(g, st);
     }
+}
+
+#define RETRO_TRY(e)                     \
+    do {                                 \
+        const int rc_ = (e);             \
+        if (rc_ != RETRO_OK) return rc_; \
+    } while (0)
+
+template <typename E, Kind KIND, int PARTS>
+int launch_logits(Args g, hipStream_t st) {
+    // the padding of `across`, to whole 64s of tokens, lies in the tiles
+    const int64_t tokens = g.across ? std::max<int64_t>(g.b.rows, 33) : g.b.rows;
+    const Shape shape = shape_of(g.a.rows, tokens);
+    const int64_t most = rows_of_rounds(g.a.rows, tokens), rest = g.a.rows - most;
+    g.a.rows = most;
+    RETRO_TRY((launch_shape<E, KIND, PARTS>(shape, g, st)));
+    if (!rest) return RETRO_OK;
+    g.a.rows = rest;
+    g.a.p += most * g.a.pitch;
+    g.n0 += most;
+    g.part0 += runs_in(shape, most);
+    if (g.along) g.along += most;
+    g.along_cols -= most;
+    if (g.across) g.across += most * g.across_pitch;
+    return launch_shape<E, KIND, PARTS>(shape_of_rest(rest, tokens), g, st);
 }
 
 template <typename E, typename TO, bool ADD>
@@ -556,12 +605,6 @@ int widen(const Call& c, bool mask, float* out) {
         return host::launch_status();
     });
 }
-
-#define RETRO_TRY(e)                     \
-    do {                                 \
-        const int rc_ = (e);             \
-        if (rc_ != RETRO_OK) return rc_; \
-    } while (0)
 
 int forward(const Call& c, float* loss, float* lse, uint8_t* ws) {
     const Forward p = forward_plan(c.type, c.ldw, c.xtype, c.K, c.N, c.T);
@@ -691,9 +734,10 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
     g.along = dX ? reinterpret_cast<uint16_t*>(ws + p.along) : nullptr;
     g.across = dW ? reinterpret_cast<uint16_t*>(ws + p.across) : nullptr;
     for (g.n0 = 0; g.n0 < c.N; g.n0 += p.piece) {
-        const int64_t rows = std::min(p.piece, c.N - g.n0), rows_p = vocab::padded(rows);
+        const int64_t rows = std::min(p.piece, c.N - g.n0), rows_p = grad_pitch(rows);
         RETRO_TRY(head_rows(c, g.n0, rows, p.piece, pw, ws + p.planes, top, g.a));
         g.along_pitch = rows_p;
+        g.along_cols = vocab::padded(rows);
         g.along_plane = c.T * rows_p;
         g.across_pitch = Tp;
         g.across_plane = rows * Tp;
@@ -709,7 +753,7 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
             Args s = {};
             s.a = {ws + p.along, rows_p * 2, c.T * rows_p * 2, c.T};
             s.b = {ws + p.planes_t, rows_p * 2, c.K * rows_p * 2, c.K};
-            s.steps = uint32_t(rows_p / vocab::kStepK);
+            s.steps = uint32_t(vocab::padded(rows) / vocab::kStepK);
             s.splits = uint32_t(p.splits);
             set_pairs(s, c.xtype == RETRO_F32 ? 2 : 1, pw);
             s.out = sums;

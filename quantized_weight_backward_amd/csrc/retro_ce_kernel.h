@@ -41,15 +41,8 @@ __device__ __forceinline__ f32x16 mfma(_Float16, const i32x4& a, const i32x4& b,
                                                   0);
 }
 
-// exp(x) for x <= 0 or so: the product with log2 e in two parts, since the error of
-// one would be as large as x.
-__device__ __forceinline__ float exp_of(float x) {
-    constexpr float kLog2e = 1.44269504088896340736f, kRest = 1.92596299112661746887e-8f;
-    const float t = x * kLog2e;
-    const float r = fmaf(x, kRest, fmaf(x, kLog2e, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    return t > -126.f ? fmaf(e * 0.693147180559945f, r, e) : e;
-}
+// exp(x) for x <= 0 or so: off by |x| 2^-24 and a step, of a value that falls with x.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 
 // Rows of 16-bit elements in one or two parts.
 struct Operand {
@@ -80,7 +73,7 @@ struct Args {
     const float* weight;   // a token's factor in `across` (NULL: no `across`); 0 where it is not learnt from
     float by;              // factor of `along`
     uint16_t *along, *across;            // rows of tokens; rows of the head
-    int64_t along_pitch, along_plane;    // elements
+    int64_t along_pitch, along_plane, along_cols;  // elements; those written, whole 64s
     int64_t across_pitch, across_plane;
     // kSum
     void* out;
@@ -89,15 +82,17 @@ struct Args {
     int64_t cols;                        // of C that are written
 };
 
-// Workgroup of WA x WB waves, each BA x BB blocks of 32 x 32.
-template <int WA_, int WB_, int BA_, int BB_>
+// Workgroup of WA x WB waves, each BA x BB blocks of 32 x 32, and S steps' tiles in LDS.
+// Two steps suffice where the products take as long as a copy; tiles of few tokens are
+// bound by the head's copies, and hold more of them in flight.
+template <int WA_, int WB_, int BA_, int BB_, int S_ = 2>
 struct Tile {
-    static constexpr int WA = WA_, WB = WB_, BA = BA_, BB = BB_;
+    static constexpr int WA = WA_, WB = WB_, BA = BA_, BB = BB_, S = S_;
     static constexpr int kWaves = WA * WB;
     static constexpr int kRowsA = 32 * WA * BA, kRowsB = 32 * WB * BB;
     static constexpr int kBytes = (kRowsA + kRowsB) * kStepBytes;  // LDS of one step
     static constexpr int kCopies = kBytes / (1024 * kWaves);       // 1 KB copies a wave and step
-    static constexpr int kFit = 160 * 1024 / (2 * kBytes), kPerCU = kFit < 4 ? kFit : 4;
+    static constexpr int kFit = 160 * 1024 / (S * kBytes), kPerCU = kFit < 4 ? kFit : 4;
     static constexpr int kThreads = kWaves * 64;
     static constexpr int kPerSimd = kWaves * kPerCU / 4 < 8 ? (kWaves * kPerCU + 3) / 4 : 8;
     static_assert(kRowsA * kStepBytes % (1024 * kWaves) == 0 && kRowsB * kStepBytes % (1024 * kWaves) == 0,
@@ -124,12 +119,19 @@ __device__ __forceinline__ void copy_step(__amdgpu_buffer_rsrc_t a, __amdgpu_buf
     }
 }
 
-// Every wave's copies into LDS have landed, its reads are done, and every wave is
-// here. A wave's counters cover its own work only, so the wait comes before the
-// barrier.
+// All but every wave's last N copies into LDS have landed, its reads are done, and
+// every wave is here. A wave's counters cover its own work only, so the wait comes
+// before the barrier.
+template <int N>
 __device__ __forceinline__ void copies_done_for_all() {
+    static_assert(N < 64, "what the counter holds");
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if constexpr (N == 0)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else {
+        __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70);  // vmcnt(N) lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+    }
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -161,8 +163,11 @@ __device__ __forceinline__ void put8(uint16_t* to, int64_t left, const u16x8& w)
 template <typename E, class Z, Kind KIND, typename TO, int PARTS>
 __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const Args g) {
     constexpr int WB = Z::WB, BA = Z::BA, BB = Z::BB;
+    // arrays of their own: the compiler sees which a copy goes to
     __shared__ __align__(1024) uint8_t lds0[Z::kBytes];
     __shared__ __align__(1024) uint8_t lds1[Z::kBytes];
+    __shared__ __align__(1024) uint8_t lds2[Z::S > 2 ? Z::kBytes : 1];
+    __shared__ __align__(1024) uint8_t lds3[Z::S > 3 ? Z::kBytes : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int r = lane & 31, h = lane >> 5, wa = wave / WB, wb = wave % WB;
 
@@ -186,8 +191,13 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
     const uint32_t total = g.steps * g.pairs;
     const uint32_t begin = uint32_t(uint64_t(total) * split / g.splits);
     const uint32_t end = uint32_t(uint64_t(total) * (split + 1) / g.splits);
+    // Tiles of few tokens begin at steps of their own: rows a power of two apart, all
+    // read at one place, would come from few memory channels.
+    const uint32_t turn = Z::S > 2 ? uint32_t(a0 / Z::kRowsA * 5 % g.steps) : 0;
     auto copy = [&](uint8_t* lds, uint32_t s) {
-        const uint32_t p = (s >= g.steps) + (s >= 2 * g.steps), k = s - p * g.steps;
+        const uint32_t p = (s >= g.steps) + (s >= 2 * g.steps);
+        uint32_t k = s - p * g.steps;
+        if (Z::S > 2) k = k + turn < g.steps ? k + turn : k + turn - g.steps;
         const bool second_a = (g.order >> (2 * p)) & 1, second_b = (g.order >> (2 * p + 1)) & 1;
         copy_step<Z>(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base_of_a + (second_a ? g.a.plane : 0)), 0,
                                                        bytes_a, 0x00020000),
@@ -213,7 +223,7 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
     // One step from `cur` (its copies done, piece 0 in registers): the reads of
     // piece s + 1 are issued ahead of piece s's products; before the last piece's,
     // everyone has read all of cur and the next step's copies are in `nxt`, so cur is
-    // refilled with the step after that. Past the last step the last one is copied
+    // refilled with the step S after its own. Past the last step the last one is copied
     // again, so that the loop has no branches.
     auto run = [&](uint8_t* cur, const uint8_t* nxt, uint32_t s) {
         auto block = [&](auto which) {
@@ -232,24 +242,30 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
         read(cur, 3, fa[1], fb[1]);
         __builtin_amdgcn_sched_barrier(0);
         block(std::integral_constant<int, 2>{});
-        copies_done_for_all();
+        copies_done_for_all<(Z::S - 2) * Z::kCopies>();
         read(nxt, 0, fa[0], fb[0]);
-        copy(cur, min(s + 2, end - 1));
+        copy(cur, min(s + Z::S, end - 1));
         __builtin_amdgcn_sched_barrier(0);
         block(std::integral_constant<int, 3>{});
     };
     if (begin < end) {
         copy(lds0, begin);
-        copies_done_for_all();
         copy(lds1, min(begin + 1, end - 1));
+        if constexpr (Z::S > 2) copy(lds2, min(begin + 2, end - 1));
+        if constexpr (Z::S > 3) copy(lds3, min(begin + 3, end - 1));
+        copies_done_for_all<(Z::S - 1) * Z::kCopies>();
         read(lds0, 0, fa[0], fb[0]);
         uint32_t s = begin;
-        for (; s + 2 <= end; s += 2) {
+        for (; s + Z::S <= end; s += Z::S) {
             run(lds0, lds1, s);
-            run(lds1, lds0, s + 1);
+            run(lds1, Z::S > 2 ? lds2 : lds0, s + 1);
+            if constexpr (Z::S > 2) run(lds2, Z::S > 3 ? lds3 : lds0, s + 2);
+            if constexpr (Z::S > 3) run(lds3, lds0, s + 3);
         }
         if (s < end) run(lds0, lds1, s);
-        copies_done_for_all();  // the copies past the end are done before LDS is given up
+        if (Z::S > 2 && s + 1 < end) run(lds1, Z::S > 2 ? lds2 : lds0, s + 1);
+        if (Z::S > 3 && s + 2 < end) run(lds2, lds3, s + 2);
+        copies_done_for_all<0>();  // the copies past the end are done before LDS is given up
     }
 
     // Element v of a block: row (v / 4) * 8 + 4 h + v % 4 of A, row r of B.
@@ -325,16 +341,23 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
             if (t >= g.b.rows) continue;  // both halves of the wave alike
             scaled(j, t);
             const int64_t target = target_of(vocab::token_at(g.targets, g.wide_targets, t, g.N));
+            if (aw + BA * 32 > g.a.rows)
+#pragma unroll
+                for (int i = 0; i < BA; ++i)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (aw + 4 * h + i * 32 + (v / 4) * 8 + v % 4 >= g.a.rows) acc[i][j][v] = -__builtin_inff();
+            if (target >= 0 && target < BA * 32)
+#pragma unroll
+                for (int i = 0; i < BA; ++i)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (target == i * 32 + (v / 4) * 8 + v % 4) g.at_target[t] = acc[i][j][v];
             float top = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < BA; ++i)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int at = i * 32 + (v / 4) * 8 + v % 4;
-                    if (aw + 4 * h + at >= g.a.rows) acc[i][j][v] = -__builtin_inff();
-                    top = fmaxf(top, acc[i][j][v]);
-                    if (target == at) g.at_target[t] = acc[i][j][v];
-                }
+                for (int v = 0; v < 16; ++v) top = fmaxf(top, acc[i][j][v]);
             top = fmaxf(top, __shfl_xor(top, 32));
             const float from = top == -__builtin_inff() ? 0.f : top;
             float sum = 0.f;
@@ -362,11 +385,19 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
 #pragma unroll
             for (int i = 0; i < BA; ++i)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int at = i * 32 + (v / 4) * 8 + v % 4;
-                    const float d = exp_of(acc[i][j][v] - lse) - (target == at ? 1.f : 0.f);
-                    acc[i][j][v] = learnt[j] && aw + 4 * h + at < g.a.rows ? d : 0.f;
-                }
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = learnt[j] ? exp_of(acc[i][j][v] - lse) : 0.f;
+            if (target >= 0 && target < BA * 32)
+#pragma unroll
+                for (int i = 0; i < BA; ++i)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (target == i * 32 + (v / 4) * 8 + v % 4) acc[i][j][v] -= 1.f;
+            if (aw + BA * 32 > g.a.rows)
+#pragma unroll
+                for (int i = 0; i < BA; ++i)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (aw + 4 * h + i * 32 + (v / 4) * 8 + v % 4 >= g.a.rows) acc[i][j][v] = 0.f;
         }
         if (g.along) {
             // rows of tokens: a lane has four neighbouring elements of its token's row
@@ -394,8 +425,7 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
                     for (int p = 0; p < 32 / kRows; ++p) {
                         const int at = p * kRows + lane / kLanes, col = lane % kLanes * 8;
                         const int64_t t = bw + j * 32 + at, row = aw + i0 * 32 + col;
-                        // rows are whole 64s
-                        if (t < g.b.rows && row < g.along_pitch)
+                        if (t < g.b.rows && row < g.along_cols)
 #pragma unroll
                             for (int part = 0; part < PARTS; ++part)
                                 *reinterpret_cast<u16x8*>(g.along + part * g.along_plane + t * g.along_pitch + row) =

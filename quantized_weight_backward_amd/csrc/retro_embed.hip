@@ -13,20 +13,24 @@ using mx::Span;
 
 // The gradient. Tokens are sorted by id, stably, so that the tokens of an id lie side
 // by side in rising order: a radix sort from the low digit up, of `bits` bits a pass.
-// An id that is none sorts last, as N. The sorted list is cut into runs of 64; an id
-// whose tokens lie in several runs has the sum of each run's part made first, by
-// workgroups of their own, so that a frequent id is not one workgroup's work.
+// An id that is none sorts last, as N. The sorted list is cut into runs; a wave adds
+// up a run's rows, 512 columns of them, and writes the row of each id that lies in the
+// run alone. Of an id that goes on in other runs it writes its part, and a second
+// launch joins the parts: a frequent id is not one wave's work.
 //
-// What bounds it is the table's rows being written. With many more rows than tokens
-// all of them are cleared beside the sort, in the same launches, and only the rows of
-// tokens are then written from their sums; else each row looks its tokens up.
+// What bounds it is the table being written. All of it is cleared beside the sort, in
+// the same launches, so that the sort costs no time of its own and only rows of tokens
+// are written after it.
 
 constexpr int kMaxBits = 9, kMaxDigits = 1 << kMaxBits;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSmallT = 8192;      // sorted by one workgroup in LDS
 constexpr int kBlockItems = 2048;  // of a workgroup of a larger sort's pass
 constexpr int kBlockThreads = 256, kBlockWaves = kBlockThreads / 64;
-constexpr int kRun = 64;
+// Tokens of a run. Shorter ones are more waves for few tokens (777 of 1000 columns: 22
+// us after the sort in runs of 64, 9 in runs of 16), longer ones fewer parts to join.
+constexpr int kMaxRun = 64;
+int run_for(int64_t T) { return T <= 4096 ? 16 : kMaxRun; }
 
 // Passes and bits of each for keys 0 .. N.
 struct Radix {
@@ -50,16 +54,28 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Zeros over rows of `row` bytes `pitch` apart, 16 bytes a step, the steps begin ..
-// end of them all dealt to `workers` threads. A row is whole 2s.
+// Zeros over rows of `row` bytes `pitch` apart, 16 bytes a step: a workgroup kFill steps
+// a thread, side by side, from its own first one on. A row is whole 2s.
+constexpr int kFill = 16;
 struct Fill {
     uint8_t* p;
     int64_t pitch, row, per, begin, end;  // per: steps of a row
 };
-__device__ __forceinline__ void fill(const Fill& f, int64_t worker, int64_t workers) {
+template <int THREADS>
+__device__ __forceinline__ void fill(const Fill& f, int64_t block) {
     typedef uint32_t words __attribute__((ext_vector_type(4), aligned(2)));
-    for (int64_t at = f.begin + worker; at < f.end; at += workers) {
-        const int64_t r = f.per >= f.end ? 0 : at / f.per, b = (at - r * f.per) * 16;
+    const int64_t first = f.begin + block * (kFill * THREADS);
+    const bool one = f.per >= f.end;  // row
+    if (one && first + kFill * THREADS < f.end) {
+        words* to = reinterpret_cast<words*>(f.p) + first + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < kFill; ++j) to[j * THREADS] = words{0, 0, 0, 0};
+        return;
+    }
+    for (int j = 0; j < kFill; ++j) {
+        const int64_t at = first + j * THREADS + threadIdx.x;
+        if (at >= f.end) return;
+        const int64_t r = one ? 0 : at / f.per, b = (at - r * f.per) * 16;
         uint8_t* to = f.p + r * f.pitch + b;
         if (b + 16 <= f.row) {
             *reinterpret_cast<words*>(to) = words{0, 0, 0, 0};
@@ -106,7 +122,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __
                                                                  int T, int passes, int bits, uint32_t* __restrict__ keys,
                                                                  uint32_t* __restrict__ order, Fill f) {
     if (blockIdx.x > 0) {
-        fill(f, int64_t(blockIdx.x - 1) * kSortThreads + threadIdx.x, int64_t(gridDim.x - 1) * kSortThreads);
+        fill<kSortThreads>(f, blockIdx.x - 1);
         return;
     }
     constexpr int kPer = kSmallT / kSortThreads;
@@ -185,7 +201,7 @@ __global__ __launch_bounds__(kBlockThreads) void sort_pass_kernel(
     uint32_t* __restrict__ counts, const uint32_t* __restrict__ totals, uint32_t* __restrict__ keys,
     uint32_t* __restrict__ order, Fill f) {
     if (blockIdx.x >= blocks) {
-        fill(f, int64_t(blockIdx.x - blocks) * kBlockThreads + threadIdx.x, int64_t(gridDim.x - blocks) * kBlockThreads);
+        fill<kBlockThreads>(f, blockIdx.x - blocks);
         return;
     }
     constexpr int kRounds = kBlockItems / kBlockThreads;
@@ -264,130 +280,136 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(uint32_t* __restrict__ c
     if (threadIdx.x == 0) totals[blockIdx.x] = before;
 }
 
-// The first place at or after `from` whose key is `key` or above (list of T keys).
-__device__ __forceinline__ uint32_t first_of(const uint32_t* __restrict__ keys, uint32_t from, uint32_t T, uint32_t key) {
-    uint32_t low = from, high = T;
-    while (low < high) {
-        const uint32_t mid = low + (high - low) / 2;
-        if (keys[mid] < key)
-            low = mid + 1;
-        else
-            high = mid;
+// A wave's view of the sorted list from one place on: its lanes hold the next 64 keys
+// and tokens, in one round of loads.
+struct Window {
+    uint32_t key, token;
+};
+__device__ __forceinline__ Window window_at(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ order,
+                                            uint32_t from, uint32_t T) {
+    const uint32_t i = from + threadIdx.x % 64;
+    return i < T ? Window{keys[i], order[i]} : Window{~0u, 0};
+}
+
+// The first place in [low, high) whose key is `key` or above, 64 probes a round.
+__device__ __forceinline__ uint32_t first_of(const uint32_t* __restrict__ keys, uint32_t low, uint32_t high, uint32_t key) {
+    while (high - low > 0) {
+        const uint32_t step = (high - low + 63) / 64, i = low + threadIdx.x % 64 * step;
+        const uint64_t below = __ballot(i < high && keys[i] < key);  // some first lanes
+        if (!below) return low;
+        const uint32_t n = uint32_t(__popcll(below));
+        high = min(high, low + n * step);
+        low += (n - 1) * step + 1;
     }
     return low;
 }
 
-// The place after the last of the keys that are as at `from`: most have few, so the
-// steps double until they pass it.
-__device__ __forceinline__ uint32_t end_of(const uint32_t* __restrict__ keys, uint32_t from, uint32_t T) {
-    const uint32_t key = keys[from];
-    uint32_t step = 1;
-    while (step < T - from && keys[from + step] == key) step *= 2;
-    return first_of(keys, from + step / 2, min(T, from + step), key + 1);
+// A wave's row or run, uniform, and its 512 columns: waves are dealt `chunks` to a row.
+// Lanes past the columns stay, with nothing to load or store: the tokens that they hold
+// are read by the others.
+struct Place {
+    int64_t row, k;
+};
+__device__ __forceinline__ Place place_of(int64_t first_block, uint32_t chunks) {
+    const int64_t at = (first_block + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t row = at >> 32 ? at / chunks : int64_t(uint32_t(at) / chunks);
+    return {row, (at - row * chunks) * 512 + threadIdx.x % 64 * 8};
 }
 
-// The sum of dY's rows order[i] for begin <= i < end, in that order.
-template <typename TY>
-__device__ __forceinline__ void sum_rows(const TY* __restrict__ dY, int64_t ldy, int64_t left,
-                                         const uint32_t* __restrict__ order, uint32_t begin, uint32_t end, float e[8]) {
-    // eight rows in flight; what is past the end is the last row again, not added
-    for (uint32_t i = begin; i < end; i += 8) {
-        float v[8][8];
+template <typename TW, bool ADD>
+__device__ __forceinline__ void write_row(TW* to, int64_t left, float scale, const float sum[8]) {
+    float e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mx::load8(dY + int64_t(order[min(i + j, end - 1)]) * ldy, left, v[j]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (i + j < end)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) e[c] += v[j][c];
-    }
-}
-
-// Sums of the parts of ids whose tokens lie in several runs: of run c, slot 2c holds
-// the part that begins with the run, slot 2c + 1 one that begins inside it. A thread
-// 8 columns of a run.
-template <typename TY>
-__global__ __launch_bounds__(256) void parts_kernel(const TY* __restrict__ dY, int64_t ldy, int64_t K, int64_t T,
-                                                    int64_t N, const uint32_t* __restrict__ keys,
-                                                    const uint32_t* __restrict__ order, float* __restrict__ parts,
-                                                    uint32_t per, int64_t first_block) {
-    const int64_t at = (first_block + blockIdx.x) * 256 + threadIdx.x;
-    const int64_t c = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
-    const uint32_t begin = uint32_t(c * kRun);
-    if (begin >= T) return;
-    const int64_t k = (at - c * per) * 8, pitch = int64_t(per) * 8;
-    const uint32_t end = uint32_t(min(T, int64_t(begin) + kRun));
-    const uint32_t head = keys[begin], tail = keys[end - 1];
-    const bool from_before = begin > 0 && keys[begin - 1] == head, goes_on = end < T && keys[end] == tail;
-    auto put = [&](int slot, uint32_t b, uint32_t e) {
-        float v[8] = {};
-        sum_rows(dY + k, ldy, K - k, order, b, e, v);
-        store8(parts + (2 * c + slot) * pitch + k, 8, v);
-    };
-    if (head < N && (from_before || (goes_on && head == tail))) put(0, begin, first_of(keys, begin, end, head + 1));
-    if (goes_on && tail < N && head != tail) put(1, first_of(keys, begin, end, tail), end);
-}
-
-// Rows of dW from their tokens. A thread 8 columns: of every row (kAll), or of the
-// row of each place in the sorted list where an id begins (kHeads: written, kAdd: added).
-enum Rows { kAll, kHeads, kAdd };
-template <typename TY, typename TW, Rows ROWS>
-__global__ __launch_bounds__(256) void rows_kernel(const TY* __restrict__ dY, int64_t ldy, float scale,
-                                                   TW* __restrict__ dW, int64_t ldw, int64_t K, uint32_t T, int64_t N,
-                                                   const uint32_t* __restrict__ keys, const uint32_t* __restrict__ order,
-                                                   const float* __restrict__ parts, uint32_t per, int64_t first_block) {
-    const int64_t at = (first_block + blockIdx.x) * 256 + threadIdx.x;
-    int64_t row = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
-    const int64_t k = (at - row * per) * 8, pitch = int64_t(per) * 8;
-    if (row >= (ROWS == kAll ? N : int64_t(T))) return;
-    uint32_t begin = uint32_t(row), end;
-    if constexpr (ROWS == kAll) {
-        begin = first_of(keys, 0, T, uint32_t(row));
-        end = begin < T && keys[begin] == row ? end_of(keys, begin, T) : begin;
-    } else {
-        row = keys[begin];
-        if (row >= N || (begin > 0 && keys[begin - 1] == row)) return;
-        end = end_of(keys, begin, T);
-    }
-    float e[8] = {};
-    const uint32_t c0 = begin / kRun, c1 = end == begin ? c0 : (end - 1) / kRun;
-    if (c0 == c1) {
-        sum_rows(dY + k, ldy, K - k, order, begin, end, e);
-    } else {
-        const float* from = parts + 2 * int64_t(c0) * pitch + k;
-        mx::load8(from + (begin % kRun ? pitch : 0), 8, e);
-        for (uint32_t c = 1; c <= c1 - c0; c += 4) {
-            float v[4][8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mx::load8(from + 2 * int64_t(min(c + j, c1 - c0)) * pitch, 8, v[j]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + j <= c1 - c0)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i] += v[j][i];
-        }
-    }
-    TW* to = dW + row * ldw + k;
-    if (begin != end)  // a row of no token is zeros whatever the scale
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] *= scale;
-    if constexpr (ROWS == kAdd) {
+    for (int i = 0; i < 8; ++i) e[i] = sum[i] * scale;
+    if constexpr (ADD) {
         float old[8];
-        mx::load8(to, K - k, old);
+        mx::load8(to, left, old);
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] += old[i];
     }
-    store8(to, K - k, e);
+    store8(to, left, e);
 }
 
-// Whether all rows are cleared beside the sort and then those of tokens written: where
-// more than half of them are of no token.
-bool clears(int64_t N, int64_t T) { return 2 * T < N; }
+// The sums of run c. Of an id that lies in other runs too, the part that begins with
+// the run goes to slot 2c, one that begins inside it to slot 2c + 1.
+template <typename TY, typename TW, bool ADD>
+__global__ __launch_bounds__(256) void runs_kernel(const TY* __restrict__ dY, int64_t ldy, float scale,
+                                                   TW* __restrict__ dW, int64_t ldw, int64_t K, uint32_t T, int64_t N,
+                                                   uint32_t run, const uint32_t* __restrict__ keys,
+                                                   const uint32_t* __restrict__ order, float* __restrict__ parts,
+                                                   int64_t pitch, uint32_t chunks, int64_t first_block) {
+    const Place at = place_of(first_block, chunks);
+    if (at.row * run >= T) return;
+    const uint32_t begin = uint32_t(at.row) * run, n = min(T - begin, run);
+    const Window w = window_at(keys, order, begin, T);
+    const uint32_t none = ~0u, head = uint32_t(__builtin_amdgcn_readfirstlane(int(w.key)));
+    const uint32_t tail = uint32_t(__builtin_amdgcn_readlane(int(w.key), n - 1));
+    const uint32_t before = begin > 0 && keys[begin - 1] == head ? head : none;      // an id that began in a run before
+    const uint32_t after = begin + n < T && keys[begin + n] == tail ? tail : none;   // one that goes on
+    const TY* from = dY + at.k;
+    const int64_t left = K - at.k;
+    auto key_at = [&](uint32_t i) { return uint32_t(__builtin_amdgcn_readlane(int(w.key), i)); };
+    float e[8] = {};
+    uint32_t first = 0;
+    for (uint32_t i0 = 0; i0 < n; i0 += 8) {
+        // eight rows in flight; past the run the last one again, not added
+        float v[8][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            mx::load8(from + int64_t(uint32_t(__builtin_amdgcn_readlane(int(w.token), min(i0 + j, n - 1)))) * ldy, left, v[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t i = i0 + j;
+            if (i >= n) break;
+            const uint32_t key = key_at(i);
+            if (key >= N) return;  // the tokens of no id are the last
+#pragma unroll
+            for (int c = 0; c < 8; ++c) e[c] += v[j][c];
+            if (i + 1 < n && key_at(i + 1) == key) continue;
+            if ((key == before && first == 0) || key == after)
+                store8(parts + (2 * at.row + (first ? 1 : 0)) * pitch + at.k, pitch - at.k, e);
+            else
+                write_row<TW, ADD>(dW + key * ldw + at.k, left, scale, e);
+            first = i + 1;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) e[c] = 0.f;
+        }
+    }
+}
+
+// The rows of ids that lie in several runs, by the run in which they begin.
+template <typename TW, bool ADD>
+__global__ __launch_bounds__(256) void join_kernel(float scale, TW* __restrict__ dW, int64_t ldw, int64_t K, uint32_t T,
+                                                   int64_t N, uint32_t run, const uint32_t* __restrict__ keys,
+                                                   const float* __restrict__ parts, int64_t pitch, uint32_t chunks,
+                                                   int64_t first_block) {
+    const Place at = place_of(first_block, chunks);
+    if ((at.row + 1) * run >= T) return;  // nothing goes on after the last run
+    const uint32_t begin = uint32_t(at.row) * run, next = begin + run, key = keys[next - 1];
+    if (key >= N || keys[next] != key) return;
+    const bool inside = keys[begin] != key;  // it begins inside this run
+    if (!inside && begin > 0 && keys[begin - 1] == key) return;
+    const uint32_t last = (first_of(keys, next, T, key + 1) - 1) / run - uint32_t(at.row);
+    const float* from = parts + 2 * at.row * pitch + at.k;
+    float e[8];
+    mx::load8(from + (inside ? pitch : 0), pitch - at.k, e);
+    for (uint32_t c = 1; c <= last; c += 8) {
+        float v[8][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx::load8(from + 2 * int64_t(min(c + j, last)) * pitch, pitch - at.k, v[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j <= last)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] += v[j][i];
+    }
+    write_row<TW, ADD>(dW + key * ldw + at.k, K - at.k, scale, e);
+}
 
 struct Plan {
     Radix radix;
     int64_t keys[2], order[2], counts, totals, parts, bytes;
-    int64_t blocks;
+    int64_t blocks, run;
 };
 
 Plan plan_of(int64_t K, int64_t N, int64_t T) {
@@ -407,7 +429,8 @@ Plan plan_of(int64_t K, int64_t N, int64_t T) {
         p.counts = take(4 * p.blocks << p.radix.bits);
         p.totals = take(4 << p.radix.bits);
     }
-    p.parts = take(4 * 2 * cdiv(T, kRun) * cdiv(K, 8) * 8);
+    p.run = run_for(T);
+    p.parts = take(4 * 2 * cdiv(T, p.run) * cdiv(K, 8) * 8);
     return p;
 }
 
@@ -421,14 +444,11 @@ Plan plan_of(int64_t K, int64_t N, int64_t T) {
 // steps, is filled in shares beside the sort's launches.
 int sort(const Plan& p, const void* ids, bool wide, int64_t N, int64_t T, uint8_t* ws, int& out, Fill f, hipStream_t st) {
     auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
-    // eight waves a SIMD's worth of workgroups, or fewer where each has little to do
-    auto fillers = [](const Fill& f, int threads) {
-        return uint32_t(std::min<int64_t>(cdiv(f.end - f.begin, 4 * threads), host::kNumCUs * 2048 / threads));
-    };
+    auto fillers = [](const Fill& f, int threads) { return cdiv(f.end - f.begin, kFill * threads); };
     out = 0;
     host::clear_last_error();
     if (T <= kSmallT) {
-        sort_small_kernel<<<dim3(1 + fillers(f, kSortThreads)), dim3(kSortThreads), 0, st>>>(
+        sort_small_kernel<<<dim3(uint32_t(1 + fillers(f, kSortThreads))), dim3(kSortThreads), 0, st>>>(
             ids, wide, N, int(T), p.radix.passes, p.radix.bits, words(p.keys[0]), words(p.order[0]), f);
         return host::launch_status();
     }
@@ -441,7 +461,7 @@ int sort(const Plan& p, const void* ids, bool wide, int64_t N, int64_t T, uint8_
         auto pass = [&](int share, const uint32_t* of, uint32_t* keys, uint32_t* order) {
             f.begin = steps * share / shares;
             f.end = steps * (share + 1) / shares;
-            sort_pass_kernel<<<dim3(blocks + fillers(f, kBlockThreads)), dim3(kBlockThreads), 0, st>>>(
+            sort_pass_kernel<<<dim3(uint32_t(blocks + fillers(f, kBlockThreads))), dim3(kBlockThreads), 0, st>>>(
                 ids, wide, N, keys_in, order_in, T, shift, p.radix.bits, blocks, counts, of, keys, order, f);
         };
         pass(2 * i, nullptr, nullptr, nullptr);
@@ -510,9 +530,8 @@ int retro_embedding_backward(int idtype, const void* ids, int ytype, const void*
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* parts = reinterpret_cast<float*>(ws + p.parts);
     int out = 0;
-    const bool cleared = !accumulate && clears(N, T);
     Fill f = {};
-    if (cleared) {
+    if (!accumulate) {
         f.p = static_cast<uint8_t*>(dW);
         f.pitch = ldw * wsize;
         f.row = K * wsize;
@@ -525,24 +544,28 @@ int retro_embedding_backward(int idtype, const void* ids, int ytype, const void*
         f.end = rows * f.per;
     }
     RETRO_TRY(sort(p, ids, idtype == RETRO_I64, N, T, ws, out, f, st));
-    if (T == 0 && cleared) return RETRO_OK;
+    if (T == 0) return RETRO_OK;
     const uint32_t *keys = reinterpret_cast<uint32_t*>(ws + p.keys[out]),
                    *order = reinterpret_cast<uint32_t*>(ws + p.order[out]);
-    const uint32_t per = uint32_t(cdiv(K, 8));
+    const uint32_t chunks = uint32_t(cdiv(K, 512));
+    const int64_t pitch = cdiv(K, 8) * 8;
     return mx::with_float(ytype, [&](auto* ytag) {
         using TY = std::remove_pointer_t<decltype(ytag)>;
         const TY* dy = static_cast<const TY*>(dY);
-        if (T > kRun)  // fewer lie in one run
-            RETRO_TRY(mx::in_block_ranges(cdiv(cdiv(T, kRun) * per, 256), [&](int64_t first, uint32_t blocks) {
-                parts_kernel<TY><<<dim3(blocks), dim3(256), 0, st>>>(dy, ldy, K, T, N, keys, order, parts, per, first);
-            }));
         return mx::with_float(wtype, [&](auto* wtag) {
             using TW = std::remove_pointer_t<decltype(wtag)>;
-            const bool all = !accumulate && !cleared;
-            return mx::in_block_ranges(cdiv((all ? N : T) * per, 256), [&](int64_t first, uint32_t blocks) {
-                auto kernel = all ? rows_kernel<TY, TW, kAll> : accumulate ? rows_kernel<TY, TW, kAdd> : rows_kernel<TY, TW, kHeads>;
-                kernel<<<dim3(blocks), dim3(256), 0, st>>>(dy, ldy, scale, static_cast<TW*>(dW), ldw, K, uint32_t(T), N,
-                                                           keys, order, parts, per, first);
+            TW* w = static_cast<TW*>(dW);
+            const int64_t waves = cdiv(T, p.run) * chunks;
+            const uint32_t run = uint32_t(p.run), t = uint32_t(T);
+            RETRO_TRY(mx::in_block_ranges(cdiv(waves, 4), [&](int64_t first, uint32_t blocks) {
+                auto kernel = accumulate ? runs_kernel<TY, TW, true> : runs_kernel<TY, TW, false>;
+                kernel<<<dim3(blocks), dim3(256), 0, st>>>(dy, ldy, scale, w, ldw, K, t, N, run, keys, order, parts, pitch,
+                                                           chunks, first);
+            }));
+            if (T <= p.run) return int(RETRO_OK);  // one run
+            return mx::in_block_ranges(cdiv(waves, 4), [&](int64_t first, uint32_t blocks) {
+                auto kernel = accumulate ? join_kernel<TW, true> : join_kernel<TW, false>;
+                kernel<<<dim3(blocks), dim3(256), 0, st>>>(scale, w, ldw, K, t, N, run, keys, parts, pitch, chunks, first);
             });
         });
     });

@@ -75,17 +75,30 @@ __global__ __launch_bounds__(256) void planes_kernel(const uint8_t* __restrict__
 template <int TYPE>
 __global__ __launch_bounds__(256) void top_kernel(const uint8_t* __restrict__ W, int64_t ldw, int64_t rows, int K,
                                                   uint32_t* __restrict__ top, int wide, uint32_t per) {
+    // four groups of 8 in flight a thread
     uint32_t m = 0;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (uint32_t g = threadIdx.x; g < per; g += 256) {
-            float e[8];
-            row8<TYPE>(W + r * ldw, int(g) * 8, K, wide, e);
+    const int64_t all = rows * per, step = int64_t(gridDim.x) * 256;
+    for (int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x; at < all; at += 4 * step) {
+        float e[4][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[i]) & 0x7fffffffu);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = min(at + j * step, all - 1);  // the last group again past the end
+            const int64_t r = i >> 32 ? i / per : int64_t(uint32_t(i) / per);
+            row8<TYPE>(W + r * ldw, int(i - r * per) * 8, K, wide, e[j]);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[j][i]) & 0x7fffffffu);
+    }
+    __shared__ uint32_t tops[4];
     m = wave_max(m);
-    // a maximum is the same in whatever order
-    if (threadIdx.x % 64 == 0 && m) atomicMax(top, m);
+    if (threadIdx.x % 64 == 0) tops[threadIdx.x / 64] = m;
+    __syncthreads();
+    m = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    // a maximum is the same in whatever order. One address takes one atomic at a time:
+    // those of 2048 workgroups took longer than the reads.
+    if (threadIdx.x == 0 && m > __hip_atomic_load(top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(top, m);
 }
 
 }  // namespace vocab

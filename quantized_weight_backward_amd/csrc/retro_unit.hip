@@ -397,8 +397,9 @@ template int launch_dequant<RETRO_UNIT_TYPE>(const void*, float*, int64_t, int64
 namespace vocab {
 namespace {
 
-// Rows of 16-byte aligned floats in fours, or packed rows.
-int wide_rows(int type, int64_t ldw, int64_t K) { return K % 4 == 0 && (type > RETRO_F16 && type != RETRO_BF16 ? true : ldw % 16 == 0); }
+// Whether rows can be read four elements at a time: packed ones, and those of floats
+// that begin on 16-byte boundaries.
+int wide_rows(int type, int64_t ldw, int64_t K) { return K % 4 == 0 && (!mx::float_bytes(type) || ldw % 16 == 0); }
 
 template <typename TY, typename TI>
 int launch_embed_as(const EmbedArgs& a, hipStream_t st) {
@@ -435,8 +436,9 @@ int launch_planes(const PlaneArgs& a, hipStream_t st) {
 template <int TYPE>
 int launch_top(const uint8_t* W, int64_t ldw, int64_t rows, int64_t K, uint32_t* top, hipStream_t st) {
     host::clear_last_error();
-    top_kernel<TYPE><<<dim3(uint32_t(std::min<int64_t>(rows, 2048))), dim3(256), 0, st>>>(
-        W, ldw, rows, int(K), top, wide_rows(TYPE, ldw, K), uint32_t(host::cdiv(K, 8)));
+    const int64_t per = host::cdiv(K, 8);
+    top_kernel<TYPE><<<dim3(uint32_t(std::min<int64_t>(host::cdiv(rows * per, 1024), 2048))), dim3(256), 0, st>>>(
+        W, ldw, rows, int(K), top, wide_rows(TYPE, ldw, K), uint32_t(per));
     return host::launch_status();
 }
 

@@ -317,6 +317,16 @@ def test_cross_entropy_in_several_pieces_of_the_head(q):
         close(dx[some.cuda()], wx, bx)
 
 
+def test_cross_entropy_in_whole_rounds_and_a_rest(q):
+    """Tiles of 256 x 256 for most of the head, smaller ones for what is left of it."""
+    for dtype, T, N, K in ((torch.bfloat16, 300, 33100, 64), (torch.float16, 257, 32769, 33), (torch.float32, 300, 33000, 64)):
+        w = head(dtype, N, K, seed=T)
+        x = torch.randn((T, K), generator=gen(N)).to(dtype)
+        t = tokens(T, N, seed=K)
+        t[:9] = torch.tensor([0, 255, 256, 32511, 32512, 32767, 32768, N - 1, N])  # about the borders
+        check_cross_entropy(q, TYPE[dtype], w.cuda(), w.double(), x, t, weight_grad=True)
+
+
 def test_cross_entropy_keeps_tokens_that_are_not_learnt_from_out(q):
     """Their x, lse and dloss may hold anything."""
     T, N, K = 80, 300, 128
