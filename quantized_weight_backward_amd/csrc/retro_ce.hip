@@ -14,19 +14,19 @@ using mx::Span;
 
 // ---------------------------------------------------------------- rows of tokens
 
-// x as the matrix cores take it: rows of `pitch` elements, zeros past K, in x's own
-// 16-bit type (PARTS 0) or as F16 parts scaled by a power of two of the row's own,
+// x as the matrix cores take it, in steps of 64 elements (element k of row t at
+// (k / 64 * gridDim.x + t) * 64 + k % 64), zeros past K and past the last token, in x's
+// own 16-bit type (PARTS 0) or as F16 parts scaled by a power of two of the row's own,
 // whose inverse goes to factor[t]. With a mask (the gradients' products) the rows of
 // tokens that are not learnt from are zeros, whatever they hold. A workgroup a row.
 template <typename TX, int PARTS>
 __global__ __launch_bounds__(256) void token_rows_kernel(const TX* __restrict__ X, int64_t ldx, int64_t K,
                                                          const void* __restrict__ targets, bool wide_targets, int64_t N,
-                                                         bool mask, uint16_t* __restrict__ out, int64_t pitch,
-                                                         int64_t plane, float* __restrict__ factor) {
+                                                         bool mask, uint16_t* __restrict__ out, int64_t padded_k,
+                                                         int64_t T, float* __restrict__ factor) {
     const int64_t t = blockIdx.x;
-    const bool live = !mask || vocab::token_at(targets, wide_targets, t, N) >= 0;
+    const bool live = t < T && (!mask || vocab::token_at(targets, wide_targets, t, N) >= 0);
     const TX* x = X + t * ldx;
-    uint16_t* to = out + t * pitch;
     float s = 1.f;
     if constexpr (PARTS > 0) {
         __shared__ uint32_t tops[4];
@@ -43,49 +43,19 @@ __global__ __launch_bounds__(256) void token_rows_kernel(const TX* __restrict__ 
         __syncthreads();
         m = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
         s = vocab::scale_of(m);
-        if (threadIdx.x == 0) factor[t] = vocab::unscale_of(m);
+        if (threadIdx.x == 0 && t < T) factor[t] = vocab::unscale_of(m);
     }
-    for (int64_t k = threadIdx.x * 8; k < pitch; k += 256 * 8) {
+    for (int64_t k = threadIdx.x * 8; k < padded_k; k += 256 * 8) {
         float e[8] = {};
         if (live) mx::load8(x + k, K - k, e);
+        uint16_t* to = out + (k / 64 * gridDim.x + t) * 64 + k % 64;
         if constexpr (PARTS == 0) {
-            vocab::store_part<TX>(to + k, e);
+            vocab::store_part<TX>(to, e);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) e[i] *= s;
-            vocab::store_parts<_Float16, PARTS>(to + k, plane, e);
+            vocab::store_parts<_Float16, PARTS>(to, padded_k * gridDim.x, e);
         }
-    }
-}
-
-// out[c][r] = in[r][c] of 16-bit elements, zeros for r past the rows up to out's
-// pitch. 64 x 64 a workgroup through LDS, 16 bytes a lane both ways. in's rows are
-// 16-byte aligned and hold whole 8s up to `cols`.
-__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* __restrict__ in, int64_t pitch, int64_t rows,
-                                                        int64_t cols, uint16_t* __restrict__ out, int64_t out_pitch,
-                                                        uint32_t tiles_c, int64_t in_plane, int64_t out_plane) {
-    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-    __shared__ uint16_t tile[64][64 + 2];
-    in += blockIdx.y * in_plane;
-    out += blockIdx.y * out_plane;
-    const int64_t r0 = int64_t(blockIdx.x / tiles_c) * 64, c0 = int64_t(blockIdx.x % tiles_c) * 64;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = threadIdx.x + i * 256, r = at / 8, c = at % 8 * 8;
-        u16x8 v = {};
-        if (r0 + r < rows && c0 + c < cols) v = *reinterpret_cast<const u16x8*>(in + (r0 + r) * pitch + c0 + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) tile[r][c + j] = v[j];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = threadIdx.x + i * 256, c = at / 8, r = at % 8 * 8;
-        if (c0 + c >= cols || r0 + r >= out_pitch) continue;
-        u16x8 v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = tile[r + j][c];
-        *reinterpret_cast<u16x8*>(out + (c0 + c) * out_pitch + r0 + r) = v;
     }
 }
 
@@ -317,10 +287,6 @@ int64_t grad_piece(int64_t K, int64_t N, int64_t T) {
 }
 int64_t few_piece(int64_t N, int64_t T) { return piece_rows(N, (1 << 24) / std::max<int64_t>(T, 1)); }
 
-// Elements between rows along a piece of the head: 128 bytes more than its whole steps,
-// so that neighbouring rows do not lie a power of two apart and on one memory channel.
-int64_t grad_pitch(int64_t rows) { return vocab::padded(rows) + vocab::kStepK; }
-
 // Parts of the workspace, each on a 256-byte boundary.
 struct Bump {
     int64_t at = 0;
@@ -393,7 +359,7 @@ Forward forward_plan(int type, int64_t ldw, int xtype, int64_t K, int64_t N, int
     const bool narrow = is_narrow(type, xtype), direct = is_direct(type, xtype, ldw, K);
     // of a head read in place, at most 2^22 tiles of 128 x 128
     p.piece = direct ? piece_rows(N, std::min<int64_t>(1 << 24, (1 << 29) / cdiv(T, 128))) : plane_piece(K, N);
-    p.x = b.take(plane_bytes(narrow ? 1 : parts_of(xtype), T, vocab::padded(K)));
+    p.x = b.take(plane_bytes(narrow ? 1 : parts_of(xtype), vocab::padded(T), vocab::padded(K)));
     p.factor = b.take(4 * T);
     p.top = b.take(4);
     p.planes = direct ? 0 : b.take(plane_bytes(narrow ? 1 : parts_of(type), p.piece, vocab::padded(K)));
@@ -404,7 +370,7 @@ Forward forward_plan(int type, int64_t ldw, int xtype, int64_t K, int64_t N, int
 }
 
 struct Backward {
-    int64_t x, xt, factor, weight, unscale, top, planes, planes_t, along, across, sums, few_x, few_l, few_ws, bytes;
+    int64_t x, factor, weight, unscale, top, planes, along, across, sums, few_x, few_l, few_ws, bytes;
     int64_t piece, splits;
     Shape shape;
 };
@@ -452,19 +418,17 @@ Backward backward_plan(int type, int64_t ldw, int xtype, bool weight_grad, bool 
     const int px = narrow ? 1 : parts_of(xtype), pw = narrow ? 1 : grad_parts_of(type, xtype, weight_grad);
     const int pd = xtype == RETRO_F32 || (weight_grad && type == RETRO_F32) ? 2 : 1;
     p.piece = grad_piece(K, N, T);
-    p.x = b.take(plane_bytes(px, T, Kp));
+    p.x = b.take(plane_bytes(px, Tp, Kp));
     p.factor = b.take(4 * T);
     p.top = b.take(4);
     p.unscale = b.take(4);
     p.planes = direct ? 0 : b.take(plane_bytes(pw, p.piece, Kp));
     if (weight_grad) {
         p.weight = b.take(4 * T);
-        p.xt = b.take(plane_bytes(px, K, Tp));
         p.across = b.take(plane_bytes(pd, p.piece, Tp));
     }
     if (x_grad) {
-        p.planes_t = b.take(plane_bytes(pw, K, grad_pitch(p.piece)));
-        p.along = b.take(plane_bytes(pd, T, grad_pitch(p.piece)));
+        p.along = b.take(plane_bytes(pd, T, p.piece));
         sum_plan(K, T, p.piece / vocab::kStepK, p);
         p.sums = b.take(4 * p.splits * T * K);
     }
@@ -483,9 +447,9 @@ void set_pairs(Args& g, int parts_a, int parts_b) {
 template <typename E, class Z, Kind KIND, typename TO, int PARTS>
 int launch(Args g, hipStream_t st) {
     g.tiles_a = uint32_t(cdiv(g.a.rows, Z::kRowsA));
-    g.tiles_b = uint32_t(cdiv(g.b.rows, Z::kRowsB));
-    g.group = uint32_t(host::group_height(g.tiles_b, g.tiles_a, Z::kPerCU, double(g.b.rows) * g.steps,
-                                          double(g.a.rows) * g.steps));
+    const int64_t cols = KIND == kSum ? g.cols : g.b.rows;
+    g.tiles_b = uint32_t(cdiv(cols, Z::kRowsB));
+    g.group = uint32_t(host::group_height(g.tiles_b, g.tiles_a, Z::kPerCU, double(cols), double(g.a.rows)));
     host::clear_last_error();
     product_kernel<E, Z, KIND, TO, PARTS>
         <<<dim3(g.tiles_a * g.tiles_b * g.splits), dim3(Z::kThreads), 0, st>>>(g);
@@ -522,9 +486,10 @@ int launch_logits(Args g, hipStream_t st) {
     g.a.p += most * g.a.pitch;
     g.n0 += most;
     g.part0 += runs_in(shape, most);
-    if (g.along) g.along += most;
+    g.a.bytes -= most * g.a.pitch;
+    if (g.along) g.along += most / vocab::kStepK * g.along_stride;
     g.along_cols -= most;
-    if (g.across) g.across += most * g.across_pitch;
+    if (g.across) g.across += most * vocab::kStepK;
     return launch_shape<E, KIND, PARTS>(shape_of_rest(rest, tokens), g, st);
 }
 
@@ -545,40 +510,32 @@ int zero(void* p, int64_t words, hipStream_t st) {
 }
 
 int token_rows(const Call& c, int parts, bool mask, uint8_t* out, float* factor) {
-    const int64_t pitch = vocab::padded(c.K);
     return mx::with_float(c.xtype, [&](auto* tag) {
         using TX = std::remove_pointer_t<decltype(tag)>;
         auto kernel = parts == 2 ? token_rows_kernel<TX, 2> : token_rows_kernel<TX, 1>;
         if constexpr (sizeof(TX) == 2)
             if (parts == 0) kernel = token_rows_kernel<TX, 0>;
         host::clear_last_error();
-        kernel<<<dim3(uint32_t(c.T)), dim3(256), 0, c.st>>>(static_cast<const TX*>(c.X), c.ldx, c.K, c.targets,
-                                                           c.wide_targets, c.N, mask, reinterpret_cast<uint16_t*>(out),
-                                                           pitch, c.T * pitch, factor);
+        kernel<<<dim3(uint32_t(vocab::padded(c.T))), dim3(256), 0, c.st>>>(
+            static_cast<const TX*>(c.X), c.ldx, c.K, c.targets, c.wide_targets, c.N, mask,
+            reinterpret_cast<uint16_t*>(out), vocab::padded(c.K), c.T, factor);
         return host::launch_status();
     });
 }
 
-int transpose(const void* in, int64_t pitch, int64_t rows, int64_t cols, void* out, int64_t out_pitch, int parts,
-              int64_t in_plane, int64_t out_plane, hipStream_t st) {
-    const int64_t tiles_c = cdiv(cols, 64), tiles = cdiv(out_pitch, 64) * tiles_c;
-    host::clear_last_error();
-    transpose_kernel<<<dim3(uint32_t(tiles), uint32_t(parts)), dim3(256), 0, st>>>(
-        static_cast<const uint16_t*>(in), pitch, rows, cols, static_cast<uint16_t*>(out), out_pitch, uint32_t(tiles_c),
-        in_plane, out_plane);
-    return host::launch_status();
+// Operands in steps, of rows of K elements (K in whole 64s).
+Operand in_steps(const uint8_t* p, int64_t rows, int64_t all_rows, int64_t K) {
+    return {p, vocab::kStepK * 2, all_rows * vocab::kStepK * 2, all_rows * K * 2, all_rows * K * 2, rows};
 }
 
 // Rows n0 .. n0 + rows of the head as an operand: in place, or as planes.
-int head_rows(const Call& c, int64_t n0, int64_t rows, int64_t piece, int parts, uint8_t* planes, const uint32_t* top,
-              Operand& o) {
+int head_rows(const Call& c, int64_t n0, int64_t rows, int parts, uint8_t* planes, const uint32_t* top, Operand& o) {
     if (is_direct(c.type, c.xtype, c.ldw, c.K)) {
-        o = {c.W + n0 * c.ldw, c.ldw, 0, rows};
+        o = {c.W + n0 * c.ldw, c.ldw, vocab::kStepK * 2, 0, (rows - 1) * c.ldw + c.K * 2, rows};
         return RETRO_OK;
     }
-    const int64_t pitch = vocab::padded(c.K);
-    o = {planes, pitch * 2, piece * pitch * 2, rows};
-    vocab::PlaneArgs a{c.W + n0 * c.ldw,  c.ldw, rows, c.K, reinterpret_cast<uint16_t*>(planes), piece * pitch, top,
+    o = in_steps(planes, rows, vocab::padded(rows), vocab::padded(c.K));
+    vocab::PlaneArgs a{c.W + n0 * c.ldw, c.ldw, rows, c.K, reinterpret_cast<uint16_t*>(planes), o.plane / 2, top,
                        is_narrow(c.type, c.xtype) ? 0 : parts};
     return vocab::with_type(c.type, [&](auto type) { return vocab::launch_planes<decltype(type)::value>(a, c.st); });
 }
@@ -627,13 +584,12 @@ int forward(const Call& c, float* loss, float* lse, uint8_t* ws) {
         const bool narrow = is_narrow(c.type, c.xtype);
         float* factor = narrow ? nullptr : reinterpret_cast<float*>(ws + p.factor);
         uint32_t* top = narrow ? nullptr : reinterpret_cast<uint32_t*>(ws + p.top);
-        const int64_t pitch = vocab::padded(c.K) * 2;
         if (!narrow) RETRO_TRY(head_top(c, top));
         Args g = {};
-        g.b = {ws + p.x, pitch, c.T * pitch, c.T};
+        g.b = in_steps(ws + p.x, c.T, vocab::padded(c.T), vocab::padded(c.K));
         // x in place where its rows are whole steps on 16-byte boundaries
         if (narrow && c.K > 0 && c.K % vocab::kStepK == 0 && c.ldx % 8 == 0 && c.ldx < (1 << 23) && mx::aligned(c.X, 16))
-            g.b = {static_cast<const uint8_t*>(c.X), c.ldx * 2, 0, c.T};
+            g.b = {static_cast<const uint8_t*>(c.X), c.ldx * 2, vocab::kStepK * 2, 0, ((c.T - 1) * c.ldx + c.K) * 2, c.T};
         else
             RETRO_TRY(token_rows(c, narrow ? 0 : parts_of(c.xtype), false, ws + p.x, factor));
         g.steps = uint32_t(vocab::padded(c.K) / vocab::kStepK);
@@ -648,7 +604,7 @@ int forward(const Call& c, float* loss, float* lse, uint8_t* ws) {
         g.at_target = at_target;
         for (g.n0 = 0; g.n0 < c.N; g.n0 += p.piece) {
             const int64_t rows = std::min(p.piece, c.N - g.n0);
-            RETRO_TRY(head_rows(c, g.n0, rows, p.piece, parts_of(c.type), ws + p.planes, top, g.a));
+            RETRO_TRY(head_rows(c, g.n0, rows, parts_of(c.type), ws + p.planes, top, g.a));
             g.part0 = runs;
             RETRO_TRY(with_element(c, [&](auto e) { return launch_logits<decltype(e), kStats, 1>(g, c.st); }));
             runs += logits_runs(rows, c.T);
@@ -712,14 +668,13 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
         weights_kernel<<<dim3(1), dim3(1024), 0, c.st>>>(dloss, factor, c.targets, c.wide_targets, c.N, c.T, weight,
                                                          unscale);
         RETRO_TRY(host::launch_status());
-        RETRO_TRY(transpose(ws + p.x, Kp, c.T, c.K, ws + p.xt, Tp, px, c.T * Kp, c.K * Tp, c.st));
     }
     // F16's d, at most 1, is scaled so that what is 2^28 below it keeps its bits
     const bool f16 = !(narrow && c.type == RETRO_BF16);
     const float by = f16 ? 0x1p14f : 1.f;
 
     Args g = {};
-    g.b = {ws + p.x, Kp * 2, c.T * Kp * 2, c.T};
+    const Operand x = g.b = in_steps(ws + p.x, c.T, Tp, Kp);
     g.steps = uint32_t(Kp / vocab::kStepK);
     g.splits = 1;
     set_pairs(g, pw, px);
@@ -734,12 +689,13 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
     g.along = dX ? reinterpret_cast<uint16_t*>(ws + p.along) : nullptr;
     g.across = dW ? reinterpret_cast<uint16_t*>(ws + p.across) : nullptr;
     for (g.n0 = 0; g.n0 < c.N; g.n0 += p.piece) {
-        const int64_t rows = std::min(p.piece, c.N - g.n0), rows_p = grad_pitch(rows);
-        RETRO_TRY(head_rows(c, g.n0, rows, p.piece, pw, ws + p.planes, top, g.a));
-        g.along_pitch = rows_p;
-        g.along_cols = vocab::padded(rows);
+        const int64_t rows = std::min(p.piece, c.N - g.n0), rows_p = vocab::padded(rows);
+        RETRO_TRY(head_rows(c, g.n0, rows, pw, ws + p.planes, top, g.a));
+        g.along_stride = c.T * vocab::kStepK;
+        g.along_cols = rows_p;
         g.along_plane = c.T * rows_p;
-        g.across_pitch = Tp;
+        g.across_stride = rows * vocab::kStepK;
+        g.across_cols = Tp;
         g.across_plane = rows * Tp;
         RETRO_TRY(with_element(c, [&](auto e) {
             if constexpr (std::is_same<decltype(e), _Float16>::value)
@@ -747,13 +703,11 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
             return launch_logits<decltype(e), kProb, 1>(g, c.st);
         }));
         if (dX) {
-            // W^T of the piece, then sums[t][k] (+)= sum_n d[t][n] W[n][k]
-            RETRO_TRY(transpose(g.a.p, g.a.pitch / 2, rows, c.K, ws + p.planes_t, rows_p, pw, g.a.plane / 2,
-                                c.K * rows_p, c.st));
+            // sums[t][k] (+)= sum_n d[t][n] W[n][k]
             Args s = {};
-            s.a = {ws + p.along, rows_p * 2, c.T * rows_p * 2, c.T};
-            s.b = {ws + p.planes_t, rows_p * 2, c.K * rows_p * 2, c.K};
-            s.steps = uint32_t(vocab::padded(rows) / vocab::kStepK);
+            s.a = in_steps(ws + p.along, c.T, c.T, rows_p);
+            s.b = g.a;
+            s.steps = uint32_t(rows_p / vocab::kStepK);
             s.splits = uint32_t(p.splits);
             set_pairs(s, c.xtype == RETRO_F32 ? 2 : 1, pw);
             s.out = sums;
@@ -767,8 +721,9 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
         }
         if (dW) {
             Args s = {};
-            s.a = {ws + p.across, Tp * 2, rows * Tp * 2, rows};
-            s.b = {ws + p.xt, Tp * 2, c.K * Tp * 2, c.K};
+            // dW[n][k] = sum_t d[t][n] x[t][k]
+            s.a = in_steps(ws + p.across, rows, rows, Tp);
+            s.b = x;
             s.steps = uint32_t(Tp / vocab::kStepK);
             s.splits = 1;
             set_pairs(s, c.type == RETRO_F32 ? 2 : 1, px);

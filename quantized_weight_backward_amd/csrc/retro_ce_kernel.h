@@ -23,6 +23,8 @@ namespace ce {
 
 using mx::f32x16;
 using mx::i32x4;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -44,11 +46,15 @@ __device__ __forceinline__ f32x16 mfma(_Float16, const i32x4& a, const i32x4& b,
 // exp(x) for x <= 0 or so: off by |x| 2^-24 and a step, of a value that falls with x.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 
-// Rows of 16-bit elements in one or two parts.
+// Rows of 16-bit elements in one or two parts. A row's elements lie in steps of 64 (128
+// bytes), `stride` apart: 128 bytes for rows as they are in a tensor, or the whole
+// column of that step's 64 elements of all rows. What is made for the products is laid
+// out so: a tile's step is then one run of memory. Rows of 64 KB side by side, 256 of
+// them read at one place, took a fifth longer.
 struct Operand {
     const uint8_t* p;
-    int64_t pitch;  // bytes of a row
-    int64_t plane;  // bytes from the first part to the second
+    int64_t pitch, stride;  // bytes between rows, between steps of a row
+    int64_t plane, bytes;   // bytes from the first part to the second, and of one
     int64_t rows;
 };
 
@@ -72,9 +78,9 @@ struct Args {
     const float* lse;
     const float* weight;   // a token's factor in `across` (NULL: no `across`); 0 where it is not learnt from
     float by;              // factor of `along`
-    uint16_t *along, *across;            // rows of tokens; rows of the head
-    int64_t along_pitch, along_plane, along_cols;  // elements; those written, whole 64s
-    int64_t across_pitch, across_plane;
+    uint16_t *along, *across;            // rows of tokens; rows of the head; both in steps
+    int64_t along_stride, along_plane, along_cols;     // elements; columns written, whole 64s
+    int64_t across_stride, across_plane, across_cols;
     // kSum
     void* out;
     int64_t ldo, split_stride;           // elements
@@ -100,22 +106,31 @@ struct Tile {
 };
 
 // One step's tiles from memory into LDS, without registers: a wave's copy moves 8
-// rows of 128 bytes. The 16-byte pieces of row r land permuted by XOR with
-// (r / 2) % 8, so that the 16 lanes of a read of one piece from neighbouring rows
-// meet all banks once. Rows past the operand read as zeros (the buffer's bound).
-template <class Z>
+// pieces of 128 bytes, which become 8 rows of LDS.
+//   A and, but in kSum, B: a row is a row of the operand, its 64 elements along k. The
+//     16-byte blocks of row r land permuted by XOR with (r / 2) % 8, so that the 16 lanes
+//     of a read of one block from neighbouring rows meet all banks once.
+//   B in kSum, whose k runs over the operand's rows: LDS row 64 c + k holds columns
+//     64 c .. 64 c + 63 of row k, permuted by XOR with twice (k / 2) % 4, so that the four
+//     rows of a transposing read lie in banks of their own.
+// What lies past the operand reads as zeros (the buffer's bound).
+template <class Z, bool COLUMNS>
 __device__ __forceinline__ void copy_step(__amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b, uint8_t* lds,
-                                          uint32_t pitch_a, uint32_t pitch_b, uint32_t at_k, int wave, int lane) {
+                                          uint32_t pitch_a, uint32_t pitch_b, uint32_t stride_b, int wave, int lane) {
     const uint32_t r = lane >> 3, slot = lane & 7;
 #pragma unroll
     for (int i = 0; i < Z::kCopies; ++i) {
         const int at = (i * Z::kWaves + wave) * 8;  // first row of this copy
         const bool of_a = i * Z::kWaves * 8 < Z::kRowsA;
-        const uint32_t row = at - (of_a ? 0 : Z::kRowsA);
-        const uint32_t swz = ((row + r) >> 1) & 7;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? a : b, lds + at * kStepBytes, 16,
-                                                 (row + r) * (of_a ? pitch_a : pitch_b) + ((slot ^ swz) * 16), at_k, 0,
-                                                 0);
+        const uint32_t row = at - (of_a ? 0 : Z::kRowsA) + r;
+        if (COLUMNS && !of_a)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                b, lds + at * kStepBytes, 16,
+                row / 64 * stride_b + row % 64 * pitch_b + ((slot ^ ((row >> 1 & 3) << 1)) * 16), 0, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? a : b, lds + at * kStepBytes, 16,
+                                                     row * (of_a ? pitch_a : pitch_b) + ((slot ^ (row >> 1 & 7)) * 16),
+                                                     0, 0, 0);
     }
 }
 
@@ -139,6 +154,12 @@ __device__ __forceinline__ void copies_done_for_all() {
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// A transposing read of LDS: see `across`.
+__device__ __forceinline__ s16x4 column4(const uint8_t* lds) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(const_cast<uint8_t*>(lds)));
 }
 
 // The parts of v as element `at` of w.
@@ -183,40 +204,63 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
     const uint32_t high = min(g.group, g.tiles_b - gr * g.group);
     const int64_t b0 = int64_t(gr * g.group + in % high) * Z::kRowsB, a0 = int64_t(in / high) * Z::kRowsA;
 
-    const uint32_t pitch_a = uint32_t(g.a.pitch), pitch_b = uint32_t(g.b.pitch);
-    const uint8_t *base_of_a = g.a.p + a0 * g.a.pitch, *base_of_b = g.b.p + b0 * g.b.pitch;
-    const uint32_t bytes_a = uint32_t(min(int64_t(Z::kRowsA), g.a.rows - a0) * g.a.pitch);
-    const uint32_t bytes_b = uint32_t(min(int64_t(Z::kRowsB), g.b.rows - b0) * g.b.pitch);
+    constexpr bool kColumns = KIND == kSum;
     // Steps of this split; step s is k = s % steps of product s / steps.
     const uint32_t total = g.steps * g.pairs;
     const uint32_t begin = uint32_t(uint64_t(total) * split / g.splits);
     const uint32_t end = uint32_t(uint64_t(total) * (split + 1) / g.splits);
     // Tiles of few tokens begin at steps of their own: rows a power of two apart, all
     // read at one place, would come from few memory channels.
-    const uint32_t turn = Z::S > 2 ? uint32_t(a0 / Z::kRowsA * 5 % g.steps) : 0;
+    const uint32_t turn = Z::S > 2 && !kColumns ? uint32_t(a0 / Z::kRowsA * 5 % g.steps) : 0;
+    auto resource = [](const Operand& o, bool second, int64_t from) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.p + (second ? o.plane : 0) + from), 0,
+                                                 int(uint32_t(min(max(o.bytes - from, int64_t(0)), int64_t(0xffffffffu)))),
+                                                 0x00020000);
+    };
     auto copy = [&](uint8_t* lds, uint32_t s) {
         const uint32_t p = (s >= g.steps) + (s >= 2 * g.steps);
         uint32_t k = s - p * g.steps;
-        if (Z::S > 2) k = k + turn < g.steps ? k + turn : k + turn - g.steps;
-        const bool second_a = (g.order >> (2 * p)) & 1, second_b = (g.order >> (2 * p + 1)) & 1;
-        copy_step<Z>(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base_of_a + (second_a ? g.a.plane : 0)), 0,
-                                                       bytes_a, 0x00020000),
-                     __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base_of_b + (second_b ? g.b.plane : 0)), 0,
-                                                       bytes_b, 0x00020000),
-                     lds, pitch_a, pitch_b, k * kStepBytes, wave, lane);
+        if (Z::S > 2 && !kColumns) k = k + turn < g.steps ? k + turn : k + turn - g.steps;
+        copy_step<Z, kColumns>(
+            resource(g.a, (g.order >> (2 * p)) & 1, a0 * g.a.pitch + k * g.a.stride),
+            resource(g.b, (g.order >> (2 * p + 1)) & 1,
+                     kColumns ? b0 / 64 * g.b.stride + k * 64 * g.b.pitch : b0 * g.b.pitch + k * g.b.stride),
+            lds, uint32_t(g.a.pitch), uint32_t(g.b.pitch), uint32_t(g.b.stride), wave, lane);
     };
 
-    // LDS offsets of the lane's pieces of its first rows
+    // LDS offsets of the lane's blocks of its first rows
     uint32_t off[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) off[s] = r * kStepBytes + (((4 * h + s) ^ ((r >> 1) & 7)) * 16);
     const uint32_t base_a = wa * BA * 32 * kStepBytes, base_b = (Z::kRowsA + wb * BB * 32) * kStepBytes;
+    // Of columns: 16 lanes read 4 rows of k by 16 columns and get a column's four each.
+    // Lane l of them reads 4 elements of row l / 4 of the four, the second read's four
+    // rows follow the first's.
+    uint32_t across[2][BB];
+    if constexpr (kColumns)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int j = 0; j < BB; ++j) {
+                const uint32_t l = lane & 15, k = 32 * h + 4 * half + l / 4;
+                const uint32_t col = (wb * BB + j) * 32 + (lane >> 4 & 1) * 16 + l % 4 * 4, c = col % 64;
+                across[half][j] = (Z::kRowsA + col / 64 * 64 + k) * kStepBytes +
+                                  (((c / 8) ^ ((k >> 1 & 3) << 1)) * 16) + c % 8 * 2;
+            }
     i32x4 fa[2][BA], fb[2][BB];
     auto read = [&](const uint8_t* lds, int s, i32x4 (&a)[BA], i32x4 (&b)[BB]) {
 #pragma unroll
         for (int i = 0; i < BA; ++i) a[i] = *reinterpret_cast<const i32x4*>(lds + base_a + off[s] + i * 32 * kStepBytes);
 #pragma unroll
-        for (int i = 0; i < BB; ++i) b[i] = *reinterpret_cast<const i32x4*>(lds + base_b + off[s] + i * 32 * kStepBytes);
+        for (int i = 0; i < BB; ++i) {
+            if constexpr (kColumns) {
+                const s16x4 v0 = column4(lds + across[0][i] + s * 8 * kStepBytes);
+                const s16x4 v1 = column4(lds + across[1][i] + s * 8 * kStepBytes);
+                b[i] = __builtin_bit_cast(i32x4, s16x8{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]});
+            } else {
+                b[i] = *reinterpret_cast<const i32x4*>(lds + base_b + off[s] + i * 32 * kStepBytes);
+            }
+        }
     };
     f32x16 acc[BA][BB] = {};
 
@@ -428,7 +472,8 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
                         if (t < g.b.rows && row < g.along_cols)
 #pragma unroll
                             for (int part = 0; part < PARTS; ++part)
-                                *reinterpret_cast<u16x8*>(g.along + part * g.along_plane + t * g.along_pitch + row) =
+                                *reinterpret_cast<u16x8*>(g.along + part * g.along_plane + row / 64 * g.along_stride +
+                                                          t * 64 + row % 64) =
                                     *reinterpret_cast<const u16x8*>(stage + part * kPlane + at * kPitch + col);
                     }
                     wave_fence();
@@ -453,11 +498,12 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
 #pragma unroll
                 for (int p = 0; p < 32 / kRows; ++p) {
                     const int at = p * kRows + lane / kLanes, col = lane % kLanes * 8;
-                    const int64_t row = aw + i * 32 + at;
-                    if (row < g.a.rows && bw + col < g.across_pitch)
+                    const int64_t row = aw + i * 32 + at, t = bw + col;
+                    if (row < g.a.rows && t < g.across_cols)
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part)
-                            *reinterpret_cast<u16x8*>(g.across + part * g.across_plane + row * g.across_pitch + bw + col) =
+                            *reinterpret_cast<u16x8*>(g.across + part * g.across_plane + t / 64 * g.across_stride +
+                                                      row * 64 + t % 64) =
                                 *reinterpret_cast<const u16x8*>(stage + part * kPlane + at * kPitch + col);
                 }
                 wave_fence();

@@ -47,19 +47,20 @@ __global__ __launch_bounds__(256) void embed_kernel(const uint8_t* __restrict__ 
     store8(Y + t * ldy + k, K - k, e);
 }
 
-// Rows as planes (PlaneArgs): a thread 8 elements of a row.
+// Rows as planes (PlaneArgs): a thread 8 elements of a row. Rows past the last up to
+// whole 64s are zeros.
 template <int TYPE, int PARTS>
 __global__ __launch_bounds__(256) void planes_kernel(const uint8_t* __restrict__ W, int64_t ldw, int64_t rows, int K,
                                                      uint16_t* __restrict__ out, int64_t plane,
                                                      const uint32_t* __restrict__ top, int wide, uint32_t per,
                                                      int64_t first) {
     const int64_t at = (first + blockIdx.x) * 256 + threadIdx.x;
-    const int64_t r = at >> 32 ? at / per : int64_t(uint32_t(at) / per);
-    if (r >= rows) return;
+    const int64_t r = at >> 32 ? at / per : int64_t(uint32_t(at) / per), all = (rows + 63) / 64 * 64;
+    if (r >= all) return;
     const int k = int(at - r * per) * 8;
     float e[8] = {};
-    if (k < K) row8<TYPE>(W + r * ldw, k, K, wide, e);
-    uint16_t* to = out + r * (int64_t(per) * 8) + k;
+    if (k < K && r < rows) row8<TYPE>(W + r * ldw, k, K, wide, e);
+    uint16_t* to = out + (k / 64 * all + r) * 64 + k % 64;
     if constexpr (PARTS == 0) {
         typedef typename std::conditional<TYPE == kBF16, __bf16, _Float16>::type E;
         store_part<E>(to, e);

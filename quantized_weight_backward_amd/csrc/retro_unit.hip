@@ -425,7 +425,7 @@ template <int TYPE>
 int launch_planes(const PlaneArgs& a, hipStream_t st) {
     const uint32_t per = uint32_t(padded(a.K) / 8);
     const int wide = wide_rows(TYPE, a.ldw, a.K);
-    return mx::in_block_ranges(host::cdiv(a.rows * per, 256), [&](int64_t first, uint32_t blocks) {
+    return mx::in_block_ranges(host::cdiv(padded(a.rows) * per, 256), [&](int64_t first, uint32_t blocks) {
         auto kernel = a.parts == 2 ? planes_kernel<TYPE, 2> : planes_kernel<TYPE, 1>;
         if constexpr (TYPE == RETRO_F16 || TYPE == RETRO_BF16)
             if (a.parts == 0) kernel = planes_kernel<TYPE, 0>;

@@ -27,7 +27,8 @@ struct EmbedArgs {
     int64_t K, N, T;
 };
 
-// Rows of W as 16-bit planes of `padded(K)` elements a row, zeros past K.
+// Rows of W as 16-bit planes in steps of 64 elements: element k of row r at
+// (k / 64 * padded(rows) + r) * 64 + k % 64, zeros past K and past the rows.
 struct PlaneArgs {
     const uint8_t* W;  // the first row
     int64_t ldw;       // bytes
