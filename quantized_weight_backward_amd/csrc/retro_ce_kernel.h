@@ -115,24 +115,31 @@ struct Tile {
 //     rows of a transposing read lie in banks of their own.
 // What lies past the operand reads as zeros (the buffer's bound).
 template <class Z, bool COLUMNS>
-__device__ __forceinline__ void copy_step(__amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b, uint8_t* lds,
+__device__ __forceinline__ void copy_part(int i, __amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b, uint8_t* lds,
                                           uint32_t pitch_a, uint32_t pitch_b, uint32_t stride_b, int wave, int lane) {
     const uint32_t r = lane >> 3, slot = lane & 7;
-#pragma unroll
-    for (int i = 0; i < Z::kCopies; ++i) {
-        const int at = (i * Z::kWaves + wave) * 8;  // first row of this copy
-        const bool of_a = i * Z::kWaves * 8 < Z::kRowsA;
-        const uint32_t row = at - (of_a ? 0 : Z::kRowsA) + r;
-        if (COLUMNS && !of_a)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                b, lds + at * kStepBytes, 16,
-                row / 64 * stride_b + row % 64 * pitch_b + ((slot ^ ((row >> 1 & 3) << 1)) * 16), 0, 0, 0);
-        else
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? a : b, lds + at * kStepBytes, 16,
-                                                     row * (of_a ? pitch_a : pitch_b) + ((slot ^ (row >> 1 & 7)) * 16),
-                                                     0, 0, 0);
-    }
+    const int at = (i * Z::kWaves + wave) * 8;  // first row of this copy
+    const bool of_a = i * Z::kWaves * 8 < Z::kRowsA;
+    const uint32_t row = at - (of_a ? 0 : Z::kRowsA) + r;
+    if (COLUMNS && !of_a)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            b, lds + at * kStepBytes, 16, row / 64 * stride_b + row % 64 * pitch_b + ((slot ^ ((row >> 1 & 3) << 1)) * 16),
+            0, 0, 0);
+    else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? a : b, lds + at * kStepBytes, 16,
+                                                 row * (of_a ? pitch_a : pitch_b) + ((slot ^ (row >> 1 & 7)) * 16), 0, 0, 0);
 }
+
+// Where an operand's tile of a step begins, and the bytes from there to its end.
+struct Cursor {
+    const uint8_t* p;
+    int64_t left;
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource() const {
+        const uint64_t n = uint64_t(left);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, int(n >> 32 ? 0xffffffffu : uint32_t(n)),
+                                                 0x00020000);
+    }
+};
 
 // All but every wave's last N copies into LDS have landed, its reads are done, and
 // every wave is here. A wave's counters cover its own work only, so the wait comes
@@ -212,20 +219,42 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
     // Tiles of few tokens begin at steps of their own: rows a power of two apart, all
     // read at one place, would come from few memory channels.
     const uint32_t turn = Z::S > 2 && !kColumns ? uint32_t(a0 / Z::kRowsA * 5 % g.steps) : 0;
-    auto resource = [](const Operand& o, bool second, int64_t from) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.p + (second ? o.plane : 0) + from), 0,
-                                                 int(uint32_t(min(max(o.bytes - from, int64_t(0)), int64_t(0xffffffffu)))),
-                                                 0x00020000);
+    // The step to be copied next: its cursors move on by a step, and begin anew with a
+    // product of parts.
+    Cursor at_a, at_b;
+    uint32_t next = begin, next_k = 0;
+    const int64_t step_a = g.a.stride, step_b = kColumns ? 64 * g.b.pitch : g.b.stride;
+    const int64_t tile_a = a0 * g.a.pitch, tile_b = kColumns ? b0 / 64 * g.b.stride : b0 * g.b.pitch;
+    auto seek = [&]() {
+        const uint32_t p = (next >= g.steps) + (next >= 2 * g.steps);
+        next_k = next - p * g.steps;
+        const uint32_t k = Z::S > 2 && !kColumns ? (next_k + turn < g.steps ? next_k + turn : next_k + turn - g.steps) : next_k;
+        const int64_t from_a = tile_a + k * step_a, from_b = tile_b + k * step_b;
+        at_a = {g.a.p + ((g.order >> (2 * p)) & 1 ? g.a.plane : 0) + from_a, g.a.bytes - from_a};
+        at_b = {g.b.p + ((g.order >> (2 * p + 1)) & 1 ? g.b.plane : 0) + from_b, g.b.bytes - from_b};
     };
-    auto copy = [&](uint8_t* lds, uint32_t s) {
-        const uint32_t p = (s >= g.steps) + (s >= 2 * g.steps);
-        uint32_t k = s - p * g.steps;
-        if (Z::S > 2 && !kColumns) k = k + turn < g.steps ? k + turn : k + turn - g.steps;
-        copy_step<Z, kColumns>(
-            resource(g.a, (g.order >> (2 * p)) & 1, a0 * g.a.pitch + k * g.a.stride),
-            resource(g.b, (g.order >> (2 * p + 1)) & 1,
-                     kColumns ? b0 / 64 * g.b.stride + k * 64 * g.b.pitch : b0 * g.b.pitch + k * g.b.stride),
-            lds, uint32_t(g.a.pitch), uint32_t(g.b.pitch), uint32_t(g.b.stride), wave, lane);
+    // To the step after it, or nowhere from the last one.
+    auto advance = [&]() {
+        if (next + 1 >= end) return;
+        ++next;
+        ++next_k;
+        if (next_k == g.steps || (Z::S > 2 && !kColumns && next_k + turn == g.steps)) {
+            seek();
+        } else {
+            at_a.p += step_a;
+            at_a.left -= step_a;
+            at_b.p += step_b;
+            at_b.left -= step_b;
+        }
+    };
+    auto part = [&](uint8_t* lds, int i) {
+        copy_part<Z, kColumns>(i, at_a.resource(), at_b.resource(), lds, uint32_t(g.a.pitch), uint32_t(g.b.pitch),
+                               uint32_t(g.b.stride), wave, lane);
+    };
+    auto copy = [&](uint8_t* lds) {
+#pragma unroll
+        for (int i = 0; i < Z::kCopies; ++i) part(lds, i);
+        advance();
     };
 
     // LDS offsets of the lane's blocks of its first rows
@@ -248,67 +277,69 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
                                   (((c / 8) ^ ((k >> 1 & 3) << 1)) * 16) + c % 8 * 2;
             }
     i32x4 fa[2][BA], fb[2][BB];
-    auto read = [&](const uint8_t* lds, int s, i32x4 (&a)[BA], i32x4 (&b)[BB]) {
-#pragma unroll
-        for (int i = 0; i < BA; ++i) a[i] = *reinterpret_cast<const i32x4*>(lds + base_a + off[s] + i * 32 * kStepBytes);
-#pragma unroll
-        for (int i = 0; i < BB; ++i) {
-            if constexpr (kColumns) {
-                const s16x4 v0 = column4(lds + across[0][i] + s * 8 * kStepBytes);
-                const s16x4 v1 = column4(lds + across[1][i] + s * 8 * kStepBytes);
-                b[i] = __builtin_bit_cast(i32x4, s16x8{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]});
-            } else {
-                b[i] = *reinterpret_cast<const i32x4*>(lds + base_b + off[s] + i * 32 * kStepBytes);
-            }
+    // Block s of the wave's i-th 32 rows, A's and then B's.
+    auto read = [&](const uint8_t* lds, int s, int i, i32x4 (&a)[BA], i32x4 (&b)[BB]) {
+        if (i < BA) {
+            a[i] = *reinterpret_cast<const i32x4*>(lds + base_a + off[s] + i * 32 * kStepBytes);
+        } else if constexpr (kColumns) {
+            const s16x4 v0 = column4(lds + across[0][i - BA] + s * 8 * kStepBytes);
+            const s16x4 v1 = column4(lds + across[1][i - BA] + s * 8 * kStepBytes);
+            b[i - BA] = __builtin_bit_cast(i32x4, s16x8{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]});
+        } else {
+            b[i - BA] = *reinterpret_cast<const i32x4*>(lds + base_b + off[s] + (i - BA) * 32 * kStepBytes);
         }
     };
     f32x16 acc[BA][BB] = {};
 
-    // One step from `cur` (its copies done, piece 0 in registers): the reads of
-    // piece s + 1 are issued ahead of piece s's products; before the last piece's,
-    // everyone has read all of cur and the next step's copies are in `nxt`, so cur is
-    // refilled with the step S after its own. Past the last step the last one is copied
-    // again, so that the loop has no branches.
-    auto run = [&](uint8_t* cur, const uint8_t* nxt, uint32_t s) {
+    // One step from `cur` (its copies done, block 0 in registers): the reads of block
+    // s + 1 are issued among block s's products; before the last block's, everyone has
+    // read all of cur and the next step's copies are in `nxt`, so that among them cur is
+    // refilled with the step S after its own. A product occupies the matrix core for 32
+    // cycles, in which what stands between it and the next is issued; all reads or copies
+    // before a block's products kept the matrix core waiting. Past the last step the last
+    // one is copied again, so that the loop has no branches.
+    auto run = [&](uint8_t* cur, const uint8_t* nxt) {
         auto block = [&](auto which) {
-            constexpr int B = decltype(which)::value % 2;
+            constexpr int B = decltype(which)::value;
+            constexpr int kProducts = BA * BB, kReads = BA + BB;
 #pragma unroll
-            for (int i = 0; i < BA; ++i)
+            for (int m = 0; m < kProducts; ++m) {
+                acc[m / BB][m % BB] = mfma(E(), fa[B % 2][m / BB], fb[B % 2][m % BB], acc[m / BB][m % BB]);
 #pragma unroll
-                for (int j = 0; j < BB; ++j) acc[i][j] = mfma(E(), fa[B][i], fb[B][j], acc[i][j]);
+                for (int i = m * kReads / kProducts; i < (m + 1) * kReads / kProducts; ++i)
+                    read(B < 3 ? cur : nxt, (B + 1) % 4, i, fa[(B + 1) % 2], fb[(B + 1) % 2]);
+                if constexpr (B == 3)
+#pragma unroll
+                    for (int i = m * Z::kCopies / kProducts; i < (m + 1) * Z::kCopies / kProducts; ++i) part(cur, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         };
-        read(cur, 1, fa[1], fb[1]);
-        __builtin_amdgcn_sched_barrier(0);
         block(std::integral_constant<int, 0>{});
-        read(cur, 2, fa[0], fb[0]);
-        __builtin_amdgcn_sched_barrier(0);
         block(std::integral_constant<int, 1>{});
-        read(cur, 3, fa[1], fb[1]);
-        __builtin_amdgcn_sched_barrier(0);
         block(std::integral_constant<int, 2>{});
         copies_done_for_all<(Z::S - 2) * Z::kCopies>();
-        read(nxt, 0, fa[0], fb[0]);
-        copy(cur, min(s + Z::S, end - 1));
-        __builtin_amdgcn_sched_barrier(0);
         block(std::integral_constant<int, 3>{});
+        advance();
     };
     if (begin < end) {
-        copy(lds0, begin);
-        copy(lds1, min(begin + 1, end - 1));
-        if constexpr (Z::S > 2) copy(lds2, min(begin + 2, end - 1));
-        if constexpr (Z::S > 3) copy(lds3, min(begin + 3, end - 1));
+        seek();
+        copy(lds0);
+        copy(lds1);
+        if constexpr (Z::S > 2) copy(lds2);
+        if constexpr (Z::S > 3) copy(lds3);
         copies_done_for_all<(Z::S - 1) * Z::kCopies>();
-        read(lds0, 0, fa[0], fb[0]);
+#pragma unroll
+        for (int i = 0; i < BA + BB; ++i) read(lds0, 0, i, fa[0], fb[0]);
         uint32_t s = begin;
         for (; s + Z::S <= end; s += Z::S) {
-            run(lds0, lds1, s);
-            run(lds1, Z::S > 2 ? lds2 : lds0, s + 1);
-            if constexpr (Z::S > 2) run(lds2, Z::S > 3 ? lds3 : lds0, s + 2);
-            if constexpr (Z::S > 3) run(lds3, lds0, s + 3);
+            run(lds0, lds1);
+            run(lds1, Z::S > 2 ? lds2 : lds0);
+            if constexpr (Z::S > 2) run(lds2, Z::S > 3 ? lds3 : lds0);
+            if constexpr (Z::S > 3) run(lds3, lds0);
         }
-        if (s < end) run(lds0, lds1, s);
-        if (Z::S > 2 && s + 1 < end) run(lds1, Z::S > 2 ? lds2 : lds0, s + 1);
-        if (Z::S > 3 && s + 2 < end) run(lds2, lds3, s + 2);
+        if (s < end) run(lds0, lds1);
+        if (Z::S > 2 && s + 1 < end) run(lds1, Z::S > 2 ? lds2 : lds0);
+        if (Z::S > 3 && s + 2 < end) run(lds2, lds3);
         copies_done_for_all<0>();  // the copies past the end are done before LDS is given up
     }
 
