@@ -2,6 +2,7 @@
 // (retro_vocab.h), in pieces of the head.
 #include <algorithm>
 
+#include "retro_ce_few.h"
 #include "retro_ce_kernel.h"
 #include "retro_vocab_host.h"
 
@@ -267,9 +268,9 @@ bool is_direct(int type, int xtype, int64_t ldw, int64_t K) {
     return is_narrow(type, xtype) && K > 0 && K % vocab::kStepK == 0 && ldw % 16 == 0 && ldw < (1 << 24);
 }
 
-// Few tokens through packed blocks: the library's F32 products, which decode in
-// registers, read each block once; making planes would write and read 4 bytes and
-// more for every element.
+// Few tokens through packed blocks: decoded in registers, each block read once; making
+// planes would write and read 4 bytes and more for every element. Of the types that
+// few_kernel does not take the logits are the library's F32 products.
 constexpr int64_t kFewT = 64;
 bool is_few(int type, int64_t ldw, int64_t K, int64_t T) {
     return !is_float(type) && T <= kFewT && K > 0 && ldw == host::row_bytes_of(type, K);
@@ -286,6 +287,8 @@ int64_t grad_piece(int64_t K, int64_t N, int64_t T) {
     return std::min(plane_piece(K, N), piece_rows(N, std::max<int64_t>((1 << 27) / std::max<int64_t>(T, 1), 4096)));
 }
 int64_t few_piece(int64_t N, int64_t T) { return piece_rows(N, (1 << 24) / std::max<int64_t>(T, 1)); }
+// Elements of a token's row that few_kernel reads.
+int64_t few_padded(int64_t K) { return cdiv(K, kFewK) * kFewK; }
 
 // Parts of the workspace, each on a 256-byte boundary.
 struct Bump {
@@ -349,10 +352,17 @@ Forward forward_plan(int type, int64_t ldw, int xtype, int64_t K, int64_t N, int
     Bump b;
     p.at_target = b.take(4 * T);
     if (is_few(type, ldw, K, T)) {
-        p.piece = few_piece(N, T);
-        p.part = b.take(8 * T * (cdiv(N, p.piece) * cdiv(p.piece, kRun)));
-        p.few_x = b.take(4 * T * K);
-        p.few_l = b.take(4 * T * p.piece);
+        if (vocab::few_type(type)) {  // 2^24 rows are 2^17 workgroups
+            p.piece = piece_rows(N, 1 << 24);
+            p.part = b.take(8 * T * cdiv(N, p.piece) * vocab::few_runs(p.piece));
+            p.factor = b.take(4 * T);
+            p.x = b.take(plane_bytes(parts_of(xtype), vocab::padded(T), few_padded(K)));
+        } else {
+            p.piece = few_piece(N, T);
+            p.part = b.take(8 * T * (cdiv(N, p.piece) * cdiv(p.piece, kRun)));
+            p.few_x = b.take(4 * T * K);
+            p.few_l = b.take(4 * T * p.piece);
+        }
         p.bytes = b.at;
         return p;
     }
@@ -406,7 +416,12 @@ Backward backward_plan(int type, int64_t ldw, int xtype, bool weight_grad, bool 
     if (is_few(type, ldw, K, T)) {
         p.piece = few_piece(N, T);
         p.splits = cdiv(N, p.piece);
-        p.few_x = b.take(4 * T * K);
+        if (vocab::few_type(type)) {
+            p.factor = b.take(4 * T);
+            p.x = b.take(plane_bytes(parts_of(xtype), vocab::padded(T), few_padded(K)));
+        } else {
+            p.few_x = b.take(4 * T * K);
+        }
         p.few_l = b.take(4 * T * p.piece);
         p.sums = b.take(4 * p.splits * T * K);
         p.few_ws = b.take(host::kSplitWorkspaceMax);
@@ -509,7 +524,7 @@ int zero(void* p, int64_t words, hipStream_t st) {
     return host::launch_status();
 }
 
-int token_rows(const Call& c, int parts, bool mask, uint8_t* out, float* factor) {
+int token_rows(const Call& c, int parts, bool mask, uint8_t* out, int64_t padded_k, float* factor) {
     return mx::with_float(c.xtype, [&](auto* tag) {
         using TX = std::remove_pointer_t<decltype(tag)>;
         auto kernel = parts == 2 ? token_rows_kernel<TX, 2> : token_rows_kernel<TX, 1>;
@@ -518,7 +533,7 @@ int token_rows(const Call& c, int parts, bool mask, uint8_t* out, float* factor)
         host::clear_last_error();
         kernel<<<dim3(uint32_t(vocab::padded(c.T))), dim3(256), 0, c.st>>>(
             static_cast<const TX*>(c.X), c.ldx, c.K, c.targets, c.wide_targets, c.N, mask,
-            reinterpret_cast<uint16_t*>(out), vocab::padded(c.K), c.T, factor);
+            reinterpret_cast<uint16_t*>(out), padded_k, c.T, factor);
         return host::launch_status();
     });
 }
@@ -563,12 +578,48 @@ int widen(const Call& c, bool mask, float* out) {
     });
 }
 
+// What few_kernel takes of a call, but rows and results.
+FewArgs few_args(const Call& c, const uint8_t* x, const float* factor) {
+    FewArgs a = {};
+    a.ldw = c.ldw;
+    a.N = c.N;
+    a.K = int(c.K);
+    a.T = int(c.T);
+    a.x = reinterpret_cast<const uint16_t*>(x);
+    a.plane = vocab::padded(c.T) * few_padded(c.K);
+    a.factor = factor;
+    a.targets = c.targets;
+    a.wide_targets = c.wide_targets;
+    return a;
+}
+
+int few(const Call& c, FewArgs& a, int64_t n0, int64_t rows, bool prob) {
+    a.W = c.W + n0 * c.ldw;
+    a.n0 = n0;
+    a.rows = rows;
+    return vocab::with_type(c.type, [&](auto type) {
+        return vocab::launch_few<decltype(type)::value>(prob, parts_of(c.xtype), a, c.st);
+    });
+}
+
 int forward(const Call& c, float* loss, float* lse, uint8_t* ws) {
     const Forward p = forward_plan(c.type, c.ldw, c.xtype, c.K, c.N, c.T);
     float* at_target = reinterpret_cast<float*>(ws + p.at_target);
     float2* part = reinterpret_cast<float2*>(ws + p.part);
     int64_t runs = 0;
-    if (c.N > 0 && is_few(c.type, c.ldw, c.K, c.T)) {
+    if (c.N > 0 && is_few(c.type, c.ldw, c.K, c.T) && vocab::few_type(c.type)) {
+        float* factor = reinterpret_cast<float*>(ws + p.factor);
+        RETRO_TRY(token_rows(c, parts_of(c.xtype), false, ws + p.x, few_padded(c.K), factor));
+        FewArgs a = few_args(c, ws + p.x, factor);
+        a.part = part;
+        a.at_target = at_target;
+        for (int64_t n0 = 0; n0 < c.N; n0 += p.piece) {
+            const int64_t rows = std::min(p.piece, c.N - n0);
+            a.part0 = runs;
+            RETRO_TRY(few(c, a, n0, rows, false));
+            runs += vocab::few_runs(rows);
+        }
+    } else if (c.N > 0 && is_few(c.type, c.ldw, c.K, c.T)) {
         float *x = reinterpret_cast<float*>(ws + p.few_x), *l = reinterpret_cast<float*>(ws + p.few_l);
         RETRO_TRY(widen(c, false, x));
         for (int64_t n0 = 0; n0 < c.N; n0 += p.piece) {
@@ -591,7 +642,7 @@ int forward(const Call& c, float* loss, float* lse, uint8_t* ws) {
         if (narrow && c.K > 0 && c.K % vocab::kStepK == 0 && c.ldx % 8 == 0 && c.ldx < (1 << 23) && mx::aligned(c.X, 16))
             g.b = {static_cast<const uint8_t*>(c.X), c.ldx * 2, vocab::kStepK * 2, 0, ((c.T - 1) * c.ldx + c.K) * 2, c.T};
         else
-            RETRO_TRY(token_rows(c, narrow ? 0 : parts_of(c.xtype), false, ws + p.x, factor));
+            RETRO_TRY(token_rows(c, narrow ? 0 : parts_of(c.xtype), false, ws + p.x, vocab::padded(c.K), factor));
         g.steps = uint32_t(vocab::padded(c.K) / vocab::kStepK);
         g.splits = 1;
         set_pairs(g, narrow ? 1 : parts_of(c.type), narrow ? 1 : parts_of(c.xtype));
@@ -637,17 +688,29 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
     float* sums = reinterpret_cast<float*>(ws + p.sums);
     if (is_few(c.type, c.ldw, c.K, c.T)) {
         float *x = reinterpret_cast<float*>(ws + p.few_x), *l = reinterpret_cast<float*>(ws + p.few_l);
-        RETRO_TRY(widen(c, true, x));
+        const bool fused = vocab::few_type(c.type);
+        float* factor = reinterpret_cast<float*>(ws + p.factor);
+        if (fused)
+            RETRO_TRY(token_rows(c, parts_of(c.xtype), true, ws + p.x, few_padded(c.K), factor));
+        else
+            RETRO_TRY(widen(c, true, x));
+        FewArgs a = few_args(c, ws + p.x, factor);
+        a.lse = lse;
+        a.out = l;
         RETRO_TRY(zero(ws + p.few_ws, host::kSplitCountBytes / 4, c.st));
         int64_t done = 0;
         for (int64_t n0 = 0; n0 < c.N; n0 += p.piece, ++done) {
             const int64_t rows = std::min(p.piece, c.N - n0);
             const uint8_t* W = c.W + n0 * c.ldw;
-            RETRO_TRY(retro_mul_mat(c.type, W, x, l, c.K, rows, c.T, c.st));
-            host::clear_last_error();
-            run_prob_kernel<<<dim3(uint32_t(cdiv(rows, kRun)), uint32_t(c.T)), dim3(256), 0, c.st>>>(
-                l, rows, c.targets, c.wide_targets, c.N, n0, lse);
-            RETRO_TRY(host::launch_status());
+            if (fused) {
+                RETRO_TRY(few(c, a, n0, rows, true));
+            } else {
+                RETRO_TRY(retro_mul_mat(c.type, W, x, l, c.K, rows, c.T, c.st));
+                host::clear_last_error();
+                run_prob_kernel<<<dim3(uint32_t(cdiv(rows, kRun)), uint32_t(c.T)), dim3(256), 0, c.st>>>(
+                    l, rows, c.targets, c.wide_targets, c.N, n0, lse);
+                RETRO_TRY(host::launch_status());
+            }
             RETRO_TRY(retro_out_prod_ws(RETRO_VARIANT_AUTO, c.type, W, l, sums + done * c.T * c.K, c.K, rows, c.T,
                                         ws + p.few_ws, host::kSplitWorkspaceMax, c.st));
         }
@@ -662,7 +725,7 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
     const int pd = c.xtype == RETRO_F32 || (dW && c.type == RETRO_F32) ? 2 : 1;
     const int64_t Kp = vocab::padded(c.K), Tp = vocab::padded(c.T);
     if (!narrow) RETRO_TRY(head_top(c, top));
-    RETRO_TRY(token_rows(c, narrow ? 0 : px, true, ws + p.x, factor));
+    RETRO_TRY(token_rows(c, narrow ? 0 : px, true, ws + p.x, Kp, factor));
     if (dW) {
         host::clear_last_error();
         weights_kernel<<<dim3(1), dim3(1024), 0, c.st>>>(dloss, factor, c.targets, c.wide_targets, c.N, c.T, weight,

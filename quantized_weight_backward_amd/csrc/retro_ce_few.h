@@ -1,0 +1,283 @@
+// retro_ce_few.h - the logits of up to 64 tokens through a packed head, read once as it
+// is: codes become F16 in registers, and the matrix cores multiply them as they are.
+//
+//   l[t][n] = sum over sub-blocks b of 32: a[n][b] sum_k q[n][k] x[t][k] + c[n][b] sum_k x[t][k]
+//
+// A code q has at most 8 bits and x (scaled by a power of two, in one F16 part or two)
+// 11 a part, so their products are exact; the F32 sum of a sub-block is scaled by its
+// a and c as the format defines them. Tokens are the rows of a 16 x 16 block, rows of the
+// head its columns: a lane decodes 8 codes of the row whose scale it applies to the four
+// results that it gets.
+//
+// What bounds it is memory where few tokens are given: Q4_K 131072 x 4096 and 16 tokens
+// take MEASURED, against 252 us with the weights decoded to F32 in front of
+// F32 matrix instructions.
+#pragma once
+
+#include "retro_ce_kernel.h"
+#include "retro_kernels.h"
+
+namespace retro {
+namespace ce {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x2b __attribute__((ext_vector_type(2), aligned(1)));
+typedef _Float16 f16x2v __attribute__((ext_vector_type(2)));
+using mx::f32x4;
+using mx::u32x4;
+
+// Two F16 of 1024 + the bytes lo and hi of w.
+template <int LO, int HI>
+__device__ __forceinline__ f16x2v bytes_above_1024(uint32_t w) {
+    return __builtin_bit_cast(f16x2v, __builtin_amdgcn_perm(0x64646464u, w, 0x04000400u | (HI << 16) | LO));
+}
+
+// Eight unsigned bytes less `less` as F16.
+__device__ __forceinline__ f16x8 bytes_to_f16(uint32_t w0, uint32_t w1, float less) {
+    const _Float16 s = _Float16(-1024.f - less);
+    const f16x2v off = {s, s};
+    const f16x2v v0 = bytes_above_1024<0, 1>(w0) + off, v1 = bytes_above_1024<2, 3>(w0) + off;
+    const f16x2v v2 = bytes_above_1024<0, 1>(w1) + off, v3 = bytes_above_1024<2, 3>(w1) + off;
+    return f16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+}
+
+// Codes 8g .. 8g + 7 of a sub-block of 32, its factor and its offset.
+struct Codes {
+    f16x8 q, q2;  // q2: a second product's, where a code times its scale has more bits than one holds
+    float a, c;
+};
+
+template <int TYPE>
+constexpr bool kFewType = kNibbleLayout<TYPE> || TYPE == kQ8_0 || TYPE == kQ4_K || TYPE == kQ5_K || TYPE == kQ6_K;
+template <int TYPE>
+constexpr bool kOffset = kHasOffset<TYPE> || TYPE == kQ4_K || TYPE == kQ5_K;
+
+// Sub-block b (of 32) of a row.
+template <int TYPE>
+__device__ __forceinline__ Codes codes_of(const uint8_t* row, int b, int g) {
+    Codes r;
+    r.c = 0.f;
+    if constexpr (TYPE == kQ8_0) {
+        const uint8_t* blk = row + b * 34;
+        const u32x2 w = *reinterpret_cast<const u32x2*>(blk + 2 + 8 * g);
+        r.a = half_to_f32(*reinterpret_cast<const uint16_t*>(blk));
+        r.q = bytes_to_f16(w[0] ^ 0x80808080u, w[1] ^ 0x80808080u, 128.f);
+    } else if constexpr (kNibbleLayout<TYPE>) {
+        // low nibbles of the code bytes, then high ones
+        const uint8_t* blk = row + b * Format<TYPE>::kBytes;
+        const u32x2b w = *reinterpret_cast<const u32x2b*>(blk + kHeader<TYPE> + 8 * (g & 1));
+        const int sh = g >= 2 ? 4 : 0;
+        uint32_t w0 = (w[0] >> sh) & 0x0F0F0F0Fu, w1 = (w[1] >> sh) & 0x0F0F0F0Fu;
+        if constexpr (TYPE == kMXFP4) {
+            // two codes to a byte, which the conversion takes
+            r.a = mx_scale(blk[0]);
+            const uint32_t p0 = w0 | (w0 >> 4), p1 = w1 | (w1 >> 4);
+            const f16x2v v0 = __builtin_bit_cast(f16x2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(p0, 1.f, 0));
+            const f16x2v v1 = __builtin_bit_cast(f16x2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(p0, 1.f, 2));
+            const f16x2v v2 = __builtin_bit_cast(f16x2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(p1, 1.f, 0));
+            const f16x2v v3 = __builtin_bit_cast(f16x2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(p1, 1.f, 2));
+            r.q = f16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(blk);
+            r.a = half_to_f32(h[0]);
+            if constexpr (kHasOffset<TYPE>) r.c = half_to_f32(h[1]);
+            if constexpr (kHasFifth<TYPE>) {
+                constexpr int at = kHasOffset<TYPE> ? 2 : 1;
+                const uint32_t qh = uint32_t(h[at]) | (uint32_t(h[at + 1]) << 16);
+                w0 |= fifth_bits(qh, 8 * g);
+                w1 |= fifth_bits(qh, 8 * g + 4);
+            }
+            r.q = bytes_to_f16(w0, w1, kHasOffset<TYPE> ? 0.f : kHasFifth<TYPE> ? 16.f : 8.f);
+        }
+    } else if constexpr (TYPE == kQ4_K || TYPE == kQ5_K) {
+        const uint8_t* sb = row + (b >> 3) * Format<TYPE>::kBytes;
+        const int j = b & 7;
+        const u32x4 hw = *reinterpret_cast<const u32x4*>(sb);
+        float m;
+        q4_k_coeffs(hw[0], hw[1], hw[2], hw[3], j, r.a, m);
+        r.c = -m;
+        const u32x2 w = *reinterpret_cast<const u32x2*>(sb + (TYPE == kQ5_K ? 48 : 16) + 32 * (j / 2) + 8 * g);
+        uint32_t w0 = (w[0] >> (4 * (j & 1))) & 0x0F0F0F0Fu, w1 = (w[1] >> (4 * (j & 1))) & 0x0F0F0F0Fu;
+        if constexpr (TYPE == kQ5_K) {
+            const u32x2 qh = *reinterpret_cast<const u32x2*>(sb + 16 + 8 * g);
+            w0 |= ((qh[0] >> j) & 0x01010101u) << 4;
+            w1 |= ((qh[1] >> j) & 0x01010101u) << 4;
+        }
+        r.q = bytes_to_f16(w0, w1, 0.f);
+    } else {
+        // Q6_K: a scale covers 16 codes, half of the sub-block's lanes. (q - 32) times it
+        // has up to 13 bits: its four low bits and the rest make products of their own.
+        const uint8_t* sb = row + (b >> 3) * 210;
+        const int i = b & 7, half = i >> 2, p = i & 3;
+        const u32x2 ql = *reinterpret_cast<const u32x2*>(sb + 64 * half + 32 * (p & 1) + 8 * g);
+        const u32x2 qh = *reinterpret_cast<const u32x2*>(sb + 128 + 32 * half + 8 * g);
+        const int sc = static_cast<int8_t>(sb[192 + 8 * half + 2 * p + (g >> 1)]);
+        r.a = half_to_f32(*reinterpret_cast<const uint16_t*>(sb + 208));
+        const int sh = 4 * (p >> 1);
+        const f16x8 q = bytes_to_f16(((ql[0] >> sh) & 0x0F0F0F0Fu) | (((qh[0] >> (2 * p)) & 0x03030303u) << 4),
+                                     ((ql[1] >> sh) & 0x0F0F0F0Fu) | (((qh[1] >> (2 * p)) & 0x03030303u) << 4), 32.f);
+        r.q = q * _Float16(float(sc & 15));
+        r.q2 = q * _Float16(float(sc & ~15));
+    }
+    return r;
+}
+
+struct FewArgs {
+    const uint8_t* W;  // of this piece
+    int64_t ldw, rows, N, n0;
+    int K, T;
+    const uint16_t* x;  // planes in steps of 64 rows, K in whole 256s
+    int64_t plane;      // elements
+    const float* factor;
+    const void* targets;
+    bool wide_targets;
+    // kStats
+    float2* part;
+    int64_t part0;
+    float* at_target;
+    // kProb: d, rows of tokens
+    const float* lse;
+    float* out;
+};
+
+constexpr int kFewWaves = 4, kFewRows = 32 * kFewWaves;  // rows of the head a wave, a workgroup
+constexpr int kFewK = 256;                               // of x in LDS
+
+__device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Up to 16 TB tokens, x in PX parts.
+template <int TYPE, int TB, int PX, Kind KIND>
+__global__ __launch_bounds__(kFewWaves * 64) void few_kernel(const FewArgs g) {
+    constexpr int kRows = kFewK / 64 * 16 * TB * PX;  // of 128 bytes in LDS: step, part, token
+    constexpr int kCopies = kRows * 128 / (1024 * kFewWaves);
+    __shared__ __align__(1024) uint8_t lds0[kRows * 128];
+    __shared__ __align__(1024) uint8_t lds1[kRows * 128];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int r = lane & 15, gr = lane >> 4;
+    const int64_t row0 = int64_t(blockIdx.x) * kFewRows + wave * 32;
+
+    // x's rows of a chunk: row (step, part, token) of 128 bytes, its 16-byte blocks
+    // permuted by XOR with (row / 2) % 8
+    const __amdgpu_buffer_rsrc_t x = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(g.x), 0,
+                                                                       int(uint32_t(PX * g.plane * 2)), 0x00020000);
+    auto copy = [&](uint8_t* lds, int chunk) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int at = (i * kFewWaves + wave) * 8;
+            const uint32_t row = at + (lane >> 3);
+            const uint32_t token = row % (16 * TB), part = row / (16 * TB) % PX, step = row / (16 * TB * PX);
+            const uint32_t from = uint32_t(part * g.plane * 2) + (step * 64 + token) * 128 +
+                                  ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(x, lds + at * 128, 16, from, uint32_t(chunk) * (kFewK / 64 * 64 * 128),
+                                                     0, 0);
+        }
+    };
+    const uint8_t* w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[i] = g.W + min(row0 + i * 16 + r, g.rows - 1) * g.ldw;
+    f32x4 acc[2][TB] = {};
+    const f16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
+    auto sub_blocks = [&](const uint8_t* lds, int chunk, auto whole) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kFewK / 32; ++i) {
+            const int b = chunk * (kFewK / 32) + i;
+            if (!decltype(whole)::value && b * 32 >= g.K) break;
+            f16x8 xs[TB][PX];
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int p = 0; p < PX; ++p) {
+                    const int row = ((i / 2) * PX + p) * (16 * TB) + t * 16 + r, block = (i % 2) * 4 + gr;
+                    xs[t][p] = *reinterpret_cast<const f16x8*>(lds + row * 128 + ((block ^ ((row >> 1) & 7)) * 16));
+                }
+            f32x4 sum[TB];
+            if constexpr (kOffset<TYPE>)
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    sum[t] = mfma16(xs[t][0], ones, f32x4{0, 0, 0, 0});
+                    if constexpr (PX == 2) sum[t] = mfma16(xs[t][1], ones, sum[t]);
+                }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const Codes c = codes_of<TYPE>(w[n], b, gr);
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+                    for (int p = PX - 1; p >= 0; --p) {
+                        v = mfma16(xs[t][p], c.q, v);
+                        if constexpr (TYPE == kQ6_K) v = mfma16(xs[t][p], c.q2, v);
+                    }
+#pragma unroll
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        acc[n][t][i4] = fmaf(c.a, v[i4], acc[n][t][i4]);
+                        if constexpr (kOffset<TYPE>) acc[n][t][i4] = fmaf(c.c, sum[t][i4], acc[n][t][i4]);
+                    }
+                }
+            }
+        }
+    };
+    auto run = [&](const uint8_t* lds, int chunk) __attribute__((always_inline)) {
+        if ((chunk + 1) * kFewK <= g.K)
+            sub_blocks(lds, chunk, std::true_type{});
+        else
+            sub_blocks(lds, chunk, std::false_type{});
+    };
+    const int chunks = (g.K + kFewK - 1) / kFewK;
+    copy(lds0, 0);
+    for (int c = 0; c < chunks; c += 2) {
+        copies_done_for_all<0>();
+        if (c + 1 < chunks) copy(lds1, c + 1);
+        run(lds0, c);
+        if (c + 1 >= chunks) break;
+        copies_done_for_all<0>();
+        if (c + 2 < chunks) copy(lds0, c + 2);
+        run(lds1, c + 1);
+    }
+
+    // A lane: tokens 16 t + 4 gr + i, rows row0 + 16 n + r.
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int token = 16 * t + 4 * gr + i;
+            const bool live = token < g.T;
+            const float f = live ? g.factor[token] : 0.f;
+            const int64_t target = live ? vocab::token_at(g.targets, g.wide_targets, token, g.N) : -1;
+            float l[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) l[n] = acc[n][t][i] * f;
+            if constexpr (KIND == kStats) {
+                float top = -__builtin_inff();
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int64_t row = row0 + n * 16 + r;
+                    if (row >= g.rows) l[n] = -__builtin_inff();
+                    if (live && target == g.n0 + row && row < g.rows) g.at_target[token] = l[n];
+                    top = fmaxf(top, l[n]);
+                }
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+                const float from = top == -__builtin_inff() ? 0.f : top;
+                float sum = exp_of(l[0] - from) + exp_of(l[1] - from);
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) sum += __shfl_xor(sum, d);
+                if (live && r == 0)
+                    g.part[(g.part0 + int64_t(blockIdx.x) * kFewWaves + wave) * g.T + token] = make_float2(top, sum);
+            } else {
+                const float lse = target >= 0 ? g.lse[token] : 0.f;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int64_t row = row0 + n * 16 + r;
+                    if (!live || row >= g.rows) continue;
+                    g.out[token * g.rows + row] =
+                        target >= 0 ? exp_of(l[n] - lse) - (g.n0 + row == target ? 1.f : 0.f) : 0.f;
+                }
+            }
+        }
+}
+
+}  // namespace ce
+}  // namespace retro

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "retro_ce_few.h"
 #include "retro_host.h"
 #include "retro_kernels.h"
 #include "retro_mm_kernel.h"
@@ -442,6 +443,27 @@ int launch_top(const uint8_t* W, int64_t ldw, int64_t rows, int64_t K, uint32_t*
     return host::launch_status();
 }
 
+template <int TYPE>
+int launch_few(bool prob, int parts, const ce::FewArgs& a, hipStream_t st) {
+    if constexpr (!ce::kFewType<TYPE>) {
+        return RETRO_E_TYPE;
+    } else {
+        auto kernel_of = [&](auto tokens) {
+            constexpr int TB = decltype(tokens)::value;
+            return prob ? (parts == 2 ? ce::few_kernel<TYPE, TB, 2, ce::kProb> : ce::few_kernel<TYPE, TB, 1, ce::kProb>)
+                        : (parts == 2 ? ce::few_kernel<TYPE, TB, 2, ce::kStats> : ce::few_kernel<TYPE, TB, 1, ce::kStats>);
+        };
+        auto kernel = a.T <= 16   ? kernel_of(std::integral_constant<int, 1>{})
+                      : a.T <= 32 ? kernel_of(std::integral_constant<int, 2>{})
+                                  : kernel_of(std::integral_constant<int, 4>{});
+        const int64_t blocks = host::cdiv(a.rows, ce::kFewRows);
+        host::clear_last_error();
+        kernel<<<dim3(uint32_t(blocks)), dim3(ce::kFewWaves * 64), 0, st>>>(a);
+        return host::launch_status();
+    }
+}
+
+template int launch_few<RETRO_UNIT_TYPE>(bool, int, const ce::FewArgs&, hipStream_t);
 template int launch_embed<RETRO_UNIT_TYPE>(int, const EmbedArgs&, hipStream_t);
 template int launch_planes<RETRO_UNIT_TYPE>(const PlaneArgs&, hipStream_t);
 template int launch_top<RETRO_UNIT_TYPE>(const uint8_t*, int64_t, int64_t, int64_t, uint32_t*, hipStream_t);

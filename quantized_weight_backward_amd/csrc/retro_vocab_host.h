@@ -7,6 +7,9 @@
 #include "retro_vocab.h"
 
 namespace retro {
+namespace ce {
+struct FewArgs;
+}
 namespace vocab {
 
 // The 16-byte pieces of 16-bit rows that a matrix-core step takes: K in whole 64s.
@@ -46,6 +49,17 @@ int launch_planes(const PlaneArgs& a, hipStream_t st);
 // *top = the larger of *top and the largest magnitude's bits of `rows` rows.
 template <int TYPE>
 int launch_top(const uint8_t* W, int64_t ldw, int64_t rows, int64_t K, uint32_t* top, hipStream_t st);
+
+// The logits of up to 64 tokens through packed rows, in one launch (retro_ce_few.h).
+// The weight types that it takes:
+inline bool few_type(int type) {
+    return type == RETRO_Q4_0 || type == RETRO_Q4_1 || type == RETRO_Q5_0 || type == RETRO_Q5_1 || type == RETRO_Q8_0 ||
+           type == RETRO_MXFP4 || type == RETRO_Q4_K || type == RETRO_Q5_K || type == RETRO_Q6_K;
+}
+// Runs of the head's rows that it gives statistics of.
+inline int64_t few_runs(int64_t rows) { return host::cdiv(rows, 128) * 4; }
+template <int TYPE>
+int launch_few(bool prob, int parts, const ce::FewArgs& a, hipStream_t st);
 
 // Calls f with a std::integral_constant of a weight type.
 template <typename F>
