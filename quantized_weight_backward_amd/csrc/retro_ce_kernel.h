@@ -314,9 +314,11 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
+        __builtin_amdgcn_s_setprio(1);
         block(std::integral_constant<int, 0>{});
         block(std::integral_constant<int, 1>{});
         block(std::integral_constant<int, 2>{});
+        __builtin_amdgcn_s_setprio(0);
         copies_done_for_all<(Z::S - 2) * Z::kCopies>();
         block(std::integral_constant<int, 3>{});
         advance();
