@@ -9,9 +9,8 @@
 //           times dloss
 //   kSum    C itself, in F32 (added to what is there) or rounded to the result's type
 //
-// Tokens are the columns of a matrix-core block: a lane then holds 16 rows of the
-// head of one token, whose maximum and sum need one exchange, with the other half
-// of the wave.
+// Tokens are the columns of a matrix-core block: a lane then holds rows of the head of
+// one token, whose maximum and sum need two exchanges, with the three other lanes of it.
 #pragma once
 
 #include <type_traits>
@@ -21,7 +20,7 @@
 namespace retro {
 namespace ce {
 
-using mx::f32x16;
+using mx::f32x4;
 using mx::i32x4;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -34,14 +33,20 @@ enum Kind { kStats, kProb, kSum };
 
 constexpr int kStepBytes = 128;  // 64 elements of a row
 
-__device__ __forceinline__ f32x16 mfma(__bf16, const i32x4& a, const i32x4& b, const f32x16& c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
+// c += a b, 16 x 16 results of 32 k. 32 x 32 of 16 k move twice the results through the
+// registers for the same work, which costs power, and power is what bounds the clock:
+// alone, on random operands, they run at 1.86 PFLOP/s, these at 2.13. Written as
+// assembly so that a result stays in its registers: the compiler moves results of this
+// size from one set to another, runs out of them and spills in the loop. The wait states
+// are for operands that a vector instruction has just written.
+__device__ __forceinline__ void mfma(__bf16, const i32x4& a, const i32x4& b, f32x4& c) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
-__device__ __forceinline__ f32x16 mfma(_Float16, const i32x4& a, const i32x4& b, const f32x16& c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                  0);
+__device__ __forceinline__ void mfma(_Float16, const i32x4& a, const i32x4& b, f32x4& c) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
+// Results of products issued before can be read after it: of 8 passes, 11 wait states.
+__device__ __forceinline__ void results_ready(f32x4& c) { asm volatile("s_nop 15\n\ts_nop 3" : "+v"(c)); }
 
 // exp(x) for x <= 0 or so: off by |x| 2^-24 and a step, of a value that falls with x.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
@@ -114,30 +119,24 @@ struct Tile {
 //     64 c .. 64 c + 63 of row k, permuted by XOR with twice (k / 2) % 4, so that the four
 //     rows of a transposing read lie in banks of their own.
 // What lies past the operand reads as zeros (the buffer's bound).
-template <class Z, bool COLUMNS>
-__device__ __forceinline__ void copy_part(int i, __amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b, uint8_t* lds,
-                                          uint32_t pitch_a, uint32_t pitch_b, uint32_t stride_b, int wave, int lane) {
+// The lane's bytes from its wave's first row of a copy. What else differs between a
+// wave's copies of an operand is uniform and part of the buffer's address, so that one
+// register serves all of them.
+__device__ __forceinline__ uint32_t lane_bytes(uint32_t pitch, bool columns, int wave, int lane) {
     const uint32_t r = lane >> 3, slot = lane & 7;
-    const int at = (i * Z::kWaves + wave) * 8;  // first row of this copy
-    const bool of_a = i * Z::kWaves * 8 < Z::kRowsA;
-    const uint32_t row = at - (of_a ? 0 : Z::kRowsA) + r;
-    if (COLUMNS && !of_a)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            b, lds + at * kStepBytes, 16, row / 64 * stride_b + row % 64 * pitch_b + ((slot ^ ((row >> 1 & 3) << 1)) * 16),
-            0, 0, 0);
-    else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? a : b, lds + at * kStepBytes, 16,
-                                                 row * (of_a ? pitch_a : pitch_b) + ((slot ^ (row >> 1 & 7)) * 16), 0, 0, 0);
+    return (wave * 8 + r) * pitch + (slot ^ (columns ? (r >> 1) << 1 : (wave & 1) * 4 + (r >> 1))) * 16;
 }
 
 // Where an operand's tile of a step begins, and the bytes from there to its end.
 struct Cursor {
     const uint8_t* p;
     int64_t left;
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource() const {
-        const uint64_t n = uint64_t(left);
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, int(n >> 32 ? 0xffffffffu : uint32_t(n)),
-                                                 0x00020000);
+    // What lies `further` on, nothing of it where that is past the end.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(int64_t further) const {
+        const int64_t n = left - further;
+        const int32_t high = int32_t(n >> 32);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + further), 0,
+                                                 int(high < 0 ? 0u : high > 0 ? 0xffffffffu : uint32_t(n)), 0x00020000);
     }
 };
 
@@ -191,13 +190,14 @@ __device__ __forceinline__ void put8(uint16_t* to, int64_t left, const u16x8& w)
 template <typename E, class Z, Kind KIND, typename TO, int PARTS>
 __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const Args g) {
     constexpr int WB = Z::WB, BA = Z::BA, BB = Z::BB;
+    constexpr int NA = 2 * BA, NB = 2 * BB;  // 16 x 16 blocks
     // arrays of their own: the compiler sees which a copy goes to
     __shared__ __align__(1024) uint8_t lds0[Z::kBytes];
     __shared__ __align__(1024) uint8_t lds1[Z::kBytes];
     __shared__ __align__(1024) uint8_t lds2[Z::S > 2 ? Z::kBytes : 1];
     __shared__ __align__(1024) uint8_t lds3[Z::S > 3 ? Z::kBytes : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-    const int r = lane & 31, h = lane >> 5, wa = wave / WB, wb = wave % WB;
+    const int r = lane & 15, h = lane >> 4, wa = wave / WB, wb = wave % WB;
 
     // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous range of
     // tiles, in groups of `group` tiles of B by all of A, so that the workgroups
@@ -247,9 +247,20 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
             at_b.left -= step_b;
         }
     };
+    // A wave's i-th copy of an operand is kTurn rows further on than the one before.
+    constexpr int kTurn = 8 * Z::kWaves, kCopiesA = Z::kRowsA / kTurn;
+    static_assert(Z::kWaves % 2 == 0 && kTurn <= 64, "a wave's copies are permuted alike");
+    const uint32_t lane_a = lane_bytes(uint32_t(g.a.pitch), false, wave, lane);
+    const uint32_t lane_b = lane_bytes(uint32_t(g.b.pitch), kColumns, wave, lane);
     auto part = [&](uint8_t* lds, int i) {
-        copy_part<Z, kColumns>(i, at_a.resource(), at_b.resource(), lds, uint32_t(g.a.pitch), uint32_t(g.b.pitch),
-                               uint32_t(g.b.stride), wave, lane);
+        uint8_t* to = lds + (i * Z::kWaves + wave) * 8 * kStepBytes;
+        const int row = (i < kCopiesA ? i : i - kCopiesA) * kTurn;
+        if (i < kCopiesA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(at_a.resource(row * g.a.pitch), to, 16, lane_a, 0, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                at_b.resource(kColumns ? row / 64 * g.b.stride + row % 64 * g.b.pitch : row * g.b.pitch), to, 16, lane_b, 0,
+                0, 0);
     };
     auto copy = [&](uint8_t* lds) {
 #pragma unroll
@@ -257,70 +268,77 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
         advance();
     };
 
-    // LDS offsets of the lane's blocks of its first rows
-    uint32_t off[4];
+    // LDS offsets of the lane's elements of its first row, k 0 .. 31 and 32 .. 63
+    uint32_t off[2];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) off[s] = r * kStepBytes + (((4 * h + s) ^ ((r >> 1) & 7)) * 16);
+    for (int s = 0; s < 2; ++s) off[s] = r * kStepBytes + (((4 * s + h) ^ ((r >> 1) & 7)) * 16);
     const uint32_t base_a = wa * BA * 32 * kStepBytes, base_b = (Z::kRowsA + wb * BB * 32) * kStepBytes;
     // Of columns: 16 lanes read 4 rows of k by 16 columns and get a column's four each.
     // Lane l of them reads 4 elements of row l / 4 of the four, the second read's four
     // rows follow the first's.
-    uint32_t across[2][BB];
+    uint32_t across[2][NB];
     if constexpr (kColumns)
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int j = 0; j < BB; ++j) {
-                const uint32_t l = lane & 15, k = 32 * h + 4 * half + l / 4;
-                const uint32_t col = (wb * BB + j) * 32 + (lane >> 4 & 1) * 16 + l % 4 * 4, c = col % 64;
+            for (int j = 0; j < NB; ++j) {
+                const uint32_t k = 8 * h + 4 * half + r / 4, col = wb * BB * 32 + j * 16 + r % 4 * 4, c = col % 64;
                 across[half][j] = (Z::kRowsA + col / 64 * 64 + k) * kStepBytes +
                                   (((c / 8) ^ ((k >> 1 & 3) << 1)) * 16) + c % 8 * 2;
             }
-    i32x4 fa[2][BA], fb[2][BB];
-    // Block s of the wave's i-th 32 rows, A's and then B's.
-    auto read = [&](const uint8_t* lds, int s, int i, i32x4 (&a)[BA], i32x4 (&b)[BB]) {
-        if (i < BA) {
-            a[i] = *reinterpret_cast<const i32x4*>(lds + base_a + off[s] + i * 32 * kStepBytes);
-        } else if constexpr (kColumns) {
-            const s16x4 v0 = column4(lds + across[0][i - BA] + s * 8 * kStepBytes);
-            const s16x4 v1 = column4(lds + across[1][i - BA] + s * 8 * kStepBytes);
-            b[i - BA] = __builtin_bit_cast(i32x4, s16x8{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]});
+    i32x4 fa[NA], fb[2][NB];
+    // The wave's i-th 16 rows of A and of B, half s of a step.
+    auto read_a = [&](const uint8_t* lds, int s, int i) {
+        fa[i] = *reinterpret_cast<const i32x4*>(lds + base_a + off[s] + i * 16 * kStepBytes);
+    };
+    auto read_b = [&](const uint8_t* lds, int s, int j) {
+        if constexpr (kColumns) {
+            const s16x4 v0 = column4(lds + across[0][j] + s * 32 * kStepBytes);
+            const s16x4 v1 = column4(lds + across[1][j] + s * 32 * kStepBytes);
+            fb[s][j] = __builtin_bit_cast(i32x4, s16x8{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]});
         } else {
-            b[i - BA] = *reinterpret_cast<const i32x4*>(lds + base_b + off[s] + (i - BA) * 32 * kStepBytes);
+            fb[s][j] = *reinterpret_cast<const i32x4*>(lds + base_b + off[s] + j * 16 * kStepBytes);
         }
     };
-    f32x16 acc[BA][BB] = {};
+    f32x4 acc[NA][NB] = {};
 
-    // One step from `cur` (its copies done, block 0 in registers): the reads of block
-    // s + 1 are issued among block s's products; before the last block's, everyone has
-    // read all of cur and the next step's copies are in `nxt`, so that among them cur is
-    // refilled with the step S after its own. A product occupies the matrix core for 32
-    // cycles, in which what stands between it and the next is issued; all reads or copies
-    // before a block's products kept the matrix core waiting. Past the last step the last
-    // one is copied again, so that the loop has no branches.
+    // One step from `cur`, whose copies are done and whose first half is in registers:
+    // its products, and among them the reads of its second half, and then of the next
+    // step's first. A's registers hold one half: 16 rows' are read again as soon as their
+    // products are issued. A quarter into the second half's products everyone has read
+    // all of cur and the next step's copies are in `nxt`; from there on cur is refilled
+    // with the step S after its own. A product occupies the matrix core for 16 cycles, in
+    // which what stands between it and the next is issued; all reads or copies before the
+    // products kept the matrix core waiting. Past the last step the last one is copied
+    // again, so that the loop has no branches.
     auto run = [&](uint8_t* cur, const uint8_t* nxt) {
-        auto block = [&](auto which) {
+        auto half = [&](auto which) {
             constexpr int B = decltype(which)::value;
-            constexpr int kProducts = BA * BB, kReads = BA + BB;
+            constexpr int kProducts = NA * NB, kSync = kProducts / 4, kFrom = B ? kSync : 0;
 #pragma unroll
             for (int m = 0; m < kProducts; ++m) {
-                acc[m / BB][m % BB] = mfma(E(), fa[B % 2][m / BB], fb[B % 2][m % BB], acc[m / BB][m % BB]);
+                if (B == 1 && m == kSync) {
+                    __builtin_amdgcn_s_setprio(0);
+                    copies_done_for_all<(Z::S - 2) * Z::kCopies>();
+                }
+                mfma(E(), fa[m / NB], fb[B][m % NB], acc[m / NB][m % NB]);
+                const uint8_t* from = B ? nxt : cur;
 #pragma unroll
-                for (int i = m * kReads / kProducts; i < (m + 1) * kReads / kProducts; ++i)
-                    read(B < 3 ? cur : nxt, (B + 1) % 4, i, fa[(B + 1) % 2], fb[(B + 1) % 2]);
-                if constexpr (B == 3)
+                for (int i = 0; i < NA; ++i)
+                    if (m == (i * NB + NB > kFrom + i ? i * NB + NB - 1 : kFrom + i)) read_a(from, 1 - B, i);
 #pragma unroll
-                    for (int i = m * Z::kCopies / kProducts; i < (m + 1) * Z::kCopies / kProducts; ++i) part(cur, i);
+                for (int j = 0; j < NB; ++j)
+                    if (m == (kFrom + 1 + 2 * j < kProducts ? kFrom + 1 + 2 * j : kProducts - 1)) read_b(from, 1 - B, j);
+                if constexpr (B == 1)
+#pragma unroll
+                    for (int i = 0; i < Z::kCopies; ++i)
+                        if (m == kSync + (i + 1) * (kProducts - 1 - kSync) / Z::kCopies) part(cur, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
         __builtin_amdgcn_s_setprio(1);
-        block(std::integral_constant<int, 0>{});
-        block(std::integral_constant<int, 1>{});
-        block(std::integral_constant<int, 2>{});
-        __builtin_amdgcn_s_setprio(0);
-        copies_done_for_all<(Z::S - 2) * Z::kCopies>();
-        block(std::integral_constant<int, 3>{});
+        half(std::integral_constant<int, 0>{});
+        half(std::integral_constant<int, 1>{});
         advance();
     };
     if (begin < end) {
@@ -331,7 +349,9 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
         if constexpr (Z::S > 3) copy(lds3);
         copies_done_for_all<(Z::S - 1) * Z::kCopies>();
 #pragma unroll
-        for (int i = 0; i < BA + BB; ++i) read(lds0, 0, i, fa[0], fb[0]);
+        for (int i = 0; i < NA; ++i) read_a(lds0, 0, i);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) read_b(lds0, 0, j);
         uint32_t s = begin;
         for (; s + Z::S <= end; s += Z::S) {
             run(lds0, lds1);
@@ -344,8 +364,12 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
         if (Z::S > 3 && s + 2 < end) run(lds2, lds3);
         copies_done_for_all<0>();  // the copies past the end are done before LDS is given up
     }
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) results_ready(acc[i][j]);
 
-    // Element v of a block: row (v / 4) * 8 + 4 h + v % 4 of A, row r of B.
+    // Element v of a block: row 4 h + v of A, row r of B.
     const int64_t aw = a0 + wa * BA * 32, bw = b0 + wb * BB * 32;
     // The wave's own part of LDS, in which 16-bit results change places so that a lane
     // stores 16 bytes of a row and a row's lanes whole lines.
@@ -360,11 +384,13 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
 #pragma unroll
             for (int i = 0; i < BA; ++i) {
 #pragma unroll
-                for (int v = 0; v < 16; ++v)
+                for (int v = 0; v < 8; ++v)
 #pragma unroll
-                    for (int j = 0; j < BB; ++j)
-                        stage[((v / 4) * 8 + 4 * h + v % 4) * kPitch + j * 32 + r] =
-                            __builtin_bit_cast(uint16_t, mx::from_f32<TO>(g.out_factor ? acc[i][j][v] * f : acc[i][j][v]));
+                    for (int j = 0; j < NB; ++j) {
+                        const float c = acc[2 * i + v / 4][j][v % 4];
+                        stage[(v / 4 * 16 + 4 * h + v % 4) * kPitch + j * 16 + r] =
+                            __builtin_bit_cast(uint16_t, mx::from_f32<TO>(g.out_factor ? c * f : c));
+                    }
                 wave_fence();
                 constexpr int kLanes = BB * 4, kRows = 64 / kLanes;  // lanes of a row, rows a store
 #pragma unroll
@@ -378,14 +404,14 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < BA; ++i)
+            for (int i = 0; i < NA; ++i)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int64_t row = aw + i * 32 + (v / 4) * 8 + 4 * h + v % 4;
+                for (int v = 0; v < 4; ++v) {
+                    const int64_t row = aw + i * 16 + 4 * h + v;
                     if (row >= g.a.rows) continue;
 #pragma unroll
-                    for (int j = 0; j < BB; ++j) {
-                        const int64_t col = bw + j * 32 + r;
+                    for (int j = 0; j < NB; ++j) {
+                        const int64_t col = bw + j * 16 + r;
                         if (col >= g.cols) continue;
                         TO* to = out + row * g.ldo + col;
                         const float c = g.out_factor ? acc[i][j][v] * f : acc[i][j][v];
@@ -404,55 +430,57 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
         if (!g.factor || t >= g.b.rows) return;
         const float f = g.factor[t];
 #pragma unroll
-        for (int i = 0; i < BA; ++i)
+        for (int i = 0; i < NA; ++i)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = acc[i][j][v] * f * by_top;
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = acc[i][j][v] * f * by_top;
     };
     // the target as a row of this lane's, were it one
     auto target_of = [&](int token) { return int64_t(token) - g.n0 - aw - 4 * h; };
 
     if constexpr (KIND == kStats) {
 #pragma unroll
-        for (int j = 0; j < BB; ++j) {
-            const int64_t t = bw + j * 32 + r;
-            if (t >= g.b.rows) continue;  // both halves of the wave alike
+        for (int j = 0; j < NB; ++j) {
+            const int64_t t = bw + j * 16 + r;
+            if (t >= g.b.rows) continue;  // all lanes of a token alike
             scaled(j, t);
             const int64_t target = target_of(vocab::token_at(g.targets, g.wide_targets, t, g.N));
             if (aw + BA * 32 > g.a.rows)
 #pragma unroll
-                for (int i = 0; i < BA; ++i)
+                for (int i = 0; i < NA; ++i)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (aw + 4 * h + i * 32 + (v / 4) * 8 + v % 4 >= g.a.rows) acc[i][j][v] = -__builtin_inff();
+                    for (int v = 0; v < 4; ++v)
+                        if (aw + 4 * h + i * 16 + v >= g.a.rows) acc[i][j][v] = -__builtin_inff();
             if (target >= 0 && target < BA * 32)
 #pragma unroll
-                for (int i = 0; i < BA; ++i)
+                for (int i = 0; i < NA; ++i)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (target == i * 32 + (v / 4) * 8 + v % 4) g.at_target[t] = acc[i][j][v];
+                    for (int v = 0; v < 4; ++v)
+                        if (target == i * 16 + v) g.at_target[t] = acc[i][j][v];
             float top = -__builtin_inff();
 #pragma unroll
-            for (int i = 0; i < BA; ++i)
+            for (int i = 0; i < NA; ++i)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) top = fmaxf(top, acc[i][j][v]);
+                for (int v = 0; v < 4; ++v) top = fmaxf(top, acc[i][j][v]);
+            top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const float from = top == -__builtin_inff() ? 0.f : top;
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < BA; ++i)
+            for (int i = 0; i < NA; ++i)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) sum += exp_of(acc[i][j][v] - from);
+                for (int v = 0; v < 4; ++v) sum += exp_of(acc[i][j][v] - from);
+            sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             if (h == 0) g.part[(g.part0 + (a0 / 32 + wa * BA) / BA) * g.b.rows + t] = make_float2(top, sum);
         }
     }
     if constexpr (KIND == kProb) {
-        float weight[BB];
-        bool learnt[BB];
+        float weight[NB];
+        bool learnt[NB];
 #pragma unroll
-        for (int j = 0; j < BB; ++j) {
+        for (int j = 0; j < NB; ++j) {
             // logits become d; the padding past the last token and the last row is zeros
-            const int64_t t = bw + j * 32 + r;
+            const int64_t t = bw + j * 16 + r;
             const int token = t < g.b.rows ? vocab::token_at(g.targets, g.wide_targets, t, g.N) : -1;
             learnt[j] = token >= 0;
             weight[j] = learnt[j] && g.weight ? g.weight[t] : 0.f;
@@ -460,21 +488,21 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
             const int64_t target = target_of(token);
             scaled(j, t);
 #pragma unroll
-            for (int i = 0; i < BA; ++i)
+            for (int i = 0; i < NA; ++i)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = learnt[j] ? exp_of(acc[i][j][v] - lse) : 0.f;
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = learnt[j] ? exp_of(acc[i][j][v] - lse) : 0.f;
             if (target >= 0 && target < BA * 32)
 #pragma unroll
-                for (int i = 0; i < BA; ++i)
+                for (int i = 0; i < NA; ++i)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (target == i * 32 + (v / 4) * 8 + v % 4) acc[i][j][v] -= 1.f;
+                    for (int v = 0; v < 4; ++v)
+                        if (target == i * 16 + v) acc[i][j][v] -= 1.f;
             if (aw + BA * 32 > g.a.rows)
 #pragma unroll
-                for (int i = 0; i < BA; ++i)
+                for (int i = 0; i < NA; ++i)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (aw + 4 * h + i * 32 + (v / 4) * 8 + v % 4 >= g.a.rows) acc[i][j][v] = 0.f;
+                    for (int v = 0; v < 4; ++v)
+                        if (aw + 4 * h + i * 16 + v >= g.a.rows) acc[i][j][v] = 0.f;
         }
         if (g.along) {
             // rows of tokens: a lane has four neighbouring elements of its token's row
@@ -486,15 +514,15 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
 #pragma unroll
                 for (int i0 = 0; i0 < BA; i0 += kBlocks) {
 #pragma unroll
-                    for (int i = 0; i < kBlocks; ++i)
+                    for (int i = 0; i < 2 * kBlocks; ++i)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             u16x4 w[PARTS];
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) put_parts<E, PARTS>(acc[i0 + i][j][q * 4 + v] * g.by, v, w);
+                            for (int v = 0; v < 4; ++v) put_parts<E, PARTS>(acc[2 * i0 + i][2 * j + q][v] * g.by, v, w);
 #pragma unroll
                             for (int part = 0; part < PARTS; ++part)
-                                *reinterpret_cast<u16x4*>(stage + part * kPlane + r * kPitch + i * 32 + q * 8 + 4 * h) =
+                                *reinterpret_cast<u16x4*>(stage + part * kPlane + (q * 16 + r) * kPitch + i * 16 + 4 * h) =
                                     w[part];
                         }
                     wave_fence();
@@ -518,14 +546,14 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
 #pragma unroll
             for (int i = 0; i < BA; ++i) {
 #pragma unroll
-                for (int v = 0; v < 16; ++v)
+                for (int v = 0; v < 8; ++v)
 #pragma unroll
-                    for (int j = 0; j < BB; ++j) {
+                    for (int j = 0; j < NB; ++j) {
                         u16x4 w[PARTS];
-                        put_parts<E, PARTS>(learnt[j] ? acc[i][j][v] * weight[j] : 0.f, 0, w);
+                        put_parts<E, PARTS>(learnt[j] ? acc[2 * i + v / 4][j][v % 4] * weight[j] : 0.f, 0, w);
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part)
-                            stage[part * kPlane + ((v / 4) * 8 + 4 * h + v % 4) * kPitch + j * 32 + r] = w[part][0];
+                            stage[part * kPlane + (v / 4 * 16 + 4 * h + v % 4) * kPitch + j * 16 + r] = w[part][0];
                     }
                 wave_fence();
 #pragma unroll
