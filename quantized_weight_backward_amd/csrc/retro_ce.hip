@@ -393,11 +393,11 @@ void sum_plan(int64_t K, int64_t T, int64_t steps, Backward& p) {
     if (T <= 32) {
         p.shape = kSmall32;
         tiles = cdiv(K, 128);
-        want = 1024;
+        want = 512;
     } else if (T <= 64) {
         p.shape = kSmall64;
         tiles = cdiv(K, 128);
-        want = 768;
+        want = 512;
     } else if (T <= 128) {
         p.shape = kMid;
         tiles = cdiv(T, 128) * cdiv(K, 128);

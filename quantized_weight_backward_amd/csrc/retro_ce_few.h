@@ -140,7 +140,8 @@ struct FewArgs {
     float* out;
 };
 
-constexpr int kFewWaves = 4, kFewRows = 32 * kFewWaves;  // rows of the head a wave, a workgroup
+constexpr int kFewBlocks = 2;  // of 16 rows of the head a wave, which share the reads of x
+constexpr int kFewWaves = 4, kFewRows = 16 * kFewBlocks * kFewWaves;  // rows a workgroup
 constexpr int kFewK = 256;                               // of x in LDS
 
 __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f32x4& c) {
@@ -149,14 +150,14 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
 
 // Up to 16 TB tokens, x in PX parts.
 template <int TYPE, int TB, int PX, Kind KIND>
-__global__ __launch_bounds__(kFewWaves * 64) void few_kernel(const FewArgs g) {
+__global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g) {
     constexpr int kRows = kFewK / 64 * 16 * TB * PX;  // of 128 bytes in LDS: step, part, token
     constexpr int kCopies = kRows * 128 / (1024 * kFewWaves);
     __shared__ __align__(1024) uint8_t lds0[kRows * 128];
     __shared__ __align__(1024) uint8_t lds1[kRows * 128];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int r = lane & 15, gr = lane >> 4;
-    const int64_t row0 = int64_t(blockIdx.x) * kFewRows + wave * 32;
+    const int64_t row0 = int64_t(blockIdx.x) * kFewRows + wave * 16 * kFewBlocks;
 
     // x's rows of a chunk: row (step, part, token) of 128 bytes, its 16-byte blocks
     // permuted by XOR with (row / 2) % 8
@@ -174,10 +175,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(const FewArgs g) {
                                                      0, 0);
         }
     };
-    const uint8_t* w[2];
+    const uint8_t* w[kFewBlocks];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = g.W + min(row0 + i * 16 + r, g.rows - 1) * g.ldw;
-    f32x4 acc[2][TB] = {};
+    for (int i = 0; i < kFewBlocks; ++i) w[i] = g.W + min(row0 + i * 16 + r, g.rows - 1) * g.ldw;
+    f32x4 acc[kFewBlocks][TB] = {};
     const f16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
     auto sub_blocks = [&](const uint8_t* lds, int chunk, auto whole) __attribute__((always_inline)) {
 #pragma unroll
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(const FewArgs g) {
                     if constexpr (PX == 2) sum[t] = mfma16(xs[t][1], ones, sum[t]);
                 }
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < kFewBlocks; ++n) {
                 const Codes c = codes_of<TYPE>(w[n], b, gr);
 #pragma unroll
                 for (int t = 0; t < TB; ++t) {
@@ -246,13 +247,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(const FewArgs g) {
             const bool live = token < g.T;
             const float f = live ? g.factor[token] : 0.f;
             const int64_t target = live ? vocab::token_at(g.targets, g.wide_targets, token, g.N) : -1;
-            float l[2];
+            float l[kFewBlocks];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) l[n] = acc[n][t][i] * f;
+            for (int n = 0; n < kFewBlocks; ++n) l[n] = acc[n][t][i] * f;
             if constexpr (KIND == kStats) {
                 float top = -__builtin_inff();
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < kFewBlocks; ++n) {
                     const int64_t row = row0 + n * 16 + r;
                     if (row >= g.rows) l[n] = -__builtin_inff();
                     if (live && target == g.n0 + row && row < g.rows) g.at_target[token] = l[n];
@@ -261,7 +262,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(const FewArgs g) {
 #pragma unroll
                 for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
                 const float from = top == -__builtin_inff() ? 0.f : top;
-                float sum = exp_of(l[0] - from) + exp_of(l[1] - from);
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < kFewBlocks; ++n) sum += exp_of(l[n] - from);
 #pragma unroll
                 for (int d = 1; d < 16; d *= 2) sum += __shfl_xor(sum, d);
                 if (live && r == 0)
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_kernel(const FewArgs g) {
             } else {
                 const float lse = target >= 0 ? g.lse[token] : 0.f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < kFewBlocks; ++n) {
                     const int64_t row = row0 + n * 16 + r;
                     if (!live || row >= g.rows) continue;
                     g.out[token * g.rows + row] =
