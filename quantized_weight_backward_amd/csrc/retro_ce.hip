@@ -18,7 +18,7 @@ using mx::Span;
 // x as the matrix cores take it, in steps of 64 elements (element k of row t at
 // (k / 64 * gridDim.x + t) * 64 + k % 64), zeros past K and past the last token, in x's
 // own 16-bit type (PARTS 0) or as F16 parts scaled by a power of two of the row's own,
-// whose inverse goes to factor[t]. With a mask (the gradients' products) the rows of
+// whose inverse goes to factor[t]. Memory bounds it, or its launch. With a mask (the gradients' products) the rows of
 // tokens that are not learnt from are zeros, whatever they hold. A workgroup a row.
 template <typename TX, int PARTS>
 __global__ __launch_bounds__(256) void token_rows_kernel(const TX* __restrict__ X, int64_t ldx, int64_t K,
@@ -253,8 +253,8 @@ int parts_of(int type) {
 
 // And in the gradients of a BF16 x, where one part of 11 bits leaves the result's 8 as
 // they are: what the logits lose by it is an eighth of what x's own rounding put into
-// them. Two parts double both products: 2048 x 131072 x 4096 through Q8_0 7.6 ms
-// against 3.9. An F32 dW takes its parts in full.
+// them. Two parts double both products: loss and gradient of 2048 x 131072 x 4096
+// through Q8_0 took 13.2 ms with two and 9.0 with one. An F32 dW takes its parts in full.
 int grad_parts_of(int type, int xtype, bool weight_grad) {
     return xtype == RETRO_BF16 && !(weight_grad && type == RETRO_F32) ? 1 : parts_of(type);
 }
@@ -315,7 +315,8 @@ Shape shape_of(int64_t rows, int64_t tokens) {
 
 // Rows of the head in whole rounds of 256 x 256 tiles over the CUs, where what is left
 // would fill less than half of another: it goes to smaller tiles in a launch of its
-// own. 50001 x 2048 and 1021 tokens: 784 tiles, three rounds and 16.
+// own. 50001 x 2048 and 1021 tokens: 784 tiles, three rounds and 16, 243 us in one launch
+// and 219 in two.
 int64_t rows_of_rounds(int64_t rows, int64_t tokens) {
     if (shape_of(rows, tokens) != kBig) return rows;
     const int64_t across = cdiv(tokens, 256), tiles = cdiv(rows, 256) * across, over = tiles % host::kNumCUs;
@@ -386,7 +387,9 @@ struct Backward {
 };
 
 // Tile and splits of dX's product, whose rows of the head are cut into splits so that
-// every CU has work.
+// every CU has work: one workgroup of 256 x 256 each, two of the smaller tiles, which is
+// what fits at once (as many as fit and a rest took 178 us for the step of 64 tokens
+// through 32768 x 4096, one round 169).
 void sum_plan(int64_t K, int64_t T, int64_t steps, Backward& p) {
     const int64_t big = cdiv(T, 256) * cdiv(K, 256);
     int64_t tiles, want;
@@ -508,14 +511,20 @@ int launch_logits(Args g, hipStream_t st) {
     return launch_shape<E, KIND, PARTS>(shape_of_rest(rest, tokens), g, st);
 }
 
-template <typename E, typename TO, bool ADD>
-int launch_sum(Shape shape, const Args& g, hipStream_t st) {
+template <typename E, bool ADD>
+int launch_dx(Shape shape, const Args& g, hipStream_t st) {
     switch (shape) {
-        case kBig: return launch<E, Big, kSum, TO, ADD>(g, st);
-        case kMid: return launch<E, Mid, kSum, TO, ADD>(g, st);
-        case kSmall64: return launch<E, Cols64, kSum, TO, ADD>(g, st);
-        default: return launch<E, Cols32, kSum, TO, ADD>(g, st);
+        case kBig: return launch<E, Big, kSum, float, ADD>(g, st);
+        case kMid: return launch<E, Mid, kSum, float, ADD>(g, st);
+        case kSmall64: return launch<E, Cols64, kSum, float, ADD>(g, st);
+        default: return launch<E, Cols32, kSum, float, ADD>(g, st);
     }
+}
+
+template <typename E, typename TW>
+int launch_dw(const Args& g, hipStream_t st) {
+    if (cdiv(g.a.rows, 256) * cdiv(g.cols, 256) >= 128) return launch<E, Big, kSum, TW, 0>(g, st);
+    return launch<E, Mid, kSum, TW, 0>(g, st);
 }
 
 int zero(void* p, int64_t words, hipStream_t st) {
@@ -778,8 +787,8 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
             s.split_stride = c.T * c.K;
             s.cols = c.K;
             RETRO_TRY(with_element(c, [&](auto e) {
-                return g.n0 ? launch_sum<decltype(e), float, true>(p.shape, s, c.st)
-                            : launch_sum<decltype(e), float, false>(p.shape, s, c.st);
+                return g.n0 ? launch_dx<decltype(e), true>(p.shape, s, c.st)
+                            : launch_dx<decltype(e), false>(p.shape, s, c.st);
             }));
         }
         if (dW) {
@@ -793,11 +802,12 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
             s.ldo = lddw;
             s.cols = c.K;
             s.out_factor = unscale;
-            const Shape shape = cdiv(rows, 256) * cdiv(c.K, 256) >= 128 ? kBig : kMid;
             RETRO_TRY(mx::with_float(c.type, [&](auto* tag) {
                 using TW = std::remove_pointer_t<decltype(tag)>;
                 s.out = static_cast<TW*>(dW) + g.n0 * lddw;
-                return with_element(c, [&](auto e) { return launch_sum<decltype(e), TW, false>(shape, s, c.st); });
+                if constexpr (std::is_same<TW, __bf16>::value)
+                    if (narrow) return launch_dw<__bf16, TW>(s, c.st);
+                return launch_dw<_Float16, TW>(s, c.st);
             }));
         }
     }

@@ -10,8 +10,9 @@
 // results that it gets.
 //
 // What bounds it is memory where few tokens are given: Q4_K 131072 x 4096 and 16 tokens
-// take MEASURED, against 252 us with the weights decoded to F32 in front of
-// F32 matrix instructions.
+// take 114 to 118 us for 302 MB, against 252 us with the weights decoded to F32 in front of
+// F32 matrix instructions. Blocks of 34 bytes, which only 2-byte loads reach, take longer
+// than their bytes: Q8_0 317 us for 570 MB.
 #pragma once
 
 #include "retro_ce_kernel.h"
@@ -49,6 +50,9 @@ struct Codes {
 
 template <int TYPE>
 constexpr bool kFewType = kNibbleLayout<TYPE> || TYPE == kQ8_0 || TYPE == kQ4_K || TYPE == kQ5_K || TYPE == kQ6_K;
+// Whose scales pass what F32 holds above a sum of scaled x: the token's factor goes first.
+template <int TYPE>
+constexpr bool kFactorFirst = TYPE == kMXFP4;
 template <int TYPE>
 constexpr bool kOffset = kHasOffset<TYPE> || TYPE == kQ4_K || TYPE == kQ5_K;
 
@@ -140,9 +144,11 @@ struct FewArgs {
     float* out;
 };
 
-constexpr int kFewBlocks = 2;  // of 16 rows of the head a wave, which share the reads of x
+// Blocks of 16 rows of the head a wave, which share the reads of x: with one, 142 us
+// where two take 114 to 121 (Q4_K 131072 x 4096, 16 tokens).
+constexpr int kFewBlocks = 2;
 constexpr int kFewWaves = 4, kFewRows = 16 * kFewBlocks * kFewWaves;  // rows a workgroup
-constexpr int kFewK = 256;                               // of x in LDS
+constexpr int kFewK = 256;  // of x in LDS
 
 __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -179,6 +185,11 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
 #pragma unroll
     for (int i = 0; i < kFewBlocks; ++i) w[i] = g.W + min(row0 + i * 16 + r, g.rows - 1) * g.ldw;
     f32x4 acc[kFewBlocks][TB] = {};
+    float factor[TB][4];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) factor[t][i] = 16 * t + 4 * gr + i < g.T ? g.factor[16 * t + 4 * gr + i] : 0.f;
     const f16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
     auto sub_blocks = [&](const uint8_t* lds, int chunk, auto whole) __attribute__((always_inline)) {
 #pragma unroll
@@ -213,7 +224,8 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
                     }
 #pragma unroll
                     for (int i4 = 0; i4 < 4; ++i4) {
-                        acc[n][t][i4] = fmaf(c.a, v[i4], acc[n][t][i4]);
+                        const float by = kFactorFirst<TYPE> ? v[i4] * factor[t][i4] : v[i4];
+                        acc[n][t][i4] = fmaf(c.a, by, acc[n][t][i4]);
                         if constexpr (kOffset<TYPE>) acc[n][t][i4] = fmaf(c.c, sum[t][i4], acc[n][t][i4]);
                     }
                 }
@@ -245,7 +257,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
         for (int i = 0; i < 4; ++i) {
             const int token = 16 * t + 4 * gr + i;
             const bool live = token < g.T;
-            const float f = live ? g.factor[token] : 0.f;
+            const float f = kFactorFirst<TYPE> ? 1.f : factor[t][i];
             const int64_t target = live ? vocab::token_at(g.targets, g.wide_targets, token, g.N) : -1;
             float l[kFewBlocks];
 #pragma unroll

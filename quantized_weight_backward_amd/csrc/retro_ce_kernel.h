@@ -11,6 +11,13 @@
 //
 // Tokens are the columns of a matrix-core block: a lane then holds rows of the head of
 // one token, whose maximum and sum need two exchanges, with the three other lanes of it.
+//
+// The power that the matrix cores draw bounds the large tiles: 4096 x 131072 x 4096 in
+// BF16 takes 3.37 ms as kStats (1.31 PFLOP/s), 3.41 as dW and dX and 3.62 as kProb, which
+// writes 2.1 GB besides; a library product of that size, its result written and nothing
+// more, takes 2.9 to 3.2. Eight waves of 128 x 64 results: four of 128 x 128 ran at 1.17
+// PFLOP/s, and three steps of A in LDS with two of B at 1.27. Few tokens are bound by the
+// head's reading: 5.7 TB/s with one token, 32768 x 2048.
 #pragma once
 
 #include <type_traits>
@@ -45,8 +52,14 @@ __device__ __forceinline__ void mfma(__bf16, const i32x4& a, const i32x4& b, f32
 __device__ __forceinline__ void mfma(_Float16, const i32x4& a, const i32x4& b, f32x4& c) {
     asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
-// Results of products issued before can be read after it: of 8 passes, 11 wait states.
-__device__ __forceinline__ void results_ready(f32x4& c) { asm volatile("s_nop 15\n\ts_nop 3" : "+v"(c)); }
+// Results of products issued before can be read after it: of 8 passes, 11 wait states
+// after the last. The compiler sees each result written anew.
+template <int N>
+__device__ __forceinline__ void results_ready(f32x4 (&c)[N], bool first) {
+    if (first) asm volatile("s_nop 15\n\ts_nop 3" : "+v"(c[0]));
+#pragma unroll
+    for (int j = 0; j < N; ++j) asm volatile("" : "+v"(c[j]));
+}
 
 // exp(x) for x <= 0 or so: off by |x| 2^-24 and a step, of a value that falls with x.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
@@ -55,7 +68,7 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // bytes), `stride` apart: 128 bytes for rows as they are in a tensor, or the whole
 // column of that step's 64 elements of all rows. What is made for the products is laid
 // out so: a tile's step is then one run of memory. Rows of 64 KB side by side, 256 of
-// them read at one place, took a fifth longer.
+// them read at one place, took a sixth longer (4096 x 131072 x 4096 4.2 ms against 3.6).
 struct Operand {
     const uint8_t* p;
     int64_t pitch, stride;  // bytes between rows, between steps of a row
@@ -365,9 +378,7 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
         copies_done_for_all<0>();  // the copies past the end are done before LDS is given up
     }
 #pragma unroll
-    for (int i = 0; i < NA; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) results_ready(acc[i][j]);
+    for (int i = 0; i < NA; ++i) results_ready(acc[i], i == 0);
 
     // Element v of a block: row 4 h + v of A, row r of B.
     const int64_t aw = a0 + wa * BA * 32, bw = b0 + wb * BB * 32;
@@ -428,11 +439,11 @@ __global__ __launch_bounds__(Z::kThreads, Z::kPerSimd) void product_kernel(const
     const float by_top = g.factor ? vocab::unscale_of(*g.top) : 1.f;
     auto scaled = [&](int j, int64_t t) {
         if (!g.factor || t >= g.b.rows) return;
-        const float f = g.factor[t];
+        const float f = g.factor[t] * by_top;  // first: either alone may be far from a logit's size
 #pragma unroll
         for (int i = 0; i < NA; ++i)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[i][j][v] = acc[i][j][v] * f * by_top;
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = acc[i][j][v] * f;
     };
     // the target as a row of this lane's, were it one
     auto target_of = [&](int token) { return int64_t(token) - g.n0 - aw - 4 * h; };

@@ -20,15 +20,18 @@ using mx::Span;
 //
 // What bounds it is the table being written. All of it is cleared beside the sort, in
 // the same launches, so that the sort costs no time of its own and only rows of tokens
-// are written after it.
+// are written after it. 16384 tokens of 4096 BF16 columns into 131072 F32
+// rows: 472 us, of which 372 in the four launches that clear 2.15 GB and sort (5.8
+// TB/s), 88 in the rows' sums, 6 in joining them.
 
 constexpr int kMaxBits = 9, kMaxDigits = 1 << kMaxBits;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSmallT = 8192;      // sorted by one workgroup in LDS
 constexpr int kBlockItems = 2048;  // of a workgroup of a larger sort's pass
 constexpr int kBlockThreads = 256, kBlockWaves = kBlockThreads / 64;
-// Tokens of a run. Shorter ones are more waves for few tokens (777 of 1000 columns: 22
-// us after the sort in runs of 64, 9 in runs of 16), longer ones fewer parts to join.
+// Tokens of a run. Shorter ones are more waves for few tokens (777 of 1000 columns into
+// 32000 rows: 59 us in runs of 64, 33 in runs of 16), longer ones fewer parts to join; at
+// 16384 tokens of 4096 columns either takes 472 us.
 constexpr int kMaxRun = 64;
 int run_for(int64_t T) { return T <= 4096 ? 16 : kMaxRun; }
 

@@ -57,10 +57,11 @@ __device__ __forceinline__ void store_parts(uint16_t* to, int64_t plane, float e
 
 // The power of two that puts a largest magnitude, given by its bits, into
 // 2^13 .. 2^14: F16 then holds what is 2^28 below it with all its 11 bits, and
-// products of two such rows stay far inside F32. 1 where there is no such power.
+// products of two such rows stay far inside F32. 1 where that is no number, 2^126 where it
+// would be more: its inverse is a normal number.
 __device__ __forceinline__ int scale_log2(uint32_t top) {
     const int field = int(top >> 23);
-    return field == 0 || field == 255 ? 0 : max(-112, min(112, 140 - field));
+    return field == 255 ? 0 : min(126, 140 - field);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 __device__ __forceinline__ float scale_of(uint32_t top) { return pow2(scale_log2(top)); }

@@ -374,7 +374,8 @@ def test_cross_entropy_of_wide_ranges(q):
     """Logits of hundreds, tokens and tables of very different sizes."""
     T, N, K = 80, 300, 128
     for dtype, sx, sw in ((torch.bfloat16, 30.0, 1.0), (torch.float32, 1e-20, 1e18), (torch.float32, 1e15, 1e-14),
-                          (torch.float32, 1e-30, 1e-30), (torch.float16, 20.0, 1.0)):
+                          (torch.float32, 1e-30, 1e-30), (torch.float16, 20.0, 1.0), (torch.float32, 1e-37, 1e37),
+                          (torch.float32, 1e37, 1e-37)):
         w = head(dtype, N, K, seed=1) * sw
         x = (torch.randn((T, K), generator=gen(2)) * sx).to(dtype)
         check = dtype, sx, sw
@@ -387,6 +388,25 @@ def test_cross_entropy_of_wide_ranges(q):
     x[::2] *= 2.0 ** -60
     t = tokens(T, N, seed=5, none=0)
     check_cross_entropy(q, wl.F32, w.cuda(), w.double(), x, t, weight_grad=True)
+
+
+def test_cross_entropy_of_a_head_of_the_largest_scales(q):
+    """MXFP4 blocks up to scales whose largest code would be infinite."""
+    N, K = 200, 256
+    W = wl.make_weight(wl.MXFP4, N, K, np.random.Generator(np.random.PCG64(3)))
+    W = W.reshape(N, K // 32, 17)
+    W[..., 0] = 252
+    W[..., 1:] &= 0xBB  # magnitudes up to 1.5
+    W[:, ::2, 0] = 253
+    W = np.ascontiguousarray(W.reshape(N, -1))
+    values = torch.from_numpy(oracle.dequantize(wl.MXFP4, W, K)).reshape(N, K).double()
+    assert torch.isfinite(values).all()
+    for T in (5, 70):
+        x = (torch.randn((T, K), generator=gen(7)) * 2.0 ** -130).float()
+        t = tokens(T, N, seed=T)
+        want, want_lse, _, _ = ref.cross_entropy(values, x.double(), t)
+        loss, lse = q.cross_entropy(wl.MXFP4, torch.from_numpy(W).cuda(), x.cuda(), t.cuda())
+        close(lse, want_lse, ref.loss_error(values, x.double(), want_lse) + values.abs().max() * x.double().abs().sum(1) * 2.0 ** -20)
 
 
 def test_cross_entropy_of_an_empty_head_and_of_no_tokens(q):

@@ -27,10 +27,12 @@ def cross_entropy(w, x, targets):
 
 def logit_error(w, x):
     """What a logit may be off by: K / 16 instructions' sums, and the parts that the
-    operands are taken in (2^-22 of each, and 2^-39 of the largest of x's row and of W)."""
+    operands are taken in (2^-22 of each, and 2^-38 of the largest of x's row and of W, or 2^-151)."""
     K = x.shape[1]
     size = x.abs() @ w.abs().T
-    small = 2.0 ** -39 * (x.abs().amax(1, keepdim=True) * w.abs().sum(1) + w.abs().max() * x.abs().sum(1, keepdim=True))
+    of_x = torch.clamp(2.0 ** -38 * x.abs().amax(1, keepdim=True), min=2.0 ** -151)
+    of_w = torch.clamp(2.0 ** -38 * w.abs().max(), min=2.0 ** -151)
+    small = of_x * w.abs().sum(1) + of_w * x.abs().sum(1, keepdim=True)
     return ((K / 16 + 4) * STEP + 3 * 2.0 ** -22) * size + small
 
 
