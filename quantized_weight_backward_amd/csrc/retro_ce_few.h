@@ -185,11 +185,16 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
 #pragma unroll
     for (int i = 0; i < kFewBlocks; ++i) w[i] = g.W + min(row0 + i * 16 + r, g.rows - 1) * g.ldw;
     f32x4 acc[kFewBlocks][TB] = {};
+    auto factor_of = [&](int t, int i) {
+        const int token = 16 * t + 4 * gr + i;
+        return token < g.T ? g.factor[token] : 0.f;
+    };
     float factor[TB][4];
+    if constexpr (kFactorFirst<TYPE>)
 #pragma unroll
-    for (int t = 0; t < TB; ++t)
+        for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) factor[t][i] = 16 * t + 4 * gr + i < g.T ? g.factor[16 * t + 4 * gr + i] : 0.f;
+            for (int i = 0; i < 4; ++i) factor[t][i] = factor_of(t, i);
     const f16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
     auto sub_blocks = [&](const uint8_t* lds, int chunk, auto whole) __attribute__((always_inline)) {
 #pragma unroll
@@ -257,7 +262,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
         for (int i = 0; i < 4; ++i) {
             const int token = 16 * t + 4 * gr + i;
             const bool live = token < g.T;
-            const float f = kFactorFirst<TYPE> ? 1.f : factor[t][i];
+            const float f = kFactorFirst<TYPE> ? 1.f : factor_of(t, i);
             const int64_t target = live ? vocab::token_at(g.targets, g.wide_targets, token, g.N) : -1;
             float l[kFewBlocks];
 #pragma unroll

@@ -17,7 +17,7 @@
 // writes 2.1 GB besides; a library product of that size, its result written and nothing
 // more, takes 2.9 to 3.2. Eight waves of 128 x 64 results: four of 128 x 128 ran at 1.17
 // PFLOP/s, and three steps of A in LDS with two of B at 1.27. Few tokens are bound by the
-// head's reading: 5.7 TB/s with one token, 32768 x 2048.
+// head's reading: one through 32768 x 2048, 134 MB, takes 22 us.
 #pragma once
 
 #include <type_traits>
