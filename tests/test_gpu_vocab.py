@@ -317,6 +317,71 @@ def test_cross_entropy_in_several_pieces_of_the_head(q):
         close(dx[some.cuda()], wx, bx)
 
 
+@pytest.mark.parametrize("wtype,K,T", [(wl.Q8_0, 32, 3), (wl.BF16, 64, 2), (wl.Q3_K, 256, 64), (wl.F32, 64, 1)], ids=str)
+def test_losses_of_many_pieces(q, wtype, K, T):
+    """512 rows again and again: as many pieces as a head has past 2^24 logits or rows."""
+    base, N = 512, (1 << 24) // (64 if T == 64 else 1) + 512
+    if wtype in TYPE.values():
+        dtype = torch.bfloat16 if wtype == wl.BF16 else torch.float32
+        rows = head(dtype, base, K, seed=1).cuda()
+        values, W = rows.cpu().double(), rows.repeat(N // base, 1)
+    else:
+        rows, values = packed(wtype, base, K, seed=1)
+        W = rows.view(base, -1).repeat(N // base, 1)
+    x = torch.randn((T, K), generator=gen(2)) / (float(values.std()) * K ** 0.5)
+    x = x.to(torch.bfloat16 if wtype == wl.BF16 else torch.float32)
+    t = torch.tensor([N - 5, 1, (1 << 18) - 1, 1 << 18, N])[torch.arange(T) % 5]
+    loss, lse = q.cross_entropy(wtype, W, x.cuda(), t.cuda())
+    inside = torch.where(t < N, t % base, -1)
+    want, want_lse, learnt, _ = ref.cross_entropy(values, x.double(), inside)
+    # every run again has the same sum, so that F32's log2(runs) joins of them are off by a step each
+    bound = ref.loss_error(values, x.double(), want_lse) + N / (64 * 256) * 2.0 ** -24
+    more = torch.log(torch.tensor(N / base, dtype=torch.float64))
+    close(lse, want_lse + more, bound + more * 2.0 ** -22)
+    close(loss, torch.where(learnt, want + more, 0.0), bound + more * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("wtype,K", [(wl.Q8_0, 32), (wl.Q2_K, 256)], ids=str)
+def test_gradients_of_few_tokens_in_several_pieces(q, wtype, K):
+    N, T = (1 << 18) + 37, 64
+    W, values = packed(wtype, 1001, K, seed=5)
+    again = torch.arange(N) % 1001
+    x = torch.randn((T, K), generator=gen(2)) / (float(values.std()) * K ** 0.5)
+    t = tokens(T, N, seed=3)
+    t[0], t[1], t[2] = (1 << 18) - 1, 1 << 18, N - 1
+    check_cross_entropy(q, wtype, W.view(1001, -1)[again.cuda()], values[again], x, t)
+
+
+@pytest.mark.parametrize("wtype", [wl.BF16, wl.Q4_K, wl.MXFP4, wl.Q2_K], ids=wl.TYPE_NAMES.get)
+def test_cross_entropy_of_long_rows(q, wtype):
+    N, K = 90, 20480
+    if wtype == wl.BF16:
+        w = head(torch.bfloat16, N, K, seed=1)
+        W, values = w.cuda(), w.double()
+    else:
+        W, values = packed(wtype, N, K, seed=1)
+    for T in (1, 40, 130):
+        x = (torch.randn((T, K), generator=gen(7)) / (float(values.std()) * K ** 0.5)).bfloat16()
+        check_cross_entropy(q, wtype, W, values, x, tokens(T, N, seed=T))
+
+
+def test_cross_entropy_of_rows_of_nothing(q):
+    """K = 0: every logit is 0."""
+    N, T = 37, 5
+    t = torch.tensor([0, 36, 37, -1, 3], device="cuda")
+    for wtype in (wl.F32, wl.BF16, wl.Q8_0):
+        for xtype in (wl.F32, wl.BF16):
+            need = q.lib.retro_cross_entropy_workspace_size(wtype, 0, xtype, 0, N, T)
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            out = torch.full((2, T), 9.0, device="cuda")
+            assert q.lib.retro_cross_entropy(wtype, None, 0, xtype, None, 0, 27, t.data_ptr(), out[0].data_ptr(),
+                                             out[1].data_ptr(), 0, N, T, ws.data_ptr(), need, None) == 0
+            torch.cuda.synchronize()
+            want = torch.log(torch.tensor(float(N), dtype=torch.float64))
+            close(out[1], want.expand(T), torch.full((T,), 2.0 ** -20))
+            close(out[0], torch.tensor([1.0, 1, 0, 0, 1]).double() * want, torch.full((T,), 2.0 ** -20))
+
+
 def test_cross_entropy_in_whole_rounds_and_a_rest(q):
     """Tiles of 256 x 256 for most of the head, smaller ones for what is left of it."""
     for dtype, T, N, K in ((torch.bfloat16, 300, 33100, 64), (torch.float16, 257, 32769, 33), (torch.float32, 300, 33000, 64)):
@@ -368,6 +433,20 @@ def test_cross_entropy_of_a_token_that_is_not_finite(q):
         assert torch.isnan(loss2[7]) and torch.isnan(dx2[7]).all()
         rest = torch.arange(T, device="cuda") != 7
         assert torch.equal(loss[rest], loss2[rest]) and torch.equal(dx[rest], dx2[rest])
+    for wtype in (wl.Q4_K, wl.MXFP4, wl.Q3_K):
+        W, values = packed(wtype, N, 256, seed=1)
+        for T in (9, 70):
+            x = (torch.randn((T, 256), generator=gen(2)) / (float(values.std()) * 16)).bfloat16().cuda()
+            t, g = torch.randint(0, N, (T,), generator=gen(3)).cuda(), torch.ones(T, device="cuda")
+            loss, lse = q.cross_entropy(wtype, W, x, t)
+            dx, _ = q.cross_entropy_backward(wtype, W, x, t, lse, g)
+            bad = x.clone()
+            bad[7, 3] = float("nan")
+            loss2, lse2 = q.cross_entropy(wtype, W, bad, t)
+            dx2, _ = q.cross_entropy_backward(wtype, W, bad, t, lse2, g)
+            assert torch.isnan(loss2[7]) and torch.isnan(dx2[7]).all()
+            rest = torch.arange(T, device="cuda") != 7
+            assert torch.equal(loss[rest], loss2[rest]) and torch.equal(dx[rest], dx2[rest])
 
 
 def test_cross_entropy_of_wide_ranges(q):
