@@ -56,25 +56,81 @@ constexpr bool kFactorFirst = TYPE == kMXFP4;
 template <int TYPE>
 constexpr bool kOffset = kHasOffset<TYPE> || TYPE == kQ4_K || TYPE == kQ5_K;
 
-// Sub-block b (of 32) of a row.
+// What a lane needs of 256 elements of a row, as they lie there: loaded a chunk before it
+// is decoded, so that memory answers while the chunk before is multiplied.
+template <int TYPE, bool SUPER = TYPE == kQ4_K || TYPE == kQ5_K || TYPE == kQ6_K>
+struct Raw {
+    u32x2b w[8];
+    uint32_t h[8], qh[8];
+};
 template <int TYPE>
-__device__ __forceinline__ Codes codes_of(const uint8_t* row, int b, int g) {
+struct Raw<TYPE, true> {
+    u32x4 h;
+    u32x2 w[4], qh[2];
+    uint32_t d;
+};
+
+// Of chunk `chunk`; blocks past the row's `last` are the last again.
+template <int TYPE>
+__device__ __forceinline__ void load_raw(Raw<TYPE>& r, const uint8_t* row, int chunk, int last, int g) {
+    if constexpr (TYPE == kQ8_0 || kNibbleLayout<TYPE>) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint8_t* blk = row + min(chunk * 8 + i, last) * Format<TYPE>::kBytes;
+            if constexpr (TYPE == kQ8_0) {
+                r.w[i] = *reinterpret_cast<const u32x2*>(blk + 2 + 8 * g);
+                r.h[i] = *reinterpret_cast<const uint16_t*>(blk);
+            } else {
+                r.w[i] = *reinterpret_cast<const u32x2b*>(blk + kHeader<TYPE> + 8 * (g & 1));
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(blk);
+                if constexpr (TYPE == kMXFP4)
+                    r.h[i] = blk[0];
+                else if constexpr (kHasOffset<TYPE>)
+                    r.h[i] = uint32_t(h[0]) | (uint32_t(h[1]) << 16);
+                else
+                    r.h[i] = h[0];
+                if constexpr (kHasFifth<TYPE>) {
+                    constexpr int at = kHasOffset<TYPE> ? 2 : 1;
+                    r.qh[i] = uint32_t(h[at]) | (uint32_t(h[at + 1]) << 16);
+                }
+            }
+        }
+    } else if constexpr (TYPE == kQ4_K || TYPE == kQ5_K) {
+        const uint8_t* sb = row + int64_t(chunk) * Format<TYPE>::kBytes;
+        r.h = *reinterpret_cast<const u32x4*>(sb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = *reinterpret_cast<const u32x2*>(sb + (TYPE == kQ5_K ? 48 : 16) + 32 * i + 8 * g);
+        if constexpr (TYPE == kQ5_K) r.qh[0] = *reinterpret_cast<const u32x2*>(sb + 16 + 8 * g);
+    } else {
+        // Q6_K: 4 bits of two sub-blocks a byte, 2 of four; 16 scales; d
+        const uint8_t* sb = row + int64_t(chunk) * 210;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = *reinterpret_cast<const u32x2*>(sb + 32 * i + 8 * g);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) r.qh[i] = *reinterpret_cast<const u32x2*>(sb + 128 + 32 * i + 8 * g);
+        // the scales of this lane's halves of two sub-blocks in a word: bytes 8 (g / 2) and 16 above
+        const u32x2 s0 = *reinterpret_cast<const u32x2*>(sb + 192), s1 = *reinterpret_cast<const u32x2*>(sb + 200);
+        r.h = u32x4{s0[0], s0[1], s1[0], s1[1]};
+        r.d = *reinterpret_cast<const uint16_t*>(sb + 208);
+    }
+}
+
+// Sub-block i (of 32) of a chunk of 256.
+template <int TYPE>
+__device__ __forceinline__ Codes codes_of(const Raw<TYPE>& raw, int i, int g) {
     Codes r;
     r.c = 0.f;
     if constexpr (TYPE == kQ8_0) {
-        const uint8_t* blk = row + b * 34;
-        const u32x2 w = *reinterpret_cast<const u32x2*>(blk + 2 + 8 * g);
-        r.a = half_to_f32(*reinterpret_cast<const uint16_t*>(blk));
-        r.q = bytes_to_f16(w[0] ^ 0x80808080u, w[1] ^ 0x80808080u, 128.f);
+        r.a = half_to_f32(uint16_t(raw.h[i]));
+        r.q = bytes_to_f16(raw.w[i][0] ^ 0x80808080u, raw.w[i][1] ^ 0x80808080u, 128.f);
     } else if constexpr (kNibbleLayout<TYPE>) {
         // low nibbles of the code bytes, then high ones
-        const uint8_t* blk = row + b * Format<TYPE>::kBytes;
-        const u32x2b w = *reinterpret_cast<const u32x2b*>(blk + kHeader<TYPE> + 8 * (g & 1));
         const int sh = g >= 2 ? 4 : 0;
-        uint32_t w0 = (w[0] >> sh) & 0x0F0F0F0Fu, w1 = (w[1] >> sh) & 0x0F0F0F0Fu;
+        uint32_t w0 = (raw.w[i][0] >> sh) & 0x0F0F0F0Fu, w1 = (raw.w[i][1] >> sh) & 0x0F0F0F0Fu;
         if constexpr (TYPE == kMXFP4) {
             // two codes to a byte, which the conversion takes
-            r.a = mx_scale(blk[0]);
+            r.a = mx_scale(raw.h[i]);
             const uint32_t p0 = w0 | (w0 >> 4), p1 = w1 | (w1 >> 4);
             const f16x2v v0 = __builtin_bit_cast(f16x2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(p0, 1.f, 0));
             const f16x2v v1 = __builtin_bit_cast(f16x2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(p0, 1.f, 2));
@@ -82,41 +138,32 @@ __device__ __forceinline__ Codes codes_of(const uint8_t* row, int b, int g) {
             const f16x2v v3 = __builtin_bit_cast(f16x2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(p1, 1.f, 2));
             r.q = f16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
         } else {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(blk);
-            r.a = half_to_f32(h[0]);
-            if constexpr (kHasOffset<TYPE>) r.c = half_to_f32(h[1]);
+            r.a = half_to_f32(uint16_t(raw.h[i]));
+            if constexpr (kHasOffset<TYPE>) r.c = half_to_f32(uint16_t(raw.h[i] >> 16));
             if constexpr (kHasFifth<TYPE>) {
-                constexpr int at = kHasOffset<TYPE> ? 2 : 1;
-                const uint32_t qh = uint32_t(h[at]) | (uint32_t(h[at + 1]) << 16);
-                w0 |= fifth_bits(qh, 8 * g);
-                w1 |= fifth_bits(qh, 8 * g + 4);
+                w0 |= fifth_bits(raw.qh[i], 8 * g);
+                w1 |= fifth_bits(raw.qh[i], 8 * g + 4);
             }
             r.q = bytes_to_f16(w0, w1, kHasOffset<TYPE> ? 0.f : kHasFifth<TYPE> ? 16.f : 8.f);
         }
     } else if constexpr (TYPE == kQ4_K || TYPE == kQ5_K) {
-        const uint8_t* sb = row + (b >> 3) * Format<TYPE>::kBytes;
-        const int j = b & 7;
-        const u32x4 hw = *reinterpret_cast<const u32x4*>(sb);
         float m;
-        q4_k_coeffs(hw[0], hw[1], hw[2], hw[3], j, r.a, m);
+        q4_k_coeffs(raw.h[0], raw.h[1], raw.h[2], raw.h[3], i, r.a, m);
         r.c = -m;
-        const u32x2 w = *reinterpret_cast<const u32x2*>(sb + (TYPE == kQ5_K ? 48 : 16) + 32 * (j / 2) + 8 * g);
-        uint32_t w0 = (w[0] >> (4 * (j & 1))) & 0x0F0F0F0Fu, w1 = (w[1] >> (4 * (j & 1))) & 0x0F0F0F0Fu;
+        const u32x2 w = raw.w[i / 2];
+        uint32_t w0 = (w[0] >> (4 * (i & 1))) & 0x0F0F0F0Fu, w1 = (w[1] >> (4 * (i & 1))) & 0x0F0F0F0Fu;
         if constexpr (TYPE == kQ5_K) {
-            const u32x2 qh = *reinterpret_cast<const u32x2*>(sb + 16 + 8 * g);
-            w0 |= ((qh[0] >> j) & 0x01010101u) << 4;
-            w1 |= ((qh[1] >> j) & 0x01010101u) << 4;
+            w0 |= ((raw.qh[0][0] >> i) & 0x01010101u) << 4;
+            w1 |= ((raw.qh[0][1] >> i) & 0x01010101u) << 4;
         }
         r.q = bytes_to_f16(w0, w1, 0.f);
     } else {
         // Q6_K: a scale covers 16 codes, half of the sub-block's lanes. (q - 32) times it
         // has up to 13 bits: its four low bits and the rest make products of their own.
-        const uint8_t* sb = row + (b >> 3) * 210;
-        const int i = b & 7, half = i >> 2, p = i & 3;
-        const u32x2 ql = *reinterpret_cast<const u32x2*>(sb + 64 * half + 32 * (p & 1) + 8 * g);
-        const u32x2 qh = *reinterpret_cast<const u32x2*>(sb + 128 + 32 * half + 8 * g);
-        const int sc = static_cast<int8_t>(sb[192 + 8 * half + 2 * p + (g >> 1)]);
-        r.a = half_to_f32(*reinterpret_cast<const uint16_t*>(sb + 208));
+        const int half = i >> 2, p = i & 3;
+        const u32x2 ql = raw.w[2 * half + (p & 1)], qh = raw.qh[half];
+        const int sc = static_cast<int8_t>(raw.h[i / 2] >> (16 * (i & 1) + 8 * (g >> 1)));
+        r.a = half_to_f32(uint16_t(raw.d));
         const int sh = 4 * (p >> 1);
         const f16x8 q = bytes_to_f16(((ql[0] >> sh) & 0x0F0F0F0Fu) | (((qh[0] >> (2 * p)) & 0x03030303u) << 4),
                                      ((ql[1] >> sh) & 0x0F0F0F0Fu) | (((qh[1] >> (2 * p)) & 0x03030303u) << 4), 32.f);
@@ -196,11 +243,15 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
 #pragma unroll
             for (int i = 0; i < 4; ++i) factor[t][i] = factor_of(t, i);
     const f16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
-    auto sub_blocks = [&](const uint8_t* lds, int chunk, auto whole) __attribute__((always_inline)) {
+    const int last = g.K / Format<TYPE>::kBlock - 1;
+    auto load = [&](Raw<TYPE>* raw, int chunk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < kFewBlocks; ++n) load_raw<TYPE>(raw[n], w[n], chunk, last, gr);
+    };
+    auto sub_blocks = [&](const uint8_t* lds, const Raw<TYPE>* raw, int chunk, auto whole) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kFewK / 32; ++i) {
-            const int b = chunk * (kFewK / 32) + i;
-            if (!decltype(whole)::value && b * 32 >= g.K) break;
+            if (!decltype(whole)::value && chunk * kFewK + i * 32 >= g.K) break;
             f16x8 xs[TB][PX];
 #pragma unroll
             for (int t = 0; t < TB; ++t)
@@ -218,7 +269,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
                 }
 #pragma unroll
             for (int n = 0; n < kFewBlocks; ++n) {
-                const Codes c = codes_of<TYPE>(w[n], b, gr);
+                const Codes c = codes_of<TYPE>(raw[n], i, gr);
 #pragma unroll
                 for (int t = 0; t < TB; ++t) {
                     f32x4 v = {0, 0, 0, 0};
@@ -237,22 +288,30 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
             }
         }
     };
-    auto run = [&](const uint8_t* lds, int chunk) __attribute__((always_inline)) {
-        if ((chunk + 1) * kFewK <= g.K)
-            sub_blocks(lds, chunk, std::true_type{});
+    auto run = [&](const uint8_t* lds, const Raw<TYPE>* raw, int chunk) __attribute__((always_inline)) {
+        if (Format<TYPE>::kBlock == kFewK || (chunk + 1) * kFewK <= g.K)
+            sub_blocks(lds, raw, chunk, std::true_type{});
         else
-            sub_blocks(lds, chunk, std::false_type{});
+            sub_blocks(lds, raw, chunk, std::false_type{});
     };
+    Raw<TYPE> raw0[kFewBlocks], raw1[kFewBlocks];
     const int chunks = (g.K + kFewK - 1) / kFewK;
     copy(lds0, 0);
+    load(raw0, 0);
     for (int c = 0; c < chunks; c += 2) {
         copies_done_for_all<0>();
-        if (c + 1 < chunks) copy(lds1, c + 1);
-        run(lds0, c);
+        if (c + 1 < chunks) {
+            copy(lds1, c + 1);
+            load(raw1, c + 1);
+        }
+        run(lds0, raw0, c);
         if (c + 1 >= chunks) break;
         copies_done_for_all<0>();
-        if (c + 2 < chunks) copy(lds0, c + 2);
-        run(lds1, c + 1);
+        if (c + 2 < chunks) {
+            copy(lds0, c + 2);
+            load(raw0, c + 2);
+        }
+        run(lds1, raw1, c + 1);
     }
 
     // A lane: tokens 16 t + 4 gr + i, rows row0 + 16 n + r.
