@@ -201,9 +201,31 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// A wave's rows of 256 elements go from memory to LDS in pieces of 16 bytes, side by side:
+// a lane needs bytes here and there of 16 rows, which asked of memory take a cache line
+// each time. The last piece ends with the row's. Beside x of many tokens LDS has no room.
+template <int TYPE>
+struct Staged {
+    static constexpr int kBytes = kFewK / Format<TYPE>::kBlock * Format<TYPE>::kBytes;
+    static constexpr int kPitch = (kBytes + 15) / 16 * 16 + (kBytes % 64 == 0 ? 16 : 0);
+    static constexpr int kPieces = (kBytes + 15) / 16, kRows = 16 * kFewBlocks;
+    static constexpr int kLoads = (kRows * kPieces + 63) / 64;  // a lane
+};
+template <int TB, int PX>
+constexpr bool kStaged = TB * PX <= 2;
+template <int TYPE, int TB, int PX>
+constexpr int few_per_cu() {
+    if (!kStaged<TB, PX>) return 2;
+    const int fit = 160 * 1024 / (2 * kFewK / 64 * 16 * TB * PX * 128 + kFewWaves * Staged<TYPE>::kRows * Staged<TYPE>::kPitch);
+    return fit < 4 ? fit : 4;
+}
+typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
+template <int TYPE>
+using LdsPiece = uint32_t __attribute__((ext_vector_type(4), aligned(Staged<TYPE>::kBytes % 16 == 0 ? 16 : 2)));
+
 // Up to 16 TB tokens, x in PX parts.
 template <int TYPE, int TB, int PX, Kind KIND>
-__global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g) {
+__global__ __launch_bounds__(kFewWaves * 64, (few_per_cu<TYPE, TB, PX>())) void few_kernel(const FewArgs g) {
     constexpr int kRows = kFewK / 64 * 16 * TB * PX;  // of 128 bytes in LDS: step, part, token
     constexpr int kCopies = kRows * 128 / (1024 * kFewWaves);
     __shared__ __align__(1024) uint8_t lds0[kRows * 128];
@@ -294,24 +316,77 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void few_kernel(const FewArgs g)
         else
             sub_blocks(lds, raw, chunk, std::false_type{});
     };
-    Raw<TYPE> raw0[kFewBlocks], raw1[kFewBlocks];
+
     const int chunks = (g.K + kFewK - 1) / kFewK;
     copy(lds0, 0);
-    load(raw0, 0);
-    for (int c = 0; c < chunks; c += 2) {
-        copies_done_for_all<0>();
-        if (c + 1 < chunks) {
-            copy(lds1, c + 1);
-            load(raw1, c + 1);
+    if constexpr (kStaged<TB, PX>) {
+        typedef Staged<TYPE> Z;
+        __shared__ __align__(16) uint8_t staged[kFewWaves][Z::kRows * Z::kPitch];
+        uint8_t* mine = staged[wave];
+        const int64_t base = min(row0, g.rows - 1);
+        const uint8_t* from = g.W + base * g.ldw;
+        const int below = int(min(g.rows - 1 - base, int64_t(Z::kRows - 1)));
+        uint32_t at[Z::kLoads], to[Z::kLoads];
+#pragma unroll
+        for (int i = 0; i < Z::kLoads; ++i) {
+            const int piece = min(i * 64 + lane, Z::kRows * Z::kPieces - 1), row = piece / Z::kPieces;
+            const int byte = min(piece % Z::kPieces * 16, Z::kBytes - 16);
+            at[i] = uint32_t(min(row, below)) * uint32_t(g.ldw) + byte;
+            to[i] = row * Z::kPitch + byte;
         }
-        run(lds0, raw0, c);
-        if (c + 1 >= chunks) break;
-        copies_done_for_all<0>();
-        if (c + 2 < chunks) {
-            copy(lds0, c + 2);
-            load(raw0, c + 2);
+        u32x4 pieces[Z::kLoads];
+        auto whole = [&](int chunk) { return (chunk + 1) * kFewK <= g.K; };
+        auto fetch = [&](int chunk) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < Z::kLoads; ++i)
+                pieces[i] = *reinterpret_cast<const u32x4b*>(from + int64_t(chunk) * Z::kBytes + at[i]);
+        };
+        auto step = [&](const uint8_t* lds, uint8_t* next, int chunk) __attribute__((always_inline)) {
+            copies_done_for_all<0>();
+            const bool here = whole(chunk);
+            if (here)
+#pragma unroll
+                for (int i = 0; i < Z::kLoads; ++i) *reinterpret_cast<LdsPiece<TYPE>*>(mine + to[i]) = pieces[i];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (chunk + 1 < chunks) {
+                copy(next, chunk + 1);
+                if (whole(chunk + 1)) fetch(chunk + 1);
+            }
+            Raw<TYPE> raw[kFewBlocks];
+            if (here) {
+#pragma unroll
+                for (int n = 0; n < kFewBlocks; ++n) load_raw<TYPE>(raw[n], mine + (n * 16 + r) * Z::kPitch, 0, 7, gr);
+                sub_blocks(lds, raw, chunk, std::true_type{});
+            } else if (Format<TYPE>::kBlock < kFewK) {  // the last blocks of a row
+                load(raw, chunk);
+                sub_blocks(lds, raw, chunk, std::false_type{});
+            }
+        };
+        if (whole(0)) fetch(0);
+        for (int c = 0; c < chunks; c += 2) {
+            step(lds0, lds1, c);
+            if (c + 1 >= chunks) break;
+            step(lds1, lds0, c + 1);
         }
-        run(lds1, raw1, c + 1);
+    } else {
+        Raw<TYPE> raw0[kFewBlocks], raw1[kFewBlocks];
+        load(raw0, 0);
+        for (int c = 0; c < chunks; c += 2) {
+            copies_done_for_all<0>();
+            if (c + 1 < chunks) {
+                copy(lds1, c + 1);
+                load(raw1, c + 1);
+            }
+            run(lds0, raw0, c);
+            if (c + 1 >= chunks) break;
+            copies_done_for_all<0>();
+            if (c + 2 < chunks) {
+                copy(lds0, c + 2);
+                load(raw0, c + 2);
+            }
+            run(lds1, raw1, c + 1);
+        }
     }
 
     // A lane: tokens 16 t + 4 gr + i, rows row0 + 16 n + r.
