@@ -194,7 +194,7 @@ struct FewArgs {
 // Blocks of 16 rows of the head a wave, which share the reads of x: with one, 142 us
 // where two take 114 to 121 (Q4_K 131072 x 4096, 16 tokens).
 constexpr int kFewBlocks = 2;
-constexpr int kFewWaves = 4, kFewRows = 16 * kFewBlocks * kFewWaves;  // rows a workgroup
+constexpr int kFewRows = 16 * kFewBlocks;  // of the head a wave
 constexpr int kFewK = 256;  // of x in LDS
 
 __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f32x4& c) {
@@ -208,15 +208,20 @@ template <int TYPE>
 struct Staged {
     static constexpr int kBytes = kFewK / Format<TYPE>::kBlock * Format<TYPE>::kBytes;
     static constexpr int kPitch = (kBytes + 15) / 16 * 16 + (kBytes % 64 == 0 ? 16 : 0);
-    static constexpr int kPieces = (kBytes + 15) / 16, kRows = 16 * kFewBlocks;
-    static constexpr int kLoads = (kRows * kPieces + 63) / 64;  // a lane
+    static constexpr int kPieces = (kBytes + 15) / 16;
+    static constexpr int kLoads = (kFewRows * kPieces + 63) / 64;  // a lane
+    static constexpr int kLds = kFewRows * kPitch;                 // a wave
 };
 template <int TB, int PX>
-constexpr bool kStaged = TB * PX <= 2;
+constexpr bool kStaged = TB * PX <= 4;
+// Waves that share the chunks of x in LDS.
+template <int TB, int PX>
+constexpr int kFewWaves = TB * PX >= 4 ? 8 : 4;
 template <int TYPE, int TB, int PX>
-constexpr int few_per_cu() {
-    if (!kStaged<TB, PX>) return 2;
-    const int fit = 160 * 1024 / (2 * kFewK / 64 * 16 * TB * PX * 128 + kFewWaves * Staged<TYPE>::kRows * Staged<TYPE>::kPitch);
+constexpr int few_waves_a_simd() {
+    constexpr int waves = kFewWaves<TB, PX>;
+    const int lds = 2 * kFewK / 64 * 16 * TB * PX * 128 + (kStaged<TB, PX> ? waves * Staged<TYPE>::kLds : 0);
+    const int fit = 160 * 1024 / lds * waves / 4;
     return fit < 4 ? fit : 4;
 }
 typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
@@ -225,14 +230,15 @@ using LdsPiece = uint32_t __attribute__((ext_vector_type(4), aligned(Staged<TYPE
 
 // Up to 16 TB tokens, x in PX parts.
 template <int TYPE, int TB, int PX, Kind KIND>
-__global__ __launch_bounds__(kFewWaves * 64, (few_per_cu<TYPE, TB, PX>())) void few_kernel(const FewArgs g) {
+__global__ __launch_bounds__((kFewWaves<TB, PX> * 64), (few_waves_a_simd<TYPE, TB, PX>())) void few_kernel(const FewArgs g) {
+    constexpr int kWaves = kFewWaves<TB, PX>;
     constexpr int kRows = kFewK / 64 * 16 * TB * PX;  // of 128 bytes in LDS: step, part, token
-    constexpr int kCopies = kRows * 128 / (1024 * kFewWaves);
+    constexpr int kCopies = kRows * 128 / (1024 * kWaves);
     __shared__ __align__(1024) uint8_t lds0[kRows * 128];
     __shared__ __align__(1024) uint8_t lds1[kRows * 128];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int r = lane & 15, gr = lane >> 4;
-    const int64_t row0 = int64_t(blockIdx.x) * kFewRows + wave * 16 * kFewBlocks;
+    const int64_t run = int64_t(blockIdx.x) * kWaves + wave, row0 = run * kFewRows;
 
     // x's rows of a chunk: row (step, part, token) of 128 bytes, its 16-byte blocks
     // permuted by XOR with (row / 2) % 8
@@ -241,7 +247,7 @@ __global__ __launch_bounds__(kFewWaves * 64, (few_per_cu<TYPE, TB, PX>())) void 
     auto copy = [&](uint8_t* lds, int chunk) {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const int at = (i * kFewWaves + wave) * 8;
+            const int at = (i * kWaves + wave) * 8;
             const uint32_t row = at + (lane >> 3);
             const uint32_t token = row % (16 * TB), part = row / (16 * TB) % PX, step = row / (16 * TB * PX);
             const uint32_t from = uint32_t(part * g.plane * 2) + (step * 64 + token) * 128 +
@@ -310,7 +316,7 @@ __global__ __launch_bounds__(kFewWaves * 64, (few_per_cu<TYPE, TB, PX>())) void 
             }
         }
     };
-    auto run = [&](const uint8_t* lds, const Raw<TYPE>* raw, int chunk) __attribute__((always_inline)) {
+    auto any = [&](const uint8_t* lds, const Raw<TYPE>* raw, int chunk) __attribute__((always_inline)) {
         if (Format<TYPE>::kBlock == kFewK || (chunk + 1) * kFewK <= g.K)
             sub_blocks(lds, raw, chunk, std::true_type{});
         else
@@ -321,15 +327,15 @@ __global__ __launch_bounds__(kFewWaves * 64, (few_per_cu<TYPE, TB, PX>())) void 
     copy(lds0, 0);
     if constexpr (kStaged<TB, PX>) {
         typedef Staged<TYPE> Z;
-        __shared__ __align__(16) uint8_t staged[kFewWaves][Z::kRows * Z::kPitch];
+        __shared__ __align__(16) uint8_t staged[kWaves][Z::kLds];
         uint8_t* mine = staged[wave];
         const int64_t base = min(row0, g.rows - 1);
         const uint8_t* from = g.W + base * g.ldw;
-        const int below = int(min(g.rows - 1 - base, int64_t(Z::kRows - 1)));
+        const int below = int(min(g.rows - 1 - base, int64_t(kFewRows - 1)));
         uint32_t at[Z::kLoads], to[Z::kLoads];
 #pragma unroll
         for (int i = 0; i < Z::kLoads; ++i) {
-            const int piece = min(i * 64 + lane, Z::kRows * Z::kPieces - 1), row = piece / Z::kPieces;
+            const int piece = min(i * 64 + lane, kFewRows * Z::kPieces - 1), row = piece / Z::kPieces;
             const int byte = min(piece % Z::kPieces * 16, Z::kBytes - 16);
             at[i] = uint32_t(min(row, below)) * uint32_t(g.ldw) + byte;
             to[i] = row * Z::kPitch + byte;
@@ -378,14 +384,14 @@ __global__ __launch_bounds__(kFewWaves * 64, (few_per_cu<TYPE, TB, PX>())) void 
                 copy(lds1, c + 1);
                 load(raw1, c + 1);
             }
-            run(lds0, raw0, c);
+            any(lds0, raw0, c);
             if (c + 1 >= chunks) break;
             copies_done_for_all<0>();
             if (c + 2 < chunks) {
                 copy(lds0, c + 2);
                 load(raw0, c + 2);
             }
-            run(lds1, raw1, c + 1);
+            any(lds1, raw1, c + 1);
         }
     }
 
@@ -418,8 +424,7 @@ __global__ __launch_bounds__(kFewWaves * 64, (few_per_cu<TYPE, TB, PX>())) void 
                 for (int n = 0; n < kFewBlocks; ++n) sum += exp_of(l[n] - from);
 #pragma unroll
                 for (int d = 1; d < 16; d *= 2) sum += __shfl_xor(sum, d);
-                if (live && r == 0)
-                    g.part[(g.part0 + int64_t(blockIdx.x) * kFewWaves + wave) * g.T + token] = make_float2(top, sum);
+                if (live && r == 0 && row0 < g.rows) g.part[(g.part0 + run) * g.T + token] = make_float2(top, sum);
             } else {
                 const float lse = target >= 0 ? g.lse[token] : 0.f;
 #pragma unroll

@@ -448,18 +448,20 @@ int launch_few(bool prob, int parts, const ce::FewArgs& a, hipStream_t st) {
     if constexpr (!ce::kFewType<TYPE>) {
         return RETRO_E_TYPE;
     } else {
-        auto kernel_of = [&](auto tokens) {
-            constexpr int TB = decltype(tokens)::value;
-            return prob ? (parts == 2 ? ce::few_kernel<TYPE, TB, 2, ce::kProb> : ce::few_kernel<TYPE, TB, 1, ce::kProb>)
-                        : (parts == 2 ? ce::few_kernel<TYPE, TB, 2, ce::kStats> : ce::few_kernel<TYPE, TB, 1, ce::kStats>);
+        static_assert(ce::kFewRows == 32, "few_runs");
+        auto launch = [&](auto tokens, auto of_x) {
+            constexpr int TB = decltype(tokens)::value, PX = decltype(of_x)::value, kWaves = ce::kFewWaves<TB, PX>;
+            auto kernel = prob ? ce::few_kernel<TYPE, TB, PX, ce::kProb> : ce::few_kernel<TYPE, TB, PX, ce::kStats>;
+            host::clear_last_error();
+            kernel<<<dim3(uint32_t(host::cdiv(a.rows, kWaves * ce::kFewRows))), dim3(kWaves * 64), 0, st>>>(a);
+            return host::launch_status();
         };
-        auto kernel = a.T <= 16   ? kernel_of(std::integral_constant<int, 1>{})
-                      : a.T <= 32 ? kernel_of(std::integral_constant<int, 2>{})
-                                  : kernel_of(std::integral_constant<int, 4>{});
-        const int64_t blocks = host::cdiv(a.rows, ce::kFewRows);
-        host::clear_last_error();
-        kernel<<<dim3(uint32_t(blocks)), dim3(ce::kFewWaves * 64), 0, st>>>(a);
-        return host::launch_status();
+        auto launch_parts = [&](auto tokens) {
+            return parts == 2 ? launch(tokens, std::integral_constant<int, 2>{}) : launch(tokens, std::integral_constant<int, 1>{});
+        };
+        return a.T <= 16   ? launch_parts(std::integral_constant<int, 1>{})
+               : a.T <= 32 ? launch_parts(std::integral_constant<int, 2>{})
+                           : launch_parts(std::integral_constant<int, 4>{});
     }
 }
 

@@ -57,7 +57,7 @@ inline bool few_type(int type) {
            type == RETRO_MXFP4 || type == RETRO_Q4_K || type == RETRO_Q5_K || type == RETRO_Q6_K;
 }
 // Runs of the head's rows that it gives statistics of.
-inline int64_t few_runs(int64_t rows) { return host::cdiv(rows, 128) * 4; }
+inline int64_t few_runs(int64_t rows) { return host::cdiv(rows, 32); }
 template <int TYPE>
 int launch_few(bool prob, int parts, const ce::FewArgs& a, hipStream_t st);
 
