@@ -10,9 +10,9 @@
 // results that it gets.
 //
 // What bounds it is memory where few tokens are given: Q4_K 131072 x 4096 and 16 tokens
-// take 114 to 118 us for 302 MB, against 252 us with the weights decoded to F32 in front of
-// F32 matrix instructions. Blocks of 34 bytes, which only 2-byte loads reach, take longer
-// than their bytes: Q8_0 317 us for 570 MB.
+// take 93 us for 302 MB (Q8_0 139 for 570), against 252 us with the weights decoded to
+// F32 in front of F32 matrix instructions. Half of that is decoding: 16 VALU instructions
+// for the 8 codes and four results of a lane.
 #pragma once
 
 #include "retro_ce_kernel.h"
@@ -192,7 +192,7 @@ struct FewArgs {
 };
 
 // Blocks of 16 rows of the head a wave, which share the reads of x: with one, 142 us
-// where two take 114 to 121 (Q4_K 131072 x 4096, 16 tokens).
+// where two took 114 to 121 (Q4_K 131072 x 4096, 16 tokens, rows not yet through LDS).
 constexpr int kFewBlocks = 2;
 constexpr int kFewRows = 16 * kFewBlocks;  // of the head a wave
 constexpr int kFewK = 256;  // of x in LDS
@@ -203,7 +203,8 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
 
 // A wave's rows of 256 elements go from memory to LDS in pieces of 16 bytes, side by side:
 // a lane needs bytes here and there of 16 rows, which asked of memory take a cache line
-// each time. The last piece ends with the row's. Beside x of many tokens LDS has no room.
+// each time (16 tokens through 131072 x 4096: Q8_0 313 us against 139, Q4_0 307 and 116,
+// Q4_K 109 and 93). The last piece ends with the row's.
 template <int TYPE>
 struct Staged {
     static constexpr int kBytes = kFewK / Format<TYPE>::kBlock * Format<TYPE>::kBytes;
@@ -212,9 +213,12 @@ struct Staged {
     static constexpr int kLoads = (kFewRows * kPieces + 63) / 64;  // a lane
     static constexpr int kLds = kFewRows * kPitch;                 // a wave
 };
+// Beside 64 tokens in two parts, 128 KB, LDS has no room for it.
 template <int TB, int PX>
 constexpr bool kStaged = TB * PX <= 4;
-// Waves that share the chunks of x in LDS.
+// Waves that share the chunks of x in LDS. Four, of which several workgroups fit, while x
+// is small; with 64 tokens four are one workgroup a CU (Q8_0 327 us, Q4_K 323), eight as
+// well (197 and 199).
 template <int TB, int PX>
 constexpr int kFewWaves = TB * PX >= 4 ? 8 : 4;
 template <int TYPE, int TB, int PX>

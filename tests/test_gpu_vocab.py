@@ -270,6 +270,25 @@ def test_cross_entropy_of_packed_heads(q, wtype, T):
         check_cross_entropy(q, wtype, W, values, x, tokens(T, N, seed=T), where=NAME[xtype])
 
 
+@pytest.mark.parametrize("wtype", [wl.Q4_0, wl.Q4_1, wl.Q5_0, wl.Q5_1, wl.Q8_0, wl.MXFP4], ids=wl.TYPE_NAMES.get)
+def test_cross_entropy_of_few_tokens_and_odd_rows(q, wtype):
+    """Rows that end inside a chunk of 256, heads that end inside a wave's 32 rows."""
+    for N, K, T in ((1, 32, 1), (31, 224, 16), (33, 256, 17), (127, 288, 33), (129, 480, 64), (257, 544, 32), (300, 1056, 5)):
+        W, values = packed(wtype, N, K, seed=K)
+        for xtype in (torch.bfloat16, torch.float32):
+            x = (torch.randn((T, K), generator=gen(7)) / (float(values.std()) * K ** 0.5)).to(xtype)
+            check_cross_entropy(q, wtype, W, values, x, tokens(T, N, seed=T), where=f"{N} {K} {T} {NAME[xtype]}")
+
+
+@pytest.mark.parametrize("wtype", [wl.Q4_K, wl.Q5_K, wl.Q6_K], ids=wl.TYPE_NAMES.get)
+def test_cross_entropy_of_few_tokens_and_several_blocks(q, wtype):
+    for N, K, T in ((1, 256, 1), (33, 512, 16), (127, 768, 33), (300, 1280, 64)):
+        W, values = packed(wtype, N, K, seed=K)
+        for xtype in (torch.bfloat16, torch.float32):
+            x = (torch.randn((T, K), generator=gen(7)) / (float(values.std()) * K ** 0.5)).to(xtype)
+            check_cross_entropy(q, wtype, W, values, x, tokens(T, N, seed=T), where=f"{N} {K} {T} {NAME[xtype]}")
+
+
 def test_cross_entropy_of_strided_operands(q):
     T, N, K = 90, 500, 256
     for dtype, pad in ((torch.bfloat16, 8), (torch.bfloat16, 3), (torch.float32, 5)):
