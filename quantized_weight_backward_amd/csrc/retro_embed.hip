@@ -21,19 +21,23 @@ using mx::Span;
 // What bounds it is the table being written. All of it is cleared beside the sort, in
 // the same launches, so that the sort costs no time of its own and only rows of tokens
 // are written after it. 16384 tokens of 4096 BF16 columns into 131072 F32
-// rows: 472 us, of which 372 in the four launches that clear 2.15 GB and sort (5.8
-// TB/s), 88 in the rows' sums, 6 in joining them.
+// rows: 435 us, of which 344 in the launch that clears 2.15 GB and sorts (6.2 TB/s), 88
+// in the rows' sums, 6 in joining them.
 
 constexpr int kMaxBits = 9, kMaxDigits = 1 << kMaxBits;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSmallT = 8192;      // sorted by one workgroup in LDS
+// Tokens that one workgroup sorts in LDS. 12000 of 1000 rows take 41 us so and 46 in the
+// larger sort's launches; 16384 take 51 and 48 there, and beside a table of 131072 x 4096
+// being cleared 435 and 470.
+constexpr int kSmallT = 16384;
 constexpr int kBlockItems = 2048;  // of a workgroup of a larger sort's pass
 constexpr int kBlockThreads = 256, kBlockWaves = kBlockThreads / 64;
-// Tokens of a run. Shorter ones are more waves for few tokens (777 of 1000 columns into
-// 32000 rows: 59 us in runs of 64, 33 in runs of 16), longer ones fewer parts to join; at
-// 16384 tokens of 4096 columns either takes 472 us.
+// Tokens of a run. Shorter ones are more waves, which few tokens of few columns need (777
+// of 1000 columns into 32000 rows: 59 us in runs of 64, 33 in runs of 16; 16384 of 512:
+// 115 and 93), longer ones fewer parts to join; at 16384 tokens of 4096 columns, 2048
+// waves in runs of 64, either takes as long.
 constexpr int kMaxRun = 64;
-int run_for(int64_t T) { return T <= 4096 ? 16 : kMaxRun; }
+int run_for(int64_t K, int64_t T) { return cdiv(T, kMaxRun) * cdiv(K, 512) < 2048 ? 16 : kMaxRun; }
 
 // Passes and bits of each for keys 0 .. N.
 struct Radix {
@@ -118,9 +122,11 @@ __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* waves) {
     return before + in - v;
 }
 
-// Up to kSmallT tokens: all passes in one workgroup, the other workgroups fill. Wave w takes items w * per ..,
-// 64 at a time, and keeps a count a digit: an item's place is its digit's first, the
-// counts of the waves before, its wave's count so far, and the lanes before it.
+// Up to kSmallT tokens, PER a thread: all passes in one workgroup, the other workgroups
+// fill. Wave w takes items w * per .., 64 at a time, and keeps a count a digit: an item's
+// place is its digit's first, the counts of the waves before, its wave's count so far,
+// and the lanes before it.
+template <int PER>
 __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __restrict__ ids, bool wide, int64_t N,
                                                                  int T, int passes, int bits, uint32_t* __restrict__ keys,
                                                                  uint32_t* __restrict__ order, Fill f) {
@@ -128,15 +134,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __
         fill<kSortThreads>(f, blockIdx.x - 1);
         return;
     }
-    constexpr int kPer = kSmallT / kSortThreads;
-    __shared__ uint32_t key[kSmallT];
-    __shared__ uint16_t from[kSmallT];
+    __shared__ uint32_t key[PER * kSortThreads];
+    __shared__ uint16_t from[PER * kSortThreads];
     __shared__ uint16_t count[kSortWaves][kMaxDigits];
     __shared__ uint32_t waves[kSortWaves];
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, rounds = (T + kSortThreads - 1) / kSortThreads;
-    uint32_t k[kPer], at[kPer], place[kPer];
+    uint32_t k[PER], at[PER], place[PER];
     auto item = [&](int i) { return (wave * rounds + i) * 64 + lane; };
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const bool live = i < rounds && item(i) < T;
         k[i] = live ? key_of(ids, wide, item(i), N) : 0;
         at[i] = uint32_t(item(i));
@@ -145,7 +150,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __
         for (int d = threadIdx.x; d < kSortWaves * kMaxDigits; d += kSortThreads) (&count[0][0])[d] = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             if (i >= rounds) break;
             const bool live = item(i) < T;
             const uint32_t digit = (k[i] >> (p * bits)) & ((1u << bits) - 1);
@@ -171,7 +176,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __
             }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             if (i >= rounds || item(i) >= T) break;
             const uint32_t to = count[wave][(k[i] >> (p * bits)) & ((1u << bits) - 1)] + place[i];
             key[to] = k[i];
@@ -179,7 +184,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             if (i >= rounds || item(i) >= T) break;
             k[i] = key[item(i)];
             at[i] = from[item(i)];
@@ -187,7 +192,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(const void* __
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         if (i >= rounds || item(i) >= T) break;
         keys[item(i)] = k[i];
         order[item(i)] = at[i];
@@ -432,7 +437,7 @@ Plan plan_of(int64_t K, int64_t N, int64_t T) {
         p.counts = take(4 * p.blocks << p.radix.bits);
         p.totals = take(4 << p.radix.bits);
     }
-    p.run = run_for(T);
+    p.run = run_for(K, T);
     p.parts = take(4 * 2 * cdiv(T, p.run) * cdiv(K, 8) * 8);
     return p;
 }
@@ -451,7 +456,9 @@ int sort(const Plan& p, const void* ids, bool wide, int64_t N, int64_t T, uint8_
     out = 0;
     host::clear_last_error();
     if (T <= kSmallT) {
-        sort_small_kernel<<<dim3(uint32_t(1 + fillers(f, kSortThreads))), dim3(kSortThreads), 0, st>>>(
+        // a thread that can hold 16 items takes 4 us longer over 8
+        auto kernel = T <= 8 * kSortThreads ? sort_small_kernel<8> : sort_small_kernel<16>;
+        kernel<<<dim3(uint32_t(1 + fillers(f, kSortThreads))), dim3(kSortThreads), 0, st>>>(
             ids, wide, N, int(T), p.radix.passes, p.radix.bits, words(p.keys[0]), words(p.order[0]), f);
         return host::launch_status();
     }

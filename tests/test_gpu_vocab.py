@@ -133,7 +133,7 @@ def gradient_bound(dw, size, count, dtype, old=None):
 
 @pytest.mark.parametrize("T,N,K", [(1, 1, 1), (2, 5, 3), (63, 7, 8), (64, 1, 40), (65, 1, 9), (129, 3, 100),
                                    (300, 1000, 17), (1000, 511, 64), (1025, 513, 12), (5000, 20, 8), (8192, 40000, 8),
-                                   (8193, 70000, 8), (20000, 300, 33), (30011, 2, 16), (40000, 300000, 4)], ids=str)
+                                   (8193, 70000, 8), (16384, 5000, 12), (16385, 90, 5), (20000, 300, 33), (30011, 2, 16), (40000, 300000, 4)], ids=str)
 @pytest.mark.parametrize("dtype", FLOATS, ids=NAME.get)
 def test_embedding_backward(q, dtype, T, N, K):
     ids = tokens(T, N, seed=T, dtype=torch.int32 if T % 2 else torch.int64)
@@ -599,7 +599,7 @@ def test_a_tied_table_in_one_step(q):
 
 def test_a_captured_step(q):
     """The step recorded once and replayed on new ids, beside eager work."""
-    for N, K, T in ((600, 128, 200), (40000, 64, 9000)):
+    for N, K, T in ((600, 128, 200), (40000, 64, 9000), (3000, 64, 17000)):
         w = head(torch.bfloat16, N, K, seed=1).cuda()
         g = torch.full((T,), 1 / T, device="cuda")
         ids, targets = tokens(T, N, seed=2).cuda(), tokens(T, N, seed=3).cuda()
