@@ -74,24 +74,12 @@ __global__ __launch_bounds__(256) void planes_kernel(const uint8_t* __restrict__
     }
 }
 
-// No smaller than any magnitude of a block, from its scale alone (which bounds it
-// within a power of two or so: it chooses a power of two).
-template <int TYPE>
-constexpr bool kBoundByScale = TYPE == kQ8_0 || TYPE == kQ4_0 || TYPE == kQ5_0 || TYPE == kMXFP4;
-template <int TYPE>
-__device__ __forceinline__ float block_bound(const uint8_t* blk) {
-    if constexpr (TYPE == kMXFP4)
-        return fminf(6.f * mx_scale(blk[0]), 0x1.fffffep127f);  // codes below 6 may be finite where this is not
-    else
-        return half_to_f32(*reinterpret_cast<const uint16_t*>(blk)) * (TYPE == kQ8_0 ? 128.f : TYPE == kQ4_0 ? 8.f : 16.f);
-}
-
-// The largest magnitude's bits of a table, or its bound's; NaN above all. A group is 8
-// elements, or a block where that is bounded by its scale.
+// The largest magnitude's bits of a table, NaN above all: of the values themselves, since
+// a block's scale says nothing of them where its codes are small or zero.
 template <int TYPE>
 __global__ __launch_bounds__(256) void top_kernel(const uint8_t* __restrict__ W, int64_t ldw, int64_t rows, int K,
                                                   uint32_t* __restrict__ top, int wide, uint32_t per) {
-    // four groups in flight a thread
+    // four groups of 8 in flight a thread
     uint32_t m = 0;
     const int64_t all = rows * per, step = int64_t(gridDim.x) * 256;
     for (int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x; at < all; at += 4 * step) {
@@ -100,16 +88,12 @@ __global__ __launch_bounds__(256) void top_kernel(const uint8_t* __restrict__ W,
         for (int j = 0; j < 4; ++j) {
             const int64_t i = min(at + j * step, all - 1);  // the last group again past the end
             const int64_t r = i >> 32 ? i / per : int64_t(uint32_t(i) / per);
-            const int g = int(i - r * per);
-            if constexpr (kBoundByScale<TYPE>)
-                e[j][0] = block_bound<TYPE>(W + r * ldw + int64_t(g) * Format<TYPE>::kBytes);
-            else
-                row8<TYPE>(W + r * ldw, g * 8, K, wide, e[j]);
+            row8<TYPE>(W + r * ldw, int(i - r * per) * 8, K, wide, e[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < (kBoundByScale<TYPE> ? 1 : 8); ++i) m = max(m, __float_as_uint(e[j][i]) & 0x7fffffffu);
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[j][i]) & 0x7fffffffu);
     }
     __shared__ uint32_t tops[4];
     m = wave_max(m);

@@ -437,7 +437,7 @@ int launch_planes(const PlaneArgs& a, hipStream_t st) {
 template <int TYPE>
 int launch_top(const uint8_t* W, int64_t ldw, int64_t rows, int64_t K, uint32_t* top, hipStream_t st) {
     host::clear_last_error();
-    const int64_t per = kBoundByScale<TYPE> ? K / Format<TYPE>::kBlock : host::cdiv(K, 8);
+    const int64_t per = host::cdiv(K, 8);
     top_kernel<TYPE><<<dim3(uint32_t(std::min<int64_t>(host::cdiv(rows * per, 1024), 2048))), dim3(256), 0, st>>>(
         W, ldw, rows, int(K), top, wide_rows(TYPE, ldw, K), uint32_t(per));
     return host::launch_status();
