@@ -71,11 +71,12 @@ int64_t retro_embedding_backward_workspace_size(int64_t K, int64_t N, int64_t T)
  * as they are where x and W are both F16 or both BF16; otherwise in one or two F16
  * parts scaled by powers of two (one a row of x, one for W): F16, BF16, MXFP4 and
  * NVFP4 in one, the others in two, which leaves at most 2^-22 of a value and
- * 2^-38 of the largest one of x's row, or of W (or 2^-151). Up to 64 tokens through a
+ * 2^-38 of the largest one of x's row, or of W's finite ones (or 2^-151). Up to 64 tokens through a
  * packed table of contiguous rows meet its codes as they are, x in the same parts; those
  * of Q2_K, Q3_K and NVFP4 meet its F32 values in F32. Sums are F32. An infinite or NaN
  * logit gives a NaN or infinite loss for its token, only -inf counts as a probability
- * of 0. N == 0 gives lse = -inf.
+ * of 0; an infinity in W makes the logits of an F32 x NaN where it meets x's two parts.
+ * N == 0 gives lse = -inf.
  * workspace: retro_cross_entropy_workspace_size bytes.
  */
 int retro_cross_entropy(int type, const void *W, int64_t ldw, int xtype, const void *X, int64_t ldx, int idtype,

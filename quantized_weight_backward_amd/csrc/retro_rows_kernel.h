@@ -74,8 +74,9 @@ __global__ __launch_bounds__(256) void planes_kernel(const uint8_t* __restrict__
     }
 }
 
-// The largest magnitude's bits of a table, NaN above all: of the values themselves, since
-// a block's scale says nothing of them where its codes are small or zero.
+// The largest finite magnitude's bits of a table: of the values themselves, since a
+// block's scale says nothing of them where its codes are small or zero. An infinity or NaN
+// is its own row's logit and says nothing of the others.
 template <int TYPE>
 __global__ __launch_bounds__(256) void top_kernel(const uint8_t* __restrict__ W, int64_t ldw, int64_t rows, int K,
                                                   uint32_t* __restrict__ top, int wide, uint32_t per) {
@@ -93,7 +94,10 @@ __global__ __launch_bounds__(256) void top_kernel(const uint8_t* __restrict__ W,
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(e[j][i]) & 0x7fffffffu);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = mx::abs_bits(e[j][i]);
+                m = max(m, bits < 0x7f800000u ? bits : 0u);
+            }
     }
     __shared__ uint32_t tops[4];
     m = wave_max(m);

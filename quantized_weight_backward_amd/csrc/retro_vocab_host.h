@@ -38,7 +38,7 @@ struct PlaneArgs {
     int64_t rows, K;
     uint16_t* out;
     int64_t plane;        // elements from the first part's plane to the second's
-    const uint32_t* top;  // bits of the table's largest magnitude (parts > 0)
+    const uint32_t* top;  // bits of the table's largest finite magnitude (parts > 0)
     int parts;            // 0: W's own 16-bit elements; 1, 2: F16 parts scaled by top's power of two
 };
 
@@ -46,7 +46,7 @@ template <int TYPE>
 int launch_embed(int ytype, const EmbedArgs& a, hipStream_t st);
 template <int TYPE>
 int launch_planes(const PlaneArgs& a, hipStream_t st);
-// *top = the larger of *top and the largest magnitude's bits of `rows` rows.
+// *top = the larger of *top and the largest finite magnitude's bits of `rows` rows.
 template <int TYPE>
 int launch_top(const uint8_t* W, int64_t ldw, int64_t rows, int64_t K, uint32_t* top, hipStream_t st);
 

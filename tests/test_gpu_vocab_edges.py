@@ -80,3 +80,32 @@ def test_a_block_of_zeros_under_a_large_scale(q, wtype, scale, zeros):
             (wx, bx), _ = ref.gradients(values, x.double(), t, g, part, dtype, torch.float32,
                                         2.0 ** -11 if dtype == torch.bfloat16 else 0.0)
             close(dx, wx, bx, "dx")
+
+
+@pytest.mark.parametrize("xtype,size", [(torch.bfloat16, 1e6), (torch.bfloat16, 1e-30), (torch.float16, 1e5),
+                                        (torch.float16, 1e-4)], ids=lambda v: NAME.get(v, str(v)))
+def test_a_row_of_the_head_that_holds_an_infinity(q, xtype, size):
+    """A logit of -inf is a probability of 0; the other rows' logits are what they were."""
+    T, N, K, row = 80, 200, 64, 5
+    w = torch.randn((N, K), generator=gen(1)) * size
+    w[row, 0] = -float("inf")
+    x = torch.randn((T, K), generator=gen(2)) / (size * K ** 0.5)
+    x[:, 0] = x[:, 0].abs() + x.abs().max() / 8
+    x = x.to(xtype)
+    assert (x[:, 0] > 0).all() and torch.isfinite(x).all()
+    t = torch.randint(row + 1, N, (T,), generator=gen(3))
+    want, want_lse, _, l = ref.cross_entropy(w.double(), x.double(), t)
+    assert (l[:, row] == -float("inf")).all()
+    finite = w.double()
+    finite[row, 0] = 0
+    bound = ref.loss_error(finite, x.double(), want_lse)
+    loss, lse = q.cross_entropy(wl.F32, w.cuda(), x.cuda(), t.cuda())
+    close(lse, want_lse, bound, "lse")
+    close(loss, want, bound, "loss")
+    g = torch.full((T,), 2.0 ** -10)
+    dx, _ = q.cross_entropy_backward(wl.F32, w.cuda(), x.cuda(), t.cuda(), lse, g.cuda())
+    # the row without its infinity has nothing of the probability either: take it out
+    keep = torch.arange(N) != row
+    (wx, bx), _ = ref.gradients(finite[keep], x.double(), t - 1, g, 2.0 ** -11, xtype, torch.float32, 2.0 ** -11)
+    close(dx[:, 1:], wx[:, 1:], bx[:, 1:], "dx")
+    assert torch.isnan(dx[:, 0]).all()  # 0 times an infinity
