@@ -251,11 +251,12 @@ int parts_of(int type) {
     return type == RETRO_F16 || type == RETRO_BF16 || type == RETRO_MXFP4 || type == RETRO_NVFP4 ? 1 : 2;
 }
 
-// And in the gradients of a BF16 x, where one part of 11 bits leaves the result's 8 as
-// they are: what the logits lose by it is an eighth of what x's own rounding put into
-// them. Two parts double both products: loss and gradient of 2048 x 131072 x 4096
-// through Q8_0 took 13.2 ms with two and 9.0 with one. An F32 dW takes its parts in full.
-int grad_parts_of(int type, int xtype, bool weight_grad) {
+// And in dX of a BF16 x, where a value's 11 bits leave the sum's 8 as they are: an error
+// of 2^-12 of each weight, beside d's; two parts double the product. (Not in the logits
+// that d is made of: d = p - 1 of a confident token is a small difference, off by what its
+// logits and lse are. Logits of one part, beside an lse of two, put an error of 1e-3 into
+// d, several times 1 - p.) Beside an F32 dW, for which d has two parts, W has them too.
+int sum_parts_of(int type, int xtype, bool weight_grad) {
     return xtype == RETRO_BF16 && !(weight_grad && type == RETRO_F32) ? 1 : parts_of(type);
 }
 
@@ -433,7 +434,7 @@ Backward backward_plan(int type, int64_t ldw, int xtype, bool weight_grad, bool 
     }
     const bool narrow = is_narrow(type, xtype), direct = is_direct(type, xtype, ldw, K);
     const int64_t Kp = vocab::padded(K), Tp = vocab::padded(T);
-    const int px = narrow ? 1 : parts_of(xtype), pw = narrow ? 1 : grad_parts_of(type, xtype, weight_grad);
+    const int px = narrow ? 1 : parts_of(xtype), pw = narrow ? 1 : parts_of(type);
     const int pd = xtype == RETRO_F32 || (weight_grad && type == RETRO_F32) ? 2 : 1;
     p.piece = grad_piece(K, N, T);
     p.x = b.take(plane_bytes(px, Tp, Kp));
@@ -730,7 +731,7 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
     float* factor = narrow ? nullptr : reinterpret_cast<float*>(ws + p.factor);
     uint32_t* top = narrow ? nullptr : reinterpret_cast<uint32_t*>(ws + p.top);
     float *weight = reinterpret_cast<float*>(ws + p.weight), *unscale = reinterpret_cast<float*>(ws + p.unscale);
-    const int px = narrow ? 1 : parts_of(c.xtype), pw = narrow ? 1 : grad_parts_of(c.type, c.xtype, dW != nullptr);
+    const int px = narrow ? 1 : parts_of(c.xtype), pw = narrow ? 1 : parts_of(c.type);
     const int pd = c.xtype == RETRO_F32 || (dW && c.type == RETRO_F32) ? 2 : 1;
     const int64_t Kp = vocab::padded(c.K), Tp = vocab::padded(c.T);
     if (!narrow) RETRO_TRY(head_top(c, top));
@@ -781,7 +782,7 @@ int backward(const Call& c, const float* lse, const float* dloss, void* dX, int6
             s.b = g.a;
             s.steps = uint32_t(rows_p / vocab::kStepK);
             s.splits = uint32_t(p.splits);
-            set_pairs(s, c.xtype == RETRO_F32 ? 2 : 1, pw);
+            set_pairs(s, c.xtype == RETRO_F32 ? 2 : 1, narrow ? 1 : sum_parts_of(c.type, c.xtype, dW != nullptr));
             s.out = sums;
             s.ldo = c.K;
             s.split_stride = c.T * c.K;

@@ -109,3 +109,68 @@ def test_a_row_of_the_head_that_holds_an_infinity(q, xtype, size):
     (wx, bx), _ = ref.gradients(finite[keep], x.double(), t - 1, g, 2.0 ** -11, xtype, torch.float32, 2.0 ** -11)
     close(dx[:, 1:], wx[:, 1:], bx[:, 1:], "dx")
     assert torch.isnan(dx[:, 0]).all()  # 0 times an infinity
+
+
+# ---------------------------------------------------------------- confident tokens, small losses
+
+def confident(wtype, T):
+    """(W, values, x, targets): a head of values d q, d of 11 bits and q of 8, and tokens of
+    one 1 or -1 for each of up to 16 columns, the largest of their target's row: their
+    probabilities are from 0.9 to 0.9999. Each logit is a whole number of steps of d, below
+    2^11 * 127 * 16 < 2^22 of them, as is each partial sum of parts of it, so that F32's sums
+    of it are exact in whatever order."""
+    N, K = 257, 64
+    rng = np.random.Generator(np.random.PCG64(21))
+    d, code = np.float16(0.010765), rng.integers(-127, 128, size=(N, K), dtype=np.int8)
+    assert int(d.view(np.uint16)) & 1  # all its 11 bits are used
+    values = torch.from_numpy(code.astype(np.float64)) * float(d)
+    if wtype == wl.Q8_0:
+        blocks = np.zeros((N, K // 32, 34), dtype=np.uint8)
+        blocks[..., :2] = np.frombuffer(d.tobytes(), dtype=np.uint8)
+        blocks[..., 2:] = code.reshape(N, K // 32, 32).view(np.uint8)
+        W = torch.from_numpy(blocks.reshape(N, -1))
+    else:
+        W = values.float()
+        assert torch.equal(W.double(), values)
+    targets = torch.randint(0, N, (T,), generator=gen(5))
+    rows = values[targets]
+    columns = torch.topk(rows.abs(), 16, 1).indices
+    some = torch.arange(16)[None] < (9 + torch.arange(T) % 8)[:, None]
+    x = torch.zeros((T, K), dtype=torch.float64).scatter_(1, columns, torch.gather(rows, 1, columns).sign() * some)
+    return W, values, x, targets
+
+
+@pytest.mark.parametrize("T", [33, 70, 300])
+@pytest.mark.parametrize("wtype", [wl.Q8_0, wl.F32], ids=wl.TYPE_NAMES.get)
+def test_gradient_of_confident_tokens(q, wtype, T):
+    """d = p - 1 is a small difference: the logits of the gradients are those that lse is of."""
+    W, values, x, t = confident(wtype, T)
+    g = torch.rand(T, generator=gen(6)) + 0.5
+    d_x, d_w, d_t = x.bfloat16().cuda(), W.cuda(), t.cuda()
+    loss, lse = q.cross_entropy(wtype, d_w, d_x, d_t)
+    l = x @ values.T
+    exact_lse = torch.logsumexp(l, 1)
+    p = torch.exp(l - exact_lse[:, None])
+    rest = 1 - p[torch.arange(T), t]
+    assert ((rest < 0.2) & (rest > 1e-6)).all() and (rest < 1e-3).any() and (rest > 1e-2).any()
+    # logits are exact: what is left is the sum of exponentials (up to 128 a lane, 32 runs a
+    # thread, 16 joins), exp and log below 2^-20, and lse's own steps
+    off = (128 + 32 + 16) * 2.0 ** -24 + 2.0 ** -20 + exact_lse.abs() * 2.0 ** -23
+    close(lse, exact_lse, off, "lse")
+    dx, _ = q.cross_entropy_backward(wtype, d_w, d_x, d_t, lse, g.cuda())
+    d = p.clone()
+    d[torch.arange(T), t] = -rest
+    w = values.abs()
+    # exp's argument is off by lse's error and a rounding, exp itself by |argument| 2^-24 and a step
+    ed = 2 * p * (off[:, None] + 2.0 ** -22 * (1 + (l - exact_lse[:, None]).abs()))
+    ed = ed + 2.0 ** -11 * d.abs() + 2.0 ** -38
+    N = len(values)
+    # the products: d and the head's values in 11 bits each, F32 sums over the head
+    bound = ed @ w + (2.0 ** -11 + (N / 16 + 64) * ref.STEP) * (d.abs() @ w) + 2.0 ** -38 * w.max() * d.abs().sum(1, keepdim=True)
+    want = g.double()[:, None] * (d @ values)
+    bound = g.double()[:, None] * bound
+    bound = bound + ref.half_step(torch.bfloat16) * (want.abs() + bound)
+    # it says something: below a tenth of the gradient of a token that p leaves a thousandth
+    size = want.norm(dim=1)
+    assert (bound.norm(dim=1) < size / 10)[rest > 1e-3].all()
+    close(dx, want, bound, "dx")
