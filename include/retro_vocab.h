@@ -67,6 +67,8 @@ int64_t retro_embedding_backward_workspace_size(int64_t K, int64_t N, int64_t T)
  *     l[t][n] = sum_k x[t][k] W[n][k]
  *     lse[t]  = log sum_n exp l[t][n]                           F32, of every token
  *     loss[t] = lse[t] - l[t][targets[t]]                       F32; 0 where the target is no token
+ * (the loss is made of differences of logits: a small one has digits that lse, beside a
+ * large logit, has not).
  * x is T x K of xtype, rows ldx elements apart. The operands enter the matrix cores
  * as they are where x and W are both F16 or both BF16; otherwise in one or two F16
  * parts scaled by powers of two (one a row of x, one for W): F16, BF16, MXFP4 and

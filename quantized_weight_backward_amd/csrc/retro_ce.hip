@@ -95,9 +95,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const float2* __restrict__
         __syncthreads();
     }
     if (p || t >= T) return;
-    const float l = sum == 0.f ? top : top + logf(sum);
-    lse[t] = l;
-    loss[t] = vocab::token_at(targets, wide_targets, t, N) >= 0 ? l - at_target[t] : 0.f;
+    // the loss from differences: a small one beside a large logit has its digits below lse's
+    const float over = sum == 0.f ? 0.f : logf(sum);
+    lse[t] = top + over;
+    loss[t] = vocab::token_at(targets, wide_targets, t, N) >= 0 ? top - at_target[t] + over : 0.f;
 }
 
 // Each token's factor in d^T: dloss and x's own, 0 where it is not learnt from, all

@@ -174,3 +174,31 @@ def test_gradient_of_confident_tokens(q, wtype, T):
     size = want.norm(dim=1)
     assert (bound.norm(dim=1) < size / 10)[rest > 1e-3].all()
     close(dx, want, bound, "dx")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("T", [5, 90, 600])
+def test_small_losses_beside_large_logits(q, kind, T):
+    """Logits of 4096, the target's 5 to 14 above: whole eighths, exact in F32."""
+    N, K = 127, 128
+    w = torch.zeros((N, K))
+    w[:, 0] = 64
+    w[torch.arange(N), torch.arange(N) + 1] = 8
+    t = torch.randint(0, N, (T,), generator=gen(1))
+    a = 5 + torch.arange(T) % 10
+    x = torch.zeros((T, K))
+    x[:, 0] = 64
+    x[torch.arange(T), t + 1] = a / 8
+    if kind == "q8_0":
+        blocks = np.zeros((N, K // 32, 34), dtype=np.uint8)
+        blocks[..., :2] = np.frombuffer(np.float16(1).tobytes(), dtype=np.uint8)
+        blocks[..., 2:] = w.numpy().astype(np.int8).view(np.uint8).reshape(N, K // 32, 32)
+        wtype, W, x = wl.Q8_0, torch.from_numpy(blocks.reshape(N, -1)), x.bfloat16()
+    else:
+        dtype = {v: k for k, v in NAME.items()}[kind]
+        wtype, W, x = TYPE[dtype], w.to(dtype), x.to(dtype)
+    loss, lse = q.cross_entropy(wtype, W.cuda(), x.cuda(), t.cuda())
+    want = torch.log1p((N - 1) * torch.exp(-a.double()))
+    # (sums of exponentials, exp and log) as for any loss, and no step of a logit of 4096 (2^-11)
+    close(loss, want, torch.full_like(want, (128 + 32 + 16) * 2.0 ** -24 + 2.0 ** -20), "loss")
+    close(lse, want + 4096 + a, torch.full_like(want, 2.0 ** -11), "lse")
