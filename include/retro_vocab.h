@@ -52,9 +52,9 @@ int retro_embedding(int type, const void *W, int64_t ldw, int idtype, const void
  * dY is T x K of ytype; dW is N x K of wtype (RETRO_F32, RETRO_F16 or RETRO_BF16),
  * rows ldw elements apart. Without accumulate every row is written, zeros where no
  * token has it; with it only the rows that a token has are touched. The sum is
- * taken in F32 over rising t, in runs (the list sorted by id and t is cut into 64s, or
- * 16s up to 4096 tokens) whose sums are then added in their order; scale and dW's old
- * value enter in F32, and the result is rounded to wtype once.
+ * taken in F32 over rising t, in runs (the list sorted by id and t is cut into 16s, or into
+ * 64s where ceil(T / 64) * ceil(K / 512) is 2048 and more) whose sums are then added in
+ * their order; scale and dW's old value enter in F32, and the result is rounded to wtype once.
  * workspace: retro_embedding_backward_workspace_size bytes.
  */
 int retro_embedding_backward(int idtype, const void *ids, int ytype, const void *dY, int64_t ldy, float scale, int wtype,

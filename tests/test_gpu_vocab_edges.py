@@ -202,3 +202,82 @@ def test_small_losses_beside_large_logits(q, kind, T):
     # (sums of exponentials, exp and log) as for any loss, and no step of a logit of 4096 (2^-11)
     close(loss, want, torch.full_like(want, (128 + 32 + 16) * 2.0 ** -24 + 2.0 ** -20), "loss")
     close(lse, want + 4096 + a, torch.full_like(want, 2.0 ** -11), "lse")
+
+
+# ---------------------------------------------------------------- the gradient of wide tables
+
+def wide_gradient(ids, dy, N, scale):
+    """(dW, sum of magnitudes, tokens a row) in 64 bits, on the device."""
+    known = (ids >= 0) & (ids < N)
+    at = torch.where(known, ids, N).long()
+    y = dy.double() * scale
+    dw = torch.zeros((N + 1, dy.shape[1]), dtype=torch.float64, device=dy.device)
+    size = dw.clone()
+    dw.index_add_(0, at, y)
+    size.index_add_(0, at, y.abs_())
+    return dw[:N], size[:N], torch.bincount(at, minlength=N + 1)[:N].double()
+
+
+def wide_bound(dw, size, count, dtype, old=None):
+    # each addition of a row's F32 sum, and the scale's product, rounds what is at most the sum of magnitudes
+    b = (count[:, None] + 2) * 2.0 ** -24 * size
+    if old is not None:
+        b += 2.0 ** -24 * (old.abs() + size)
+    return b + ref.half_step(dtype) * (dw.abs() + b) + torch.finfo(dtype).smallest_normal * ref.half_step(dtype)
+
+
+def ids_of(T, N, seed, kind):
+    g = gen(seed)
+    if kind == "one":
+        ids = torch.full((T,), N // 2)
+    elif kind == "frequent":  # half of them one id, the others spread
+        ids = torch.where(torch.rand(T, generator=g) < 0.5, 1, torch.randint(0, N, (T,), generator=g))
+    else:
+        ids = torch.randint(0, N, (T,), generator=g)
+    return torch.where(torch.rand(T, generator=g) < 0.1, torch.tensor([-1, N])[torch.randint(0, 2, (T,), generator=g)], ids)
+
+
+# several chunks of 512 columns, the last one ragged; runs of 16 tokens, and, where tokens times
+# columns are 2048 waves and more, of 64, on both sides of that
+WIDE = [(1, 9, 513, "spread"), (63, 5, 1000, "frequent"), (300, 40, 1029, "spread"), (777, 3200, 1000, "frequent"),
+        (2000, 7, 520, "one"), (8128, 30, 8192, "frequent"), (8200, 30, 8191, "spread"), (16320, 100, 4096, "spread"),
+        (16384, 100, 4096, "frequent"), (16385, 2, 4100, "spread"), (43700, 11, 1029, "one"), (65600, 900, 520, "frequent"),
+        (131009, 500, 24, "spread"), (131072, 3, 8, "frequent"), (140001, 5000, 33, "one")]
+
+
+@pytest.mark.parametrize("T,N,K,kind", WIDE, ids=str)
+def test_embedding_backward_of_wide_tables(q, T, N, K, kind):
+    dtype = FLOATS[(T + K) % 3]
+    ids = ids_of(T, N, T, kind).to(torch.int32 if T % 2 else torch.int64).cuda()
+    dy = torch.randn((T, K), generator=torch.Generator(device="cuda").manual_seed(T), device="cuda").to(dtype)
+    dw, size, count = wide_gradient(ids, dy, N, 0.75)
+
+    def near(got, want, bound):
+        assert torch.isfinite(got).all()
+        assert ((got.double() - want).abs() <= bound).all()
+
+    got = q.embedding_backward(ids, dy, N, scale=0.75)
+    near(got, dw, wide_bound(dw, size, count, torch.float32))
+    assert not got[count == 0].any()
+    assert torch.equal(got, q.embedding_backward(ids, dy, N, scale=0.75))
+    # rows of a wider tensor, of the gradient's own type: written, and added to
+    base = torch.randn((N, K + 5), generator=gen(5)).to(dtype).cuda()
+    out = base.clone()
+    q.embedding_backward(ids, dy, N, scale=0.75, out=out[:, 2:2 + K], dtype=dtype)
+    near(out[:, 2:2 + K], dw, wide_bound(dw, size, count, dtype))
+    assert torch.equal(out[:, :2], base[:, :2]) and torch.equal(out[:, 2 + K:], base[:, 2 + K:])
+    out = base.clone()
+    q.embedding_backward(ids, dy, N, scale=0.75, out=out[:, 2:2 + K], accumulate=True)
+    old = base[:, 2:2 + K].double()
+    near(out[:, 2:2 + K], dw + old, wide_bound(dw + old, size, count, dtype, old))
+    assert torch.equal(out[count == 0], base[count == 0])
+    assert torch.equal(out[:, :2], base[:, :2]) and torch.equal(out[:, 2 + K:], base[:, 2 + K:])
+
+
+def test_embedding_backward_of_whole_tokens(q):
+    """Whole numbers, whose sums are exact: equal, whatever the runs are."""
+    for T, N, K in ((16384, 50, 4096), (3000, 9, 700), (131100, 77, 16)):
+        ids = ids_of(T, N, 3, "frequent").cuda()
+        dy = torch.randint(-8, 9, (T, K), generator=gen(2)).to(torch.bfloat16).cuda()
+        dw, _, _ = wide_gradient(ids, dy, N, 0.5)
+        assert torch.equal(q.embedding_backward(ids, dy, N, scale=0.5).double(), dw)
