@@ -281,3 +281,31 @@ def test_embedding_backward_of_whole_tokens(q):
         dy = torch.randint(-8, 9, (T, K), generator=gen(2)).to(torch.bfloat16).cuda()
         dw, _, _ = wide_gradient(ids, dy, N, 0.5)
         assert torch.equal(q.embedding_backward(ids, dy, N, scale=0.5).double(), dw)
+
+
+# ---------------------------------------------------------------- the head's gradient alone
+
+@pytest.mark.parametrize("xtype,wdtype,T,N,K", [
+    (torch.bfloat16, torch.bfloat16, 70, 500, 128), (torch.bfloat16, torch.bfloat16, 300, 33100, 40),
+    (torch.float32, torch.float32, 70, 33000, 64), (torch.float16, torch.float32, 5, 300, 33),
+    (torch.float32, torch.bfloat16, 129, 1000, 72), (torch.float16, torch.float16, 1, 7, 3)], ids=str)
+def test_the_gradient_of_the_head_alone(q, xtype, wdtype, T, N, K):
+    """dX not asked for: the same bits of dW, through a workspace that is not cleared."""
+    w = (torch.randn((N, K), generator=gen(1)) * 0.3).to(wdtype).cuda()
+    x = torch.randn((T, K), generator=gen(2)).to(xtype).cuda()
+    t = torch.randint(-1, N, (T,), generator=gen(3)).cuda()
+    g = torch.rand(T, generator=gen(4)).cuda()
+    wt, xt = TYPE[wdtype], TYPE[xtype]
+    _, lse = q.cross_entropy(wt, w, x, t)
+    _, want = q.cross_entropy_backward(wt, w, x, t, lse, g, weight_grad=True)
+    ldw = K * w.element_size()
+    need = q.lib.retro_cross_entropy_backward_workspace_size(wt, ldw, xt, 1, K, N, T)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    got = torch.full((N, K + 3), 9.0, dtype=wdtype, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for _ in range(2):
+        assert q.lib.retro_cross_entropy_backward(
+            wt, w.data_ptr(), ldw, xt, x.data_ptr(), K, 27, t.data_ptr(), lse.data_ptr(), g.data_ptr(), None, 0,
+            got.data_ptr(), K + 3, K, N, T, ws.data_ptr(), need, stream) == 0
+        assert torch.equal(got[:, :K], want) and (got[:, K:] == 9.0).all()
+        assert (ws[need:] == 255).all()
