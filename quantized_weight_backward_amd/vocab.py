@@ -6,10 +6,10 @@ marshals torch tensors into the C ABI and nothing else.
     cross_entropy           softmax cross entropy through a resident head, no logits kept
     cross_entropy_backward  its gradients with respect to the tokens and a float head
 
-A table W of N rows x K is given as elsewhere in this package: a contiguous device
-tensor of N * row_bytes(wtype, K) bytes, or a 2-D uint8 view of N rows whose first
-row_bytes bytes hold a row; one of floats also as a 2-D view of its own dtype with
-contiguous rows. Ids and targets are 1-D contiguous int32 or int64 device tensors;
+A table W of N rows x K is a 2-D uint8 tensor or view of N rows whose first
+row_bytes(wtype, K) bytes hold a row; or, without such rows, a contiguous device tensor
+of N * row_bytes bytes; one of floats also a 2-D view of its own dtype with contiguous
+rows. Ids and targets are 1-D contiguous int32 or int64 device tensors;
 a value outside 0 .. N - 1 is no token (padding, or not learnt from).
 
 Every call runs asynchronously on `stream` (default: torch's current stream of the
@@ -41,14 +41,14 @@ def _table(wtype, W, K):
         raise ValueError("K must be positive")
     if W.dim() == 2 and W.dtype == _DTYPES.get(wtype) and W.shape[1] == K:
         return W.shape[0], _row_stride(W, "W") * W.element_size()
+    if W.dim() == 2 and W.dtype == torch.uint8 and W.shape[1] >= rb:
+        return W.shape[0], (_row_stride(W, "W") if W.shape[0] > 1 else rb)
     if W.is_contiguous():
         nbytes = W.numel() * W.element_size()
         if nbytes % rb:
             raise ValueError(f"W holds {nbytes} bytes, no whole number of rows of {rb}")
         return nbytes // rb, rb
-    if W.dtype != torch.uint8 or W.dim() != 2 or W.shape[1] < rb:
-        raise ValueError(f"a strided W must be a uint8 view of rows of at least {rb} bytes")
-    return W.shape[0], (_row_stride(W, "W") if W.shape[0] > 1 else rb)
+    raise ValueError(f"a strided W must be a uint8 view of rows of at least {rb} bytes")
 
 
 def _tokens(t, name, T=None):
