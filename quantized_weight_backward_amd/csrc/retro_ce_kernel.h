@@ -45,7 +45,9 @@ constexpr int kStepBytes = 128;  // 64 elements of a row
 // alone, on random operands, they run at 1.86 PFLOP/s, these at 2.13. Written as
 // assembly so that a result stays in its registers: the compiler moves results of this
 // size from one set to another, runs out of them and spills in the loop. The wait states
-// are for operands that a vector instruction has just written.
+// are for operands that a vector instruction has just written. That no result is moved or
+// read too early is the compiler's doing, and read from the built code by a test
+// (tests/test_vocab_products_build.py).
 __device__ __forceinline__ void mfma(__bf16, const i32x4& a, const i32x4& b, f32x4& c) {
     asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
