@@ -97,7 +97,7 @@ int64_t retro_cross_entropy_workspace_size(int type, int64_t ldw, int xtype, int
  * dX may be NULL where dW is not. Both are overwritten. d and dloss * d (scaled by a
  * power of two) enter the products in as many bits as the result has: one part of
  * 11 bits (8 where x and W are BF16), two for F32 results. The logits are those of
- * retro_cross_entropy, so that d keeps its digits where it is small. W enters dX's sum as it
+ * retro_cross_entropy, so that d is off by their F32 sums and a step of lse alone. W enters dX's sum as it
  * does them, but where x is BF16 in one part of 11 bits (unless an F32 dW is wanted).
  * workspace: retro_cross_entropy_backward_workspace_size bytes.
  */

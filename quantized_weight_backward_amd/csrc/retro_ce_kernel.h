@@ -183,7 +183,8 @@ __device__ __forceinline__ s16x4 column4(const uint8_t* lds) {
         (__attribute__((address_space(3))) s16x4*)(const_cast<uint8_t*>(lds)));
 }
 
-// The parts of v as element `at` of w.
+// The parts of v as element `at` of w: d in the bits that the result has (8 or 11, two parts
+// for F32), whose rounding is that of the result's own size; two parts of it double a product.
 template <typename E, int PARTS>
 __device__ __forceinline__ void put_parts(float v, int at, u16x4 (&w)[PARTS]) {
     w[0][at] = __builtin_bit_cast(uint16_t, E(v));

@@ -76,7 +76,8 @@ __global__ __launch_bounds__(256) void planes_kernel(const uint8_t* __restrict__
 
 // The largest finite magnitude's bits of a table: of the values themselves, since a
 // block's scale says nothing of them where its codes are small or zero. An infinity or NaN
-// is its own row's logit and says nothing of the others.
+// is its own row's logit and says nothing of the others. Q8_0 131072 x 4096 223 us, 2.5 TB/s:
+// bound by decoding (the scales alone took 98).
 template <int TYPE>
 __global__ __launch_bounds__(256) void top_kernel(const uint8_t* __restrict__ W, int64_t ldw, int64_t rows, int K,
                                                   uint32_t* __restrict__ top, int wide, uint32_t per) {
