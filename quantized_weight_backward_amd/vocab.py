@@ -42,7 +42,8 @@ def _table(wtype, W, K):
     if W.dim() == 2 and W.dtype == _DTYPES.get(wtype) and W.shape[1] == K:
         return W.shape[0], _row_stride(W, "W") * W.element_size()
     if W.dim() == 2 and W.dtype == torch.uint8 and W.shape[1] >= rb:
-        return W.shape[0], (_row_stride(W, "W") if W.shape[0] > 1 else rb)
+        ldw = _row_stride(W, "W")
+        return W.shape[0], (ldw if W.shape[0] > 1 else rb)
     if W.is_contiguous():
         nbytes = W.numel() * W.element_size()
         if nbytes % rb:

@@ -46,6 +46,6 @@ def test_views(table):
     assert table(q.Q8_0, wide[:, :34], 32) == (9, 100)
     assert table(q.Q8_0, wide[:, 2:80], 32) == (9, 100)
     assert table(q.Q8_0, wide[::2, :34], 32) == (5, 200)
-    for W in (wide[:, :33], wide.T, wide.view(torch.int16)[:, :20]):
+    for W in (wide[:, :33], wide.T, wide.view(torch.int16)[:, :20], wide[:, ::2], wide[:1, ::2]):
         with pytest.raises(ValueError):
             table(q.Q8_0, W, 32)
